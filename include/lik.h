@@ -405,6 +405,147 @@ lik_status lik_maxsim_kd_ce_step(const void* Q, const void* D, lik_dtype dtype, 
                                  float* grad_scores, void* grad_Q, void* grad_D,
                                  int grads_in_input_dtype, cudaStream_t stream);
 
+/* ------------------------------------ training objectives over logits --
+ * Losses over rows of logits, each with its gradient in the logits.  A row
+ * is a query's scores over its candidate documents (the rows the MaxSim
+ * entry points write) or a token's logits over a vocabulary.  The pages have
+ * no counterpart: they train with cross-entropy losses only.  Three losses:
+ *   lik_distill_topk_*     divergence from a teacher's top logits
+ *   lik_policy_loss_*      clipped policy loss with a KL term to a reference
+ *   lik_preference_loss_*  paired log ratios of chosen and rejected sequences
+ * in three forms: _fwd (the loss, and the row_state its backward needs),
+ * _bwd (the gradient from a row_state), and _step (loss and gradient in one
+ * call, each row of logits read from memory once where it fits on chip).
+ *
+ * Shared by all of them, for a row z[0, cols) and a logit scale s (1 /
+ * temperature), 0 < s finite:
+ *     q = softmax(s * z),   log q_c = s * (z_c - max z) - log sum exp(s * (z - max z))
+ *   - logits [rows, cols], fp32, fp16 or bf16; row r starts at element r *
+ *     row_stride, row_stride >= cols (its elements are contiguous).  Any
+ *     element-aligned address: rows need no 16-byte alignment.
+ *   - grad_logits [rows, cols], the logits' dtype, row r at element r *
+ *     grad_stride, overwritten.  Every row is written, zeros included; the
+ *     gaps between rows are not touched.  It may be the logits buffer itself
+ *     (same address and stride); it must not overlap it otherwise.  Rows
+ *     whose gradient starts at the same address modulo 16 as their logits
+ *     are written with 16-byte stores.
+ *   - Sums, softmax statistics and losses are fp32 or wider; a gradient is
+ *     rounded to its dtype once.  Results do not depend on the run: sums are
+ *     taken in a fixed order (no atomics).
+ *   - Rows that are left out: a weight of 0, a target outside [0, cols), no
+ *     teacher entry with any mass, every logit -inf.  They have loss 0 and a
+ *     zero gradient whatever else they hold (their logits may be NaN, except
+ *     for the last two kinds).  A logit of -inf in any other row is a masked
+ *     column: probability 0, gradient 0.  A row with a NaN or +inf logit that
+ *     is not left out gives NaN.
+ *   - weights are fp32 and carry mask, normalisation and any loss scale
+ *     (fp16 gradients usually need one) together; NULL weighs every row (or
+ *     pair) 1 / rows (1 / pairs).
+ *   - row_state [rows, 4], fp32, 16-byte aligned: written by _fwd, read by
+ *     _bwd with the same arguments, otherwise opaque.
+ *   - grad_loss [1], fp32 device: the upstream gradient that _bwd multiplies
+ *     by; NULL means 1.
+ *   - Sizes: 0 <= rows <= 2^31 - 1, 1 <= cols <= 2^30.  Zero rows write a
+ *     loss of 0.
+ */
+
+/*
+ * Distillation from a teacher's top logits: the Kullback-Leibler divergence
+ * of the row's softmax from a teacher known at k columns,
+ *     p_j = exp(s * t_j) / sum over the valid entries of exp(s * t)   (teacher_lse NULL)
+ *     p_j = exp(s * t_j - teacher_lse[r])                             (else)
+ *     row_loss[r] = sum_j p_j * (log p_j - log q[index_j])
+ *     *loss       = sum_r weight[r] * row_loss[r]
+ *     grad[r, c]  = weight[r] * s * ((sum_j p_j) * q_c - sum over index_j == c of p_j)
+ * The teacher's logits get the same scale s; teacher_lse is the log-sum-exp
+ * of its scaled logits over all its columns.  An entry whose index is
+ * outside [0, cols) is padding, an entry of -inf has no mass; an index that
+ * occurs twice in a row counts twice.
+ *   teacher_index [rows, k] int32, teacher_logits [rows, k] of teacher_dtype
+ *   (fp32, fp16, bf16), 0 <= k <= 1024, contiguous; teacher_lse [rows] fp32
+ *   or NULL; row_weight [rows] fp32 or NULL; loss [1], row_loss [rows] fp32.
+ */
+lik_status lik_distill_topk_fwd(const void* logits, lik_dtype dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                                const int32_t* teacher_index, const void* teacher_logits, lik_dtype teacher_dtype,
+                                int64_t k, const float* teacher_lse, const float* row_weight, float scale,
+                                float* loss, float* row_loss, float* row_state, cudaStream_t stream);
+
+lik_status lik_distill_topk_bwd(const void* logits, lik_dtype dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                                const int32_t* teacher_index, const void* teacher_logits, lik_dtype teacher_dtype,
+                                int64_t k, const float* teacher_lse, float scale, const float* row_state,
+                                const float* grad_loss, void* grad_logits, int64_t grad_stride,
+                                cudaStream_t stream);
+
+lik_status lik_distill_topk_step(const void* logits, lik_dtype dtype, int64_t rows, int64_t cols,
+                                 int64_t row_stride, const int32_t* teacher_index, const void* teacher_logits,
+                                 lik_dtype teacher_dtype, int64_t k, const float* teacher_lse,
+                                 const float* row_weight, float scale, float* loss, float* row_loss,
+                                 void* grad_logits, int64_t grad_stride, cudaStream_t stream);
+
+/*
+ * Clipped policy loss with a KL term: row r is a token that was sampled,
+ * y = target[r], lp = log q_y, ratio = exp(lp - old_logp[r]), A = advantage[r]
+ *     row_loss[r] = -min(ratio * A, clip(ratio, 1 - clip_low, 1 + clip_high) * A)
+ *                   + kl_coef * (exp(ref - lp) - (ref - lp) - 1)      (ref = ref_logp[r]; no term when NULL)
+ *     *loss       = sum_r weight[r] * row_loss[r]
+ *     d           = -ratio * A where ratio * A <= clip(ratio) * A, else 0;  + kl_coef * (1 - exp(ref - lp))
+ *     grad[r, c]  = weight[r] * s * d * ([c == y] - q_c)
+ *   target [rows] int32; old_logp, advantage, row_loss, row_logp (lp, 0 for a
+ *   row left out) [rows] fp32; ref_logp, row_weight [rows] fp32 or NULL;
+ *   clip_low in [0, 1], clip_high >= 0, kl_coef finite.
+ */
+lik_status lik_policy_loss_fwd(const void* logits, lik_dtype dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                               const int32_t* target, const float* old_logp, const float* advantage,
+                               const float* ref_logp, const float* row_weight, float clip_low, float clip_high,
+                               float kl_coef, float scale, float* loss, float* row_loss, float* row_logp,
+                               float* row_state, cudaStream_t stream);
+
+lik_status lik_policy_loss_bwd(const void* logits, lik_dtype dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                               const int32_t* target, float scale, const float* row_state, const float* grad_loss,
+                               void* grad_logits, int64_t grad_stride, cudaStream_t stream);
+
+lik_status lik_policy_loss_step(const void* logits, lik_dtype dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                                const int32_t* target, const float* old_logp, const float* advantage,
+                                const float* ref_logp, const float* row_weight, float clip_low, float clip_high,
+                                float kl_coef, float scale, float* loss, float* row_loss, float* row_logp,
+                                void* grad_logits, int64_t grad_stride, cudaStream_t stream);
+
+/*
+ * Preference loss over pairs of sequences: the rows are the tokens of 2 *
+ * pairs ragged sequences, sequence i the rows [offsets[i], offsets[i + 1]);
+ * pair p sets sequence p (chosen) against sequence pairs + p (rejected).
+ * With lp_r = log q[target[r]] over the rows that are not left out,
+ *     seq_logp[i]  = sum (average == 0) or mean (else) of lp over sequence i; 0 if it counts no row
+ *     x_p          = beta * ((seq_logp[p] - ref_logp[p]) - (seq_logp[P + p] - ref_logp[P + p])) - margin
+ *     pair_loss[p] = (1 - smoothing) * log(1 + exp(-x_p)) + smoothing * log(1 + exp(x_p))
+ *     *loss        = sum_p weight[p] * pair_loss[p]     (a pair of weight 0 is left out: pair_loss 0, no gradient)
+ *     grad[r, c]   = s * dloss/dlp_r * ([c == target] - q_c)
+ *   target [rows] int32; offsets [2 * pairs + 1] int32, device, not falling,
+ *   within [0, rows] (values outside are clamped; a row in no sequence has a
+ *   zero gradient); ref_logp [2 * pairs] fp32 or NULL (0); pair_weight
+ *   [pairs] fp32 or NULL; pair_loss [pairs], seq_logp [2 * pairs] fp32;
+ *   beta, margin finite, 0 <= smoothing <= 1, 0 <= pairs <= 2^20.
+ * Both _fwd and _step need row_state (a pair's gradient waits for all its
+ * rows): written, and read again inside _step.
+ */
+lik_status lik_preference_loss_fwd(const void* logits, lik_dtype dtype, int64_t rows, int64_t cols,
+                                   int64_t row_stride, const int32_t* target, const int32_t* offsets, int64_t pairs,
+                                   const float* ref_logp, const float* pair_weight, float beta, float margin,
+                                   float smoothing, int average, float scale, float* loss, float* pair_loss,
+                                   float* seq_logp, float* row_state, cudaStream_t stream);
+
+lik_status lik_preference_loss_bwd(const void* logits, lik_dtype dtype, int64_t rows, int64_t cols,
+                                   int64_t row_stride, const int32_t* target, float scale, const float* row_state,
+                                   const float* grad_loss, void* grad_logits, int64_t grad_stride,
+                                   cudaStream_t stream);
+
+lik_status lik_preference_loss_step(const void* logits, lik_dtype dtype, int64_t rows, int64_t cols,
+                                    int64_t row_stride, const int32_t* target, const int32_t* offsets, int64_t pairs,
+                                    const float* ref_logp, const float* pair_weight, float beta, float margin,
+                                    float smoothing, int average, float scale, float* loss, float* pair_loss,
+                                    float* seq_logp, float* row_state, void* grad_logits, int64_t grad_stride,
+                                    cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -22,7 +22,8 @@ STATUS = {0: "LIK_OK", 1: "LIK_ERR_INVALID_ARG", 2: "LIK_ERR_UNSUPPORTED", 3: "L
           4: "LIK_ERR_TIMEOUT"}
 
 # Every entry point include/lik.h declares, with its ctypes signature.
-_P, _I64, _I32 = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int
+_P, _I64, _I32, _F = ctypes.c_void_p, ctypes.c_int64, ctypes.c_int, ctypes.c_float
+_LOGITS = [_P, _I32] + [_I64] * 3  # logits, dtype, rows, cols, row_stride
 SIGNATURES = {
     "lik_status_string": (ctypes.c_char_p, [_I32]),
     "lik_last_error_message": (ctypes.c_char_p, []),
@@ -51,6 +52,16 @@ SIGNATURES = {
                                     + [_P] * 7 + [_I32, _P]),
     "lik_maxsim_kd_ce_step": (_I32, [_P, _P, _I32] + [_I64] * 5 + [_P] * 3 + [ctypes.c_float]
                               + [_P] * 7 + [_I32, _P]),
+    "lik_distill_topk_fwd": (_I32, _LOGITS + [_P, _P, _I32, _I64, _P, _P, _F] + [_P] * 4),
+    "lik_distill_topk_bwd": (_I32, _LOGITS + [_P, _P, _I32, _I64, _P, _F] + [_P] * 3 + [_I64, _P]),
+    "lik_distill_topk_step": (_I32, _LOGITS + [_P, _P, _I32, _I64, _P, _P, _F] + [_P] * 3 + [_I64, _P]),
+    "lik_policy_loss_fwd": (_I32, _LOGITS + [_P] * 5 + [_F] * 4 + [_P] * 5),
+    "lik_policy_loss_bwd": (_I32, _LOGITS + [_P, _F] + [_P] * 3 + [_I64, _P]),
+    "lik_policy_loss_step": (_I32, _LOGITS + [_P] * 5 + [_F] * 4 + [_P] * 4 + [_I64, _P]),
+    "lik_preference_loss_fwd": (_I32, _LOGITS + [_P, _P, _I64, _P, _P] + [_F] * 3 + [_I32, _F] + [_P] * 5),
+    "lik_preference_loss_bwd": (_I32, _LOGITS + [_P, _F] + [_P] * 3 + [_I64, _P]),
+    "lik_preference_loss_step": (_I32, _LOGITS + [_P, _P, _I64, _P, _P] + [_F] * 3 + [_I32, _F] + [_P] * 5
+                                 + [_I64, _P]),
 }
 
 _DTYPES = {torch.float32: LIK_F32, torch.float16: LIK_F16, torch.bfloat16: LIK_BF16}
@@ -456,6 +467,177 @@ def lik_maxsim_kd_ce_step(Q, D, qmask, dmask, target, scores, argmax, loss, row_
     """Per-query-candidate cross-entropy head in one call: forward, loss, backward."""
     _ce_step("kd", Q, D, qmask, dmask, target, scale, scores, argmax, loss, row_loss,
              grad_scores, grad_Q, grad_D, stream)
+
+
+# ------------------------------------ training objectives over logits --
+
+def _rows(t: torch.Tensor, name: str):
+    """Address, rows, cols and row stride of a [rows, cols] CUDA tensor whose rows are contiguous."""
+    if t.dim() != 2:
+        raise ValueError(f"{name} must be [rows, cols]")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32/float16/bfloat16 (got {t.dtype})")
+    if t.device.type != "cuda":
+        raise ValueError(f"{name} must be a CUDA tensor")
+    rows, cols = t.shape
+    if cols > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name} must have contiguous rows")
+    return t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else max(cols, 1)
+
+
+def _grad_rows(grad, logits):
+    if grad is None:
+        raise ValueError("grad_logits is required")
+    if grad.shape != logits.shape or grad.dtype != logits.dtype or grad.device != logits.device:
+        raise ValueError(f"grad_logits must have the logits' shape, dtype and device (got {tuple(grad.shape)}, "
+                         f"{grad.dtype}, {grad.device})")
+    ptr, _, _, stride = _rows(grad, "grad_logits")
+    return ptr, stride
+
+
+def _teacher(logits, teacher_index, teacher_logits, teacher_lse, rows):
+    if teacher_logits.dtype not in _DTYPES:
+        raise ValueError(f"teacher_logits must be float32/float16/bfloat16 (got {teacher_logits.dtype})")
+    if teacher_logits.dim() != 2:
+        raise ValueError("teacher_logits must be [rows, k]")
+    dev, k = logits.device, teacher_logits.shape[1]
+    _need(teacher_logits, "teacher_logits", (rows, k), teacher_logits.dtype, dev)
+    _need(teacher_index, "teacher_index", (rows, k), torch.int32, dev)
+    _need(teacher_lse, "teacher_lse", (rows,), torch.float32, dev, optional=True)
+    return teacher_index.data_ptr(), teacher_logits.data_ptr(), _DTYPES[teacher_logits.dtype], k, _ptr(teacher_lse)
+
+
+def _distill(form, logits, teacher_index, teacher_logits, teacher_lse, row_weight, scale, loss, row_loss, tail, stream):
+    z, rows, cols, stride = _rows(logits, "logits")
+    dev = logits.device
+    t = _teacher(logits, teacher_index, teacher_logits, teacher_lse, rows)
+    _need(row_weight, "row_weight", (rows,), torch.float32, dev, optional=True)
+    _need(loss, "loss", (1,), torch.float32, dev)
+    _need(row_loss, "row_loss", (rows,), torch.float32, dev)
+    _check(getattr(load(), form)(z, _DTYPES[logits.dtype], rows, cols, stride, *t, _ptr(row_weight), scale,
+                                 loss.data_ptr(), row_loss.data_ptr(), *tail, _stream(dev, stream)))
+
+
+def lik_distill_topk_fwd(logits, teacher_index, teacher_logits, loss, row_loss, row_state=None, teacher_lse=None,
+                         row_weight=None, scale=1.0, stream=None):
+    """Divergence of each row's softmax from a teacher's top logits; row_state
+    [rows, 4] is written for lik_distill_topk_bwd unless None."""
+    _need(row_state, "row_state", (logits.shape[0], 4), torch.float32, logits.device, optional=True)
+    _distill("lik_distill_topk_fwd", logits, teacher_index, teacher_logits, teacher_lse, row_weight, scale, loss,
+             row_loss, (_ptr(row_state),), stream)
+
+
+def lik_distill_topk_bwd(logits, teacher_index, teacher_logits, row_state, grad_logits, grad_loss=None,
+                         teacher_lse=None, scale=1.0, stream=None):
+    """Gradient of lik_distill_topk_fwd's loss, times grad_loss [1] (None: 1)."""
+    z, rows, cols, stride = _rows(logits, "logits")
+    dev = logits.device
+    g, g_stride = _grad_rows(grad_logits, logits)
+    t = _teacher(logits, teacher_index, teacher_logits, teacher_lse, rows)
+    _need(row_state, "row_state", (rows, 4), torch.float32, dev)
+    _need(grad_loss, "grad_loss", (1,), torch.float32, dev, optional=True)
+    _check(load().lik_distill_topk_bwd(z, _DTYPES[logits.dtype], rows, cols, stride, *t, scale, row_state.data_ptr(),
+                                       _ptr(grad_loss), g, g_stride, _stream(dev, stream)))
+
+
+def lik_distill_topk_step(logits, teacher_index, teacher_logits, loss, row_loss, grad_logits, teacher_lse=None,
+                          row_weight=None, scale=1.0, stream=None):
+    """Loss and gradient in one call (grad_logits may be the logits tensor itself)."""
+    _distill("lik_distill_topk_step", logits, teacher_index, teacher_logits, teacher_lse, row_weight, scale, loss,
+             row_loss, _grad_rows(grad_logits, logits), stream)
+
+
+def _policy(form, logits, target, old_logp, advantage, ref_logp, row_weight, clip_low, clip_high, kl_coef, scale,
+            loss, row_loss, row_logp, tail, stream):
+    z, rows, cols, stride = _rows(logits, "logits")
+    dev, f32 = logits.device, torch.float32
+    _need(target, "target", (rows,), torch.int32, dev)
+    _need(old_logp, "old_logp", (rows,), f32, dev)
+    _need(advantage, "advantage", (rows,), f32, dev)
+    _need(ref_logp, "ref_logp", (rows,), f32, dev, optional=True)
+    _need(row_weight, "row_weight", (rows,), f32, dev, optional=True)
+    _need(loss, "loss", (1,), f32, dev)
+    _need(row_loss, "row_loss", (rows,), f32, dev)
+    _need(row_logp, "row_logp", (rows,), f32, dev)
+    _check(getattr(load(), form)(z, _DTYPES[logits.dtype], rows, cols, stride, target.data_ptr(),
+                                 old_logp.data_ptr(), advantage.data_ptr(), _ptr(ref_logp), _ptr(row_weight),
+                                 clip_low, clip_high, kl_coef, scale, loss.data_ptr(), row_loss.data_ptr(),
+                                 row_logp.data_ptr(), *tail, _stream(dev, stream)))
+
+
+def lik_policy_loss_fwd(logits, target, old_logp, advantage, loss, row_loss, row_logp, row_state=None, ref_logp=None,
+                        row_weight=None, clip_low=0.2, clip_high=0.2, kl_coef=0.0, scale=1.0, stream=None):
+    """Clipped policy loss of sampled tokens; row_state [rows, 4] is written for
+    lik_policy_loss_bwd unless None."""
+    _need(row_state, "row_state", (logits.shape[0], 4), torch.float32, logits.device, optional=True)
+    _policy("lik_policy_loss_fwd", logits, target, old_logp, advantage, ref_logp, row_weight, clip_low, clip_high,
+            kl_coef, scale, loss, row_loss, row_logp, (_ptr(row_state),), stream)
+
+
+def lik_policy_loss_step(logits, target, old_logp, advantage, loss, row_loss, row_logp, grad_logits, ref_logp=None,
+                         row_weight=None, clip_low=0.2, clip_high=0.2, kl_coef=0.0, scale=1.0, stream=None):
+    """Loss and gradient in one call (grad_logits may be the logits tensor itself)."""
+    _policy("lik_policy_loss_step", logits, target, old_logp, advantage, ref_logp, row_weight, clip_low, clip_high,
+            kl_coef, scale, loss, row_loss, row_logp, _grad_rows(grad_logits, logits), stream)
+
+
+def _target_bwd(form, logits, target, row_state, grad_logits, grad_loss, scale, stream):
+    z, rows, cols, stride = _rows(logits, "logits")
+    dev = logits.device
+    g, g_stride = _grad_rows(grad_logits, logits)
+    _need(target, "target", (rows,), torch.int32, dev)
+    _need(row_state, "row_state", (rows, 4), torch.float32, dev)
+    _need(grad_loss, "grad_loss", (1,), torch.float32, dev, optional=True)
+    _check(getattr(load(), form)(z, _DTYPES[logits.dtype], rows, cols, stride, target.data_ptr(), scale,
+                                 row_state.data_ptr(), _ptr(grad_loss), g, g_stride, _stream(dev, stream)))
+
+
+def lik_policy_loss_bwd(logits, target, row_state, grad_logits, grad_loss=None, scale=1.0, stream=None):
+    """Gradient of lik_policy_loss_fwd's loss, times grad_loss [1] (None: 1)."""
+    _target_bwd("lik_policy_loss_bwd", logits, target, row_state, grad_logits, grad_loss, scale, stream)
+
+
+def _preference(form, logits, target, offsets, ref_logp, pair_weight, beta, margin, smoothing, average, scale, loss,
+                pair_loss, seq_logp, row_state, tail, stream):
+    z, rows, cols, stride = _rows(logits, "logits")
+    dev, f32 = logits.device, torch.float32
+    if pair_loss.dim() != 1:
+        raise ValueError("pair_loss must be [pairs]")
+    pairs = pair_loss.shape[0]
+    _need(target, "target", (rows,), torch.int32, dev)
+    _need(offsets, "offsets", (2 * pairs + 1,), torch.int32, dev)
+    _need(ref_logp, "ref_logp", (2 * pairs,), f32, dev, optional=True)
+    _need(pair_weight, "pair_weight", (pairs,), f32, dev, optional=True)
+    _need(loss, "loss", (1,), f32, dev)
+    _need(pair_loss, "pair_loss", (pairs,), f32, dev)
+    _need(seq_logp, "seq_logp", (2 * pairs,), f32, dev)
+    _need(row_state, "row_state", (rows, 4), f32, dev)
+    _check(getattr(load(), form)(z, _DTYPES[logits.dtype], rows, cols, stride, target.data_ptr(), offsets.data_ptr(),
+                                 pairs, _ptr(ref_logp), _ptr(pair_weight), beta, margin, smoothing,
+                                 1 if average else 0, scale, loss.data_ptr(), pair_loss.data_ptr(),
+                                 seq_logp.data_ptr(), row_state.data_ptr(), *tail, _stream(dev, stream)))
+
+
+def lik_preference_loss_fwd(logits, target, offsets, loss, pair_loss, seq_logp, row_state, ref_logp=None,
+                            pair_weight=None, beta=0.1, margin=0.0, smoothing=0.0, average=False, scale=1.0,
+                            stream=None):
+    """Preference loss over pairs of ragged sequences: sequence i holds the rows
+    offsets[i]..offsets[i + 1], pair p is (chosen p, rejected pairs + p)."""
+    _preference("lik_preference_loss_fwd", logits, target, offsets, ref_logp, pair_weight, beta, margin, smoothing,
+                average, scale, loss, pair_loss, seq_logp, row_state, (), stream)
+
+
+def lik_preference_loss_step(logits, target, offsets, loss, pair_loss, seq_logp, row_state, grad_logits,
+                             ref_logp=None, pair_weight=None, beta=0.1, margin=0.0, smoothing=0.0, average=False,
+                             scale=1.0, stream=None):
+    """Loss and gradient in one call (grad_logits may be the logits tensor itself)."""
+    _preference("lik_preference_loss_step", logits, target, offsets, ref_logp, pair_weight, beta, margin, smoothing,
+                average, scale, loss, pair_loss, seq_logp, row_state, _grad_rows(grad_logits, logits), stream)
+
+
+def lik_preference_loss_bwd(logits, target, row_state, grad_logits, grad_loss=None, scale=1.0, stream=None):
+    """Gradient of lik_preference_loss_fwd's loss, times grad_loss [1] (None: 1)."""
+    _target_bwd("lik_preference_loss_bwd", logits, target, row_state, grad_logits, grad_loss, scale, stream)
 
 
 def lik_check_device_error(stream=None, device=None):

@@ -14,6 +14,7 @@
 
 #include "lik.h"
 #include "lik_internal.h"
+#include "validate.h"
 
 namespace lik {
 
@@ -42,6 +43,8 @@ ErrorWordSlot g_error_words[kMaxDevices];
 
 thread_local char t_message[512];
 
+}  // namespace
+
 lik_status fail(lik_status s, const char* fmt, ...) {
     va_list ap;
     va_start(ap, fmt);
@@ -54,7 +57,7 @@ lik_status cuda_fail(cudaError_t e, const char* what) {
     return fail(LIK_ERR_CUDA, "%s: %s (%s)", what, cudaGetErrorName(e), cudaGetErrorString(e));
 }
 
-}  // namespace
+void clear_message() { t_message[0] = 0; }
 
 // For entry points defined in other files: records `message` as the calling
 // thread's lik_last_error_message() and returns `s`.
@@ -88,8 +91,6 @@ unsigned int* device_error_word() {
 }
 
 // ------------------------------------------------------------ validation --
-
-namespace {
 
 bool known_dtype(lik_dtype t) { return t == LIK_F32 || t == LIK_F16 || t == LIK_BF16; }
 
@@ -127,12 +128,7 @@ lik_status check_pointer(const void* p, int dev, const char* name) {
     return LIK_OK;
 }
 
-struct Spec {
-    const char* name;
-    const void* ptr;
-    bool required;  // must be non-NULL when the buffer has elements
-    int64_t elems;
-};
+namespace {
 
 lik_status check_common(lik_dtype dtype, int64_t n_query, int64_t n_doc, int64_t ppq,
                         int64_t Lq, int64_t Ld, int64_t dim, bool* nothing_to_do) {
@@ -148,6 +144,8 @@ lik_status check_common(lik_dtype dtype, int64_t n_query, int64_t n_doc, int64_t
     return LIK_OK;
 }
 
+}  // namespace
+
 lik_status check_buffers(int dev, const Spec* specs, int n) {
     for (int k = 0; k < n; ++k) {
         const Spec& s = specs[k];
@@ -160,17 +158,23 @@ lik_status check_buffers(int dev, const Spec* specs, int n) {
     return LIK_OK;
 }
 
+namespace {
+
 lik_status check_alignment(const void* Q, const void* D) {
     if ((reinterpret_cast<uintptr_t>(Q) & 15) || (reinterpret_cast<uintptr_t>(D) & 15))
         return fail(LIK_ERR_INVALID_ARG, "Q and D must be 16-byte aligned");
     return LIK_OK;
 }
 
+}  // namespace
+
 lik_status check_aligned(const void* p, uintptr_t bytes, const char* name) {
     if (reinterpret_cast<uintptr_t>(p) & (bytes - 1))
         return fail(LIK_ERR_INVALID_ARG, "%s must be %d-byte aligned", name, static_cast<int>(bytes));
     return LIK_OK;
 }
+
+namespace {
 
 Problem make_problem(int layout, lik_dtype dtype, const void* Q, const void* D,
                      const bool* qmask, const bool* dmask, int64_t n_query, int64_t n_doc,

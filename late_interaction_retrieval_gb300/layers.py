@@ -16,6 +16,16 @@ input dtype directly (summed in fp32, rounded once); otherwise it asks for
 fp32 gradients and casts them.  This module only allocates tensors and calls
 the binding.  With recompute=True the forward saves no argmax: the
 backward re-runs the forward into a transient workspace.
+
+Training objectives over logits [..., cols] (a query's candidate scores, a
+token's vocabulary), each a scalar fp32 loss differentiable in the logits:
+
+  distill_topk     divergence from a teacher's top logits
+  policy_loss      clipped policy loss with a KL term to a reference
+  preference_loss  paired log ratios of chosen and rejected sequences
+
+Their forward saves four floats per row; the backward writes the gradient in
+the logits' dtype from the logits and those.
 """
 from __future__ import annotations
 
@@ -121,3 +131,175 @@ class MaxSimKD(torch.nn.Module):
 
     def forward(self, Q, D, qmask=None, dmask=None):
         return maxsim_kd(Q, D, qmask, dmask, self.recompute)
+
+
+# ------------------------------------ training objectives over logits --
+
+def _logit_rows(logits):
+    """logits [..., cols] as [rows, cols] with contiguous rows (a view where possible)."""
+    rows = logits.reshape(-1, logits.shape[-1])
+    return rows if rows.stride(1) == 1 or rows.shape[1] <= 1 else rows.contiguous()
+
+
+def _flat(t, dtype):
+    return None if t is None else t.detach().reshape(-1).to(dtype).contiguous()
+
+
+def _grad_buffer(rows):
+    """A gradient whose rows lie as the logits' rows do modulo 16 bytes (they
+    are then written with 16-byte stores): row strides are kept where they
+    carry no more than padding."""
+    n, cols = rows.shape
+    if n > 1 and cols < rows.stride(0) <= cols + cols // 8:
+        return torch.empty((n, rows.stride(0)), dtype=rows.dtype, device=rows.device)[:, :cols]
+    return torch.empty((n, cols), dtype=rows.dtype, device=rows.device)
+
+
+def _upstream(g):
+    return g.detach().reshape(1).to(torch.float32).contiguous()
+
+
+class _DistillFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, index, teacher, teacher_lse, weight, scale):
+        z = _logit_rows(logits)
+        n, k = z.shape[0], teacher.shape[-1]
+        index = index.detach().reshape(n, k).to(torch.int32).contiguous()
+        teacher = teacher.detach().reshape(n, k).contiguous()
+        teacher_lse, weight = _flat(teacher_lse, torch.float32), _flat(weight, torch.float32)
+        loss = torch.empty(1, device=z.device)
+        row_loss = torch.empty(n, device=z.device)
+        state = torch.empty((n, 4), device=z.device) if ctx.needs_input_grad[0] else None
+        binding.lik_distill_topk_fwd(z, index, teacher, loss, row_loss, state, teacher_lse=teacher_lse,
+                                     row_weight=weight, scale=scale)
+        ctx.scale, ctx.shape = scale, logits.shape
+        ctx.save_for_backward(z, index, teacher, teacher_lse, state)
+        row_loss = row_loss.view(logits.shape[:-1])
+        ctx.mark_non_differentiable(row_loss)
+        return loss.view(()), row_loss
+
+    @staticmethod
+    def backward(ctx, g, _):
+        z, index, teacher, teacher_lse, state = ctx.saved_tensors
+        grad = _grad_buffer(z)
+        binding.lik_distill_topk_bwd(z, index, teacher, state, grad, grad_loss=_upstream(g), teacher_lse=teacher_lse,
+                                     scale=ctx.scale)
+        return grad.reshape(ctx.shape), None, None, None, None, None
+
+
+class _PolicyFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, target, old_logp, advantage, ref_logp, weight, clip_low, clip_high, kl_coef, scale):
+        z = _logit_rows(logits)
+        n, f32 = z.shape[0], torch.float32
+        target = _flat(target, torch.int32)
+        loss = torch.empty(1, device=z.device)
+        row_loss, row_logp = torch.empty(n, device=z.device), torch.empty(n, device=z.device)
+        state = torch.empty((n, 4), device=z.device) if ctx.needs_input_grad[0] else None
+        binding.lik_policy_loss_fwd(z, target, _flat(old_logp, f32), _flat(advantage, f32), loss, row_loss, row_logp,
+                                    state, ref_logp=_flat(ref_logp, f32), row_weight=_flat(weight, f32),
+                                    clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef, scale=scale)
+        ctx.scale, ctx.shape = scale, logits.shape
+        ctx.save_for_backward(z, target, state)
+        row_loss, row_logp = row_loss.view(logits.shape[:-1]), row_logp.view(logits.shape[:-1])
+        ctx.mark_non_differentiable(row_loss, row_logp)
+        return loss.view(()), row_loss, row_logp
+
+    @staticmethod
+    def backward(ctx, g, *_):
+        z, target, state = ctx.saved_tensors
+        grad = _grad_buffer(z)
+        binding.lik_policy_loss_bwd(z, target, state, grad, grad_loss=_upstream(g), scale=ctx.scale)
+        return (grad.reshape(ctx.shape),) + (None,) * 9
+
+
+class _PreferenceFn(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, logits, target, offsets, ref_logp, weight, beta, margin, smoothing, average, scale):
+        z = _logit_rows(logits)
+        n, f32 = z.shape[0], torch.float32
+        target, offsets = _flat(target, torch.int32), _flat(offsets, torch.int32)
+        pairs = offsets.numel() // 2
+        loss = torch.empty(1, device=z.device)
+        pair_loss, seq_logp = torch.empty(pairs, device=z.device), torch.empty(2 * pairs, device=z.device)
+        state = torch.empty((n, 4), device=z.device)
+        binding.lik_preference_loss_fwd(z, target, offsets, loss, pair_loss, seq_logp, state,
+                                        ref_logp=_flat(ref_logp, f32), pair_weight=_flat(weight, f32), beta=beta,
+                                        margin=margin, smoothing=smoothing, average=average, scale=scale)
+        ctx.scale, ctx.shape = scale, logits.shape
+        ctx.save_for_backward(z, target, state)
+        ctx.mark_non_differentiable(pair_loss, seq_logp)
+        return loss.view(()), pair_loss, seq_logp
+
+    @staticmethod
+    def backward(ctx, g, *_):
+        z, target, state = ctx.saved_tensors
+        grad = _grad_buffer(z)
+        binding.lik_preference_loss_bwd(z, target, state, grad, grad_loss=_upstream(g), scale=ctx.scale)
+        return (grad.reshape(ctx.shape),) + (None,) * 9
+
+
+def distill_topk(logits, teacher_index, teacher_logits, teacher_lse=None, row_weight=None, scale=1.0,
+                 return_rows=False):
+    """Kullback-Leibler divergence of softmax(scale * logits) [..., cols] from a
+    teacher known at its top columns (teacher_index, teacher_logits [..., k];
+    indices outside [0, cols) are padding), summed with row_weight [...] (None:
+    the mean over rows).  teacher_lse [...] makes the teacher's probabilities
+    exp(scale * teacher_logits - teacher_lse) instead of normalising them over
+    the k entries.  Differentiable in the logits only.  With return_rows also
+    the row losses (no gradient)."""
+    loss, row_loss = _DistillFn.apply(logits, teacher_index, teacher_logits, teacher_lse, row_weight, scale)
+    return (loss, row_loss) if return_rows else loss
+
+
+def policy_loss(logits, target, old_logp, advantage, ref_logp=None, row_weight=None, clip_low=0.2, clip_high=0.2,
+                kl_coef=0.0, scale=1.0, return_rows=False):
+    """Clipped policy loss of the sampled tokens target [...] under logits
+    [..., cols], with kl_coef times the KL term to ref_logp; summed with
+    row_weight (None: the mean over rows).  A target outside [0, cols) leaves
+    its token out.  With return_rows also the token losses and the tokens'
+    log-probabilities (no gradient)."""
+    out = _PolicyFn.apply(logits, target, old_logp, advantage, ref_logp, row_weight, clip_low, clip_high, kl_coef,
+                          scale)
+    return out if return_rows else out[0]
+
+
+def preference_loss(logits, target, offsets, ref_logp=None, pair_weight=None, beta=0.1, margin=0.0, smoothing=0.0,
+                    average=False, scale=1.0, return_rows=False):
+    """Preference loss over pairs of sequences packed along the rows of logits
+    [rows, cols]: sequence i holds the rows offsets[i]..offsets[i + 1], pair p
+    sets sequence p (chosen) against sequence pairs + p (rejected).  With
+    return_rows also the pair losses and the sequences' log-probabilities (no
+    gradient)."""
+    out = _PreferenceFn.apply(logits, target, offsets, ref_logp, pair_weight, beta, margin, smoothing, average, scale)
+    return out if return_rows else out[0]
+
+
+class DistillTopK(torch.nn.Module):
+    def __init__(self, scale: float = 1.0):
+        super().__init__()
+        self.scale = scale
+
+    def forward(self, logits, teacher_index, teacher_logits, teacher_lse=None, row_weight=None):
+        return distill_topk(logits, teacher_index, teacher_logits, teacher_lse, row_weight, self.scale)
+
+
+class PolicyLoss(torch.nn.Module):
+    def __init__(self, clip_low: float = 0.2, clip_high: float = 0.2, kl_coef: float = 0.0, scale: float = 1.0):
+        super().__init__()
+        self.clip_low, self.clip_high, self.kl_coef, self.scale = clip_low, clip_high, kl_coef, scale
+
+    def forward(self, logits, target, old_logp, advantage, ref_logp=None, row_weight=None):
+        return policy_loss(logits, target, old_logp, advantage, ref_logp, row_weight, self.clip_low, self.clip_high,
+                           self.kl_coef, self.scale)
+
+
+class PreferenceLoss(torch.nn.Module):
+    def __init__(self, beta: float = 0.1, margin: float = 0.0, smoothing: float = 0.0, average: bool = False,
+                 scale: float = 1.0):
+        super().__init__()
+        self.beta, self.margin, self.smoothing, self.average, self.scale = beta, margin, smoothing, average, scale
+
+    def forward(self, logits, target, offsets, ref_logp=None, pair_weight=None):
+        return preference_loss(logits, target, offsets, ref_logp, pair_weight, self.beta, self.margin, self.smoothing,
+                               self.average, self.scale)
