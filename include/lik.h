@@ -418,7 +418,7 @@ lik_status lik_maxsim_kd_ce_step(const void* Q, const void* D, lik_dtype dtype, 
  * call, each row of logits read from memory once where it fits on chip).
  *
  * Shared by all of them, for a row z[0, cols) and a logit scale s (1 /
- * temperature), 0 < s finite:
+ * temperature), 1e-30 <= s <= 1e30:
  *     q = softmax(s * z),   log q_c = s * (z_c - max z) - log sum exp(s * (z - max z))
  *   - logits [rows, cols], fp32, fp16 or bf16; row r starts at element r *
  *     row_stride, row_stride >= cols (its elements are contiguous).  Any
@@ -516,6 +516,7 @@ lik_status lik_policy_loss_step(const void* logits, lik_dtype dtype, int64_t row
  * pair p sets sequence p (chosen) against sequence pairs + p (rejected).
  * With lp_r = log q[target[r]] over the rows that are not left out,
  *     seq_logp[i]  = sum (average == 0) or mean (else) of lp over sequence i; 0 if it counts no row
+ *     (in fp64, rounded to the fp32 that is returned and used from here on)
  *     x_p          = beta * ((seq_logp[p] - ref_logp[p]) - (seq_logp[P + p] - ref_logp[P + p])) - margin
  *     pair_loss[p] = (1 - smoothing) * log(1 + exp(-x_p)) + smoothing * log(1 + exp(x_p))
  *     *loss        = sum_p weight[p] * pair_loss[p]     (a pair of weight 0 is left out: pair_loss 0, no gradient)

@@ -30,8 +30,8 @@ lik_status check_rows(lik_dtype dtype, int64_t rows, int64_t cols, int64_t row_s
     if (row_stride > (int64_t(1) << 31))
         return fail(LIK_ERR_UNSUPPORTED, "row_stride %lld > 2^31", static_cast<long long>(row_stride));
     if (span(rows, cols, row_stride) > kMaxSpan) return fail(LIK_ERR_UNSUPPORTED, "logits span more than 2^48 elements");
-    if (!(scale > 0.0f) || !std::isfinite(scale))
-        return fail(LIK_ERR_INVALID_ARG, "scale must be positive and finite (got %g)", static_cast<double>(scale));
+    if (!(scale >= 1e-30f && scale <= 1e30f))
+        return fail(LIK_ERR_INVALID_ARG, "scale must lie in [1e-30, 1e30] (got %g)", static_cast<double>(scale));
     return LIK_OK;
 }
 
@@ -79,6 +79,8 @@ LossRows make_rows(const void* logits, lik_dtype dtype, int64_t rows, int64_t co
     L.cols = cols;
     L.stride = row_stride;
     L.scale = scale;
+    L.c = static_cast<float>(static_cast<double>(scale) * 1.4426950408889634074);
+    L.even_weight = rows > 0 ? 1.0f / static_cast<float>(rows) : 0.0f;
     return L;
 }
 
@@ -300,13 +302,19 @@ lik_status preference(const PreferenceArgs& a, float* loss, float* pair_loss, fl
     P.seq_logp = seq_logp;
     P.state = L.state;
     cudaError_t e = cudaSuccess;
+    const bool grad_rows = bwd && a.rows > 0;
     if (a.rows > 0) e = launch_loss_rows(kHeadToken, L, stream);
     if (e == cudaSuccess && a.pairs > 0) e = launch_loss_pairs(P, stream);
-    if (e == cudaSuccess) e = launch_loss_sum(pair_loss, a.weight, a.pairs, loss, stream);
-    if (e == cudaSuccess && bwd && a.rows > 0) {
+    if (e == cudaSuccess && grad_rows) {  // sums the loss on the way
         L.grad = grad;
         L.grad_stride = grad_stride;
+        L.sum_value = pair_loss;
+        L.sum_weight = a.weight;
+        L.sum_n = a.pairs;
+        L.sum_out = loss;
         e = launch_loss_grad(kHeadToken, L, stream);
+    } else if (e == cudaSuccess) {
+        e = launch_loss_sum(pair_loss, a.weight, a.pairs, loss, stream);
     }
     return e == cudaSuccess ? LIK_OK : cuda_fail(e, "preference loss launch");
 }

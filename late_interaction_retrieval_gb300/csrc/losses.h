@@ -20,7 +20,9 @@ struct LossRows {
     int dtype = 0;
     int64_t rows = 0, cols = 0, stride = 0, grad_stride = 0;
     float scale = 1.0f;
-    const float* weight = nullptr;  // [rows] or nullptr: 1 / rows each
+    float c = 0.0f;  // scale * log2(e), rounded
+    const float* weight = nullptr;  // [rows] or nullptr: even_weight each
+    float even_weight = 0.0f;
     // distillation
     const int32_t* t_index = nullptr;  // [rows, k]
     const void* t_logits = nullptr;    // [rows, k] of t_dtype
@@ -40,6 +42,11 @@ struct LossRows {
     // 1 / sum is 0 for a row left out
     float4* state = nullptr;
     const float* grad_loss = nullptr;  // upstream gradient, backward only; nullptr: 1
+    // Gradient of a target head: also *sum_out = the weighted sum of sum_value (as launch_loss_sum).
+    const float* sum_value = nullptr;
+    const float* sum_weight = nullptr;
+    int64_t sum_n = 0;
+    float* sum_out = nullptr;
 };
 
 // The pairs of a preference loss, over the row states of a token-head forward.
