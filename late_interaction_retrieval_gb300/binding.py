@@ -113,8 +113,14 @@ def _check(status: int):
         raise LIKError(status, msg)
 
 
+# The current stream's address without a Stream object (2 us on the host), where torch has it.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
 def _stream(device: torch.device, stream) -> int:
     if stream is None:
+        if _raw_stream is not None and device.index is not None:
+            return _raw_stream(device.index)
         stream = torch.cuda.current_stream(device)
     return stream.cuda_stream if hasattr(stream, "cuda_stream") else int(stream)
 
@@ -477,18 +483,40 @@ def _rows(t: torch.Tensor, name: str):
         raise ValueError(f"{name} must be [rows, cols]")
     if t.dtype not in _DTYPES:
         raise ValueError(f"{name} must be float32/float16/bfloat16 (got {t.dtype})")
-    if t.device.type != "cuda":
+    if not t.is_cuda:
         raise ValueError(f"{name} must be a CUDA tensor")
     rows, cols = t.shape
-    if cols > 1 and t.stride(1) != 1:
+    stride, inner = t.stride()
+    if inner != 1 and cols > 1:
         raise ValueError(f"{name} must have contiguous rows")
-    return t.data_ptr(), rows, cols, t.stride(0) if rows > 1 else max(cols, 1)
+    return t.data_ptr(), rows, cols, stride if rows > 1 else max(cols, 1)
+
+
+def _vector(t, name, shape, dtype, device, optional=False):
+    """Address of a contiguous tensor of this shape, dtype and device (None for a missing optional one)."""
+    if t is None and optional:
+        return None
+    if t is not None and t.shape == shape and t.dtype is dtype and t.device == device and t.is_contiguous():
+        return t.data_ptr()
+    _need(t, name, shape, dtype, device)  # says what is wrong
+
+
+_entries = {}
+
+
+def _call(name, *args):
+    fn = _entries.get(name)
+    if fn is None:
+        fn = _entries[name] = getattr(load(), name)
+    status = fn(*args)
+    if status != 0:
+        _check(status)
 
 
 def _grad_rows(grad, logits):
     if grad is None:
         raise ValueError("grad_logits is required")
-    if grad.shape != logits.shape or grad.dtype != logits.dtype or grad.device != logits.device:
+    if grad.shape != logits.shape or grad.dtype is not logits.dtype or grad.device != logits.device:
         raise ValueError(f"grad_logits must have the logits' shape, dtype and device (got {tuple(grad.shape)}, "
                          f"{grad.dtype}, {grad.device})")
     ptr, _, _, stride = _rows(grad, "grad_logits")
@@ -501,43 +529,41 @@ def _teacher(logits, teacher_index, teacher_logits, teacher_lse, rows):
     if teacher_logits.dim() != 2:
         raise ValueError("teacher_logits must be [rows, k]")
     dev, k = logits.device, teacher_logits.shape[1]
-    _need(teacher_logits, "teacher_logits", (rows, k), teacher_logits.dtype, dev)
-    _need(teacher_index, "teacher_index", (rows, k), torch.int32, dev)
-    _need(teacher_lse, "teacher_lse", (rows,), torch.float32, dev, optional=True)
-    return teacher_index.data_ptr(), teacher_logits.data_ptr(), _DTYPES[teacher_logits.dtype], k, _ptr(teacher_lse)
+    t = _vector(teacher_logits, "teacher_logits", (rows, k), teacher_logits.dtype, dev)
+    i = _vector(teacher_index, "teacher_index", (rows, k), torch.int32, dev)
+    lse = _vector(teacher_lse, "teacher_lse", (rows,), torch.float32, dev, optional=True)
+    return i, t, _DTYPES[teacher_logits.dtype], k, lse
 
 
 def _distill(form, logits, teacher_index, teacher_logits, teacher_lse, row_weight, scale, loss, row_loss, tail, stream):
     z, rows, cols, stride = _rows(logits, "logits")
-    dev = logits.device
-    t = _teacher(logits, teacher_index, teacher_logits, teacher_lse, rows)
-    _need(row_weight, "row_weight", (rows,), torch.float32, dev, optional=True)
-    _need(loss, "loss", (1,), torch.float32, dev)
-    _need(row_loss, "row_loss", (rows,), torch.float32, dev)
-    _check(getattr(load(), form)(z, _DTYPES[logits.dtype], rows, cols, stride, *t, _ptr(row_weight), scale,
-                                 loss.data_ptr(), row_loss.data_ptr(), *tail, _stream(dev, stream)))
+    dev, f32 = logits.device, torch.float32
+    _call(form, z, _DTYPES[logits.dtype], rows, cols, stride,
+          *_teacher(logits, teacher_index, teacher_logits, teacher_lse, rows),
+          _vector(row_weight, "row_weight", (rows,), f32, dev, optional=True), scale,
+          _vector(loss, "loss", (1,), f32, dev), _vector(row_loss, "row_loss", (rows,), f32, dev), *tail,
+          _stream(dev, stream))
 
 
 def lik_distill_topk_fwd(logits, teacher_index, teacher_logits, loss, row_loss, row_state=None, teacher_lse=None,
                          row_weight=None, scale=1.0, stream=None):
     """Divergence of each row's softmax from a teacher's top logits; row_state
     [rows, 4] is written for lik_distill_topk_bwd unless None."""
-    _need(row_state, "row_state", (logits.shape[0], 4), torch.float32, logits.device, optional=True)
+    state = _vector(row_state, "row_state", (logits.shape[0], 4), torch.float32, logits.device, optional=True)
     _distill("lik_distill_topk_fwd", logits, teacher_index, teacher_logits, teacher_lse, row_weight, scale, loss,
-             row_loss, (_ptr(row_state),), stream)
+             row_loss, (state,), stream)
 
 
 def lik_distill_topk_bwd(logits, teacher_index, teacher_logits, row_state, grad_logits, grad_loss=None,
                          teacher_lse=None, scale=1.0, stream=None):
     """Gradient of lik_distill_topk_fwd's loss, times grad_loss [1] (None: 1)."""
     z, rows, cols, stride = _rows(logits, "logits")
-    dev = logits.device
-    g, g_stride = _grad_rows(grad_logits, logits)
-    t = _teacher(logits, teacher_index, teacher_logits, teacher_lse, rows)
-    _need(row_state, "row_state", (rows, 4), torch.float32, dev)
-    _need(grad_loss, "grad_loss", (1,), torch.float32, dev, optional=True)
-    _check(load().lik_distill_topk_bwd(z, _DTYPES[logits.dtype], rows, cols, stride, *t, scale, row_state.data_ptr(),
-                                       _ptr(grad_loss), g, g_stride, _stream(dev, stream)))
+    dev, f32 = logits.device, torch.float32
+    _call("lik_distill_topk_bwd", z, _DTYPES[logits.dtype], rows, cols, stride,
+          *_teacher(logits, teacher_index, teacher_logits, teacher_lse, rows), scale,
+          _vector(row_state, "row_state", (rows, 4), f32, dev),
+          _vector(grad_loss, "grad_loss", (1,), f32, dev, optional=True), *_grad_rows(grad_logits, logits),
+          _stream(dev, stream))
 
 
 def lik_distill_topk_step(logits, teacher_index, teacher_logits, loss, row_loss, grad_logits, teacher_lse=None,
@@ -550,28 +576,22 @@ def lik_distill_topk_step(logits, teacher_index, teacher_logits, loss, row_loss,
 def _policy(form, logits, target, old_logp, advantage, ref_logp, row_weight, clip_low, clip_high, kl_coef, scale,
             loss, row_loss, row_logp, tail, stream):
     z, rows, cols, stride = _rows(logits, "logits")
-    dev, f32 = logits.device, torch.float32
-    _need(target, "target", (rows,), torch.int32, dev)
-    _need(old_logp, "old_logp", (rows,), f32, dev)
-    _need(advantage, "advantage", (rows,), f32, dev)
-    _need(ref_logp, "ref_logp", (rows,), f32, dev, optional=True)
-    _need(row_weight, "row_weight", (rows,), f32, dev, optional=True)
-    _need(loss, "loss", (1,), f32, dev)
-    _need(row_loss, "row_loss", (rows,), f32, dev)
-    _need(row_logp, "row_logp", (rows,), f32, dev)
-    _check(getattr(load(), form)(z, _DTYPES[logits.dtype], rows, cols, stride, target.data_ptr(),
-                                 old_logp.data_ptr(), advantage.data_ptr(), _ptr(ref_logp), _ptr(row_weight),
-                                 clip_low, clip_high, kl_coef, scale, loss.data_ptr(), row_loss.data_ptr(),
-                                 row_logp.data_ptr(), *tail, _stream(dev, stream)))
+    dev, f32, n = logits.device, torch.float32, (rows,)
+    _call(form, z, _DTYPES[logits.dtype], rows, cols, stride, _vector(target, "target", n, torch.int32, dev),
+          _vector(old_logp, "old_logp", n, f32, dev), _vector(advantage, "advantage", n, f32, dev),
+          _vector(ref_logp, "ref_logp", n, f32, dev, optional=True),
+          _vector(row_weight, "row_weight", n, f32, dev, optional=True), clip_low, clip_high, kl_coef, scale,
+          _vector(loss, "loss", (1,), f32, dev), _vector(row_loss, "row_loss", n, f32, dev),
+          _vector(row_logp, "row_logp", n, f32, dev), *tail, _stream(dev, stream))
 
 
 def lik_policy_loss_fwd(logits, target, old_logp, advantage, loss, row_loss, row_logp, row_state=None, ref_logp=None,
                         row_weight=None, clip_low=0.2, clip_high=0.2, kl_coef=0.0, scale=1.0, stream=None):
     """Clipped policy loss of sampled tokens; row_state [rows, 4] is written for
     lik_policy_loss_bwd unless None."""
-    _need(row_state, "row_state", (logits.shape[0], 4), torch.float32, logits.device, optional=True)
+    state = _vector(row_state, "row_state", (logits.shape[0], 4), torch.float32, logits.device, optional=True)
     _policy("lik_policy_loss_fwd", logits, target, old_logp, advantage, ref_logp, row_weight, clip_low, clip_high,
-            kl_coef, scale, loss, row_loss, row_logp, (_ptr(row_state),), stream)
+            kl_coef, scale, loss, row_loss, row_logp, (state,), stream)
 
 
 def lik_policy_loss_step(logits, target, old_logp, advantage, loss, row_loss, row_logp, grad_logits, ref_logp=None,
@@ -583,13 +603,11 @@ def lik_policy_loss_step(logits, target, old_logp, advantage, loss, row_loss, ro
 
 def _target_bwd(form, logits, target, row_state, grad_logits, grad_loss, scale, stream):
     z, rows, cols, stride = _rows(logits, "logits")
-    dev = logits.device
-    g, g_stride = _grad_rows(grad_logits, logits)
-    _need(target, "target", (rows,), torch.int32, dev)
-    _need(row_state, "row_state", (rows, 4), torch.float32, dev)
-    _need(grad_loss, "grad_loss", (1,), torch.float32, dev, optional=True)
-    _check(getattr(load(), form)(z, _DTYPES[logits.dtype], rows, cols, stride, target.data_ptr(), scale,
-                                 row_state.data_ptr(), _ptr(grad_loss), g, g_stride, _stream(dev, stream)))
+    dev, f32 = logits.device, torch.float32
+    _call(form, z, _DTYPES[logits.dtype], rows, cols, stride, _vector(target, "target", (rows,), torch.int32, dev),
+          scale, _vector(row_state, "row_state", (rows, 4), f32, dev),
+          _vector(grad_loss, "grad_loss", (1,), f32, dev, optional=True), *_grad_rows(grad_logits, logits),
+          _stream(dev, stream))
 
 
 def lik_policy_loss_bwd(logits, target, row_state, grad_logits, grad_loss=None, scale=1.0, stream=None):
@@ -604,18 +622,14 @@ def _preference(form, logits, target, offsets, ref_logp, pair_weight, beta, marg
     if pair_loss.dim() != 1:
         raise ValueError("pair_loss must be [pairs]")
     pairs = pair_loss.shape[0]
-    _need(target, "target", (rows,), torch.int32, dev)
-    _need(offsets, "offsets", (2 * pairs + 1,), torch.int32, dev)
-    _need(ref_logp, "ref_logp", (2 * pairs,), f32, dev, optional=True)
-    _need(pair_weight, "pair_weight", (pairs,), f32, dev, optional=True)
-    _need(loss, "loss", (1,), f32, dev)
-    _need(pair_loss, "pair_loss", (pairs,), f32, dev)
-    _need(seq_logp, "seq_logp", (2 * pairs,), f32, dev)
-    _need(row_state, "row_state", (rows, 4), f32, dev)
-    _check(getattr(load(), form)(z, _DTYPES[logits.dtype], rows, cols, stride, target.data_ptr(), offsets.data_ptr(),
-                                 pairs, _ptr(ref_logp), _ptr(pair_weight), beta, margin, smoothing,
-                                 1 if average else 0, scale, loss.data_ptr(), pair_loss.data_ptr(),
-                                 seq_logp.data_ptr(), row_state.data_ptr(), *tail, _stream(dev, stream)))
+    _call(form, z, _DTYPES[logits.dtype], rows, cols, stride, _vector(target, "target", (rows,), torch.int32, dev),
+          _vector(offsets, "offsets", (2 * pairs + 1,), torch.int32, dev), pairs,
+          _vector(ref_logp, "ref_logp", (2 * pairs,), f32, dev, optional=True),
+          _vector(pair_weight, "pair_weight", (pairs,), f32, dev, optional=True), beta, margin, smoothing,
+          1 if average else 0, scale, _vector(loss, "loss", (1,), f32, dev),
+          _vector(pair_loss, "pair_loss", (pairs,), f32, dev),
+          _vector(seq_logp, "seq_logp", (2 * pairs,), f32, dev),
+          _vector(row_state, "row_state", (rows, 4), f32, dev), *tail, _stream(dev, stream))
 
 
 def lik_preference_loss_fwd(logits, target, offsets, loss, pair_loss, seq_logp, row_state, ref_logp=None,

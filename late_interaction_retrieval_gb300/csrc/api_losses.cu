@@ -143,8 +143,10 @@ lik_status distill(const DistillArgs& a, float* loss, float* row_loss, float* ro
     }
     cudaError_t e = cudaSuccess;
     if (fwd) {
-        if (a.rows > 0) e = launch_loss_rows(kHeadDistill, L, stream);
-        if (e == cudaSuccess) e = launch_loss_sum(row_loss, a.weight, a.rows, loss, stream);
+        bool summed = false;
+        L.sum_out = loss;
+        if (a.rows > 0) e = launch_loss_rows(kHeadDistill, L, &summed, stream);
+        if (e == cudaSuccess && !summed) e = launch_loss_sum(row_loss, a.weight, a.rows, loss, stream);
     } else if (a.rows > 0) {
         e = launch_loss_grad(kHeadDistill, L, stream);
     }
@@ -206,8 +208,10 @@ lik_status policy(const PolicyArgs& a, float* loss, float* row_loss, float* row_
         L.grad_stride = grad_stride;
     }
     cudaError_t e = cudaSuccess;
-    if (a.rows > 0) e = launch_loss_rows(kHeadPolicy, L, stream);
-    if (e == cudaSuccess) e = launch_loss_sum(row_loss, a.weight, a.rows, loss, stream);
+    bool summed = false;
+    L.sum_out = loss;
+    if (a.rows > 0) e = launch_loss_rows(kHeadPolicy, L, &summed, stream);
+    if (e == cudaSuccess && !summed) e = launch_loss_sum(row_loss, a.weight, a.rows, loss, stream);
     return e == cudaSuccess ? LIK_OK : cuda_fail(e, "policy loss launch");
 }
 
@@ -303,7 +307,7 @@ lik_status preference(const PreferenceArgs& a, float* loss, float* pair_loss, fl
     P.state = L.state;
     cudaError_t e = cudaSuccess;
     const bool grad_rows = bwd && a.rows > 0;
-    if (a.rows > 0) e = launch_loss_rows(kHeadToken, L, stream);
+    if (a.rows > 0) e = launch_loss_rows(kHeadToken, L, nullptr, stream);
     if (e == cudaSuccess && a.pairs > 0) e = launch_loss_pairs(P, stream);
     if (e == cudaSuccess && grad_rows) {  // sums the loss on the way
         L.grad = grad;

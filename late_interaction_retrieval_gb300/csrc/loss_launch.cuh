@@ -2,6 +2,7 @@
 #pragma once
 
 #include "loss_rows.cuh"
+#include "loss_short.cuh"
 
 namespace lik {
 namespace loss {
@@ -16,7 +17,11 @@ namespace loss {
 // (bf16 4096 x 32000, forward and gradient: 150 us, 161 with four).  Teachers of
 // many entries leave four too little room.
 template <typename T, int kHead, int kForm>
-cudaError_t launch_form(const LossRows& L, unsigned int* err, cudaStream_t stream) {
+cudaError_t launch_form(const LossRows& L, bool* summed, unsigned int* err, cudaStream_t stream) {
+    // up to 4 KB (and the loose elements): a warp a row, in registers
+    constexpr int64_t kV = 16 / sizeof(T);
+    if (L.cols <= 64 * kV) return launch_short<T, kHead, kForm, 2>(L, summed, stream);
+    if (L.cols <= 256 * kV) return launch_short<T, kHead, kForm, 8>(L, summed, stream);
     const RingConfig four = ring_config<kHead, kForm, 4, 4, 4>(L, 1);
     const int64_t row_bytes = L.cols * static_cast<int64_t>(sizeof(T));
     const int64_t most = kForm == kFwd ? INT64_MAX : kForm == kStep ? four.hold * int64_t(8192) : 32768;
@@ -25,19 +30,19 @@ cudaError_t launch_form(const LossRows& L, unsigned int* err, cudaStream_t strea
 }
 
 template <typename T>
-cudaError_t launch_rows(LossHead head, int form, const LossRows& L, cudaStream_t stream) {
+cudaError_t launch_rows(LossHead head, int form, const LossRows& L, bool* summed, cudaStream_t stream) {
     unsigned int* err = device_error_word();
     if (!err) return cudaErrorInvalidDevice;
     if (head == kHeadDistill) {
-        if (form == kFwd) return launch_form<T, kHeadDistill, kFwd>(L, err, stream);
-        if (form == kBwd) return launch_form<T, kHeadDistill, kBwd>(L, err, stream);
-        return launch_form<T, kHeadDistill, kStep>(L, err, stream);
+        if (form == kFwd) return launch_form<T, kHeadDistill, kFwd>(L, summed, err, stream);
+        if (form == kBwd) return launch_form<T, kHeadDistill, kBwd>(L, summed, err, stream);
+        return launch_form<T, kHeadDistill, kStep>(L, summed, err, stream);
     }
     // the gradient of a target head comes from its row states alone
-    if (form == kBwd) return launch_form<T, kHeadToken, kBwd>(L, err, stream);
-    if (head == kHeadToken) return launch_form<T, kHeadToken, kFwd>(L, err, stream);
-    if (form == kFwd) return launch_form<T, kHeadPolicy, kFwd>(L, err, stream);
-    return launch_form<T, kHeadPolicy, kStep>(L, err, stream);
+    if (form == kBwd) return launch_form<T, kHeadToken, kBwd>(L, summed, err, stream);
+    if (head == kHeadToken) return launch_form<T, kHeadToken, kFwd>(L, summed, err, stream);
+    if (form == kFwd) return launch_form<T, kHeadPolicy, kFwd>(L, summed, err, stream);
+    return launch_form<T, kHeadPolicy, kStep>(L, summed, err, stream);
 }
 
 }  // namespace loss

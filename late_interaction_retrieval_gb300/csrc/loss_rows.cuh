@@ -586,21 +586,26 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
                     const float m = v.x;
                     const int* index = e.index + buf * e.pad;
                     const float *p = e.p + buf * e.pad, *x = e.z + buf * e.pad;
-                    float coef = 0.0f;  // of the teacher's probabilities; 0: no gradient
+                    Teacher sums = {0.0f, 0.0f};
+                    bool any = false;  // the row has a gradient and a loss
+                    // this lane's first entries: column and gradient there (later ones are worked out as they are met)
+                    constexpr int kOwn = 4;
+                    int own_i[kOwn];
+                    float own_g[kOwn];
+                    const float coef = kDistill ? v.w * L.scale : 0.0f;
+                    const auto entry_gradient = [&](int k) { return v.y * ex2((x[k] - m) * c) - coef * p[k]; };
                     if (kDistill) {
                         wait(&ctl->prepared[buf], (j >> 1) & 1, late, err);
                         __syncwarp();
-                        const Teacher sums = e.sums[buf];
-                        const bool any = v.z != 0.0f && sums.mass != 0.0f;
-                        coef = any ? v.w * L.scale : 0.0f;
-                        if (kStat && rank == 0) {
-                            const float loss = any ? teacher_loss(L, e, buf, sums, m, log2f(v.z), lane) : 0.0f;
-                            if (lane == 0) {
-                                L.row_loss[r] = loss;
-                                if (L.state)
-                                    L.state[r] = any ? make_float4(m, 1.0f / v.z, v.w, sums.mass) : make_float4(0.f, 0.f, 0.f, 0.f);
+                        sums = e.sums[buf];
+                        any = v.z != 0.0f && sums.mass != 0.0f;
+                        if (kGrad)
+#pragma unroll
+                            for (int h = 0; h < kOwn; ++h) {
+                                const bool in = any && lane + 32 * h < L.k;
+                                own_i[h] = in ? index[lane + 32 * h] : -1;
+                                own_g[h] = in ? entry_gradient(lane + 32 * h) : 0.0f;
                             }
-                        }
                     }
                     if (kGrad) {
                         const bool aligned = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
@@ -613,12 +618,11 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
                             if (i < 0) continue;
                             out[i] = from_f32<T>(!kDistill && i == y ? v.z : v.y * ex2((load_f32(z + i) - m) * c));
                         }
-                        if (kDistill && coef != 0.0f && rank == 0 && (s.head > 0 || s.tail_at < cols)) {
+                        if (kDistill && any && rank == 0 && (s.head > 0 || s.tail_at < cols)) {
                             __syncwarp();
                             for (int k = lane; k < L.k; k += 32) {
                                 const int i = index[k];
-                                if (i >= 0 && (i < s.head || i >= s.tail_at))
-                                    out[i] = from_f32<T>(v.y * ex2((x[k] - m) * c) - coef * p[k]);
+                                if (i >= 0 && (i < s.head || i >= s.tail_at)) out[i] = from_f32<T>(entry_gradient(k));
                             }
                         }
                         for (int k = 0; k < t.n; ++k) {
@@ -630,14 +634,21 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
                                 if (lane == 0) (aligned ? chunk : out + at)[y - at] = from_f32<T>(v.z);
                                 fence_async();
                             }
-                            if (kDistill && coef != 0.0f) {
+                            if (kDistill && any) {
                                 T* to = aligned ? chunk : out + at;
-                                for (int o = lane; o < L.k; o += 32) {
-                                    const int i = index[o] - at;
-                                    if (static_cast<unsigned>(i) < static_cast<unsigned>(n * kV))
-                                        to[i] = from_f32<T>(v.y * ex2((x[o] - m) * c) - coef * p[o]);
+                                const unsigned size = static_cast<unsigned>(n * kV);
+                                bool wrote = false;
+#pragma unroll
+                                for (int h = 0; h < kOwn; ++h) {
+                                    const int i = own_i[h] - at;
+                                    if (own_i[h] >= 0 && static_cast<unsigned>(i) < size) to[i] = from_f32<T>(own_g[h]), wrote = true;
                                 }
-                                fence_async();
+                                for (int o = lane + 32 * kOwn; o < L.k; o += 32) {
+                                    const int i = index[o] - at;
+                                    if (index[o] >= 0 && static_cast<unsigned>(i) < size)
+                                        to[i] = from_f32<T>(entry_gradient(o)), wrote = true;
+                                }
+                                if (wrote) fence_async();
                                 __syncwarp();
                             }
                             if (lane == 0) {
@@ -654,6 +665,14 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
                             }
                             unread = aligned ? slot : -1;
                             if (++slot == cfg.slots) slot = 0, phase ^= 1;
+                        }
+                    }
+                    if (kDistill && kStat && rank == 0) {
+                        const float loss = any ? teacher_loss(L, e, buf, sums, m, log2f(v.z), lane) : 0.0f;
+                        if (lane == 0) {
+                            L.row_loss[r] = loss;
+                            if (L.state)
+                                L.state[r] = any ? make_float4(m, 1.0f / v.z, v.w, sums.mass) : make_float4(0.f, 0.f, 0.f, 0.f);
                         }
                     }
                     __syncwarp();

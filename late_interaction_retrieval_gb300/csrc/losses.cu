@@ -12,19 +12,19 @@
 
 namespace lik {
 
-cudaError_t launch_loss_f32(LossHead head, int form, const LossRows& L, cudaStream_t stream);
-cudaError_t launch_loss_f16(LossHead head, int form, const LossRows& L, cudaStream_t stream);
-cudaError_t launch_loss_bf16(LossHead head, int form, const LossRows& L, cudaStream_t stream);
+cudaError_t launch_loss_f32(LossHead head, int form, const LossRows& L, bool* summed, cudaStream_t stream);
+cudaError_t launch_loss_f16(LossHead head, int form, const LossRows& L, bool* summed, cudaStream_t stream);
+cudaError_t launch_loss_bf16(LossHead head, int form, const LossRows& L, bool* summed, cudaStream_t stream);
 
 namespace {
 
 constexpr int kThreads = 256;
 constexpr int kWarps = kThreads / 32;
 
-cudaError_t launch_dtype(LossHead head, int form, const LossRows& L, cudaStream_t stream) {
-    if (L.dtype == kF32) return launch_loss_f32(head, form, L, stream);
-    if (L.dtype == kF16) return launch_loss_f16(head, form, L, stream);
-    return launch_loss_bf16(head, form, L, stream);
+cudaError_t launch_dtype(LossHead head, int form, const LossRows& L, bool* summed, cudaStream_t stream) {
+    if (L.dtype == kF32) return launch_loss_f32(head, form, L, summed, stream);
+    if (L.dtype == kF16) return launch_loss_f16(head, form, L, summed, stream);
+    return launch_loss_bf16(head, form, L, summed, stream);
 }
 
 __device__ __forceinline__ int clamp_row(int v, int64_t rows) {
@@ -135,12 +135,13 @@ cudaError_t launch(void (*kernel)(Params...), unsigned blocks, int threads, cuda
 
 }  // namespace
 
-cudaError_t launch_loss_rows(LossHead head, const LossRows& L, cudaStream_t stream) {
-    return launch_dtype(head, L.grad ? 2 : 0, L, stream);
+cudaError_t launch_loss_rows(LossHead head, const LossRows& L, bool* summed, cudaStream_t stream) {
+    if (summed) *summed = false;
+    return launch_dtype(head, L.grad ? 2 : 0, L, summed, stream);
 }
 
 cudaError_t launch_loss_grad(LossHead head, const LossRows& L, cudaStream_t stream) {
-    return launch_dtype(head, 1, L, stream);
+    return launch_dtype(head, 1, L, nullptr, stream);
 }
 
 cudaError_t launch_loss_pairs(const LossPairs& P, cudaStream_t stream) {

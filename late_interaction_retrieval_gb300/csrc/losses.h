@@ -43,6 +43,8 @@ struct LossRows {
     float4* state = nullptr;
     const float* grad_loss = nullptr;  // upstream gradient, backward only; nullptr: 1
     // Gradient of a target head: also *sum_out = the weighted sum of sum_value (as launch_loss_sum).
+    // Forward and step of the distillation and policy heads: *sum_out may be written as the weighted
+    // sum of row_loss, where launch_loss_rows says so.
     const float* sum_value = nullptr;
     const float* sum_weight = nullptr;
     int64_t sum_n = 0;
@@ -63,8 +65,9 @@ struct LossPairs {
 };
 
 // Forward (row losses or log-probabilities, and row states unless nullptr);
-// with L.grad set, forward and gradient in one launch.
-cudaError_t launch_loss_rows(LossHead head, const LossRows& L, cudaStream_t stream);
+// with L.grad set, forward and gradient in one launch.  *summed (unless
+// nullptr): whether it also wrote *L.sum_out.
+cudaError_t launch_loss_rows(LossHead head, const LossRows& L, bool* summed, cudaStream_t stream);
 
 // Gradient from the row states of a forward.
 cudaError_t launch_loss_grad(LossHead head, const LossRows& L, cudaStream_t stream);
