@@ -18,9 +18,6 @@ cudaError_t launch_loss_bf16(LossHead head, int form, const LossRows& L, bool* s
 
 namespace {
 
-constexpr int kThreads = 256;
-constexpr int kWarps = kThreads / 32;
-
 cudaError_t launch_dtype(LossHead head, int form, const LossRows& L, bool* summed, cudaStream_t stream) {
     if (L.dtype == kF32) return launch_loss_f32(head, form, L, summed, stream);
     if (L.dtype == kF16) return launch_loss_f16(head, form, L, summed, stream);
@@ -31,73 +28,72 @@ __device__ __forceinline__ int clamp_row(int v, int64_t rows) {
     return v < 0 ? 0 : static_cast<int64_t>(v) > rows ? static_cast<int>(rows) : v;
 }
 
-// Block-wide sum and count, in a fixed order.
-__device__ double block_sum(loss::Sum2 s, int n, loss::Sum2* part, int* count, int* total) {
-    s.reduce();
-    n = __reduce_add_sync(0xffffffffu, n);
-    __syncthreads();
-    if ((threadIdx.x & 31) == 0) {
-        part[threadIdx.x >> 5] = s;
-        count[threadIdx.x >> 5] = n;
-    }
-    __syncthreads();
-    s = part[0];
-    *total = count[0];
-    for (int w = 1; w < kWarps; ++w) {
-        s.add(part[w]);
-        *total += count[w];
-    }
-    return s.value();
-}
+constexpr int kPairThreads = 512;
+constexpr int kPairWarps = kPairThreads / 64;  // of one sequence
 
-// One block per pair: both sequence sums (exact to fp32: thousands of
-// log-probabilities enter a small difference), the pair's loss, and every
-// row's d loss / d log-probability into its state.
-__global__ void __launch_bounds__(kThreads) loss_pairs_kernel(const LossPairs P) {
-    __shared__ loss::Sum2 part[kWarps];
-    __shared__ int count[kWarps];
+// One block per pair, half of it per sequence: both sequence sums (exact to
+// fp32: thousands of log-probabilities enter a small difference), the pair's
+// loss, and every row's d loss / d log-probability into its state.  Latency
+// bounds it: what does not depend on the sums is loaded before them.
+__global__ void __launch_bounds__(kPairThreads) loss_pairs_kernel(const LossPairs P) {
+    __shared__ loss::Sum2 part[2][kPairWarps];
+    __shared__ int count[2][kPairWarps];
     loss::grid_launch_dependents();
     loss::grid_wait();
     const int64_t p = blockIdx.x;
-    float sum[2], share[2];
-    int lo[2], hi[2];
-    for (int h = 0; h < 2; ++h) {
-        const int64_t i = p + h * P.pairs;
-        lo[h] = clamp_row(P.offsets[i], P.rows);
-        hi[h] = clamp_row(P.offsets[i + 1], P.rows);
-        loss::Sum2 s;
-        int n = 0, all = 0;
-        for (int r = lo[h] + static_cast<int>(threadIdx.x); r < hi[h]; r += kThreads) {
-            const float4 st = P.state[r];
-            if (st.y != 0.0f) {
-                s.add(st.z);
-                ++n;
-            }
-        }
-        const double t = block_sum(s, n, part, count, &all);
-        share[h] = P.average && all > 0 ? 1.0f / static_cast<float>(all) : 1.0f;
-        sum[h] = static_cast<float>(P.average && all > 0 ? t / all : t);
-        if (threadIdx.x == 0) P.seq_logp[i] = sum[h];
-    }
+    const int h = threadIdx.x >= kPairThreads / 2, t = threadIdx.x % (kPairThreads / 2);
+    const int64_t seq = p + h * P.pairs;
+    const int lo = clamp_row(P.offsets[seq], P.rows), hi = clamp_row(P.offsets[seq + 1], P.rows);
     const float w = P.weight ? P.weight[p] : 1.0f / static_cast<float>(P.pairs);
+    double gap = 0.0;
+    if (P.ref_logp) gap = -(static_cast<double>(P.ref_logp[p]) - P.ref_logp[p + P.pairs]);
+    loss::Sum2 s;
+    int n = 0;
+    for (int r = lo + t; r < hi; r += kPairThreads / 2) {
+        const float4 st = P.state[r];
+        if (st.y != 0.0f) {
+            s.add(st.z);
+            ++n;
+        }
+    }
+    s.reduce();
+    n = __reduce_add_sync(0xffffffffu, n);
+    if ((threadIdx.x & 31) == 0) {
+        part[h][t >> 5] = s;
+        count[h][t >> 5] = n;
+    }
+    __syncthreads();
+    float sum[2], share[2];
+    for (int q = 0; q < 2; ++q) {
+        loss::Sum2 all = part[q][0];
+        int rows = count[q][0];
+        for (int i = 1; i < kPairWarps; ++i) {
+            all.add(part[q][i]);
+            rows += count[q][i];
+        }
+        const bool mean = P.average && rows > 0;
+        share[q] = mean ? 1.0f / static_cast<float>(rows) : 1.0f;
+        sum[q] = static_cast<float>(mean ? all.value() / rows : all.value());
+    }
     float g = 0.0f, loss = 0.0f;
     if (w != 0.0f) {
         // of the sums as they are returned: the loss follows from the outputs
-        double gap = static_cast<double>(sum[0]) - sum[1];
-        if (P.ref_logp) gap -= static_cast<double>(P.ref_logp[p]) - P.ref_logp[p + P.pairs];
+        gap += static_cast<double>(sum[0]) - sum[1];
         const float x = static_cast<float>(P.beta * gap - P.margin);
         const float tail = log1pf(expf(-fabsf(x)));
         loss = (1.0f - P.smoothing) * (fmaxf(-x, 0.0f) + tail) + P.smoothing * (fmaxf(x, 0.0f) + tail);
+        if (isnan(x)) loss = x;  // fmaxf drops a NaN
         // sigma(x) - (1 - smoothing), each part without cancellation
         const float pos = 1.0f / (1.0f + expf(-x)), neg = 1.0f / (1.0f + expf(x));
         g = w * P.beta * (P.smoothing * pos - (1.0f - P.smoothing) * neg);
     }
-    if (threadIdx.x == 0) P.pair_loss[p] = loss;
-    for (int h = 0; h < 2; ++h) {
-        const float v = (h ? -g : g) * share[h];
-        for (int r = lo[h] + static_cast<int>(threadIdx.x); r < hi[h]; r += kThreads)
-            if (P.state[r].y != 0.0f) P.state[r].w = v;
+    if (t == 0) {
+        P.seq_logp[seq] = sum[h];
+        if (h == 0) P.pair_loss[p] = loss;
     }
+    const float v = (h ? -g : g) * share[h];
+    for (int r = lo + t; r < hi; r += kPairThreads / 2)
+        if (P.state[r].y != 0.0f) P.state[r].w = v;
 }
 
 constexpr int kSumThreads = 1024;
@@ -145,7 +141,7 @@ cudaError_t launch_loss_grad(LossHead head, const LossRows& L, cudaStream_t stre
 }
 
 cudaError_t launch_loss_pairs(const LossPairs& P, cudaStream_t stream) {
-    return launch(loss_pairs_kernel, static_cast<unsigned>(P.pairs), kThreads, stream, P);
+    return launch(loss_pairs_kernel, static_cast<unsigned>(P.pairs), kPairThreads, stream, P);
 }
 
 cudaError_t launch_loss_sum(const float* value, const float* weight, int64_t n, float* loss, cudaStream_t stream) {
