@@ -17,7 +17,6 @@ namespace lik {
 namespace loss {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kLn2 = 0.6931471805599453f;
 
 __device__ __forceinline__ float ex2(float x) {
     float y;
@@ -214,11 +213,6 @@ __device__ __forceinline__ Stat warp_merge(Stat v, float c) {
     return {m, warp_sum(v.s * ex2((v.m - offset_of(m)) * c))};
 }
 
-// log q at a column whose logit is z.
-__device__ __forceinline__ float log_prob(float z, float m, float log2_s, float c) {
-    return fmaf(z - m, c, -log2_s) * kLn2;
-}
-
 // A thread's running statistics.  A NaN logit leaves the max alone and makes
 // the sum NaN.
 struct Running {
@@ -347,7 +341,9 @@ __device__ __forceinline__ float2 policy_head(const LossRows& L, float lp, float
 // --------------------------------------------------- the teacher's entries --
 
 struct Teacher {
-    float mass, plogp;  // sum of p, of p log2 p
+    float mass;   // sum of p
+    float pt;     // sum of p s (t - base), where log p = s (t - base) - shift
+    float shift;
 };
 
 // Two rows' entries in shared memory (the one at work and the next): column
@@ -390,7 +386,7 @@ __device__ __forceinline__ Teacher prepare_teacher(const LossRows& L, int64_t r,
     const T* row = static_cast<const T*>(L.logits) + r * L.stride;
     const int cols = static_cast<int>(L.cols);
     const float c = L.c;
-    float base = 0.0f, shift = 0.0f;  // log2 p = c (t - base) - shift
+    float base = 0.0f, shift = 0.0f;
     if (L.t_lse) shift = L.t_lse[r];
     float top = -INFINITY;
     for (int k0 = lane; k0 < L.k; k0 += 32 * kBatch) {
@@ -418,36 +414,35 @@ __device__ __forceinline__ Teacher prepare_teacher(const LossRows& L, int64_t r,
             top = fmaxf(top, t[b]);
         }
     }
-    if (L.t_lse) {
-        shift *= kLog2e;
-    } else {
+    if (!L.t_lse) {
         base = offset_of(warp_max(top));
         float s = 0.0f;
         for (int k = lane; k < L.k; k += 32) s += ex2((p[k] - base) * c);
-        shift = log2f(warp_sum(s));
+        shift = logf(warp_sum(s));
     }
-    float mass = 0.0f, plogp = 0.0f;
+    float mass = 0.0f, pt = 0.0f;
     for (int k = lane; k < L.k; k += 32) {
         float prob = 0.0f;
         if (p[k] != -INFINITY) {
-            const float lp = fmaf(p[k] - base, c, -shift);
-            prob = ex2(lp);
-            if (prob != 0.0f) plogp += prob * lp;
+            const float y = (p[k] - base) * L.scale;
+            prob = ex2((y - shift) * kLog2e);
+            if (prob != 0.0f) pt += prob * y;
         }
         p[k] = prob;
         mass += prob;
     }
-    return {warp_sum(mass), warp_sum(plogp)};
+    return {warp_sum(mass), warp_sum(pt), shift};
 }
 
-// sum of p (log p - log q) over the entries (one warp).
+// sum of p (log p - log q) over the entries (one warp).  The two normalisers
+// are taken off the sums, not every term: they are the largest parts.
 __device__ __forceinline__ float teacher_loss(const LossRows& L, const Entries& e, int buf, const Teacher& t, float m,
-                                              float log2_s, int lane) {
+                                              float log_s, int lane) {
     const float *p = e.p + buf * e.pad, *z = e.z + buf * e.pad;
     float cross = 0.0f;
     for (int k = lane; k < L.k; k += 32)
-        if (p[k] != 0.0f) cross += p[k] * fmaf(z[k] - m, L.c, -log2_s);
-    return (t.plogp - warp_sum(cross)) * kLn2;
+        if (p[k] != 0.0f) cross += p[k] * ((z[k] - m) * L.scale);
+    return (t.pt - warp_sum(cross)) - t.mass * (t.shift - log_s);
 }
 
 // Gives the first entry of a column the sum of all entries of that column and

@@ -486,7 +486,7 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
                             const float mass = ctl->mass[b][0].x;
                             v = make_float4(m, live && mass != 0.0f ? weight * L.scale * mass * inv : 0.0f, total.s, weight);
                         } else {
-                            const float lp = live ? log_prob(w.from(zy, i), m, log2f(total.s), c) : 0.0f;
+                            const float zt = w.from(zy, i), lp = live ? (zt - m) * L.scale - logf(total.s) : 0.0f;
                             float2 h = make_float2(0.0f, 0.0f);
                             if (kHead == kHeadPolicy) {
                                 const float o = w.from(old_logp, i), a = w.from(adv, i), q = w.from(ref, i);
@@ -501,7 +501,7 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
                                 if (L.state) L.state[r] = make_float4(m, inv, lp, h.y);
                             }
                             const float hot = h.y * L.scale;
-                            v = make_float4(m, -hot * inv, target_gradient(w.from(zy, i), m, -hot * inv, hot, c), 0.0f);
+                            v = make_float4(m, -hot * inv, target_gradient(zt, m, -hot * inv, hot, c), 0.0f);
                         }
                     } else {  // distillation from its saved state: (max, 1 / sum, weight, mass)
                         wait(&ctl->ready[b], phase, late, err);
@@ -586,7 +586,7 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
                     const float m = v.x;
                     const int* index = e.index + buf * e.pad;
                     const float *p = e.p + buf * e.pad, *x = e.z + buf * e.pad;
-                    Teacher sums = {0.0f, 0.0f};
+                    Teacher sums = {0.0f, 0.0f, 0.0f};
                     bool any = false;  // the row has a gradient and a loss
                     // this lane's first entries: column and gradient there (later ones are worked out as they are met)
                     constexpr int kOwn = 4;
@@ -668,7 +668,7 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
                         }
                     }
                     if (kDistill && kStat && rank == 0) {
-                        const float loss = any ? teacher_loss(L, e, buf, sums, m, log2f(v.z), lane) : 0.0f;
+                        const float loss = any ? teacher_loss(L, e, buf, sums, m, logf(v.z), lane) : 0.0f;
                         if (lane == 0) {
                             L.row_loss[r] = loss;
                             if (L.state)

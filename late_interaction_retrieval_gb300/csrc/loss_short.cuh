@@ -74,7 +74,7 @@ __global__ void __launch_bounds__(kN <= 2 ? 1024 : 256) loss_short_kernel(const 
                 if (L.ref_logp) ref = L.ref_logp[r];
             }
         }
-        float m = 0.0f, inv = 0.0f, log2_s = 0.0f;
+        float m = 0.0f, inv = 0.0f, log_s = 0.0f;
         bool live = read;
         if (kStat && read) {
             Running v;
@@ -84,17 +84,17 @@ __global__ void __launch_bounds__(kN <= 2 ? 1024 : 256) loss_short_kernel(const 
             live = total.s != 0.0f;
             m = offset_of(total.m);
             inv = live ? 1.0f / total.s : 0.0f;
-            log2_s = log2f(total.s);
+            log_s = logf(total.s);
         }
         float a = 0.0f, coef = 0.0f, at_target = 0.0f;
         if (kDistill) {
-            float mass = 0.0f, loss = 0.0f;
+            float mass = 0.0f, gap = 0.0f, loss = 0.0f;
             if (live) {
                 // the teacher: its max, its sum, then p and what follows from it
                 const int32_t* index = L.t_index + r * L.k;
                 float base = 0.0f, shift = 0.0f;
                 if (L.t_lse) {
-                    shift = L.t_lse[r] * kLog2e;
+                    shift = L.t_lse[r];
                 } else {
                     float top = -INFINITY, s = 0.0f;
                     for (int k = lane; k < L.k; k += 32) {
@@ -106,7 +106,7 @@ __global__ void __launch_bounds__(kN <= 2 ? 1024 : 256) loss_short_kernel(const 
                         const int i = index[k];
                         if (i >= 0 && i < cols) s += ex2((teacher_logit(L, r * L.k + k) - base) * c);
                     }
-                    shift = log2f(warp_sum(s));
+                    shift = logf(warp_sum(s));
                 }
                 if (kGrad) {
                     for (int i = lane; i < cols; i += 32) dense[i] = 0.0f;
@@ -120,9 +120,9 @@ __global__ void __launch_bounds__(kN <= 2 ? 1024 : 256) loss_short_kernel(const 
                     if (i >= 0) {
                         const float t = teacher_logit(L, r * L.k + k);
                         if (t != -INFINITY) {
-                            const float lp = fmaf(t - base, c, -shift);
-                            p = ex2(lp);
-                            if (kStat && p != 0.0f) loss += p * (lp - fmaf(load_f32(z + i) - m, c, -log2_s));
+                            const float y = (t - base) * L.scale;
+                            p = ex2((y - shift) * kLog2e);
+                            if (kStat && p != 0.0f) gap += p * (y - (load_f32(z + i) - m) * L.scale);
                         }
                         mass += p;
                     }
@@ -130,7 +130,7 @@ __global__ void __launch_bounds__(kN <= 2 ? 1024 : 256) loss_short_kernel(const 
                 }
                 mass = warp_sum(mass);
                 if (kStat) {
-                    loss = warp_sum(loss) * kLn2;
+                    loss = warp_sum(gap) - mass * (shift - log_s);
                     live = mass != 0.0f;
                 }
             }
@@ -150,7 +150,7 @@ __global__ void __launch_bounds__(kN <= 2 ? 1024 : 256) loss_short_kernel(const 
         } else {
             float hot = 0.0f;
             if (kStat) {
-                const float lp = live ? log_prob(zy, m, log2_s, c) : 0.0f;
+                const float lp = live ? (zy - m) * L.scale - log_s : 0.0f;
                 float2 h = make_float2(0.0f, 0.0f);
                 if (kHead == kHeadPolicy && live) {
                     h = policy_head(L, lp, old_logp, adv, ref);
