@@ -30,7 +30,7 @@ cudaError_t launch_form(const LossRows& L, bool* summed, unsigned int* err, cuda
 }
 
 template <typename T>
-cudaError_t launch_rows(LossHead head, int form, const LossRows& L, bool* summed, cudaStream_t stream) {
+cudaError_t launch_rows(LossHead head, LossForm form, const LossRows& L, bool* summed, cudaStream_t stream) {
     unsigned int* err = device_error_word();
     if (!err) return cudaErrorInvalidDevice;
     if (head == kHeadDistill) {

@@ -9,8 +9,8 @@
 //     and every warp sends its pair to the cluster's first CTA;
 //   - there the closer (one warp) merges them, computes the loss head and
 //     sends every CTA what the gradient needs: the max and the coefficients;
-//   - the consumers walk the same chunks again, after the statistics of the
-//     next row, and turn the logits into the gradient where they lie;
+//   - the consumers walk the same chunks again and turn the logits into the
+//     gradient where they lie;
 //   - the storer (one warp) writes the chunks out (cp.async.bulk) and hands
 //     them back to the loader.
 // So a step reads a row from memory once and writes its gradient once, and
@@ -29,9 +29,18 @@
 // one by one by the first CTA of the cluster.
 //
 // Every wait is bounded.  Statistics and coefficients travel as st.async
-// messages counted by mbarriers, in buffers of four rows: a sender never is
-// more than two rows ahead of the slowest reader, as the comments at the
-// barriers say.
+// messages counted by mbarriers, in buffers of four rows; the comments at the
+// barriers say why none is overwritten before it is read.
+//
+// Memory bounds it: a step moves 2 x 64 KB of a row per SM in 11,000 cycles, as
+// a copy kernel does.  What it loses against a copy of the same bytes is its
+// start and end (some 10 us with the sum's launch), the clusters' last round,
+// and that SMs get unequal shares of the memory's rate (the mean SM is done
+// at 0.88 of the slowest's time).  Measured (events, inputs beyond L2, with the
+// sum) bf16: distillation step of 4096 x 128000 371 us where its bytes take 309;
+// policy step of 8192 x 64000, a quarter of the rows left out, 299 us (271).
+// The same step as a forward and a backward reads the logits twice: 1.5 times
+// these bytes.
 #pragma once
 
 #include <atomic>
@@ -45,14 +54,10 @@
 namespace lik {
 namespace loss {
 
-// What a launch does with a row.  kFwd: statistics and loss; kBwd: the
-// gradient from saved statistics; kStep: both.
-enum Form : int { kFwd = 0, kBwd = 1, kStep = 2 };
-
 constexpr int kMaxSlots = 8;
 constexpr int kMaxCluster = 8;
 constexpr int kMaxWarps = 8;
-constexpr int kMinSliceBytes = 8192;  // a row is not split finer for want of rows
+constexpr int kMinSliceBytes = 4096;  // a row is not split finer for want of rows
 constexpr int kSideWarps = 4;         // loader, closer, storer, teacher
 constexpr int kPlanRows = 1 << 14;    // rows that are dealt out evenly by what they cost (3 KB of shared memory)
 constexpr int kZeros = 128;           // granules of zeros that rows left out are stored from
@@ -62,7 +67,7 @@ constexpr size_t ring_smem(int ctas) { return static_cast<size_t>(228 / ctas - 1
 
 struct RingConfig {
     int cluster;       // CTAs per row
-    int slots;         // ring chunks (a chunk is 32 bytes per consumer thread)
+    int slots;         // ring chunks, of kNG granules per consumer thread
     int hold;          // chunks of a row that stay in the ring between a step's two passes, at most
     int k_pad;         // teacher entries, rounded up (distillation)
     int filter_words;  // of each of the two bit sets that find duplicate columns
@@ -191,13 +196,14 @@ struct Control {
     // A chunk is loaded; the consumers have its gradient (forms with one) or are
     // done with it; the loader may refill it.
     uint64_t full[kMaxSlots], done[kMaxSlots], empty[kMaxSlots];
-    // First CTA: the pairs of every warp of the cluster.  A consumer sends row
-    // j's after it has had go of row j - 2 (j - 3 without a gradient), so the
-    // closer has used row j - 4's.
+    // First CTA: the pairs of every warp of the cluster.  With a gradient a
+    // consumer sends row j's after its CTA's storer closed row j - 4 and it has had
+    // go of row j - 1; without one, after go of row j - 3: the closer has used row
+    // j - 4's either way.
     uint64_t stat[kBuf];
     float2 parts[kBuf][kMaxCluster * kMaxWarps];
     // First CTA: the teacher mass from every CTA's teacher warp, sent for row j
-    // after go of row j - 2.
+    // after the storer freed row j - 2's entries, and so had go of it.
     uint64_t ready[kBuf];
     float2 mass[kBuf][kMaxCluster];
     // Every CTA: (max, coefficient of e, the gradient at the target or the sum,
@@ -663,7 +669,7 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
                                     arrive(&ctl->empty[slot]);
                                 }
                             }
-                            unread = aligned ? slot : -1;
+                            if (aligned) unread = slot;
                             if (++slot == cfg.slots) slot = 0, phase ^= 1;
                         }
                     }
@@ -717,10 +723,6 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
         }
     } else {
         // -------------------------------------------------- the consumers --
-        struct Row {
-            int64_t r;
-            float m, a;
-        };
         const float up = !kGo && L.grad_loss ? *L.grad_loss : 1.0f;
         int slot = 0, j = 0, q = 0;
         uint32_t phase = 0;
@@ -729,7 +731,8 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
         while (true) {
             // the next row that is read
             bool have = false;
-            Row row;
+            int64_t r = 0;
+            float m = 0.0f, a = 0.0f;  // the max; the coefficient of e
             while (w.n > 0) {
                 if (q == w.n) {
                     w.advance();
@@ -737,14 +740,14 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
                     continue;
                 }
                 if (w.live >> q & 1) {
-                    row.r = w.at(q);
+                    r = w.at(q);
                     have = true;
                     break;
                 }
                 ++q;
             }
             if (!have) break;
-            const T* z = logits + row.r * L.stride;
+            const T* z = logits + r * L.stride;
             const Slice<T> s(z, cols, rank, cfg.cluster);
             const Passes t(s.n, kChunk, cfg.hold);
             const int b = j % kBuf;
@@ -755,61 +758,59 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
                 else if (kStat) expect(&ctl->stat[b], kWarps * (cfg.cluster - 1) * 8);
             }
             if (!kGo) {
-                row.m = w.from(w.mine.st.x, q);
-                row.a = -w.from(w.mine.st.w, q) * up * L.scale * w.from(w.mine.st.y, q);
+                m = w.from(w.mine.st.x, q);
+                a = -w.from(w.mine.st.w, q) * up * L.scale * w.from(w.mine.st.y, q);
             }
-            {
-                if (kStat) {
-                    Running v;
-                    int slot2 = slot;  // where the second pass starts
-                    uint32_t phase2 = phase;
-                    for (int k = 0; k < t.n; ++k) {
-                        const int g = k * kChunk;
-                        if (k == t.n - t.kept) slot2 = slot, phase2 = phase;
-                        wait(&ctl->full[slot], phase, late, err);
-                        const uint4* chunk = ring + slot * kChunk + tid;
-                        uint4 u[kNG];
+            if (kStat) {
+                Running v;
+                int slot2 = slot;  // where the second pass starts
+                uint32_t phase2 = phase;
+                for (int k = 0; k < t.n; ++k) {
+                    const int g = k * kChunk;
+                    if (k == t.n - t.kept) slot2 = slot, phase2 = phase;
+                    wait(&ctl->full[slot], phase, late, err);
+                    const uint4* chunk = ring + slot * kChunk + tid;
+                    uint4 u[kNG];
 #pragma unroll
-                        for (int h = 0; h < kNG; ++h) u[h] = chunk[h * kNT];
-                        if (s.n - g < kChunk) {  // beyond the slice: logits of no weight
+                    for (int h = 0; h < kNG; ++h) u[h] = chunk[h * kNT];
+                    if (s.n - g < kChunk) {  // beyond the slice: logits of no weight
 #pragma unroll
-                            for (int h = 0; h < kNG; ++h)
-                                if (tid + h * kNT >= s.n - g) u[h] = Granule<T>::nothing();
-                        }
-                        v.add_granules<T, kNG>(u, c);
-                        if (kForm == kFwd || k < t.n - t.kept) {
-                            __syncwarp();
-                            if (lane == 0) arrive(kGrad ? &ctl->done[slot] : &ctl->empty[slot]);
-                        }
-                        if (++slot == cfg.slots) slot = 0, phase ^= 1;
+                        for (int h = 0; h < kNG; ++h)
+                            if (tid + h * kNT >= s.n - g) u[h] = Granule<T>::nothing();
                     }
-                    if (loose >= 0) v.add(loose_z, c);
-                    const Stat total = warp_merge(v.stat(), c);
-                    if (kGrad && j >= kBuf) wait(&ctl->closed[b], (j / kBuf - 1) & 1, late, err);
-                    if (!kGrad && j >= 3) wait(&ctl->go[(j - 3) % kBuf], ((j - 3) / kBuf) & 1, late, err);
-                    if (lane == 0) {
-                        float2* at = &ctl->parts[b][rank * kWarps + warp];
-                        if (rank == 0) {
-                            *at = make_float2(total.m, total.s);
-                            arrive(&ctl->stat[b]);
-                        } else {
-                            send(map_rank(ptx::smem_u32(at), 0), make_float2(total.m, total.s),
-                                 map_rank(ptx::smem_u32(&ctl->stat[b]), 0));
-                        }
+                    v.add_granules<T, kNG>(u, c);
+                    if (kForm == kFwd || k < t.n - t.kept) {
+                        __syncwarp();
+                        if (lane == 0) arrive(kGrad ? &ctl->done[slot] : &ctl->empty[slot]);
                     }
-                    if (kGrad) slot = slot2, phase = phase2;
+                    if (++slot == cfg.slots) slot = 0, phase ^= 1;
                 }
+                if (loose >= 0) v.add(loose_z, c);
+                const Stat total = warp_merge(v.stat(), c);
+                if (kGrad && j >= kBuf) wait(&ctl->closed[b], (j / kBuf - 1) & 1, late, err);
+                if (!kGrad && j >= 3) wait(&ctl->go[(j - 3) % kBuf], ((j - 3) / kBuf) & 1, late, err);
+                if (lane == 0) {
+                    float2* at = &ctl->parts[b][rank * kWarps + warp];
+                    if (rank == 0) {
+                        *at = make_float2(total.m, total.s);
+                        arrive(&ctl->stat[b]);
+                    } else {
+                        send(map_rank(ptx::smem_u32(at), 0), make_float2(total.m, total.s),
+                             map_rank(ptx::smem_u32(&ctl->stat[b]), 0));
+                    }
+                }
+                if (kGrad) slot = slot2, phase = phase2;
             }
             if (kGrad) {
-                T* out = static_cast<T*>(L.grad) + row.r * L.grad_stride;
+                T* out = static_cast<T*>(L.grad) + r * L.grad_stride;
                 const bool aligned = ((reinterpret_cast<uintptr_t>(out) ^ reinterpret_cast<uintptr_t>(z)) & 15) == 0;
                 if (kGo) {
                     // The row may be written (in place of the logits) from here on: whoever reads
                     // it elsewhere has done so before the closer could decide.
                     wait(&ctl->go[b], (j / kBuf) & 1, late, err);
                     const float4 v = ctl->verdict[b];
-                    row.m = v.x;
-                    row.a = v.y;
+                    m = v.x;
+                    a = v.y;
                 }
                 for (int k = 0; k < t.n; ++k) {
                     const int g = (kForm == kStep ? t.second(k) : k) * kChunk;
@@ -818,7 +819,7 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
                     const int n = s.n - g - tid;  // what is left from this thread's granule on
                     uint4 u[kNG];
 #pragma unroll
-                    for (int h = 0; h < kNG; ++h) u[h] = gradient<T>(chunk[h * kNT], row.m, row.a, c);
+                    for (int h = 0; h < kNG; ++h) u[h] = gradient<T>(chunk[h * kNT], m, a, c);
 #pragma unroll
                     for (int h = 0; h < kNG; ++h) chunk[h * kNT] = u[h];  // beyond the slice: of no use, and not stored
                     if (!aligned) {
@@ -844,15 +845,25 @@ __global__ void __launch_bounds__(kWarps * 32 + kSideWarps * 32)
 
 // CTAs that share a row.  In a step a slice has to fit what a CTA can hold
 // between its two passes (`held` bytes; where even 8 CTAs do not, the rest is
-// read again), and never is a row split finer than that needs, but where rows
-// are too few for all SMs: split in two, a row costs both CTAs the exchange of
-// its statistics (measured: 8192 x 32000 bf16 in a step, 64 KB rows: 185 us by
-// one CTA a row, 257 by two, 361 by four).
-inline int pick_cluster(int64_t rows, int64_t row_bytes, int64_t held, int ctas) {
-    int c = 1;
-    while (held > 0 && c < kMaxCluster && row_bytes > held * c) c *= 2;
-    while (c < kMaxCluster && rows * c * 2 <= ctas && row_bytes / (2 * c) >= kMinSliceBytes) c *= 2;
-    return c;
+// read again).  More than that pays where rows are few, or leave much idle in
+// their last round: a round costs a CTA its slice's bytes at its share of an
+// SM's 44 bytes a ns, and some 1.5 us of latency that the others' work does not
+// cover, 0.8 more for each halving.  Rows in many rounds are best not split
+// (8192 x 32000 bf16 in a step, 64 KB rows: 185 us by one CTA a row, 257 by two,
+// 361 by four).
+inline int pick_cluster(int64_t rows, int64_t row_bytes, int64_t held, int passes, int sm_count, int ctas) {
+    int best = 0;
+    double best_ns = 0.0;
+    for (int c = 1; c <= kMaxCluster; c *= 2) {
+        if (held > 0 && c < kMaxCluster && row_bytes > held * c) continue;
+        if (best && row_bytes / c < kMinSliceBytes) break;
+        const int64_t slots = static_cast<int64_t>(sm_count) * ctas / c;
+        const double rounds = static_cast<double>((rows + slots - 1) / slots);
+        const double wait = c == 1 ? 1500.0 : c == 2 ? 2300.0 : c == 4 ? 3100.0 : 3900.0;
+        const double ns = rounds * (wait + static_cast<double>(row_bytes / c) * passes * ctas / 44.0);
+        if (!best || ns < best_ns) best = c, best_ns = ns;
+    }
+    return best;
 }
 
 // How a CTA's shared memory is used; cluster is left open.
@@ -890,7 +901,7 @@ cudaError_t launch_ring(const LossRows& L, unsigned int* err, cudaStream_t strea
     RingConfig cfg = ring_config<kHead, kForm, kWarps, kNG, kCtas>(L, info.sm_count);
     if (cfg.slots < 3) return cudaErrorInvalidConfiguration;
     cfg.cluster = pick_cluster(L.rows, L.cols * static_cast<int64_t>(sizeof(T)),
-                               static_cast<int64_t>(cfg.hold) * kChunkBytes, info.sm_count);
+                               static_cast<int64_t>(cfg.hold) * kChunkBytes, kForm == kFwd ? 1 : 2, info.sm_count, kCtas);
 
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeClusterDimension;

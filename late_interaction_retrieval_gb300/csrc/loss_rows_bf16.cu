@@ -2,7 +2,7 @@
 #include "loss_launch.cuh"
 
 namespace lik {
-cudaError_t launch_loss_bf16(LossHead head, int form, const LossRows& L, bool* summed, cudaStream_t stream) {
+cudaError_t launch_loss_bf16(LossHead head, LossForm form, const LossRows& L, bool* summed, cudaStream_t stream) {
     return loss::launch_rows<__nv_bfloat16>(head, form, L, summed, stream);
 }
 }  // namespace lik

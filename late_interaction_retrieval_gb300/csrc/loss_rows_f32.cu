@@ -2,7 +2,7 @@
 #include "loss_launch.cuh"
 
 namespace lik {
-cudaError_t launch_loss_f32(LossHead head, int form, const LossRows& L, bool* summed, cudaStream_t stream) {
+cudaError_t launch_loss_f32(LossHead head, LossForm form, const LossRows& L, bool* summed, cudaStream_t stream) {
     return loss::launch_rows<float>(head, form, L, summed, stream);
 }
 }  // namespace lik

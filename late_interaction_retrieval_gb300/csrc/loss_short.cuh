@@ -35,7 +35,7 @@ __device__ __forceinline__ void add_in_order(float* dense, int i, float p, int l
 template <typename T, int kHead, int kForm, int kN>
 __global__ void __launch_bounds__(kN <= 2 ? 1024 : 256) loss_short_kernel(const LossRows L) {
     constexpr int kV = 16 / sizeof(T), kP = Granule<T>::kPairs;
-    constexpr bool kDistill = kHead == kHeadDistill, kGrad = kForm != 0, kStat = kForm != 1;
+    constexpr bool kDistill = kHead == kHeadDistill, kGrad = kForm != kFwd, kStat = kForm != kBwd;
     extern __shared__ float dense_all[];
     __shared__ Sum2 part[32];
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
@@ -224,13 +224,13 @@ cudaError_t launch_short(LossRows L, bool* summed, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     // Few rows of at most 1 KB: one block of 32 warps takes them all and adds up
     // the loss, which saves a launch; it costs two rows a warp in turn at most.
-    const bool alone = kForm != 1 && kN <= 2 && L.sum_out && L.rows <= 64;
-    if (kForm != 1 && !alone) L.sum_out = nullptr;
+    const bool alone = kForm != kBwd && kN <= 2 && L.sum_out && L.rows <= 64;
+    if (kForm != kBwd && !alone) L.sum_out = nullptr;
     if (summed) *summed = alone;
     const int threads = alone ? 1024 : 256;
     const int64_t warps = threads / 32, most = device_info(dev).sm_count * int64_t(8);
     const int64_t blocks = (L.rows + warps - 1) / warps;
-    const size_t smem = kHead == kHeadDistill && kForm != 0 ? static_cast<size_t>(warps) * L.cols * 4 : 0;
+    const size_t smem = kHead == kHeadDistill && kForm != kFwd ? static_cast<size_t>(warps) * L.cols * 4 : 0;
     auto kernel = loss_short_kernel<T, kHead, kForm, kN>;
     if (smem > 48 * 1024) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));

@@ -12,13 +12,13 @@
 
 namespace lik {
 
-cudaError_t launch_loss_f32(LossHead head, int form, const LossRows& L, bool* summed, cudaStream_t stream);
-cudaError_t launch_loss_f16(LossHead head, int form, const LossRows& L, bool* summed, cudaStream_t stream);
-cudaError_t launch_loss_bf16(LossHead head, int form, const LossRows& L, bool* summed, cudaStream_t stream);
+cudaError_t launch_loss_f32(LossHead head, LossForm form, const LossRows& L, bool* summed, cudaStream_t stream);
+cudaError_t launch_loss_f16(LossHead head, LossForm form, const LossRows& L, bool* summed, cudaStream_t stream);
+cudaError_t launch_loss_bf16(LossHead head, LossForm form, const LossRows& L, bool* summed, cudaStream_t stream);
 
 namespace {
 
-cudaError_t launch_dtype(LossHead head, int form, const LossRows& L, bool* summed, cudaStream_t stream) {
+cudaError_t launch_dtype(LossHead head, LossForm form, const LossRows& L, bool* summed, cudaStream_t stream) {
     if (L.dtype == kF32) return launch_loss_f32(head, form, L, summed, stream);
     if (L.dtype == kF16) return launch_loss_f16(head, form, L, summed, stream);
     return launch_loss_bf16(head, form, L, summed, stream);
@@ -133,11 +133,11 @@ cudaError_t launch(void (*kernel)(Params...), unsigned blocks, int threads, cuda
 
 cudaError_t launch_loss_rows(LossHead head, const LossRows& L, bool* summed, cudaStream_t stream) {
     if (summed) *summed = false;
-    return launch_dtype(head, L.grad ? 2 : 0, L, summed, stream);
+    return launch_dtype(head, L.grad ? kStep : kFwd, L, summed, stream);
 }
 
 cudaError_t launch_loss_grad(LossHead head, const LossRows& L, cudaStream_t stream) {
-    return launch_dtype(head, 1, L, nullptr, stream);
+    return launch_dtype(head, kBwd, L, nullptr, stream);
 }
 
 cudaError_t launch_loss_pairs(const LossPairs& P, cudaStream_t stream) {

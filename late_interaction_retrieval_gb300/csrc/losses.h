@@ -9,6 +9,9 @@
 namespace lik {
 
 enum LossHead : int { kHeadDistill = 0, kHeadPolicy = 1, kHeadToken = 2 };
+// What a launch does with a row: statistics and loss; the gradient from saved
+// statistics; both.
+enum LossForm : int { kFwd = 0, kBwd = 1, kStep = 2 };
 
 constexpr int kMaxTeacher = 1024;  // teacher entries per row
 

@@ -396,6 +396,82 @@ def test_no_rows():
         assert all(abs(f[0].item() - np.log(2.0)) < 1e-6 for f in forms)
 
 
+# --------------------------------------------- what only large calls come to --
+
+@pytest.mark.parametrize("rows,cols,dtype", [(3000, 2500, "bf16"), (700, 21000, "f16"), (1300, 5003, "f32")])
+def test_many_masked_rows(rows, cols, dtype):
+    """Every block takes several rows; left-out rows lie in runs and alone."""
+    gen = _gen(rows)
+    off = (torch.arange(rows) // 37 % 3 == 1) | (torch.rand(rows, generator=gen) < 0.3)
+    z, y, old, adv, refp, w = policy_inputs(rows, cols, dtype, 101)
+    w[off] = 0.0
+    check_policy(z, y, old, adv, refp, w, kl=0.1)
+    z, i, t, lse, w = distill_inputs(rows, cols, dtype, 40, 102)
+    w[off] = 0.0
+    t[::29] = NEG
+    check_distill(z, i, t, lse, w)
+    z, y, cuts, refp, w = preference_inputs(rows, cols, dtype, 9, 103)
+    y[off] = -100
+    check_preference(z, y, cuts, refp, w)
+
+
+def test_more_rows_than_are_planned():
+    """Above 16384 rows the blocks take them in turn, whatever the mask."""
+    rows, cols = 16500, 2100
+    z, y, old, adv, refp, w = policy_inputs(rows, cols, "bf16", 111)
+    w[torch.rand(rows, generator=_gen(1)) < 0.5] = 0.0
+    check_policy(z, y, old, adv, refp, w, kl=0.1)
+
+
+@pytest.mark.parametrize("inplace", [False, True])
+def test_rows_longer_than_the_chip_holds(inplace):
+    """800 KB a row, more than eight SMs keep between the two passes of a step."""
+    rows, cols = 9, 200003
+    z, i, t, lse, w = distill_inputs(rows, cols, "f32", 50, 121, full=True)
+    check_distill(z, i, t, lse, w, inplace=inplace)
+    z, y, old, adv, refp, w = policy_inputs(rows, cols, "f32", 122)
+    check_policy(z, y, old, adv, refp, w, kl=0.1, inplace=inplace)
+
+
+@pytest.mark.parametrize("rows,cols,dtype", [(3000, 2501, "bf16"), (900, 20001, "bf16"), (700, 9003, "f32")])
+def test_gradient_rows_at_other_alignments(rows, cols, dtype):
+    """Logits on 16-byte boundaries, gradient rows on any: rows that can be copied out whole and rows that cannot
+    follow each other in one block."""
+    pad = (-cols) % 8
+    z, y, old, adv, refp, w = policy_inputs(rows, cols, dtype, 131)
+    w[torch.rand(rows, generator=_gen(2)) < 0.4] = 0.0
+    want = ref.policy(z, y, old, adv, refp, w, kl=0.1)
+    zv = torch.zeros(rows, cols + pad, dtype=DT[dtype], device="cuda")[:, :cols]
+    zv.copy_(z)
+    y, old, adv, refp, w = _cuda(y, old, adv, refp, w)
+    state = _out(rows, 4)
+    binding.lik_policy_loss_fwd(zv, y, old, adv, _out(1), _out(rows), _out(rows), state, ref_logp=refp, row_weight=w,
+                                kl_coef=0.1)
+    g, g2 = (torch.full((rows, cols), NAN, dtype=DT[dtype], device="cuda") for _ in range(2))
+    binding.lik_policy_loss_bwd(zv, y, state, g, scale=1.0)
+    binding.lik_policy_loss_step(zv, y, old, adv, _out(1), _out(rows), _out(rows), g2, ref_logp=refp, row_weight=w,
+                                 kl_coef=0.1)
+    binding.lik_check_device_error()
+    ref.assert_grad(g, want[3], DT[dtype])
+    ref.assert_grad(g2, want[3], DT[dtype])
+    z, i, t, lse, w = distill_inputs(rows, cols, dtype, 40, 132)
+    want = ref.distill(z, i, t, lse, w)
+    zv.copy_(z)
+    i, t, w = _cuda(i, t, w)
+    binding.lik_distill_topk_fwd(zv, i, t, _out(1), _out(rows), state, row_weight=w)
+    binding.lik_distill_topk_bwd(zv, i, t, state, g)
+    binding.lik_distill_topk_step(zv, i, t, _out(1), _out(rows), g2, row_weight=w)
+    binding.lik_check_device_error()
+    ref.assert_grad(g, want[2], DT[dtype])
+    ref.assert_grad(g2, want[2], DT[dtype])
+
+
+@pytest.mark.parametrize("cols,dtype", [(4500, "f32"), (40000, "bf16"), (131072, "f32")])
+def test_many_teacher_entries_over_long_rows(cols, dtype):
+    z, i, t, lse, w = distill_inputs(170, cols, dtype, 1024, 141, teacher="bf16")
+    check_distill(z, i, t, lse, w)
+
+
 # ---------------------------------------------------------------- gradients --
 
 @pytest.mark.parametrize("op", ["distill", "policy", "preference"])
