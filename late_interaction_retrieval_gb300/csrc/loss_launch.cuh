@@ -1,31 +1,35 @@
 // loss_launch.cuh -- the instances of the row kernel for one type of logits.
 #pragma once
 
+#include "loss_block.cuh"
 #include "loss_rows.cuh"
 #include "loss_short.cuh"
 
 namespace lik {
 namespace loss {
 
-// Two CTAs of 8 consumer warps share an SM, or four of 4.  A CTA takes a row
-// from its loads to its stores in some 3 us, mostly latency, so short rows want
-// more CTAs (8192 rows of bf16, a step: 16 KB rows 73 us with four CTAs, 87 with
-// two; 32 KB 117 and 121).  Two hold up to 64 KB of a row each, four up to 32 KB:
-// longer rows take two (64 KB: 185 us, 274 with four).  The forms with one pass
-// over the logits hold nothing: forward four are as good or better throughout
-// (64 KB rows 91 us and 95), for the gradient two are better where rows are long
-// (bf16 4096 x 32000, forward and gradient: 150 us, 161 with four).  Teachers of
-// many entries leave four too little room.
+// By the length of a row (bf16 unless said, 8192 rows of logits, a step with the
+// sum, inputs beyond L2):
+//   to 1 KB   a warp a row, its granules in registers;
+//   to 40 KB  a block a row, likewise: 4 KB rows 18 us (21 by a warp a row of 8
+//             granules a lane; distillation 24 and 35), 8 KB 28 (53 through the
+//             ring), 16 KB 48 (74), 32 KB 90 (109), 40 KB 117 (149); forward 8 KB
+//             18 (33), 16 KB 28 (41), 32 KB 51 (57), 40 KB 65 (64).  Few blocks of
+//             longer rows fit an SM's registers, and their latencies show: 48 KB
+//             153 (151), 64 KB 234 (181);
+//   longer    through the ring, by CTAs that share an SM: two of 8 consumer warps,
+//             which hold up to 64 KB of a row each between a step's passes.  A
+//             forward holds nothing, and four CTAs of 4 warps are as good or better
+//             throughout (64 KB rows 91 us and 95); teachers of many entries leave
+//             four too little room.
 template <typename T, int kHead, int kForm>
 cudaError_t launch_form(const LossRows& L, bool* summed, unsigned int* err, cudaStream_t stream) {
-    // up to 4 KB (and the loose elements): a warp a row, in registers
-    constexpr int64_t kV = 16 / sizeof(T);
-    if (L.cols <= 64 * kV) return launch_short<T, kHead, kForm, 2>(L, summed, stream);
-    if (L.cols <= 256 * kV) return launch_short<T, kHead, kForm, 8>(L, summed, stream);
-    const RingConfig four = ring_config<kHead, kForm, 4, 4, 4>(L, 1);
     const int64_t row_bytes = L.cols * static_cast<int64_t>(sizeof(T));
-    const int64_t most = kForm == kFwd ? INT64_MAX : kForm == kStep ? four.hold * int64_t(8192) : 32768;
-    if (four.slots >= 4 && row_bytes <= most) return launch_ring<T, kHead, kForm, 4, 4, 4>(L, err, stream);
+    if (row_bytes <= kShortBytes) return launch_short<T, kHead, kForm>(L, summed, stream);
+    if (row_bytes <= kBlockBytes) return launch_block<T, kHead, kForm>(L, stream);
+    if constexpr (kForm == kFwd) {
+        if (ring_config<kHead, kForm, 4, 4, 4>(L, 1).slots >= 4) return launch_ring<T, kHead, kForm, 4, 4, 4>(L, err, stream);
+    }
     return launch_ring<T, kHead, kForm, 8, 4, 2>(L, err, stream);
 }
 

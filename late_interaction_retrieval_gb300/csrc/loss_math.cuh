@@ -346,6 +346,18 @@ struct Teacher {
     float shift;
 };
 
+// Duplicate columns are found by two bit sets over a hash of the column, so that
+// only the few entries that may have a double are compared with others: bits
+// for 16 times the entries at least, one entry in 16 is compared in vain.
+inline int filter_words(int k) {
+    int n = 32;
+    while (n < k / 2) n *= 2;
+    return n;
+}
+__device__ __forceinline__ uint32_t filter_hash(int column, int words) {
+    return (static_cast<uint32_t>(column) * 2654435761u) >> __clz(words * 32 - 1);  // log2(32 words) bits
+}
+
 // Two rows' entries in shared memory (the one at work and the next): column
 // (-1: padding), probability, the student's logit there, and their sums; and
 // the duplicate filter's two bit sets.
@@ -447,15 +459,13 @@ __device__ __forceinline__ float teacher_loss(const LossRows& L, const Entries& 
 
 // Gives the first entry of a column the sum of all entries of that column and
 // turns the others into padding without mass, so that each column is written
-// once (one warp).  Two bit sets over a hash of the column find the few entries that may
-// have a double; only those are compared with the rest.
+// once (one warp).
 static __device__ __noinline__ void merge_duplicates(const Entries& e, int buf, int n, int lane) {
     int* index = e.index + buf * e.pad;
     float* p = e.p + buf * e.pad;
-    const int shift = __clz(e.words * 32 - 1);  // keeps log2(words * 32) bits of the hash
     for (int k = lane; k < n; k += 32) {
         if (index[k] < 0) continue;
-        const uint32_t h = (static_cast<uint32_t>(index[k]) * 2654435761u) >> shift;
+        const uint32_t h = filter_hash(index[k], e.words);
         const uint32_t bit = 1u << (h & 31);
         if (atomicOr(&e.seen[h >> 5], bit) & bit) atomicOr(&e.twice[h >> 5], bit);
     }
@@ -464,7 +474,7 @@ static __device__ __noinline__ void merge_duplicates(const Entries& e, int buf, 
         const int k = k0 + lane;
         bool maybe = false;
         if (k < n && index[k] >= 0) {
-            const uint32_t h = (static_cast<uint32_t>(index[k]) * 2654435761u) >> shift;
+            const uint32_t h = filter_hash(index[k], e.words);
             maybe = (e.twice[h >> 5] >> (h & 31)) & 1;
         }
         uint32_t todo = __ballot_sync(0xffffffffu, maybe);

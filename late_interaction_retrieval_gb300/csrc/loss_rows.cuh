@@ -872,11 +872,7 @@ RingConfig ring_config(const LossRows& L, int sm_count) {
     RingConfig cfg;
     cfg.cluster = 1;
     cfg.k_pad = kHead == kHeadDistill ? (L.k + 31) / 32 * 32 : 0;
-    cfg.filter_words = 0;
-    if (kHead == kHeadDistill) {  // 16 bits an entry at least: one entry in 16 is compared in vain
-        cfg.filter_words = 32;
-        while (cfg.filter_words < L.k / 2) cfg.filter_words *= 2;
-    }
+    cfg.filter_words = kHead == kHeadDistill ? filter_words(L.k) : 0;
     const bool masks = kHead != kHeadDistill || kForm == kBwd || L.weight;
     cfg.planned = masks && L.rows > sm_count && L.rows <= kPlanRows;
     const size_t fixed = sizeof(Control) + (kHead == kHeadDistill ? Entries::bytes(cfg.k_pad, cfg.filter_words) : 0) +
