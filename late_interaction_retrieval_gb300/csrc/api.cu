@@ -73,6 +73,7 @@ const DeviceInfo& device_info(int device) {
         if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d.minor, cudaDevAttrComputeCapabilityMinor, device);
         if (e == cudaSuccess)
             e = cudaDeviceGetAttribute(&d.max_smem_optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, device);
+        if (e == cudaSuccess) e = cudaDeviceGetAttribute(&d.l2_bytes, cudaDevAttrL2CacheSize, device);
         slot.init_error = e;
     });
     return slot.info;

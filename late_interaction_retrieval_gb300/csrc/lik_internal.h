@@ -63,6 +63,7 @@ struct DeviceInfo {
     int sm_count;
     int major, minor;
     int max_smem_optin;
+    int l2_bytes;
 };
 const DeviceInfo& device_info(int device);
 

@@ -317,11 +317,6 @@ __device__ __forceinline__ bool is_read(const LossRows& L, const Peek& p) {
     return p.st.y != 0.0f && (kHead == kHeadDistill ? p.st.z : p.st.w) != 0.0f;
 }
 
-__device__ __forceinline__ void left_out(const LossRows& L, int64_t r) {
-    L.row_loss[r] = 0.0f;
-    if (L.state) L.state[r] = make_float4(0.f, 0.f, 0.f, 0.f);
-}
-
 // The policy loss of a token, and d loss / d log-probability.
 __device__ __forceinline__ float2 policy_head(const LossRows& L, float lp, float old_logp, float adv, float ref) {
     const float ratio = expf(lp - old_logp);
@@ -340,164 +335,10 @@ __device__ __forceinline__ float2 policy_head(const LossRows& L, float lp, float
 
 // --------------------------------------------------- the teacher's entries --
 
-struct Teacher {
-    float mass;   // sum of p
-    float pt;     // sum of p s (t - base), where log p = s (t - base) - shift
-    float shift;
-};
-
-// Duplicate columns are found by two bit sets over a hash of the column, so that
-// only the few entries that may have a double are compared with others: bits
-// for 16 times the entries at least, one entry in 16 is compared in vain.
-inline int filter_words(int k) {
-    int n = 32;
-    while (n < k / 2) n *= 2;
-    return n;
-}
-__device__ __forceinline__ uint32_t filter_hash(int column, int words) {
-    return (static_cast<uint32_t>(column) * 2654435761u) >> __clz(words * 32 - 1);  // log2(32 words) bits
-}
-
-// Two rows' entries in shared memory (the one at work and the next): column
-// (-1: padding), probability, the student's logit there, and their sums; and
-// the duplicate filter's two bit sets.
-struct Entries {
-    int* index;
-    float *p, *z;
-    Teacher* sums;
-    uint32_t *seen, *twice;
-    int pad, words;
-
-    static __host__ __device__ size_t bytes(int k_pad, int words) { return 24u * k_pad + 2 * sizeof(Teacher) + 8u * words; }
-    __device__ Entries(void* base, int k_pad, int filter_words) {
-        pad = k_pad;
-        words = filter_words;
-        index = static_cast<int*>(base);
-        p = reinterpret_cast<float*>(index + 2 * k_pad);
-        z = p + 2 * k_pad;
-        sums = reinterpret_cast<Teacher*>(z + 2 * k_pad);
-        seen = reinterpret_cast<uint32_t*>(sums + 2);
-        twice = seen + words;
-    }
-};
-
 __device__ __forceinline__ float teacher_logit(const LossRows& L, int64_t i) {
     if (L.t_dtype == kF32) return static_cast<const float*>(L.t_logits)[i];
     if (L.t_dtype == kF16) return to_f32(static_cast<const __half*>(L.t_logits)[i]);
     return to_f32(static_cast<const __nv_bfloat16*>(L.t_logits)[i]);
-}
-
-// Loads row r's entries into buffer `buf` and turns them into probabilities
-// (one warp).  The loads go out in batches: a column, then the student's logit
-// there, is two memory latencies.
-template <typename T>
-__device__ __forceinline__ Teacher prepare_teacher(const LossRows& L, int64_t r, const Entries& e, int buf, int lane) {
-    constexpr int kBatch = 4;
-    int* index = e.index + buf * e.pad;
-    float *p = e.p + buf * e.pad, *z = e.z + buf * e.pad;
-    const T* row = static_cast<const T*>(L.logits) + r * L.stride;
-    const int cols = static_cast<int>(L.cols);
-    const float c = L.c;
-    float base = 0.0f, shift = 0.0f;
-    if (L.t_lse) shift = L.t_lse[r];
-    float top = -INFINITY;
-    for (int k0 = lane; k0 < L.k; k0 += 32 * kBatch) {
-        int i[kBatch];
-        float t[kBatch], x[kBatch];
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const bool in = k0 + 32 * b < L.k;
-            i[b] = in ? L.t_index[r * L.k + k0 + 32 * b] : -1;
-            t[b] = in ? teacher_logit(L, r * L.k + k0 + 32 * b) : -INFINITY;
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const bool in = i[b] >= 0 && i[b] < cols;
-            x[b] = in ? load_f32(row + i[b]) : 0.0f;
-            if (!in) i[b] = -1, t[b] = -INFINITY;
-        }
-#pragma unroll
-        for (int b = 0; b < kBatch; ++b) {
-            const int k = k0 + 32 * b;
-            if (k >= L.k) break;
-            index[k] = i[b];
-            p[k] = t[b];
-            z[k] = x[b];
-            top = fmaxf(top, t[b]);
-        }
-    }
-    if (!L.t_lse) {
-        base = offset_of(warp_max(top));
-        float s = 0.0f;
-        for (int k = lane; k < L.k; k += 32) s += ex2((p[k] - base) * c);
-        shift = logf(warp_sum(s));
-    }
-    float mass = 0.0f, pt = 0.0f;
-    for (int k = lane; k < L.k; k += 32) {
-        float prob = 0.0f;
-        if (p[k] != -INFINITY) {
-            const float y = (p[k] - base) * L.scale;
-            prob = ex2((y - shift) * kLog2e);
-            if (prob != 0.0f) pt += prob * y;
-        }
-        p[k] = prob;
-        mass += prob;
-    }
-    return {warp_sum(mass), warp_sum(pt), shift};
-}
-
-// sum of p (log p - log q) over the entries (one warp).  The two normalisers
-// are taken off the sums, not every term: they are the largest parts.
-__device__ __forceinline__ float teacher_loss(const LossRows& L, const Entries& e, int buf, const Teacher& t, float m,
-                                              float log_s, int lane) {
-    const float *p = e.p + buf * e.pad, *z = e.z + buf * e.pad;
-    float cross = 0.0f;
-    for (int k = lane; k < L.k; k += 32)
-        if (p[k] != 0.0f) cross += p[k] * ((z[k] - m) * L.scale);
-    return (t.pt - warp_sum(cross)) - t.mass * (t.shift - log_s);
-}
-
-// Gives the first entry of a column the sum of all entries of that column and
-// turns the others into padding without mass, so that each column is written
-// once (one warp).
-static __device__ __noinline__ void merge_duplicates(const Entries& e, int buf, int n, int lane) {
-    int* index = e.index + buf * e.pad;
-    float* p = e.p + buf * e.pad;
-    for (int k = lane; k < n; k += 32) {
-        if (index[k] < 0) continue;
-        const uint32_t h = filter_hash(index[k], e.words);
-        const uint32_t bit = 1u << (h & 31);
-        if (atomicOr(&e.seen[h >> 5], bit) & bit) atomicOr(&e.twice[h >> 5], bit);
-    }
-    __syncwarp();
-    for (int k0 = 0; k0 < n; k0 += 32) {
-        const int k = k0 + lane;
-        bool maybe = false;
-        if (k < n && index[k] >= 0) {
-            const uint32_t h = filter_hash(index[k], e.words);
-            maybe = (e.twice[h >> 5] >> (h & 31)) & 1;
-        }
-        uint32_t todo = __ballot_sync(0xffffffffu, maybe);
-        while (todo) {
-            const int first = k0 + __ffs(todo) - 1;
-            todo &= todo - 1;
-            const int i = index[first];
-            if (i < 0) continue;  // merged into an earlier entry
-            __syncwarp();
-            float sum = 0.0f;
-            for (int j = lane; j < n; j += 32)
-                if (index[j] == i) {
-                    sum += p[j];
-                    if (j != first) index[j] = -1, p[j] = 0.0f;
-                }
-            sum = warp_sum(sum);
-            if (lane == 0) p[first] = sum;
-            __syncwarp();
-        }
-    }
-    __syncwarp();
-    for (int i = lane; i < e.words; i += 32) e.seen[i] = 0, e.twice[i] = 0;
-    __syncwarp();
 }
 
 }  // namespace loss

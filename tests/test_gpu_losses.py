@@ -400,7 +400,7 @@ def test_no_rows():
 
 @pytest.mark.parametrize("rows,cols,dtype", [(3000, 2500, "bf16"), (700, 21000, "f16"), (1300, 5003, "f32")])
 def test_many_masked_rows(rows, cols, dtype):
-    """Every block takes several rows; left-out rows lie in runs and alone."""
+    """Left-out rows lie in runs and alone."""
     gen = _gen(rows)
     off = (torch.arange(rows) // 37 % 3 == 1) | (torch.rand(rows, generator=gen) < 0.3)
     z, y, old, adv, refp, w = policy_inputs(rows, cols, dtype, 101)
@@ -415,8 +415,8 @@ def test_many_masked_rows(rows, cols, dtype):
     check_preference(z, y, cuts, refp, w)
 
 
-def test_more_rows_than_are_planned():
-    """Above 16384 rows the blocks take them in turn, whatever the mask."""
+def test_thousands_of_left_out_rows():
+    """Many short-lived blocks, half of them over rows that are left out."""
     rows, cols = 16500, 2100
     z, y, old, adv, refp, w = policy_inputs(rows, cols, "bf16", 111)
     w[torch.rand(rows, generator=_gen(1)) < 0.5] = 0.0
@@ -425,7 +425,7 @@ def test_more_rows_than_are_planned():
 
 @pytest.mark.parametrize("inplace", [False, True])
 def test_rows_longer_than_the_chip_holds(inplace):
-    """800 KB a row, more than eight SMs keep between the two passes of a step."""
+    """800 KB a row: many batches a thread, from the largest blocks."""
     rows, cols = 9, 200003
     z, i, t, lse, w = distill_inputs(rows, cols, "f32", 50, 121, full=True)
     check_distill(z, i, t, lse, w, inplace=inplace)
@@ -435,8 +435,7 @@ def test_rows_longer_than_the_chip_holds(inplace):
 
 @pytest.mark.parametrize("rows,cols,dtype", [(3000, 2501, "bf16"), (900, 20001, "bf16"), (700, 9003, "f32")])
 def test_gradient_rows_at_other_alignments(rows, cols, dtype):
-    """Logits on 16-byte boundaries, gradient rows on any: rows that can be copied out whole and rows that cannot
-    follow each other in one block."""
+    """Logits on 16-byte boundaries, gradient rows on any."""
     pad = (-cols) % 8
     z, y, old, adv, refp, w = policy_inputs(rows, cols, dtype, 131)
     w[torch.rand(rows, generator=_gen(2)) < 0.4] = 0.0
