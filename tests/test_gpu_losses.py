@@ -1,5 +1,7 @@
 """Training objectives over logits (GPU) against their fp64 definitions
 (loss_reference.py, which also derives the bars)."""
+import gc
+
 import numpy as np
 import pytest
 import torch
@@ -15,6 +17,13 @@ NEG, NAN, INF = float("-inf"), float("nan"), float("inf")
 # every kernel, an odd vocabulary, a large one
 SIZES = [(1, 1), (3, 2), (5, 17), (9, 128), (4, 1000), (3, 1025), (2, 4096), (7, 8191), (3, 32003), (2, 50001),
          (2, 131072), (300, 33), (1, 70000), (40, 2050)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _leave_no_garbage():
+    """No device memory of these tests is left to be freed inside another."""
+    yield
+    gc.collect()
 
 
 def _gen(seed):
