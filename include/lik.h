@@ -415,7 +415,7 @@ lik_status lik_maxsim_kd_ce_step(const void* Q, const void* D, lik_dtype dtype, 
  *   lik_preference_loss_*  paired log ratios of chosen and rejected sequences
  * in three forms: _fwd (the loss, and the row_state its backward needs),
  * _bwd (the gradient from a row_state), and _step (loss and gradient in one
- * call, each row of logits read from memory once where it fits on chip).
+ * call; the second pass over a row comes from the L2 cache).
  *
  * Shared by all of them, for a row z[0, cols) and a logit scale s (1 /
  * temperature), 1e-30 <= s <= 1e30:
