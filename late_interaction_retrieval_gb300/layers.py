@@ -145,6 +145,17 @@ def _flat(t, dtype):
     return None if t is None else t.detach().reshape(-1).to(dtype).contiguous()
 
 
+def _int32(t):
+    """Columns or offsets as int32.  Values beyond it stay out of range: none wraps into a valid one."""
+    if t.dtype == torch.int64:
+        t = t.clamp(-1, 2 ** 31 - 1)
+    return t.detach().to(torch.int32).contiguous()
+
+
+def _fp32(like, *shape):
+    return torch.empty(shape, dtype=torch.float32, device=like.device)
+
+
 def _grad_buffer(rows):
     """A gradient whose rows lie as the logits' rows do modulo 16 bytes (they
     are then written with 16-byte stores): row strides are kept where they
@@ -164,12 +175,12 @@ class _DistillFn(torch.autograd.Function):
     def forward(ctx, logits, index, teacher, teacher_lse, weight, scale):
         z = _logit_rows(logits)
         n, k = z.shape[0], teacher.shape[-1]
-        index = index.detach().reshape(n, k).to(torch.int32).contiguous()
+        index = _int32(index.reshape(n, k))
         teacher = teacher.detach().reshape(n, k).contiguous()
         teacher_lse, weight = _flat(teacher_lse, torch.float32), _flat(weight, torch.float32)
-        loss = torch.empty(1, device=z.device)
-        row_loss = torch.empty(n, device=z.device)
-        state = torch.empty((n, 4), device=z.device) if ctx.needs_input_grad[0] else None
+        loss = _fp32(z, 1)
+        row_loss = _fp32(z, n)
+        state = _fp32(z, n, 4) if ctx.needs_input_grad[0] else None
         binding.lik_distill_topk_fwd(z, index, teacher, loss, row_loss, state, teacher_lse=teacher_lse,
                                      row_weight=weight, scale=scale)
         ctx.scale, ctx.shape = scale, logits.shape
@@ -192,10 +203,10 @@ class _PolicyFn(torch.autograd.Function):
     def forward(ctx, logits, target, old_logp, advantage, ref_logp, weight, clip_low, clip_high, kl_coef, scale):
         z = _logit_rows(logits)
         n, f32 = z.shape[0], torch.float32
-        target = _flat(target, torch.int32)
-        loss = torch.empty(1, device=z.device)
-        row_loss, row_logp = torch.empty(n, device=z.device), torch.empty(n, device=z.device)
-        state = torch.empty((n, 4), device=z.device) if ctx.needs_input_grad[0] else None
+        target = _int32(target.reshape(-1))
+        loss = _fp32(z, 1)
+        row_loss, row_logp = _fp32(z, n), _fp32(z, n)
+        state = _fp32(z, n, 4) if ctx.needs_input_grad[0] else None
         binding.lik_policy_loss_fwd(z, target, _flat(old_logp, f32), _flat(advantage, f32), loss, row_loss, row_logp,
                                     state, ref_logp=_flat(ref_logp, f32), row_weight=_flat(weight, f32),
                                     clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef, scale=scale)
@@ -218,11 +229,11 @@ class _PreferenceFn(torch.autograd.Function):
     def forward(ctx, logits, target, offsets, ref_logp, weight, beta, margin, smoothing, average, scale):
         z = _logit_rows(logits)
         n, f32 = z.shape[0], torch.float32
-        target, offsets = _flat(target, torch.int32), _flat(offsets, torch.int32)
+        target, offsets = _int32(target.reshape(-1)), _int32(offsets.reshape(-1))
         pairs = offsets.numel() // 2
-        loss = torch.empty(1, device=z.device)
-        pair_loss, seq_logp = torch.empty(pairs, device=z.device), torch.empty(2 * pairs, device=z.device)
-        state = torch.empty((n, 4), device=z.device)
+        loss = _fp32(z, 1)
+        pair_loss, seq_logp = _fp32(z, pairs), _fp32(z, 2 * pairs)
+        state = _fp32(z, n, 4)
         binding.lik_preference_loss_fwd(z, target, offsets, loss, pair_loss, seq_logp, state,
                                         ref_logp=_flat(ref_logp, f32), pair_weight=_flat(weight, f32), beta=beta,
                                         margin=margin, smoothing=smoothing, average=average, scale=scale)

@@ -549,6 +549,43 @@ def test_layers_backward(dtype):
                                         ).requires_grad
 
 
+def test_layers_padding_beyond_int32():
+    """int64 columns and targets that do not fit in 32 bits are padding, whatever their low bits say."""
+    z, i, t, lse, w = distill_inputs(6, 300, "f32", 8, 91, padded=False)
+    wide = i.long()
+    wide[:, 3], wide[:, 5], wide[1, 0] = -2 ** 63, 2 ** 32 + 7, 2 ** 63 - 1
+    i[:, 3], i[:, 5], i[1, 0] = -1, -1, -1
+    loss = layers.distill_topk(z.cuda(), wide.cuda(), t.cuda(), None, w.cuda())
+    ref.assert_loss(loss, ref.distill(z, i, t, None, w)[0])
+    z, y, old, adv, refp, w = policy_inputs(6, 300, "f32", 92)
+    wide = y.long()
+    wide[0], wide[1], wide[4] = -2 ** 63, 2 ** 32, 2 ** 63 - 1
+    y[0], y[1], y[4] = -1, -1, -1
+    loss = layers.policy_loss(z.cuda(), wide.cuda(), old.cuda(), adv.cuda(), None, torch.ones(6).cuda())
+    ref.assert_loss(loss, ref.policy(z, y, old, adv, None, torch.ones(6))[0])
+    z, y, _, _, _ = preference_inputs(12, 64, "f32", 1, 93)
+    far = layers.preference_loss(z.cuda(), y.cuda(), torch.tensor([-2 ** 63, 6, 2 ** 63 - 1]).cuda())
+    near = layers.preference_loss(z.cuda(), y.cuda(), torch.tensor([0, 6, 12]).cuda())
+    assert torch.equal(far, near)
+
+
+@pytest.mark.parametrize("default", [torch.float64, torch.bfloat16])
+def test_layers_under_another_default_dtype(default):
+    z, i, t, lse, w = distill_inputs(6, 300, "bf16", 8, 94)
+    before = torch.get_default_dtype()
+    torch.set_default_dtype(default)
+    try:
+        leaf = z.cuda().requires_grad_()
+        loss = layers.distill_topk(leaf, i.cuda(), t.cuda(), None, w.cuda())
+        loss.backward()
+    finally:
+        torch.set_default_dtype(before)
+    want = ref.distill(z, i, t, None, w)
+    assert loss.dtype == torch.float32
+    ref.assert_loss(loss, want[0])
+    ref.assert_grad(leaf.grad, want[2], torch.bfloat16)
+
+
 # -------------------------------------------------------- streams, repetition --
 
 def test_repeated_calls_are_bit_identical():
