@@ -25,6 +25,8 @@
 // of CTAs, loaded and stored by bulk copies, took 373 and 181.
 #pragma once
 
+#include <algorithm>
+
 #include "dtype_load.cuh"
 #include "lik_internal.h"
 #include "loss_math.cuh"
@@ -319,14 +321,18 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) loss_row_kernel(const LossR
 //   - Two batches a thread at least: a block's second loads cover its first sums
 //     (forward 16 KB 26 us, 29 with one; 32 KB 44 and 51; distillation step 32 KB 93
 //     and 104).  Batches are of equal size.
-inline int row_warps(int64_t rows, int64_t row_bytes, bool step, const DeviceInfo& dev) {
+//   - A warp for 224 of a teacher's entries at least (8192 x 4000 bf16, a step: 256
+//     entries 49 us, 62 by one warp; 1000 entries 123 by five, 360 by one; but
+//     8192 x 1000 fp32 200 entries 35, 42 by two).
+inline int row_warps(int64_t rows, int64_t row_bytes, int entries, bool step, const DeviceInfo& dev) {
     const int64_t at_once = row_bytes * dev.sm_count;  // by blocks of 32
     int most = 8;
     if (rows <= 2 * dev.sm_count || (step && 4 * at_once > dev.l2_bytes / 2)) most = 16;
     if (rows <= dev.sm_count || (step && 2 * at_once > dev.l2_bytes / 4 * 3)) most = kRowWarps;
     const int64_t batch = 32 * kRowN * 16;
     const int64_t batches = row_bytes <= 2 * most * batch ? 2 : (row_bytes + most * batch - 1) / (most * batch);
-    return static_cast<int>((row_bytes + batches * batch - 1) / (batches * batch));
+    const int warps = static_cast<int>((row_bytes + batches * batch - 1) / (batches * batch));
+    return std::max(warps, (entries + 223) / 224);
 }
 
 template <typename T, int kHead, int kForm>
@@ -335,7 +341,8 @@ cudaError_t launch_rows_kernel(const LossRows& L, cudaStream_t stream) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     const int filter = kHead == kHeadDistill ? RowEntries::filter(L.k) : 0;
-    const int warps = row_warps(L.rows, L.cols * static_cast<int64_t>(sizeof(T)), kForm == kStep, device_info(dev));
+    const int warps = row_warps(L.rows, L.cols * static_cast<int64_t>(sizeof(T)), kHead == kHeadDistill ? L.k : 0, kForm == kStep,
+                                device_info(dev));
     auto kernel = loss_row_kernel<T, kHead, kForm>;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
