@@ -88,7 +88,10 @@ __global__ void __launch_bounds__(kPairThreads) loss_pairs_kernel(const LossPair
                                (static_cast<double>(ref_chosen) - ref_rejected);
             const float x = static_cast<float>(P.beta * gap - P.margin);
             const float tail = log1pf(expf(-fabsf(x)));
-            loss = (1.0f - P.smoothing) * (fmaxf(-x, 0.0f) + tail) + P.smoothing * (fmaxf(x, 0.0f) + tail);
+            // a side without a share has no part in it, though its own loss be infinite (x is where a
+            // sequence counts a masked column)
+            if (P.smoothing < 1.0f) loss += (1.0f - P.smoothing) * (fmaxf(-x, 0.0f) + tail);
+            if (P.smoothing > 0.0f) loss += P.smoothing * (fmaxf(x, 0.0f) + tail);
             if (isnan(x)) loss = x;  // fmaxf drops a NaN
             // sigma(x) - (1 - smoothing), each part without cancellation
             const float pos = 1.0f / (1.0f + expf(-x)), neg = 1.0f / (1.0f + expf(x));

@@ -1,0 +1,57 @@
+"""Corners of the training objectives over logits (GPU).  Where a finite row is
+compared, it is with the fp64 definitions and bars of loss_reference.py; what
+is infinite or left out has its value written down here."""
+import gc
+
+import pytest
+import torch
+
+import loss_reference as ref
+from test_gpu_losses import DT, INF, NEG, preference_inputs, run_preference
+
+pytestmark = pytest.mark.gpu
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _leave_no_garbage():
+    """No device memory of these tests is left to be freed inside another."""
+    yield
+    gc.collect()
+
+
+# ------------------------------------------------ terms whose factor is 0 --
+
+@pytest.mark.parametrize("dtype", ["f32", "bf16"])
+@pytest.mark.parametrize("cols", [60, 3001])
+def test_preference_of_a_masked_answer(cols, dtype):
+    """One pair's sequence counts a token on a masked column, so its x is +inf (rejected) or -inf (chosen).  Without
+    smoothing -log sigma(+inf) is 0 and -log sigma(-inf) is inf; all smoothing exchanges the two; with some of both
+    either is inf.  The slopes are finite."""
+    rows = 12
+    z, y, _, _, _ = preference_inputs(rows, cols, dtype, 2, 201)
+    y = y.clamp(min=0)
+    cuts = torch.tensor([0, 3, 6, 9, 12], dtype=torch.int32)  # pair 0 is rows 0..2 and 6..8, pair 1 3..5 and 9..11
+    other = torch.tensor([1.0, 0.0])
+    for row, sign in ((10, 1), (4, -1)):
+        zm = z.clone()
+        zm[row, int(y[row])] = NEG
+        for smoothing in (0.0, 1.0, 0.25):
+            beta, want = 0.1, [0.0, INF] if sign > 0 else [INF, 0.0]
+            want = INF if 0.0 < smoothing < 1.0 else want[int(smoothing)]
+            # the other pair alone, by its weight
+            alone = ref.preference(zm, y, cuts, None, other, beta=beta, smoothing=smoothing)
+            up = torch.tensor([2.0])
+            forms, g, g2 = run_preference(zm, y, cuts, None, torch.ones(2), up=up, smoothing=smoothing, beta=beta)
+            for loss, pair, seq in forms:
+                ref.assert_loss(pair[:1], alone[1][:1])
+                assert float(pair[1]) == want
+                ref.assert_loss(loss, alone[0] + want)
+                assert float(seq[3 if sign > 0 else 1]) == NEG
+            # d loss / d x is -(1 - smoothing) at x = -inf and smoothing at +inf
+            slope = beta * (smoothing if sign > 0 else smoothing - 1.0)
+            log_q, _, on, at = ref._targets(zm, y, 1.0)
+            coef = torch.zeros(rows, dtype=torch.float64)
+            coef[3:6], coef[9:12] = slope, -slope
+            grad = alone[3] + ref._target_grad(log_q, at, coef, on)
+            ref.assert_grad(g, grad, DT[dtype])
+            ref.assert_grad(g2, grad * 2.0, DT[dtype])
