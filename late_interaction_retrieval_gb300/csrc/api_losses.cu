@@ -196,7 +196,7 @@ lik_status policy(const PolicyArgs& a, float* loss, float* row_loss, float* row_
     L.target = a.target;
     L.old_logp = a.old_logp;
     L.advantage = a.advantage;
-    L.ref_logp = a.ref_logp;
+    L.ref_logp = a.kl_coef != 0.0f ? a.ref_logp : nullptr;  // no term, and no 0 * inf of a far reference
     L.clip_low = a.clip_low;
     L.clip_high = a.clip_high;
     L.kl_coef = a.kl_coef;

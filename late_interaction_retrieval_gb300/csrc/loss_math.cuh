@@ -327,7 +327,7 @@ __device__ __forceinline__ float2 policy_head(const LossRows& L, float lp, float
     float d = inner <= outer ? -inner : inner > outer ? 0.0f : NAN;
     if (L.ref_logp) {
         const float x = ref - lp, em1 = expm1f(x);  // exp(x) - 1 without cancellation near x = 0
-        loss += L.kl_coef * (em1 - x);
+        loss += L.kl_coef * (x == INFINITY ? x : em1 - x);  // of a masked target: not inf - inf
         d -= L.kl_coef * em1;
     }
     return make_float2(loss, d);

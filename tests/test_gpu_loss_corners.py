@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import loss_reference as ref
-from test_gpu_losses import DT, INF, NEG, preference_inputs, run_preference
+from test_gpu_losses import DT, INF, NAN, NEG, policy_inputs, preference_inputs, run_policy, run_preference
 
 pytestmark = pytest.mark.gpu
 
@@ -55,3 +55,34 @@ def test_preference_of_a_masked_answer(cols, dtype):
             grad = alone[3] + ref._target_grad(log_q, at, coef, on)
             ref.assert_grad(g, grad, DT[dtype])
             ref.assert_grad(g2, grad * 2.0, DT[dtype])
+
+
+@pytest.mark.parametrize("cols", [60, 3001])
+def test_policy_kl_term_without_a_coefficient(cols):
+    """kl_coef 0 with a reference given: no term, however far (or masked, or not a number) the reference is."""
+    z, y, old, adv, refp, w = policy_inputs(9, cols, "f32", 211)
+    z[5, int(y[5])] = NEG  # its ratio is 0
+    refp = refp + torch.tensor([0.0, 0.0, 0.0, 0.0, 95.0, 0.0, 1e6, INF, NAN])
+    want = ref.policy(z, y, old, adv, None, w)
+    forms, g, g2 = run_policy(z, y, old, adv, refp, w, kl_coef=0.0)
+    for form in forms:
+        for got, x in zip(form, want):
+            ref.assert_loss(got, x)
+    ref.assert_grad(g, want[3], torch.float32)
+    ref.assert_grad(g2, want[3], torch.float32)
+
+
+@pytest.mark.parametrize("cols", [60, 3001])
+def test_policy_kl_term_of_a_masked_target(cols):
+    """lp = -inf with a coefficient: exp(x) - x - 1 at x = +inf is +inf; the other rows are as without it."""
+    z, y, old, adv, refp, w = policy_inputs(9, cols, "f32", 212)
+    zm = z.clone()
+    zm[5, int(y[5])] = NEG
+    want = ref.policy(z, y, old, adv, refp, w, kl=0.1)
+    forms, g, g2 = run_policy(zm, y, old, adv, refp, w, kl_coef=0.1)
+    rest = [0, 1, 2, 3, 4, 6, 7, 8]
+    for loss, row_loss, row_logp in forms:
+        assert float(row_loss[5]) == INF and float(row_logp[5]) == NEG and float(loss) == INF
+        ref.assert_loss(row_loss[rest], want[1][rest])
+    ref.assert_grad(g[rest], want[3][rest], torch.float32)
+    ref.assert_grad(g2[rest], want[3][rest], torch.float32)
