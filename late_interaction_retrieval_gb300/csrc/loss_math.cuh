@@ -320,7 +320,8 @@ __device__ __forceinline__ bool is_read(const LossRows& L, const Peek& p) {
 // The policy loss of a token, and d loss / d log-probability.
 __device__ __forceinline__ float2 policy_head(const LossRows& L, float lp, float old_logp, float adv, float ref) {
     const float ratio = expf(lp - old_logp);
-    const float inner = ratio * adv;
+    // an advantage of 0 gives no term at a ratio past fp32's range either
+    const float inner = adv == 0.0f && ratio == INFINITY ? 0.0f : ratio * adv;
     const float outer = fminf(fmaxf(ratio, 1.0f - L.clip_low), 1.0f + L.clip_high) * adv;
     // the smaller of the two, NaN if either is (fminf would drop it)
     float loss = inner <= outer ? -inner : inner > outer ? -outer : NAN;

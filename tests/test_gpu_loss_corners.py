@@ -86,3 +86,20 @@ def test_policy_kl_term_of_a_masked_target(cols):
         ref.assert_loss(row_loss[rest], want[1][rest])
     ref.assert_grad(g[rest], want[3][rest], torch.float32)
     ref.assert_grad(g2[rest], want[3][rest], torch.float32)
+
+
+@pytest.mark.parametrize("cols", [60, 3001])
+def test_policy_without_advantage_at_any_ratio(cols):
+    """Advantage 0 at a ratio past fp32's range (log ratios of 100 and +inf): no term, no gradient."""
+    z, y, old, adv, refp, w = policy_inputs(9, cols, "f32", 213)
+    far = old.clone()
+    far[4], far[5], far[6] = old[4] - 100.0, NEG, old[6] - 100.0
+    adv[4:7] = torch.tensor([0.0, -0.0, 0.0])
+    near = torch.where(adv == 0, old, far)  # of a row without advantage, the old log-probability is of no account
+    want = ref.policy(z, y, near, adv, refp, w, kl=0.1)
+    forms, g, g2 = run_policy(z, y, far, adv, refp, w, kl_coef=0.1)
+    for form in forms:
+        for got, x in zip(form, want):
+            ref.assert_loss(got, x)
+    ref.assert_grad(g, want[3], torch.float32)
+    ref.assert_grad(g2, want[3], torch.float32)
