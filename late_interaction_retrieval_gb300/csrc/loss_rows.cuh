@@ -187,7 +187,8 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) loss_row_kernel(const LossR
             }
             t.m = L.t_lse ? 0.0f : warp_max(top);
             for (int k = tid; k < L.k; k += nt)
-                t.s += L.t_lse ? ex2((e.p[k] * L.scale - lse) * kLog2e) : ex2((e.p[k] - offset_of(t.m)) * c);
+                if (e.p[k] != -INFINITY)  // whatever the normaliser, padding has no mass
+                    t.s += L.t_lse ? ex2((e.p[k] * L.scale - lse) * kLog2e) : ex2((e.p[k] - offset_of(t.m)) * c);
             t.s = warp_sum(t.s);
         }
         if (lane == 0) teacher_parts[warp] = t;

@@ -7,7 +7,8 @@ import pytest
 import torch
 
 import loss_reference as ref
-from test_gpu_losses import DT, INF, NAN, NEG, policy_inputs, preference_inputs, run_policy, run_preference
+from test_gpu_losses import (DT, INF, NAN, NEG, check_distill, distill_inputs,
+                             policy_inputs, preference_inputs, run_policy, run_preference)
 
 pytestmark = pytest.mark.gpu
 
@@ -103,3 +104,19 @@ def test_policy_without_advantage_at_any_ratio(cols):
             ref.assert_loss(got, x)
     ref.assert_grad(g, want[3], torch.float32)
     ref.assert_grad(g2, want[3], torch.float32)
+
+
+# ---------------------------------------------------------- the teacher's --
+
+@pytest.mark.parametrize("dtype", ["f32", "f16", "bf16"])
+@pytest.mark.parametrize("cols", [50, 9000])
+def test_teacher_without_an_entry_and_any_normaliser(cols, dtype):
+    """Rows of padding alone and of -inf alone are left out whatever their log-sum-exp is (-inf is what a fully
+    masked teacher row gives)."""
+    z, index, t, _, w = distill_inputs(8, cols, dtype, 12, 221, padded=False, weighted=False)
+    index[0], index[3] = -1, cols
+    t[1], t[4], t[6] = NEG, NEG, NEG
+    lse = torch.logsumexp(t.double(), 1).float() + 0.5
+    lse[0], lse[1], lse[3], lse[4], lse[6] = NEG, NEG, NAN, NAN, INF
+    want = check_distill(z, index, t, lse=lse)
+    assert (want[1][[0, 1, 3, 4, 6]] == 0).all() and (want[1][[2, 5, 7]] != 0).all()
