@@ -188,7 +188,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) loss_row_kernel(const LossR
             t.m = L.t_lse ? 0.0f : warp_max(top);
             for (int k = tid; k < L.k; k += nt)
                 if (e.p[k] != -INFINITY)  // whatever the normaliser, padding has no mass
-                    t.s += L.t_lse ? ex2((e.p[k] * L.scale - lse) * kLog2e) : ex2((e.p[k] - offset_of(t.m)) * c);
+                    t.s += L.t_lse ? ex2(fmaf(e.p[k], L.scale, -lse) * kLog2e) : ex2((e.p[k] - offset_of(t.m)) * c);
             t.s = warp_sum(t.s);
         }
         if (lane == 0) teacher_parts[warp] = t;
@@ -219,7 +219,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) loss_row_kernel(const LossR
         m = offset_of(total.m);
         inv = live ? 1.0f / s : 0.0f;
     }
-    float a = 0.0f, coef = 0.0f, at_target = 0.0f, log_ratio = 0.0f;
+    float a = 0.0f, coef = 0.0f, at_target = 0.0f, log_s = 0.0f;
     if (kDistill) {
         Stat t = {-INFINITY, 0.0f};
         if (lane < warps) t = teacher_parts[lane];
@@ -236,9 +236,10 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) loss_row_kernel(const LossR
             for (int k = tid; k < L.k; k += nt) {
                 float p = 0.0f;
                 if (e.p[k] != -INFINITY) {
-                    const float y = (e.p[k] - base) * L.scale;
-                    p = ex2((y - shift) * kLog2e);
-                    if (kStat && p != 0.0f) gap += p * (y - (e.z[k] - m) * L.scale);
+                    // one rounding: a level that the teacher's logits and lse share cancels here
+                    const float log_p = fmaf(e.p[k] - base, L.scale, -shift);
+                    p = ex2(log_p * kLog2e);
+                    if (kStat && p != 0.0f) gap += p * (log_p - (e.z[k] - m) * L.scale);
                     if (kGrad) {
                         const uint32_t h = e.hash(e.index[k]), bit = 1u << (h & 31);
                         if (atomicOr(&e.seen[h >> 5], bit) & bit) atomicOr(&e.twice[h >> 5], bit);
@@ -252,7 +253,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) loss_row_kernel(const LossR
         if (kStat) {
             if (lane == 0) loss_parts[warp] = make_float2(gap, sum);
             if (tid == 0 && L.state) L.state[r] = live ? make_float4(m, inv, now.w, mass) : make_float4(0.f, 0.f, 0.f, 0.f);
-            log_ratio = shift - logf(s);
+            log_s = logf(s);
         }
     } else {
         float hot;
@@ -307,7 +308,7 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) loss_row_kernel(const LossR
         float2 v = make_float2(0.0f, 0.0f);
         if (lane < warps) v = loss_parts[lane];
         const float gap = warp_sum(v.x), sum = warp_sum(v.y);
-        if (lane == 0) L.row_loss[r] = live ? gap - sum * log_ratio : 0.0f;
+        if (lane == 0) L.row_loss[r] = live ? gap + sum * log_s : 0.0f;
     }
 }
 

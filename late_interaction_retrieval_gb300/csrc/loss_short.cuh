@@ -126,9 +126,10 @@ __global__ void __launch_bounds__(1024) loss_short_kernel(const LossRows L) {
                     if (i >= 0) {
                         const float t = teacher_logit(L, r * L.k + k);
                         if (t != -INFINITY) {
-                            const float y = (t - base) * L.scale;
-                            p = ex2((y - shift) * kLog2e);
-                            if (kStat && p != 0.0f) gap += p * (y - (load_f32(z + i) - m) * L.scale);
+                            // one rounding: a level that the teacher's logits and lse share cancels here
+                            const float log_p = fmaf(t - base, L.scale, -shift);
+                            p = ex2(log_p * kLog2e);
+                            if (kStat && p != 0.0f) gap += p * (log_p - (load_f32(z + i) - m) * L.scale);
                         }
                         mass += p;
                     }
@@ -136,7 +137,7 @@ __global__ void __launch_bounds__(1024) loss_short_kernel(const LossRows L) {
                 }
                 mass = warp_sum(mass);
                 if (kStat) {
-                    loss = warp_sum(gap) - mass * (shift - log_s);
+                    loss = warp_sum(gap) + mass * log_s;
                     live = mass != 0.0f;
                 }
             }

@@ -120,3 +120,15 @@ def test_teacher_without_an_entry_and_any_normaliser(cols, dtype):
     lse[0], lse[1], lse[3], lse[4], lse[6] = NEG, NEG, NAN, NAN, INF
     want = check_distill(z, index, t, lse=lse)
     assert (want[1][[0, 1, 3, 4, 6]] == 0).all() and (want[1][[2, 5, 7]] != 0).all()
+
+
+@pytest.mark.parametrize("scale", [1.0, 0.75])
+@pytest.mark.parametrize("level", [1000.0, -4000.0])
+@pytest.mark.parametrize("cols", [200, 3001, 70000])
+def test_teacher_far_from_zero(cols, level, scale):
+    """A level common to the teacher's logits and their log-sum-exp cancels.  An entry's log p is one fused
+    multiply-add, rounded once from the inputs, so the bars are the ordinary ones."""
+    z, index, t, _, w = distill_inputs(5, cols, "f32", 64, 231)
+    t = t + level
+    lse = (torch.logsumexp(t.double() * scale, 1) + 0.25).float()
+    check_distill(z, index, t, lse, w, scale=scale)
