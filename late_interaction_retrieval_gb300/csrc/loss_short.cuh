@@ -239,8 +239,10 @@ cudaError_t launch_short(LossRows L, bool* summed, cudaStream_t stream) {
     const int64_t blocks = (L.rows + warps - 1) / warps;
     const size_t smem = kHead == kHeadDistill && kForm != kFwd ? static_cast<size_t>(warps) * L.cols * 4 : 0;
     auto kernel = loss_short_kernel<T, kHead, kForm>;
+    // The limit belongs to the function, whoever calls it: always the most that any call needs.
+    constexpr size_t most_smem = 32 * (kShortBytes / sizeof(T)) * 4;
     if (smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(smem));
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(most_smem));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchAttribute attr;

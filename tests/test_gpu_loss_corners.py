@@ -2,13 +2,16 @@
 compared, it is with the fp64 definitions and bars of loss_reference.py; what
 is infinite or left out has its value written down here."""
 import gc
+import sys
+import threading
 
 import pytest
 import torch
 
 import loss_reference as ref
-from test_gpu_losses import (DT, INF, NAN, NEG, check_distill, distill_inputs,
-                             policy_inputs, preference_inputs, run_policy, run_preference)
+from late_interaction_retrieval_gb300 import binding
+from test_gpu_losses import (DT, INF, NAN, NEG, _cuda, _out, check_distill,
+                             distill_inputs, policy_inputs, preference_inputs, run_policy, run_preference)
 
 pytestmark = pytest.mark.gpu
 
@@ -132,3 +135,35 @@ def test_teacher_far_from_zero(cols, level, scale):
     t = t + level
     lse = (torch.logsumexp(t.double() * scale, 1) + 0.25).float()
     check_distill(z, index, t, lse, w, scale=scale)
+
+
+# ------------------------------------------------------------------- callers --
+
+def test_calls_from_several_threads():
+    """Steps of two row lengths at once, whose blocks need 50 and 64 KB of shared memory: no call lowers what another's
+    launch may use.  The library's entry is called directly, so that the threads meet inside it."""
+    step = binding.load().lik_distill_topk_step
+    refused = []
+
+    def work(cols):
+        torch.cuda.set_device(0)
+        stream = torch.cuda.Stream()
+        z, i, t, _, _ = _cuda(*distill_inputs(1, cols, "bf16", 4, cols, weighted=False))
+        loss, row_loss, g = _out(1), _out(1), torch.empty_like(z)
+        stream.wait_stream(torch.cuda.current_stream())
+        args = (z.data_ptr(), binding.LIK_BF16, 1, cols, cols, i.data_ptr(), t.data_ptr(), binding.LIK_F32, 4, None,
+                None, 1.0, loss.data_ptr(), row_loss.data_ptr(), g.data_ptr(), cols, stream.cuda_stream)
+        refused.append(sum(step(*args) != 0 for _ in range(20000)))
+        stream.synchronize()
+
+    threads = [threading.Thread(target=work, args=(cols,)) for cols in (512, 385) * 3]
+    interval = sys.getswitchinterval()
+    sys.setswitchinterval(1e-5)
+    try:
+        for t in threads:
+            t.start()
+        for t in threads:
+            t.join()
+    finally:
+        sys.setswitchinterval(interval)
+    assert refused == [0] * 6
