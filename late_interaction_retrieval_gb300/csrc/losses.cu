@@ -24,9 +24,7 @@ cudaError_t launch_dtype(LossHead head, LossForm form, const LossRows& L, bool* 
     return launch_loss_bf16(head, form, L, summed, stream);
 }
 
-__device__ __forceinline__ int clamp_row(int v, int64_t rows) {
-    return v < 0 ? 0 : static_cast<int64_t>(v) > rows ? static_cast<int>(rows) : v;
-}
+__device__ __forceinline__ int64_t clamp_row(int v, int64_t rows) { return v < 0 ? 0 : v > rows ? rows : v; }
 
 constexpr int kPairThreads = 512;
 constexpr int kPairWarps = kPairThreads / 64;  // of one sequence
@@ -46,13 +44,14 @@ __global__ void __launch_bounds__(kPairThreads) loss_pairs_kernel(const LossPair
     const int64_t p = blockIdx.x;
     const int h = threadIdx.x >= kPairThreads / 2, t = threadIdx.x % (kPairThreads / 2);
     const int64_t seq = p + h * P.pairs;
-    const int lo = clamp_row(P.offsets[seq], P.rows), hi = clamp_row(P.offsets[seq + 1], P.rows);
+    // 64 bits: a sequence may end at row 2^31 - 1, and the strides below go past its end
+    const int64_t lo = clamp_row(P.offsets[seq], P.rows), hi = clamp_row(P.offsets[seq + 1], P.rows);
     const float w = P.weight ? P.weight[p] : 1.0f / static_cast<float>(P.pairs);
     float ref_chosen = 0.0f, ref_rejected = 0.0f;
     if (P.ref_logp) ref_chosen = P.ref_logp[p], ref_rejected = P.ref_logp[p + P.pairs];
     loss::Sum2 s;
     int n = 0;
-    for (int r = lo + t; r < hi; r += kPairThreads / 2) {
+    for (int64_t r = lo + t; r < hi; r += kPairThreads / 2) {
         const float4 st = P.state[r];
         if (st.y != 0.0f) {
             s.add(st.z);
@@ -105,7 +104,7 @@ __global__ void __launch_bounds__(kPairThreads) loss_pairs_kernel(const LossPair
     }
     __syncthreads();
     const float v = slope[h];
-    for (int r = lo + t; r < hi; r += kPairThreads / 2)
+    for (int64_t r = lo + t; r < hi; r += kPairThreads / 2)
         if (P.state[r].y != 0.0f) P.state[r].w = v;
 }
 

@@ -10,8 +10,8 @@ import torch
 
 import loss_reference as ref
 from late_interaction_retrieval_gb300 import binding
-from test_gpu_losses import (DT, INF, NAN, NEG, _cuda, _out, check_distill,
-                             distill_inputs, policy_inputs, preference_inputs, run_policy, run_preference)
+from test_gpu_losses import (DT, INF, NAN, NEG, _cuda, _gen, _out,
+                             check_distill, distill_inputs, policy_inputs, preference_inputs, run_policy, run_preference)
 
 pytestmark = pytest.mark.gpu
 
@@ -167,3 +167,28 @@ def test_calls_from_several_threads():
     finally:
         sys.setswitchinterval(interval)
     assert refused == [0] * 6
+
+
+# --------------------------------------------------------- the longest calls --
+
+@pytest.mark.slow
+def test_sequences_that_end_at_the_last_row_there_can_be():
+    """2^31 - 1 rows of two columns; the only pair's sequences are the last 300 rows."""
+    rows = 2 ** 31 - 1
+    z = torch.zeros(rows, 2, dtype=torch.bfloat16, device="cuda")
+    target = torch.full((rows,), -1, dtype=torch.int32, device="cuda")
+    tail_z = torch.randn(300, 2, generator=_gen(271)).bfloat16()
+    tail_y = torch.randint(0, 2, (300,), generator=_gen(272)).to(torch.int32)
+    z[-300:], target[-300:] = tail_z.cuda(), tail_y.cuda()
+    state = torch.zeros(rows, 4, device="cuda")
+    cuts = torch.tensor([rows - 300, rows - 140, rows], dtype=torch.int32)
+    loss, pair, seq = _out(1), _out(1), _out(2)
+    binding.lik_preference_loss_step(z, target, cuts.cuda(), loss, pair, seq, state, z)
+    binding.lik_check_device_error()
+    want = ref.preference(tail_z, tail_y, torch.tensor([0, 160, 300]))
+    ref.assert_loss(loss, want[0])
+    ref.assert_loss(seq, want[2])
+    ref.assert_grad(z[-300:], want[3], torch.bfloat16)
+    assert not z[:-300].any()
+    del z, target, state
+    torch.cuda.empty_cache()
