@@ -516,7 +516,7 @@ lik_status lik_policy_loss_step(const void* logits, lik_dtype dtype, int64_t row
  * pair p sets sequence p (chosen) against sequence pairs + p (rejected).
  * With lp_r = log q[target[r]] over the rows that are not left out,
  *     seq_logp[i]  = sum (average == 0) or mean (else) of lp over sequence i; 0 if it counts no row
- *     (in fp64, rounded to the fp32 that is returned and used from here on)
+ *     (in two fp32 parts; returned rounded to fp32, used from here on without that rounding)
  *     x_p          = beta * ((seq_logp[p] - ref_logp[p]) - (seq_logp[P + p] - ref_logp[P + p])) - margin
  *     pair_loss[p] = (1 - smoothing) * log(1 + exp(-x_p)) + smoothing * log(1 + exp(x_p))
  *     *loss        = sum_p weight[p] * pair_loss[p]     (a pair of weight 0 is left out: pair_loss 0, no gradient)

@@ -79,12 +79,12 @@ __global__ void __launch_bounds__(kPairThreads) loss_pairs_kernel(const LossPair
             value /= rows;
             share = 1.0f / static_cast<float>(rows);
         }
-        const float sum = static_cast<float>(value), other = __shfl_xor_sync(0xffffffffu, sum, 1);
+        const double other = __shfl_xor_sync(0xffffffffu, value, 1);
         float g = 0.0f, loss = 0.0f;
         if (w != 0.0f) {
-            // of the sums as they are returned: the loss follows from the outputs
-            const double gap = (q ? static_cast<double>(other) - sum : static_cast<double>(sum) - other) -
-                               (static_cast<double>(ref_chosen) - ref_rejected);
+            // of the sums before they are rounded to the fp32 that is returned, whose step (2^-8 at 40000) would
+            // show in the loss
+            const double gap = (q ? other - value : value - other) - (static_cast<double>(ref_chosen) - ref_rejected);
             const float x = static_cast<float>(P.beta * gap - P.margin);
             const float tail = log1pf(expf(-fabsf(x)));
             // a side without a share has no part in it, though its own loss be infinite (x is where a
@@ -97,7 +97,7 @@ __global__ void __launch_bounds__(kPairThreads) loss_pairs_kernel(const LossPair
             g = w * P.beta * (P.smoothing * pos - (1.0f - P.smoothing) * neg);
         }
         if (threadIdx.x < 2) {
-            P.seq_logp[p + q * P.pairs] = sum;
+            P.seq_logp[p + q * P.pairs] = static_cast<float>(value);
             if (q == 0) P.pair_loss[p] = loss;
             slope[q] = (q ? -g : g) * share;
         }

@@ -10,8 +10,8 @@ import torch
 
 import loss_reference as ref
 from late_interaction_retrieval_gb300 import binding
-from test_gpu_losses import (DT, INF, NAN, NEG, _cuda, _gen, _out,
-                             check_distill, distill_inputs, policy_inputs, preference_inputs, run_policy, run_preference)
+from test_gpu_losses import (DT, INF, NAN, NEG, _cuda, _gen, _out, check_distill,
+                             check_preference, distill_inputs, policy_inputs, preference_inputs, run_policy, run_preference)
 
 pytestmark = pytest.mark.gpu
 
@@ -135,6 +135,23 @@ def test_teacher_far_from_zero(cols, level, scale):
     t = t + level
     lse = (torch.logsumexp(t.double() * scale, 1) + 0.25).float()
     check_distill(z, index, t, lse, w, scale=scale)
+
+
+# ------------------------------------------------------------ long sequences --
+
+@pytest.mark.parametrize("average", [False, True])
+def test_preference_of_long_sequences(average):
+    """Sums of thousands of log-probabilities, some 30000, in a difference of about 10: the fp32 of a returned sum has
+    steps of 2^-9 there, 2e-4 of beta * gap.  The loss has its ordinary bar: a row's log-probability is rounded at
+    2^-20 or less, and 3000 such roundings add up to some 1e-5 of a sum, 1e-6 of beta times it."""
+    gen = _gen(281)
+    rows, cols, pairs = 24000, 37, 4
+    z = torch.randn(rows, cols, generator=gen) * 4.0
+    y = torch.randint(0, cols, (rows,), generator=gen).to(torch.int32)
+    cuts = torch.arange(0, rows + 1, rows // (2 * pairs)).to(torch.int32)
+    seq = ref.preference(z, y, cuts, average=average)[2]
+    refp = (seq + torch.randn(2 * pairs, generator=gen) * 5.0).float()
+    check_preference(z, y, cuts, refp, torch.ones(pairs), average=average, beta=0.1)
 
 
 # ------------------------------------------------------------------- callers --
