@@ -136,9 +136,12 @@ class MaxSimKD(torch.nn.Module):
 # ------------------------------------ training objectives over logits --
 
 def _logit_rows(logits):
-    """logits [..., cols] as [rows, cols] with contiguous rows (a view where possible)."""
+    """logits [..., cols] as [rows, cols] with contiguous rows that do not overlap (a view where possible)."""
     rows = logits.reshape(-1, logits.shape[-1])
-    return rows if rows.stride(1) == 1 or rows.shape[1] <= 1 else rows.contiguous()
+    n, cols = rows.shape
+    whole = rows.stride(1) == 1 or cols <= 1
+    apart = rows.stride(0) >= cols or n <= 1
+    return rows if whole and apart else rows.contiguous()
 
 
 def _flat(t, dtype):

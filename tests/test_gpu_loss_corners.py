@@ -9,7 +9,7 @@ import pytest
 import torch
 
 import loss_reference as ref
-from late_interaction_retrieval_gb300 import binding
+from late_interaction_retrieval_gb300 import binding, layers
 from test_gpu_losses import (DT, INF, NAN, NEG, _cuda, _gen, _out, check_distill,
                              check_preference, distill_inputs, policy_inputs, preference_inputs, run_policy, run_preference)
 
@@ -152,6 +152,33 @@ def test_preference_of_long_sequences(average):
     seq = ref.preference(z, y, cuts, average=average)[2]
     refp = (seq + torch.randn(2 * pairs, generator=gen) * 5.0).float()
     check_preference(z, y, cuts, refp, torch.ones(pairs), average=average, beta=0.1)
+
+
+# -------------------------------------------------------------------- layers --
+
+@pytest.mark.parametrize("cols", [40, 3001])
+def test_layers_over_rows_that_overlap(cols):
+    """An expanded row of logits, and windows over a line of scores: gradients add up where rows share elements."""
+    z, i, t, _, w = distill_inputs(4, cols, "f32", 10, 251)
+    leaf = z[:1].cuda().requires_grad_()
+    loss = layers.distill_topk(leaf.expand(4, cols), i.cuda(), t.cuda(), None, w.cuda())
+    loss.backward()
+    want = ref.distill(z[:1].repeat(4, 1), i, t, None, w)
+    ref.assert_loss(loss, want[0])
+    ref.assert_grad(leaf.grad, want[2].sum(0, keepdim=True), torch.float32)
+    z, y, old, adv, refp, w = policy_inputs(4, cols, "f32", 252)
+    line = torch.randn(cols + 3, generator=_gen(3)) * 2.5
+    leaf = line.cuda().requires_grad_()
+    windows = leaf.unfold(0, cols, 1)
+    assert windows.shape == (4, cols) and windows.stride() == (1, 1)
+    loss = layers.policy_loss(windows, y.cuda(), old.cuda(), adv.cuda(), refp.cuda(), w.cuda(), kl_coef=0.1)
+    loss.backward()
+    want = ref.policy(line.unfold(0, cols, 1), y, old, adv, refp, w, kl=0.1)
+    total = torch.zeros(cols + 3, dtype=torch.float64)
+    for r in range(4):
+        total[r:r + cols] += want[3][r]
+    ref.assert_loss(loss, want[0])
+    ref.assert_grad(leaf.grad, total, torch.float32)
 
 
 # ------------------------------------------------------------------- callers --
