@@ -137,7 +137,7 @@ class MaxSimKD(torch.nn.Module):
 
 def _logit_rows(logits):
     """logits [..., cols] as [rows, cols] with contiguous rows that do not overlap (a view where possible)."""
-    rows = logits.reshape(-1, logits.shape[-1])
+    rows = logits if logits.dim() == 2 else logits.reshape(-1, logits.shape[-1])
     n, cols = rows.shape
     whole = rows.stride(1) == 1 or cols <= 1
     apart = rows.stride(0) >= cols or n <= 1
@@ -173,10 +173,25 @@ def _upstream(g):
     return g.detach().reshape(1).to(torch.float32).contiguous()
 
 
+class _OnceFn(torch.autograd.Function):
+    """A gradient as it is, which depends on its logits and on what is upstream but cannot be differentiated."""
+
+    @staticmethod
+    def forward(ctx, grad, z, g):
+        return grad.view_as(grad)
+
+    @staticmethod
+    def backward(ctx, _):
+        raise RuntimeError("the losses over logits have no second derivative")
+
+
+def _once(grad, z, g):
+    return _OnceFn.apply(grad, z, g) if torch.is_grad_enabled() else grad  # enabled: create_graph
+
+
 class _DistillFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, index, teacher, teacher_lse, weight, scale):
-        z = _logit_rows(logits)
+    def forward(ctx, z, index, teacher, teacher_lse, weight, scale):
         n, k = z.shape[0], teacher.shape[-1]
         index = _int32(index.reshape(n, k))
         teacher = teacher.detach().reshape(n, k).contiguous()
@@ -186,9 +201,8 @@ class _DistillFn(torch.autograd.Function):
         state = _fp32(z, n, 4) if ctx.needs_input_grad[0] else None
         binding.lik_distill_topk_fwd(z, index, teacher, loss, row_loss, state, teacher_lse=teacher_lse,
                                      row_weight=weight, scale=scale)
-        ctx.scale, ctx.shape = scale, logits.shape
+        ctx.scale = scale
         ctx.save_for_backward(z, index, teacher, teacher_lse, state)
-        row_loss = row_loss.view(logits.shape[:-1])
         ctx.mark_non_differentiable(row_loss)
         return loss.view(()), row_loss
 
@@ -198,13 +212,12 @@ class _DistillFn(torch.autograd.Function):
         grad = _grad_buffer(z)
         binding.lik_distill_topk_bwd(z, index, teacher, state, grad, grad_loss=_upstream(g), teacher_lse=teacher_lse,
                                      scale=ctx.scale)
-        return grad.reshape(ctx.shape), None, None, None, None, None
+        return (_once(grad, z, g),) + (None,) * 5
 
 
 class _PolicyFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, target, old_logp, advantage, ref_logp, weight, clip_low, clip_high, kl_coef, scale):
-        z = _logit_rows(logits)
+    def forward(ctx, z, target, old_logp, advantage, ref_logp, weight, clip_low, clip_high, kl_coef, scale):
         n, f32 = z.shape[0], torch.float32
         target = _int32(target.reshape(-1))
         loss = _fp32(z, 1)
@@ -213,9 +226,8 @@ class _PolicyFn(torch.autograd.Function):
         binding.lik_policy_loss_fwd(z, target, _flat(old_logp, f32), _flat(advantage, f32), loss, row_loss, row_logp,
                                     state, ref_logp=_flat(ref_logp, f32), row_weight=_flat(weight, f32),
                                     clip_low=clip_low, clip_high=clip_high, kl_coef=kl_coef, scale=scale)
-        ctx.scale, ctx.shape = scale, logits.shape
+        ctx.scale = scale
         ctx.save_for_backward(z, target, state)
-        row_loss, row_logp = row_loss.view(logits.shape[:-1]), row_logp.view(logits.shape[:-1])
         ctx.mark_non_differentiable(row_loss, row_logp)
         return loss.view(()), row_loss, row_logp
 
@@ -224,13 +236,12 @@ class _PolicyFn(torch.autograd.Function):
         z, target, state = ctx.saved_tensors
         grad = _grad_buffer(z)
         binding.lik_policy_loss_bwd(z, target, state, grad, grad_loss=_upstream(g), scale=ctx.scale)
-        return (grad.reshape(ctx.shape),) + (None,) * 9
+        return (_once(grad, z, g),) + (None,) * 9
 
 
 class _PreferenceFn(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, logits, target, offsets, ref_logp, weight, beta, margin, smoothing, average, scale):
-        z = _logit_rows(logits)
+    def forward(ctx, z, target, offsets, ref_logp, weight, beta, margin, smoothing, average, scale):
         n, f32 = z.shape[0], torch.float32
         target, offsets = _int32(target.reshape(-1)), _int32(offsets.reshape(-1))
         pairs = offsets.numel() // 2
@@ -240,7 +251,7 @@ class _PreferenceFn(torch.autograd.Function):
         binding.lik_preference_loss_fwd(z, target, offsets, loss, pair_loss, seq_logp, state,
                                         ref_logp=_flat(ref_logp, f32), pair_weight=_flat(weight, f32), beta=beta,
                                         margin=margin, smoothing=smoothing, average=average, scale=scale)
-        ctx.scale, ctx.shape = scale, logits.shape
+        ctx.scale = scale
         ctx.save_for_backward(z, target, state)
         ctx.mark_non_differentiable(pair_loss, seq_logp)
         return loss.view(()), pair_loss, seq_logp
@@ -250,7 +261,7 @@ class _PreferenceFn(torch.autograd.Function):
         z, target, state = ctx.saved_tensors
         grad = _grad_buffer(z)
         binding.lik_preference_loss_bwd(z, target, state, grad, grad_loss=_upstream(g), scale=ctx.scale)
-        return (grad.reshape(ctx.shape),) + (None,) * 9
+        return (_once(grad, z, g),) + (None,) * 9
 
 
 def distill_topk(logits, teacher_index, teacher_logits, teacher_lse=None, row_weight=None, scale=1.0,
@@ -262,8 +273,9 @@ def distill_topk(logits, teacher_index, teacher_logits, teacher_lse=None, row_we
     exp(scale * teacher_logits - teacher_lse) instead of normalising them over
     the k entries.  Differentiable in the logits only.  With return_rows also
     the row losses (no gradient)."""
-    loss, row_loss = _DistillFn.apply(logits, teacher_index, teacher_logits, teacher_lse, row_weight, scale)
-    return (loss, row_loss) if return_rows else loss
+    loss, row_loss = _DistillFn.apply(_logit_rows(logits), teacher_index, teacher_logits, teacher_lse, row_weight,
+                                      scale)
+    return (loss, row_loss.view(logits.shape[:-1])) if return_rows else loss
 
 
 def policy_loss(logits, target, old_logp, advantage, ref_logp=None, row_weight=None, clip_low=0.2, clip_high=0.2,
@@ -273,9 +285,10 @@ def policy_loss(logits, target, old_logp, advantage, ref_logp=None, row_weight=N
     row_weight (None: the mean over rows).  A target outside [0, cols) leaves
     its token out.  With return_rows also the token losses and the tokens'
     log-probabilities (no gradient)."""
-    out = _PolicyFn.apply(logits, target, old_logp, advantage, ref_logp, row_weight, clip_low, clip_high, kl_coef,
-                          scale)
-    return out if return_rows else out[0]
+    loss, row_loss, row_logp = _PolicyFn.apply(_logit_rows(logits), target, old_logp, advantage, ref_logp, row_weight,
+                                               clip_low, clip_high, kl_coef, scale)
+    shape = logits.shape[:-1]
+    return (loss, row_loss.view(shape), row_logp.view(shape)) if return_rows else loss
 
 
 def preference_loss(logits, target, offsets, ref_logp=None, pair_weight=None, beta=0.1, margin=0.0, smoothing=0.0,
@@ -285,7 +298,8 @@ def preference_loss(logits, target, offsets, ref_logp=None, pair_weight=None, be
     sets sequence p (chosen) against sequence pairs + p (rejected).  With
     return_rows also the pair losses and the sequences' log-probabilities (no
     gradient)."""
-    out = _PreferenceFn.apply(logits, target, offsets, ref_logp, pair_weight, beta, margin, smoothing, average, scale)
+    out = _PreferenceFn.apply(_logit_rows(logits), target, offsets, ref_logp, pair_weight, beta, margin, smoothing,
+                              average, scale)
     return out if return_rows else out[0]
 
 

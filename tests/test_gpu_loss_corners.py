@@ -181,6 +181,29 @@ def test_layers_over_rows_that_overlap(cols):
     ref.assert_grad(leaf.grad, total, torch.float32)
 
 
+def test_layers_refuse_a_second_derivative():
+    """create_graph keeps the first gradient as it is; differentiating that one is an error, not a constant."""
+    z, i, t, _, w = distill_inputs(4, 300, "f32", 10, 261)
+    _, y, old, adv, _, _ = policy_inputs(4, 300, "f32", 262)
+    i, t, w, y, old, adv = _cuda(i, t, w, y, old, adv)
+    cuts = torch.tensor([0, 2, 4], dtype=torch.int32).cuda()
+    calls = [lambda x: layers.distill_topk(x, i, t, None, w), lambda x: layers.policy_loss(x, y, old, adv, None, w),
+             lambda x: layers.preference_loss(x, y, cuts)]
+    for call in calls:
+        a = z.cuda().requires_grad_()
+        (first,) = torch.autograd.grad(call(a), a)
+        loss = call(a)
+        (g,) = torch.autograd.grad(loss, a, create_graph=True)
+        assert torch.equal(g, first)
+        with pytest.raises(RuntimeError, match="second derivative"):
+            (loss + g.square().sum()).backward()
+        inner = z.cuda().view(2, 2, 300).requires_grad_()  # through what comes before the layer
+        loss = call(torch.tanh(inner.reshape(4, 300)))
+        (g,) = torch.autograd.grad(loss, inner, create_graph=True)
+        with pytest.raises(RuntimeError, match="second derivative"):
+            torch.autograd.grad(g.square().sum(), inner)
+
+
 # ------------------------------------------------------------------- callers --
 
 def test_calls_from_several_threads():
