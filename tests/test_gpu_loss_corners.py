@@ -11,7 +11,7 @@ import torch
 import loss_reference as ref
 from late_interaction_retrieval_gb300 import binding, layers
 from test_gpu_losses import (DT, INF, NAN, NEG, _cuda, _gen, _out, check_distill,
-                             check_preference, distill_inputs, policy_inputs, preference_inputs, run_policy, run_preference)
+                             check_preference, distill_inputs, policy_inputs, preference_inputs, run_distill, run_policy, run_preference)
 
 pytestmark = pytest.mark.gpu
 
@@ -137,6 +137,24 @@ def test_teacher_far_from_zero(cols, level, scale):
     check_distill(z, index, t, lse, w, scale=scale)
 
 
+@pytest.mark.parametrize("cols", [300, 5000])
+def test_duplicate_columns_across_warps(cols):
+    """Hundreds of entries over a few columns, padding and -inf among them."""
+    gen = _gen(cols)
+    for k, of in ((40, 5), (300, 20), (1000, 50), (1024, 1), (700, 290)):
+        z = (torch.randn(5, cols, generator=gen) * 2.5)
+        pool = torch.randperm(cols, generator=gen)[:of]
+        index = pool[torch.randint(0, of, (5, k), generator=gen)].to(torch.int32)
+        t = torch.randn(5, k, generator=gen) * 2.0
+        index[torch.rand(5, k, generator=gen) < 0.1] = -1
+        t[torch.rand(5, k, generator=gen) < 0.1] = NEG
+        check_distill(z, index, t)
+        check_distill(z, index, t, lse=torch.logsumexp(t, 1) + 0.5)
+        first = run_distill(z, index, t)
+        again = run_distill(z, index, t)
+        assert torch.equal(first[1], again[1]) and torch.equal(first[2], again[2])
+
+
 # ------------------------------------------------------------ long sequences --
 
 @pytest.mark.parametrize("average", [False, True])
@@ -202,6 +220,32 @@ def test_layers_refuse_a_second_derivative():
         (g,) = torch.autograd.grad(loss, inner, create_graph=True)
         with pytest.raises(RuntimeError, match="second derivative"):
             torch.autograd.grad(g.square().sum(), inner)
+
+
+# ------------------------------------------------------------------ in place --
+
+@pytest.mark.parametrize("rows,cols,dtype", [(70, 17, "f32"), (5, 77, "bf16"), (6, 3001, "f32"), (4, 40001, "f16"),
+                                             (3, 131072, "bf16")])
+def test_backward_in_place_of_the_logits(rows, cols, dtype):
+    """The gradient from a saved state, written over the logits it is taken from, is the one written elsewhere."""
+    z, i, t, lse, w = _cuda(*distill_inputs(rows, cols, dtype, 20, 241, full=True))
+    state, apart = _out(rows, 4), torch.empty_like(z)
+    binding.lik_distill_topk_fwd(z, i, t, _out(1), _out(rows), state, teacher_lse=lse, row_weight=w)
+    binding.lik_distill_topk_bwd(z, i, t, state, apart, teacher_lse=lse)
+    binding.lik_distill_topk_bwd(z, i, t, state, z, teacher_lse=lse)
+    assert torch.equal(z, apart)
+    z, y, old, adv, refp, w = _cuda(*policy_inputs(rows, cols, dtype, 242))
+    binding.lik_policy_loss_fwd(z, y, old, adv, _out(1), _out(rows), _out(rows), state, ref_logp=refp, row_weight=w,
+                                kl_coef=0.1)
+    binding.lik_policy_loss_bwd(z, y, state, apart)
+    binding.lik_policy_loss_bwd(z, y, state, z)
+    assert torch.equal(z, apart)
+    z, y, cuts, refp, w = _cuda(*preference_inputs(rows, cols, dtype, 1, 243))
+    binding.lik_preference_loss_fwd(z, y, cuts, _out(1), _out(1), _out(2), state, ref_logp=refp, pair_weight=w)
+    binding.lik_preference_loss_bwd(z, y, state, apart)
+    binding.lik_preference_loss_bwd(z, y, state, z)
+    assert torch.equal(z, apart)
+    binding.lik_check_device_error()
 
 
 # ------------------------------------------------------------------- callers --
