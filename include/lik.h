@@ -431,13 +431,16 @@ lik_status lik_maxsim_kd_ce_step(const void* Q, const void* D, lik_dtype dtype, 
  *     are written with 16-byte stores.
  *   - Sums, softmax statistics and losses are fp32 or wider; a gradient is
  *     rounded to its dtype once.  Results do not depend on the run: sums are
- *     taken in a fixed order (no atomics).
+ *     taken in a fixed order.
  *   - Rows that are left out: a weight of 0, a target outside [0, cols), no
  *     teacher entry with any mass, every logit -inf.  They have loss 0 and a
  *     zero gradient whatever else they hold (their logits may be NaN, except
  *     for the last two kinds).  A logit of -inf in any other row is a masked
  *     column: probability 0, gradient 0.  A row with a NaN or +inf logit that
- *     is not left out gives NaN.
+ *     is not left out gives NaN.  Rows that are left out by weight or target
+ *     are not read; their zero gradient is still written.
+ *   - A term whose factor (kl_coef, the advantage, smoothing or 1 - smoothing)
+ *     is 0 adds nothing, though the term itself be infinite.
  *   - weights are fp32 and carry mask, normalisation and any loss scale
  *     (fp16 gradients usually need one) together; NULL weighs every row (or
  *     pair) 1 / rows (1 / pairs).
@@ -464,6 +467,7 @@ lik_status lik_maxsim_kd_ce_step(const void* Q, const void* D, lik_dtype dtype, 
  *   teacher_index [rows, k] int32, teacher_logits [rows, k] of teacher_dtype
  *   (fp32, fp16, bf16), 0 <= k <= 1024, contiguous; teacher_lse [rows] fp32
  *   or NULL; row_weight [rows] fp32 or NULL; loss [1], row_loss [rows] fp32.
+ *   teacher_lse does not matter in a row whose entries are all padding or -inf.
  */
 lik_status lik_distill_topk_fwd(const void* logits, lik_dtype dtype, int64_t rows, int64_t cols, int64_t row_stride,
                                 const int32_t* teacher_index, const void* teacher_logits, lik_dtype teacher_dtype,
@@ -492,7 +496,9 @@ lik_status lik_distill_topk_step(const void* logits, lik_dtype dtype, int64_t ro
  *     grad[r, c]  = weight[r] * s * d * ([c == y] - q_c)
  *   target [rows] int32; old_logp, advantage, row_loss, row_logp (lp, 0 for a
  *   row left out) [rows] fp32; ref_logp, row_weight [rows] fp32 or NULL;
- *   clip_low in [0, 1], clip_high >= 0, kl_coef finite.
+ *   clip_low in [0, 1], clip_high >= 0, kl_coef finite.  A target on a masked
+ *   column has lp = -inf: its ratio is 0, its KL term (with kl_coef not 0)
+ *   infinite, and the row's gradient then not finite.
  */
 lik_status lik_policy_loss_fwd(const void* logits, lik_dtype dtype, int64_t rows, int64_t cols, int64_t row_stride,
                                const int32_t* target, const float* old_logp, const float* advantage,

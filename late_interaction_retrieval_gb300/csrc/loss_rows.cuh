@@ -12,8 +12,9 @@
 //
 // A teacher's entries are dealt out over the threads too: their softmax runs
 // beside the row's, and after a second barrier the entries' columns are written
-// over the stored row.  A row that is left out costs its block one load, and the
-// next block takes its place, so that masks need no plan.
+// over the stored row.  A row that is left out costs its block a load or two and, with
+// a gradient, the row of zeros; the next block takes its place, so that masks need
+// no plan.
 //
 // Memory bounds it; the other rows of an SM cover a row's latencies, which is why
 // blocks are as small as the rules at the launch allow.  Measured (bf16, inputs
@@ -325,7 +326,9 @@ __global__ void __launch_bounds__(kRowWarps * 32, 1) loss_row_kernel(const LossR
 //     and 104).  Batches are of equal size.
 //   - A warp for 224 of a teacher's entries at least (8192 x 4000 bf16, a step: 256
 //     entries 49 us, 62 by one warp; 1000 entries 123 by five, 360 by one; but
-//     8192 x 1000 fp32 200 entries 35, 42 by two).
+//     8192 x 1000 fp32 200 entries 35, 42 by two).  Those are 2.3, 4.2 and 3.1 times
+//     what their bytes take: an entry's loads depend on one another, and it ends as
+//     a store of its own.
 inline int row_warps(int64_t rows, int64_t row_bytes, int entries, bool step, const DeviceInfo& dev) {
     const int64_t at_once = row_bytes * dev.sm_count;  // by blocks of 32
     int most = 8;

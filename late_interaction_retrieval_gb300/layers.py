@@ -18,7 +18,7 @@ the binding.  With recompute=True the forward saves no argmax: the
 backward re-runs the forward into a transient workspace.
 
 Training objectives over logits [..., cols] (a query's candidate scores, a
-token's vocabulary), each a scalar fp32 loss differentiable in the logits:
+token's vocabulary), each a scalar fp32 loss differentiable once, in the logits:
 
   distill_topk     divergence from a teacher's top logits
   policy_loss      clipped policy loss with a KL term to a reference
@@ -160,9 +160,10 @@ def _fp32(like, *shape):
 
 
 def _grad_buffer(rows):
-    """A gradient whose rows lie as the logits' rows do modulo 16 bytes (they
-    are then written with 16-byte stores): row strides are kept where they
-    carry no more than padding."""
+    """A gradient with the logits' row stride where that carries no more than
+    padding.  Rows of logits that start on a 16-byte boundary are then written
+    with 16-byte stores; of logits at another address, or with wider gaps, the
+    gradient's rows may lie otherwise and are written by elements."""
     n, cols = rows.shape
     if n > 1 and cols < rows.stride(0) <= cols + cols // 8:
         return torch.empty((n, rows.stride(0)), dtype=rows.dtype, device=rows.device)[:, :cols]
@@ -283,8 +284,9 @@ def policy_loss(logits, target, old_logp, advantage, ref_logp=None, row_weight=N
     """Clipped policy loss of the sampled tokens target [...] under logits
     [..., cols], with kl_coef times the KL term to ref_logp; summed with
     row_weight (None: the mean over rows).  A target outside [0, cols) leaves
-    its token out.  With return_rows also the token losses and the tokens'
-    log-probabilities (no gradient)."""
+    its token out.  Differentiable in the logits only: advantage, ref_logp and
+    row_weight get no gradient.  With return_rows also the token losses and the
+    tokens' log-probabilities (no gradient)."""
     loss, row_loss, row_logp = _PolicyFn.apply(_logit_rows(logits), target, old_logp, advantage, ref_logp, row_weight,
                                                clip_low, clip_high, kl_coef, scale)
     shape = logits.shape[:-1]
@@ -295,9 +297,9 @@ def preference_loss(logits, target, offsets, ref_logp=None, pair_weight=None, be
                     average=False, scale=1.0, return_rows=False):
     """Preference loss over pairs of sequences packed along the rows of logits
     [rows, cols]: sequence i holds the rows offsets[i]..offsets[i + 1], pair p
-    sets sequence p (chosen) against sequence pairs + p (rejected).  With
-    return_rows also the pair losses and the sequences' log-probabilities (no
-    gradient)."""
+    sets sequence p (chosen) against sequence pairs + p (rejected).
+    Differentiable in the logits only.  With return_rows also the pair losses and
+    the sequences' log-probabilities (no gradient)."""
     out = _PreferenceFn.apply(_logit_rows(logits), target, offsets, ref_logp, pair_weight, beta, margin, smoothing,
                               average, scale)
     return out if return_rows else out[0]

@@ -10,8 +10,9 @@ import torch
 
 import loss_reference as ref
 from late_interaction_retrieval_gb300 import binding, layers
-from test_gpu_losses import (DT, INF, NAN, NEG, _cuda, _gen, _out, check_distill,
-                             check_preference, distill_inputs, policy_inputs, preference_inputs, run_distill, run_policy, run_preference)
+from test_gpu_losses import (DT, INF, NAN, NEG, _cuda, _gen, _out, check_distill, check_preference, distill_inputs,
+                             policy_inputs, preference_inputs, run_distill, run_policy, run_preference)
+
 
 pytestmark = pytest.mark.gpu
 
