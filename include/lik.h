@@ -553,6 +553,167 @@ lik_status lik_preference_loss_step(const void* logits, lik_dtype dtype, int64_t
                                     float* seq_logp, float* row_state, void* grad_logits, int64_t grad_stride,
                                     cudaStream_t stream);
 
+/* ------------------------------ a serving step over a cache in 8 bits --
+ * What an answer model runs for each step of its decoding, over keys and
+ * values held in 8 bits: the tokens that lik_policy_loss_* trains on are
+ * sampled here (lik_verify_drafts returns their log-probabilities), with a
+ * draft model that lik_distill_topk_* trains.  The pages have no counterpart.
+ *   lik_cache_slots      block tables and slot maps from request lengths
+ *   lik_cache_write      new keys and values into the cache
+ *   lik_cache_attention  of new tokens over the cache
+ *   lik_verify_drafts    drafted tokens against the target's probabilities
+ *
+ * The cache is a pool of `pages` pages of `page_size` tokens (16, 32, 64, 128
+ * or 256).  For one layer of a model with `heads` key/value heads of size
+ * `dim` (a multiple of 16, at most 128):
+ *     k_cache, v_cache  [pages, heads, page_size, dim], codes of 8 bits (e4m3:
+ *                       1 sign, 4 exponent, 3 fraction bits, largest 448),
+ *                       contiguous, 16-byte aligned
+ *     k_scale, v_scale  [pages, heads] fp32: a code c stands for c * scale
+ * A token's slot is page * page_size + its offset in the page (int64).  A
+ * request's tokens 0, 1, ... lie in the pages block_table[b][0], [1], ...;
+ * several layers share one table.  A batch has `requests` requests of which
+ * request b adds the rows offsets[b] .. offsets[b + 1] - 1 of a packed batch
+ * (offsets [requests + 1] int32, device, not falling); they are its last
+ * tokens.  Rows behind offsets[requests] are padding: a batch that a graph
+ * was captured with stays as large as it was.  Sizes that only the device
+ * knows are never read back; values outside their range are clamped, so that
+ * nothing outside a buffer is read or written.
+ * Outputs must not overlap inputs, but for what is updated in place (said
+ * so).  requests <= 8192.
+ */
+
+/*
+ * Block tables and slot maps.  Request b holds `held[b]` pages with cached[b]
+ * tokens in them and gets added[b] tokens:
+ *     total[b] = cached[b] + added[b]                         -> lengths[b]
+ *     need[b]  = max(0, min(ceil(total[b] / page_size), table_cols) - held[b])
+ *     first[b] = need[0] + ... + need[b - 1]
+ *     block_table[b][held[b] + j] = free_pages[free_count - 1 - first[b] - j],  0 <= j < need[b];
+ *                                   -1 where the list has run out
+ *     held_out[b] = held[b] + the pages it got
+ *     free_left   = free_count - (need[0] + ...)    (negative: so many pages are missing)
+ *     offsets[b]  = added[0] + ... + added[b - 1]
+ *     slots[t]    = the slot of the token of row t; -1 for a token without a
+ *                   page and for the rows behind the last token
+ * Pages are taken from the end of the list, whose first free_left entries
+ * stay free.  A request may hold more pages than its tokens fill (drafts that
+ * were turned down): they are used before new ones are taken.  Other entries
+ * of the table are left as they are.
+ *   cached, added, held, held_out, lengths [requests]; offsets [requests + 1];
+ *   free_pages [free_capacity]; free_count, free_left [1]; block_table
+ *   [requests, table_cols], row b at element b * table_stride, updated in
+ *   place; all int32, device.  slots [slot_capacity] int64; tokens behind
+ *   slot_capacity are left out (offsets end there).
+ *   Negative lengths count as 0; held is clamped to [0, table_cols],
+ *   free_count to [0, free_capacity].
+ */
+lik_status lik_cache_slots(const int32_t* cached, const int32_t* added, const int32_t* held, int64_t requests,
+                           int64_t page_size, const int32_t* free_pages, int64_t free_capacity,
+                           const int32_t* free_count, int32_t* block_table, int64_t table_cols, int64_t table_stride,
+                           int32_t* held_out, int32_t* lengths, int32_t* offsets, int64_t* slots,
+                           int64_t slot_capacity, int32_t* free_left, cudaStream_t stream);
+
+/*
+ * New keys and values into the cache.  Rows t, t + 1, ... whose slots follow
+ * one another within a page are one run, written together.  For a run that
+ * starts at offset o of its page, for each head, keys and values apart:
+ *     s     = max(largest finite |x| of the run / 448, 2^-126)
+ *     scale = s if o == 0 (the page is new), else max(the page's scale, s)
+ *     codes of the offsets below o are requantised where the scale grew:
+ *             e4m3(code * (old scale * (1 / scale)))
+ *     new codes: e4m3(x * (1 / scale)), to nearest even; NaN for a value that
+ *             is not finite
+ * in fp32.  Codes behind the run are left as they are.  A slot outside
+ * [0, pages * page_size) writes nothing.  One call writes one run into a page:
+ * pages that two requests share hold full pages of a common prefix, which
+ * nobody writes; of two runs into one page the codes of both are not defined.
+ *   k, v [rows, heads, dim], fp32, fp16 or bf16; element (t, h, d) at t *
+ *   token_stride + h * head_stride + d (each its own strides); slots [rows].
+ */
+lik_status lik_cache_write(const void* k, const void* v, lik_dtype dtype, int64_t rows, int64_t heads, int64_t dim,
+                           int64_t k_token_stride, int64_t k_head_stride, int64_t v_token_stride,
+                           int64_t v_head_stride, const int64_t* slots, void* k_cache, void* v_cache, float* k_scale,
+                           float* v_scale, int64_t pages, int64_t page_size, cudaStream_t stream);
+
+/*
+ * Attention of a batch's new tokens over the cache.  Query head h reads
+ * key/value head h / (q_heads / heads).  Row t = offsets[b] + i of request b,
+ * which adds n = offsets[b + 1] - offsets[b] tokens and has lengths[b] of them
+ * in the cache, the new ones included, sees the positions j with
+ *     j < lengths[b] - n + i + 1     (its own and all before it)
+ * whose page is in the table (an entry outside [0, pages) hides its tokens):
+ *     z_j    = scale * (q . k_j)
+ *     out    = sum_j exp(z_j) v_j / sum_j exp(z_j)
+ *     lse[t, h] = log sum_j exp(z_j)
+ * A row that sees nothing has out 0 and lse -inf.  What a row does not see
+ * does not matter to it, whatever it holds (NaN codes, scales of pages that
+ * are not its own).  Rows that belong to no request are left as they are.
+ * Sums and softmax statistics are fp32; the products' operands are fp16 (q
+ * brought into its range by a power of two, the softmax weights rounded to 11
+ * bits, codes exact).  Results do not depend on the run.
+ *   q, out [rows, q_heads, dim], fp16 or bf16, element (t, h, d) at t *
+ *   token_stride + h * head_stride + d; lse [rows, q_heads] fp32 or NULL;
+ *   block_table [requests, table_cols] int32, row b at b * table_stride;
+ *   1e-30 <= scale <= 1e30.
+ *   max_added: the most tokens that a request adds, as the host knows it: it
+ *   chooses the kernel.  A wrong value costs time, not results.
+ *   workspace: 16-byte aligned, of lik_cache_attention_workspace_bytes bytes
+ *   for the same sizes; its contents do not matter before and after.  Calls
+ *   that may overlap need one each.
+ */
+lik_status lik_cache_attention_workspace_bytes(int64_t rows, int64_t q_heads, int64_t heads, int64_t dim,
+                                               int64_t requests, int64_t page_size, int64_t table_cols,
+                                               int64_t max_added, size_t* bytes);
+
+lik_status lik_cache_attention(const void* q, lik_dtype dtype, int64_t rows, int64_t q_heads, int64_t dim,
+                               int64_t q_token_stride, int64_t q_head_stride, const void* k_cache,
+                               const void* v_cache, const float* k_scale, const float* v_scale, int64_t pages,
+                               int64_t heads, int64_t page_size, const int32_t* block_table, int64_t table_cols,
+                               int64_t table_stride, const int32_t* offsets, const int32_t* lengths,
+                               int64_t requests, int64_t max_added, float scale, void* out, int64_t out_token_stride,
+                               int64_t out_head_stride, float* lse, void* workspace, size_t workspace_bytes,
+                               cudaStream_t stream);
+
+/*
+ * Drafted tokens against the target's probabilities, from given random
+ * numbers: speculative sampling, which leaves tokens distributed as the
+ * target's own.  Request b drafted the tokens x_0 .. x_{n-1} (rows offsets[b]
+ * .. of draft_logits, drafted and uniform; n may be 0: plain sampling) and
+ * the target model scored n + 1 positions (rows offsets[b] + b .. of
+ * target_logits, tokens and logp).  With p = softmax(scale * target row), q =
+ * softmax(scale * draft row), or q = 1 at the drafted token where draft_logits
+ * is NULL (drafts looked up in a text):
+ *     x_i passes            if uniform_i * q_i(x_i) < p_i(x_i)
+ *     accepted[b] = a       the drafts before the first that does not pass
+ *     r_c = max(p_a(c) - q_a(c), 0)   for a < n;   p_n(c) for a = n
+ *     y   = the column c of the largest r_c / noise[b][c] among those above 0, the lowest of equals;
+ *           where none is, of the largest p_c / noise[b][c];  -1 where none is again
+ *     tokens = x_0 .. x_{a-1}, y, then -1;   logp = log p of each token, 0 where there is none
+ * With uniform in [0, 1) and noise from the exponential distribution, y is
+ * drawn from r's distribution.  A column of -inf has probability 0.  A target
+ * row with a NaN or +inf logit, or of -inf alone, passes nothing and draws -1;
+ * a drafted token outside [0, cols) does not pass.  Probabilities are fp32,
+ * sums fp32 or wider.
+ *   target_logits [drafts + requests, cols], draft_logits [drafts, cols] of
+ *   one dtype (fp32, fp16, bf16), row r at element r * stride; drafted
+ *   [drafts] int32; offsets [requests + 1]; uniform [drafts], noise
+ *   [requests, cols] fp32; tokens [drafts + requests] int32, accepted
+ *   [requests] int32, logp [drafts + requests] fp32.  Rows behind the last
+ *   request's (offsets[requests] < drafts) are not read, and written as -1, 0.
+ *   1 <= cols <= 2^30; 1e-30 <= scale <= 1e30.
+ *   workspace: 16-byte aligned, of lik_verify_drafts_workspace_bytes bytes;
+ *   its contents do not matter before and after.  Calls that may overlap need
+ *   one each.
+ */
+lik_status lik_verify_drafts_workspace_bytes(int64_t drafts, int64_t requests, int64_t cols, size_t* bytes);
+
+lik_status lik_verify_drafts(const void* target_logits, const void* draft_logits, lik_dtype dtype, int64_t drafts,
+                             int64_t requests, int64_t cols, int64_t target_stride, int64_t draft_stride,
+                             const int32_t* drafted, const int32_t* offsets, const float* uniform, const float* noise,
+                             float scale, int32_t* tokens, int32_t* accepted, float* logp, void* workspace,
+                             size_t workspace_bytes, cudaStream_t stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -62,6 +62,13 @@ SIGNATURES = {
     "lik_preference_loss_bwd": (_I32, _LOGITS + [_P, _F] + [_P] * 3 + [_I64, _P]),
     "lik_preference_loss_step": (_I32, _LOGITS + [_P, _P, _I64, _P, _P] + [_F] * 3 + [_I32, _F] + [_P] * 5
                                  + [_I64, _P]),
+    "lik_cache_slots": (_I32, [_P] * 3 + [_I64] * 2 + [_P, _I64, _P, _P] + [_I64] * 2 + [_P] * 4 + [_I64, _P, _P]),
+    "lik_cache_write": (_I32, [_P, _P, _I32] + [_I64] * 7 + [_P] * 5 + [_I64] * 2 + [_P]),
+    "lik_cache_attention_workspace_bytes": (_I32, [_I64] * 8 + [_P]),
+    "lik_cache_attention": (_I32, [_P, _I32] + [_I64] * 5 + [_P] * 4 + [_I64] * 3 + [_P] + [_I64] * 2 + [_P] * 2
+                            + [_I64] * 2 + [_F, _P] + [_I64] * 2 + [_P] * 2 + [ctypes.c_size_t, _P]),
+    "lik_verify_drafts_workspace_bytes": (_I32, [_I64] * 3 + [_P]),
+    "lik_verify_drafts": (_I32, [_P, _P, _I32] + [_I64] * 5 + [_P] * 4 + [_F] + [_P] * 4 + [ctypes.c_size_t, _P]),
 }
 
 _DTYPES = {torch.float32: LIK_F32, torch.float16: LIK_F16, torch.bfloat16: LIK_BF16}
@@ -652,6 +659,156 @@ def lik_preference_loss_step(logits, target, offsets, loss, pair_loss, seq_logp,
 def lik_preference_loss_bwd(logits, target, row_state, grad_logits, grad_loss=None, scale=1.0, stream=None):
     """Gradient of lik_preference_loss_fwd's loss, times grad_loss [1] (None: 1)."""
     _target_bwd("lik_preference_loss_bwd", logits, target, row_state, grad_logits, grad_loss, scale, stream)
+
+
+# ------------------------------ a serving step over a cache in 8 bits --
+
+_CODES = (torch.float8_e4m3fn, torch.uint8)
+
+
+def _table(block_table, dev, requests=None):
+    """Address, requests, columns and row stride of a block table."""
+    if block_table.dim() != 2 or block_table.dtype is not torch.int32 or block_table.device != dev:
+        raise ValueError(f"block_table must be int32 [requests, columns] on {dev}")
+    rows, cols = block_table.shape
+    if requests is not None and rows != requests:
+        raise ValueError(f"block_table has {rows} rows, expected {requests}")
+    stride, inner = block_table.stride()
+    if inner != 1 and cols > 1:
+        raise ValueError("block_table must have contiguous rows")
+    return block_table.data_ptr(), rows, cols, stride if rows > 1 else max(cols, 1)
+
+
+def _heads(t, name, shape=None, dtype=None, device=None):
+    """Address, shape and strides of a [rows, heads, dim] CUDA tensor whose heads are contiguous."""
+    if t.dim() != 3:
+        raise ValueError(f"{name} must be [rows, heads, dim]")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor")
+    if t.dtype not in _DTYPES:
+        raise ValueError(f"{name} must be float32/float16/bfloat16 (got {t.dtype})")
+    if shape is not None and (t.shape != shape or t.dtype is not dtype or t.device != device):
+        raise ValueError(f"{name} must be {tuple(shape)}, {dtype} on {device} (got {tuple(t.shape)}, {t.dtype} on "
+                         f"{t.device})")
+    token, head, inner = t.stride()
+    if inner != 1 and t.shape[2] > 1:
+        raise ValueError(f"{name} must have contiguous heads (last dimension)")
+    return t.data_ptr(), t.shape, token, head
+
+
+def _pool(k_cache, v_cache, k_scale, v_scale, heads, dim, dev):
+    """Addresses of a layer's cache, its pages and page size."""
+    if k_cache.dim() != 4 or k_cache.dtype not in _CODES:
+        raise ValueError("k_cache must be [pages, heads, page_size, dim], float8_e4m3fn or uint8")
+    pages, h, page, d = k_cache.shape
+    if heads is not None and h != heads or d != dim:
+        raise ValueError(f"k_cache has {h} heads of {d}, expected {heads} of {dim}")
+    shape, f32 = k_cache.shape, torch.float32
+    return (_vector(k_cache, "k_cache", shape, k_cache.dtype, dev),
+            _vector(v_cache, "v_cache", shape, k_cache.dtype, dev),
+            _vector(k_scale, "k_scale", (pages, h), f32, dev),
+            _vector(v_scale, "v_scale", (pages, h), f32, dev)), pages, h, page
+
+
+def lik_cache_slots(cached, added, held, free_pages, free_count, block_table, held_out, lengths, offsets, slots,
+                    free_left, page_size, stream=None):
+    """Block tables (new entries, in place) and slot maps of a batch from its
+    requests' lengths: request b holds held[b] pages with cached[b] tokens and
+    gets added[b] more.  Pages come from the end of free_pages[:free_count]."""
+    if cached.dim() != 1 or free_pages.dim() != 1 or slots.dim() != 1:
+        raise ValueError("cached, free_pages and slots must have one dimension")
+    if not cached.is_cuda:
+        raise ValueError("cached must be a CUDA tensor")
+    dev, i32, n = cached.device, torch.int32, cached.shape[0]
+    table, _, cols, stride = _table(block_table, dev, n)
+    _call("lik_cache_slots", _vector(cached, "cached", (n,), i32, dev), _vector(added, "added", (n,), i32, dev),
+          _vector(held, "held", (n,), i32, dev), n, page_size,
+          _vector(free_pages, "free_pages", free_pages.shape, i32, dev), free_pages.shape[0],
+          _vector(free_count, "free_count", (1,), i32, dev), table, cols, stride,
+          _vector(held_out, "held_out", (n,), i32, dev), _vector(lengths, "lengths", (n,), i32, dev),
+          _vector(offsets, "offsets", (n + 1,), i32, dev), _vector(slots, "slots", slots.shape, torch.int64, dev),
+          slots.shape[0], _vector(free_left, "free_left", (1,), i32, dev), _stream(dev, stream))
+
+
+def lik_cache_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):
+    """New keys and values [rows, heads, dim] into the cache's slots (int64, -1: none)."""
+    kp, shape, kt, kh = _heads(k, "k")
+    dev = k.device
+    vp, _, vt, vh = _heads(v, "v", shape, k.dtype, dev)
+    rows, heads, dim = shape
+    pool, pages, _, page = _pool(k_cache, v_cache, k_scale, v_scale, heads, dim, dev)
+    _call("lik_cache_write", kp, vp, _DTYPES[k.dtype], rows, heads, dim, kt, kh, vt, vh,
+          _vector(slots, "slots", (rows,), torch.int64, dev), *pool, pages, page, _stream(dev, stream))
+
+
+def lik_cache_attention_workspace_bytes(q, k_cache, block_table, max_added) -> int:
+    """Bytes of device workspace lik_cache_attention needs for these sizes."""
+    rows, q_heads, dim = q.shape
+    out = ctypes.c_size_t(0)
+    with torch.cuda.device(q.device):
+        _call("lik_cache_attention_workspace_bytes", rows, q_heads, k_cache.shape[1], dim, block_table.shape[0],
+              k_cache.shape[2], block_table.shape[1], max_added, ctypes.byref(out))
+    return int(out.value)
+
+
+def lik_cache_attention(q, k_cache, v_cache, k_scale, v_scale, block_table, offsets, lengths, out, lse=None,
+                        workspace=None, max_added=1, scale=1.0, stream=None):
+    """Attention of the rows q [rows, q_heads, dim] (request b's are offsets[b]
+    .. offsets[b + 1], its last tokens) over lengths[b] tokens of the cache.
+    workspace: any contiguous tensor of lik_cache_attention_workspace_bytes."""
+    qp, shape, qt, qh = _heads(q, "q")
+    rows, q_heads, dim = shape
+    dev, i32 = q.device, torch.int32
+    op, _, ot, oh = _heads(out, "out", shape, q.dtype, dev)
+    pool, pages, heads, page = _pool(k_cache, v_cache, k_scale, v_scale, None, dim, dev)
+    table, requests, cols, stride = _table(block_table, dev)
+    ws, ws_bytes = _workspace(workspace, dev)
+    _call("lik_cache_attention", qp, _DTYPES[q.dtype], rows, q_heads, dim, qt, qh, *pool, pages, heads, page, table,
+          cols, stride, _vector(offsets, "offsets", (requests + 1,), i32, dev),
+          _vector(lengths, "lengths", (requests,), i32, dev), requests, max_added, scale, op, ot, oh,
+          _vector(lse, "lse", (rows, q_heads), torch.float32, dev, optional=True), ws, ws_bytes, _stream(dev, stream))
+
+
+def _workspace(workspace, dev):
+    if workspace is None:
+        return None, 0
+    if workspace.device != dev or not workspace.is_contiguous():
+        raise ValueError("workspace must be a contiguous tensor on the inputs' device")
+    return workspace.data_ptr(), workspace.numel() * workspace.element_size()
+
+
+def lik_verify_drafts_workspace_bytes(target_logits, requests) -> int:
+    """Bytes of device workspace lik_verify_drafts needs for these sizes."""
+    out = ctypes.c_size_t(0)
+    rows, cols = target_logits.shape
+    _call("lik_verify_drafts_workspace_bytes", rows - requests, requests, cols, ctypes.byref(out))
+    return int(out.value)
+
+
+def lik_verify_drafts(target_logits, draft_logits, drafted, offsets, uniform, noise, tokens, accepted, logp,
+                      workspace=None, scale=1.0, stream=None):
+    """Drafted tokens against the target's probabilities: tokens that pass, one
+    drawn token behind them, -1 then; accepted [requests]; log-probabilities.
+    draft_logits None: drafts without probabilities of their own."""
+    z, rows, cols, stride = _rows(target_logits, "target_logits")
+    dev, dt, i32, f32 = target_logits.device, target_logits.dtype, torch.int32, torch.float32
+    if accepted.dim() != 1 or drafted.dim() != 1:
+        raise ValueError("accepted must be [requests], drafted [drafts]")
+    n, requests = drafted.shape[0], accepted.shape[0]
+    if rows != n + requests:
+        raise ValueError(f"target_logits has {rows} rows, expected drafts + requests = {n + requests}")
+    y, d_stride = None, 0
+    if draft_logits is not None:
+        if draft_logits.shape != (n, cols) or draft_logits.dtype is not dt or draft_logits.device != dev:
+            raise ValueError(f"draft_logits must be {(n, cols)}, {dt} on {dev} (got {tuple(draft_logits.shape)}, "
+                             f"{draft_logits.dtype} on {draft_logits.device})")
+        y, _, _, d_stride = _rows(draft_logits, "draft_logits")
+    ws, ws_bytes = _workspace(workspace, dev)
+    _call("lik_verify_drafts", z, y, _DTYPES[dt], n, requests, cols, stride, d_stride,
+          _vector(drafted, "drafted", (n,), i32, dev), _vector(offsets, "offsets", (requests + 1,), i32, dev),
+          _vector(uniform, "uniform", (n,), f32, dev), _vector(noise, "noise", (requests, cols), f32, dev), scale,
+          _vector(tokens, "tokens", (rows,), i32, dev), _vector(accepted, "accepted", (requests,), i32, dev),
+          _vector(logp, "logp", (rows,), f32, dev), ws, ws_bytes, _stream(dev, stream))
 
 
 def lik_check_device_error(stream=None, device=None):

@@ -1,0 +1,265 @@
+// verify.cu -- drafted tokens against the target's probabilities.
+//
+// First launch: every row's largest logit and sum of exponentials, a row cut
+// into parts over blocks (a handful of rows has to fill the chip).  Second
+// launch: each block of a request joins its rows' parts, finds the first
+// draft that does not pass, and races its share of that row's columns against
+// the noise; the last block of a request to finish writes its tokens.
+#include <cuda_runtime.h>
+
+#include "dtype_load.cuh"
+#include "lik_internal.h"
+#include "serve.h"
+
+namespace lik {
+namespace {
+
+constexpr int kThreads = 256;
+constexpr int kWarps = kThreads / 32;
+constexpr int kMaxParts = 64;
+constexpr float kLn2 = 0.693147180559945309f;
+
+struct Plan {
+    int parts;        // of a row in the first launch
+    int64_t part;     // columns of a part
+    int races;        // blocks of a request in the second
+    int64_t share;    // columns of one
+    float2* stats;    // [rows, parts]: largest logit, sum of exponentials
+    unsigned long long* best;  // [requests]: the race's key, ~column
+    unsigned int* done;        // [requests]: blocks that have finished
+};
+
+// exp(scale * d), d <= 0, to about 2^-22: the product's rounding is put right.
+struct Scale {
+    float hi, lo;  // scale * log2(e) in two parts
+};
+__device__ __forceinline__ float exp_scaled(float d, Scale c) {
+    const float t = d * c.hi;
+    if (t < -200.0f) return 0.0f;  // below every fp32 value; the product may have overflowed
+    const float rest = fmaf(d, c.lo, fmaf(d, c.hi, -t));
+    const float e = exp2f(t);
+    return fmaf(e, rest * kLn2, e);
+}
+
+__device__ __forceinline__ float2 join(float2 x, float2 y, Scale c) {
+    // a NaN stays: comparisons that it fails keep the side that has it
+    const float m = x.x >= y.x ? x.x : (y.x >= x.x ? y.x : x.x + y.x);
+    if (m == -INFINITY) return make_float2(m, 0.0f);
+    return make_float2(m, x.y * exp_scaled(x.x - m, c) + y.y * exp_scaled(y.x - m, c));
+}
+
+__device__ __forceinline__ float2 warp_join(float2 v, Scale c) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const float2 o = make_float2(__shfl_xor_sync(0xffffffffu, v.x, d), __shfl_xor_sync(0xffffffffu, v.y, d));
+        v = join(v, o, c);
+    }
+    return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) verify_stats(const VerifyArgs a, const Plan w, Scale c) {
+    __shared__ float2 of_warp[kWarps];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int64_t row = blockIdx.x;
+    const int64_t targets = a.drafts + a.requests;
+    const T* const z = row < targets ? static_cast<const T*>(a.target) + row * a.target_stride
+                                     : static_cast<const T*>(a.draft) + (row - targets) * a.draft_stride;
+    if (blockIdx.y == 0 && row < a.requests && tid == 0) {
+        w.best[row] = 0;
+        w.done[row] = 0;
+    }
+    const int64_t c0 = blockIdx.y * w.part, c1 = c0 + w.part < a.cols ? c0 + w.part : a.cols;
+    float2 v = make_float2(-INFINITY, 0.0f);
+    for (int64_t k = c0 + tid; k < c1; k += kThreads) v = join(v, make_float2(load_f32(z + k), 1.0f), c);
+    v = warp_join(v, c);
+    if (lane == 0) of_warp[warp] = v;
+    __syncthreads();
+    if (tid == 0) {
+        for (int i = 1; i < kWarps; ++i) v = join(v, of_warp[i], c);
+        w.stats[row * w.parts + blockIdx.y] = v;
+    }
+}
+
+// A row's statistics from its parts, by a whole warp.
+__device__ __forceinline__ float2 row_stats(const Plan& w, int64_t row, Scale c) {
+    const int lane = threadIdx.x & 31;
+    float2 v = make_float2(-INFINITY, 0.0f);
+    for (int i = lane; i < w.parts; i += 32) v = join(v, w.stats[row * w.parts + i], c);
+    return warp_join(v, c);
+}
+
+// The sum is 0 only for a row without any mass; a NaN or +inf logit leaves a
+// NaN, which fails every comparison below.
+__device__ __forceinline__ float prob(float z, float2 s, Scale c) {
+    return s.y == 0.0f ? 0.0f : exp_scaled(z - s.x, c) / s.y;
+}
+
+__device__ __forceinline__ unsigned long long key_of(float r, float noise, int64_t col) {
+    const float k = r / noise;
+    if (!(k > 0.0f)) return 0;
+    return (static_cast<unsigned long long>(__float_as_uint(k)) << 32) | (0xffffffffu - static_cast<unsigned>(col));
+}
+
+__device__ __forceinline__ unsigned long long block_max(unsigned long long v, unsigned long long* of_warp) {
+#pragma unroll
+    for (int d = 16; d > 0; d >>= 1) {
+        const unsigned long long o = __shfl_xor_sync(0xffffffffu, v, d);
+        v = o > v ? o : v;
+    }
+    if ((threadIdx.x & 31) == 0) of_warp[threadIdx.x >> 5] = v;
+    __syncthreads();
+    for (int i = 0; i < kWarps; ++i) v = of_warp[i] > v ? of_warp[i] : v;
+    __syncthreads();
+    return v;
+}
+
+template <typename T>
+__global__ void __launch_bounds__(kThreads) verify_draw(const VerifyArgs a, const Plan w, Scale c) {
+    __shared__ unsigned long long of_warp[kWarps];
+    __shared__ int first_fail, is_last;
+    __shared__ float2 stat_p, stat_q;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
+    const int64_t targets = a.drafts + a.requests;
+    int64_t lo = a.offsets[b], hi = a.offsets[b + 1];
+    lo = lo < 0 ? 0 : (lo < a.drafts ? lo : a.drafts);
+    hi = hi < lo ? lo : (hi < a.drafts ? hi : a.drafts);
+    const int n = static_cast<int>(hi - lo);
+    const T* const target = static_cast<const T*>(a.target);
+    const T* const draft = static_cast<const T*>(a.draft);
+    if (tid == 0) first_fail = n;
+    __syncthreads();
+    for (int i = warp; i < n; i += kWarps) {
+        // one lane's view of what other warps write, so that the warp stays whole
+        if (__shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&first_fail), 0) < i) break;
+        const int64_t row = lo + i, tr = row + b;
+        const int x = a.drafted[row];
+        bool pass = x >= 0 && x < a.cols;
+        if (pass) {
+            const float p = prob(load_f32(target + tr * a.target_stride + x), row_stats(w, tr, c), c);
+            const float q = draft ? prob(load_f32(draft + row * a.draft_stride + x), row_stats(w, targets + row, c), c)
+                                  : 1.0f;
+            pass = static_cast<double>(a.uniform[row]) * q < static_cast<double>(p);
+        }
+        if (!pass && lane == 0) atomicMin(&first_fail, i);
+    }
+    __syncthreads();
+    const int kept = first_fail;
+    const int64_t tr = lo + b + kept, dr = lo + kept;
+    const bool residual = kept < n;
+    if (warp == 0) {
+        const float2 s = row_stats(w, tr, c);
+        if (lane == 0) stat_p = s;
+    } else if (warp == 1) {
+        const float2 s = residual && draft ? row_stats(w, targets + dr, c) : make_float2(0.0f, 0.0f);
+        if (lane == 0) stat_q = s;
+    }
+    __syncthreads();
+    const float2 sp = stat_p, sq = stat_q;
+    const T* const z = target + tr * a.target_stride;
+    const T* const y = residual && draft ? draft + dr * a.draft_stride : nullptr;
+    const int64_t struck = residual && !draft ? a.drafted[dr] : -1;
+    const float* const noise = a.noise + b * a.cols;
+    const int64_t c0 = blockIdx.x * w.share, c1 = c0 + w.share < a.cols ? c0 + w.share : a.cols;
+    unsigned long long best = 0;
+    for (int64_t k = c0 + tid; k < c1; k += kThreads) {
+        float r = prob(load_f32(z + k), sp, c);
+        if (y) r = fmaxf(r - prob(load_f32(y + k), sq, c), 0.0f);
+        if (k == struck) r = 0.0f;
+        const unsigned long long key = key_of(r, noise[k], k);
+        best = key > best ? key : best;
+    }
+    best = block_max(best, of_warp);
+    if (tid == 0) {
+        if (best) atomicMax(w.best + b, best);
+        __threadfence();
+        is_last = atomicAdd(w.done + b, 1u) + 1 == gridDim.x;
+        __threadfence();
+    }
+    __syncthreads();
+    if (!is_last) return;
+    best = *reinterpret_cast<volatile unsigned long long*>(w.best + b);
+    if (best == 0 && residual) {  // nothing is left of the target over the draft: the target itself
+        for (int64_t k = tid; k < a.cols; k += kThreads) {
+            const unsigned long long key = key_of(prob(load_f32(z + k), sp, c), noise[k], k);
+            best = key > best ? key : best;
+        }
+        best = block_max(best, of_warp);
+    }
+    const int token = best ? static_cast<int>(0xffffffffu - static_cast<unsigned>(best)) : -1;
+    for (int i = warp; i <= n; i += kWarps) {
+        const int64_t r = lo + b + i;
+        const int t = i < kept ? a.drafted[lo + i] : (i == kept ? token : -1);
+        float lp = 0.0f;
+        if (t >= 0) {
+            const float2 s = row_stats(w, r, c);
+            // in natural logarithms: scale * (z - max) - log(sum)
+            lp = a.scale * (load_f32(target + r * a.target_stride + t) - s.x) - logf(s.y);
+        }
+        if (lane == 0) {
+            a.tokens[r] = t;
+            a.logp[r] = lp;
+        }
+    }
+    if (tid == 0) a.accepted[b] = kept;
+    if (b == a.requests - 1) {  // rows behind the last request's
+        for (int64_t r = hi + b + 1 + tid; r < targets; r += kThreads) {
+            a.tokens[r] = -1;
+            a.logp[r] = 0.0f;
+        }
+    }
+}
+
+int parts_of(int64_t rows, int64_t cols, int sms) {
+    // 4 blocks for each SM, of 4096 columns at least
+    int64_t p = (4 * static_cast<int64_t>(sms) + rows - 1) / (rows > 0 ? rows : 1);
+    const int64_t most = (cols + 4095) / 4096;
+    p = p < most ? p : most;
+    return static_cast<int>(p < 1 ? 1 : (p < kMaxParts ? p : kMaxParts));
+}
+
+size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
+
+template <typename T>
+cudaError_t launch(const VerifyArgs& a, const Plan& w, Scale c, cudaStream_t stream) {
+    const int64_t rows = a.drafts + a.requests + (a.draft ? a.drafts : 0);
+    verify_stats<T><<<dim3(static_cast<unsigned>(rows), w.parts), kThreads, 0, stream>>>(a, w, c);
+    cudaError_t e = cudaGetLastError();
+    if (e != cudaSuccess) return e;
+    verify_draw<T><<<dim3(w.races, a.requests), kThreads, 0, stream>>>(a, w, c);
+    return cudaGetLastError();
+}
+
+}  // namespace
+
+size_t verify_workspace(int64_t drafts, int64_t requests, int64_t) {
+    return round16(sizeof(float2) * kMaxParts * static_cast<size_t>(2 * drafts + requests)) +
+           round16(sizeof(unsigned long long) * requests) + round16(sizeof(unsigned int) * requests);
+}
+
+cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const int sms = device_info(dev).sm_count;
+    Plan w;
+    w.parts = parts_of(a.drafts + a.requests + (a.draft ? a.drafts : 0), a.cols, sms);
+    w.part = (a.cols + w.parts - 1) / w.parts;
+    w.races = parts_of(a.requests, a.cols, sms);
+    w.share = (a.cols + w.races - 1) / w.races;
+    uint8_t* p = static_cast<uint8_t*>(a.workspace);
+    w.stats = reinterpret_cast<float2*>(p);
+    p += round16(sizeof(float2) * kMaxParts * static_cast<size_t>(2 * a.drafts + a.requests));
+    w.best = reinterpret_cast<unsigned long long*>(p);
+    p += round16(sizeof(unsigned long long) * a.requests);
+    w.done = reinterpret_cast<unsigned int*>(p);
+    const double c = static_cast<double>(a.scale) * 1.4426950408889634074;
+    Scale s;
+    s.hi = static_cast<float>(c);
+    s.lo = static_cast<float>(c - static_cast<double>(s.hi));
+    if (a.dtype == kF32) return launch<float>(a, w, s, stream);
+    if (a.dtype == kF16) return launch<__half>(a, w, s, stream);
+    return launch<__nv_bfloat16>(a, w, s, stream);
+}
+
+}  // namespace lik
