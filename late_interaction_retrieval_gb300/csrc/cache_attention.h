@@ -1,0 +1,67 @@
+// cache_attention.h -- what the kernels of attention over the 8-bit cache share.
+#pragma once
+
+#include <cuda.h>
+#include <cuda_bf16.h>
+#include <cuda_fp16.h>
+
+#include "lik_internal.h"
+#include "serve.h"
+#include "sm100_ptx.cuh"
+
+namespace lik {
+namespace attn {
+
+// One request as the device has it, clamped to what the buffers hold.
+struct Request {
+    int row0, n;   // its rows
+    int length;    // its tokens in the cache
+};
+
+__device__ __forceinline__ Request request_of(const AttentionArgs& a, int b) {
+    Request r;
+    const int rows = static_cast<int>(a.rows);
+    int lo = a.offsets[b], hi = a.offsets[b + 1];
+    lo = min(max(lo, 0), rows);
+    hi = min(max(hi, lo), rows);
+    r.row0 = lo;
+    r.n = hi - lo;
+    r.length = min(max(a.lengths[b], 0), static_cast<int>(a.cols << a.page_shift));
+    return r;
+}
+
+// Two e4m3 codes (low byte first) as fp16: exact, NaN stays NaN.
+__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+    uint32_t h;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(codes)));
+    return h;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
+
+// The power of two that brings a row whose largest size is `most` to [2^14, 2^15).
+__device__ __forceinline__ int row_shift(float most) {
+    if (!(most > 0.0f) || most > 3.402823466e38f) return 0;
+    return 14 - ilogbf(most);
+}
+
+__device__ __forceinline__ float2 widen_q(uint32_t v, bool bf16) {
+    if (bf16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
+    return __half22float2(*reinterpret_cast<const __half2*>(&v));
+}
+
+__device__ __forceinline__ uint32_t pack_half(float x, float y) {
+    const __half2 h = __floats2half2_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+}  // namespace attn
+
+cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t stream);
+size_t attention_split_workspace(int64_t dim, int sms);
+
+}  // namespace lik

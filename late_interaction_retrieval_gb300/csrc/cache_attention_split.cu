@@ -1,0 +1,722 @@
+// cache_attention_split.cu -- attention over the 8-bit cache for few rows a
+// key head (single tokens): the cache is read once, at the memory's rate.
+//
+// A unit is 32 tokens of one (request, key head, 16 rows).  The units of the
+// batch, laid end to end, are cut into one equal range a block, so that long
+// and short requests load the chip evenly; a request that is cut leaves
+// partial sums, which a second launch joins in the order of the cache.  In a
+// block every warp takes every eighth unit, with a ring of its own that TMA
+// fills: no warp waits for another until a request's end.
+//
+// Products are m16n8k16 with the rows as M.  The codes of 8 bits become fp16
+// in registers on their way from shared memory to the fragments (exactly, one
+// conversion for two codes), and the order of the dimensions and tokens inside
+// a fragment is chosen so that every load is 16 bytes wide: a thread's K codes
+// are 32 neighbouring dimensions of one token, its V codes 16 neighbouring
+// dimensions of 4 tokens, transposed by byte permutes.
+//
+// Rows are scaled to fp16's range by a power of two.  The softmax weights are
+// 2^15 * exp(z - max) * (the page's scale / the largest so far), rounded to
+// fp16: 11 bits over 29 binades, below which a weight's share of the sum is
+// under 2^-29.  Statistics, sums and the join are fp32.
+#include "cache_attention.h"
+#include "tmap.h"
+
+namespace lik {
+namespace {
+
+using namespace attn;
+
+constexpr int kWarps = 8;
+constexpr int kThreads = 32 * kWarps;
+constexpr int kTok = 32;     // tokens of a unit
+constexpr int kRows = 16;    // rows of a unit
+constexpr int kStages = 3;
+constexpr float kWeightTop = 32768.0f;
+
+// Where a block's pieces of cut requests lie, and whose they are.
+struct PieceInfo {
+    int request, unit;  // unit: head * row tiles + row tile; request -1: no piece
+    int begins, ends;   // whether it holds the first / the last tokens
+};
+template <int DP>
+struct Piece {
+    float m[kRows], l[kRows];
+    float4 o[kRows * DP / 4];
+};
+
+template <int DP>
+struct Smem {
+    static constexpr int kTile = kTok * DP;  // bytes of one operand's tile
+    alignas(1024) uint8_t ring[kWarps][kStages][2][kTile];
+    float4 join[kWarps][DP / 16][32];  // half of every warp's sums
+    float m[kWarps][kRows], l[kWarps][kRows];
+    uint64_t full[kWarps][kStages];
+    int2 page[kWarps][kStages];
+    long long warp_sum[kWarps];
+};
+
+struct Maps {
+    CUtensorMap k, v;
+};
+
+// A request's units.
+struct Span {
+    Request r;
+    int tiles, row_tiles;
+    __device__ __forceinline__ long long units(int heads) const {
+        return static_cast<long long>(tiles) * row_tiles * heads;
+    }
+};
+
+__device__ __forceinline__ Span span_of(const AttentionArgs& a, int b, int group) {
+    Span s;
+    s.r = request_of(a, b);
+    s.tiles = s.r.n ? max(1, (s.r.length + kTok - 1) / kTok) : 0;
+    s.row_tiles = (s.r.n * group + kRows - 1) / kRows;
+    return s;
+}
+
+// A place in the order of units.
+struct Cursor {
+    int b, item, tile;  // item: head * row_tiles + row tile
+    Span s;
+};
+
+__device__ __forceinline__ void settle(const AttentionArgs& a, Cursor& c, int group) {
+    while (c.tile >= c.s.tiles) {
+        c.tile -= c.s.tiles;
+        if (++c.item >= c.s.row_tiles * a.heads) {
+            c.item = 0;
+            do {
+                if (++c.b >= a.requests) {
+                    c.s.tiles = INT32_MAX;  // behind the last unit
+                    return;
+                }
+                c.s = span_of(a, c.b, group);
+            } while (c.s.tiles == 0);
+        }
+    }
+}
+
+__device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                         uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    return v;
+}
+
+// Shared memory offset of 16-byte chunk `c` of row `r` in a tile as TMA
+// swizzles it: rows of 128 bytes, chunk ^= row mod 8; of 64 bytes, chunk ^=
+// (row / 2) mod 4.
+template <int DP>
+__device__ __forceinline__ uint32_t chunk_at(int r, int c) {
+    return DP == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+
+// One row's 4 neighbouring dimensions to the output.
+__device__ __forceinline__ void store4(void* out, int64_t at, float4 v, bool bf16, bool wide) {
+    uint32_t lo, hi;
+    if (bf16) {
+        const __nv_bfloat162 x = __floats2bfloat162_rn(v.x, v.y), y = __floats2bfloat162_rn(v.z, v.w);
+        lo = *reinterpret_cast<const uint32_t*>(&x);
+        hi = *reinterpret_cast<const uint32_t*>(&y);
+    } else {
+        lo = pack_half(v.x, v.y);
+        hi = pack_half(v.z, v.w);
+    }
+    uint16_t* const p = static_cast<uint16_t*>(out) + at;
+    if (wide) {
+        *reinterpret_cast<uint2*>(p) = make_uint2(lo, hi);
+    } else {
+        p[0] = static_cast<uint16_t>(lo);
+        p[1] = static_cast<uint16_t>(lo >> 16);
+        p[2] = static_cast<uint16_t>(hi);
+        p[3] = static_cast<uint16_t>(hi >> 16);
+    }
+}
+
+// Register vector k of a lane: row lane / 4 (+ 8 in the upper half of the
+// vectors), 4 dimensions of the lane's DP / 4.
+template <int DP>
+__device__ __forceinline__ void vector_place(int k, int lane, int& row, int& dim) {
+    constexpr int half = DP / 16;  // vectors of a row
+    row = (lane >> 2) + (k >= half ? 8 : 0);
+    dim = (lane & 3) * (DP / 4) + (k & (half - 1)) * 4;
+}
+
+template <int DP>
+__device__ __forceinline__ void write_vector(const AttentionArgs& a, const Request& r, int head, int row_tile,
+                                             int group, int k, int lane, float4 o, float l, float m, bool wide) {
+    int row, dim;
+    vector_place<DP>(k, lane, row, dim);
+    const int rr = row_tile * kRows + row;
+    if (rr >= r.n * group) return;
+    const int64_t t = r.row0 + rr / group;
+    const int h = head * group + rr % group;
+    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+    if (l == 0.0f) o = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    o.x *= inv;
+    o.y *= inv;
+    o.z *= inv;
+    o.w *= inv;
+    if (dim < a.dim)
+        store4(a.out, t * a.out_token_stride + h * a.out_head_stride + dim, o, a.dtype == kBF16, wide);
+    if (dim == 0 && a.lse)
+        a.lse[t * a.q_heads + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_split_kernel(const AttentionArgs a, const __grid_constant__ Maps maps, unsigned int* err,
+                           PieceInfo* infos, Piece<DP>* pieces, bool q_wide, bool out_wide) {
+    extern __shared__ uint8_t raw[];
+    Smem<DP>& sm = *reinterpret_cast<Smem<DP>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
+    constexpr int KS = DP / 16;   // k-steps of a score, words of K codes a thread and token
+    constexpr int NB = DP / 8;    // n-blocks of the output
+    constexpr int VW = DP / 32;   // words of V codes a thread and token
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, q4 = lane & 3;
+    const int group = a.q_heads / a.heads;
+    const bool bf16 = a.dtype == kBF16;
+
+    if (lane == 0) {
+        for (int s = 0; s < kStages; ++s) ptx::mbar_init(ptx::smem_u32(&sm.full[warp][s]), 1);
+        ptx::fence_mbar_init();
+    }
+    // every block sums the requests' units for itself: thread i those of its
+    // neighbouring requests
+    const int B = a.requests, each = (B + kThreads - 1) / kThreads;
+    long long mine = 0;
+    for (int b = min(tid * each, B); b < min(tid * each + each, B); ++b) mine += span_of(a, b, group).units(a.heads);
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) sm.warp_sum[warp] = incl;
+    __syncthreads();
+    long long units = 0;
+    for (int w = 0; w < kWarps; ++w) {
+        if (w < warp) incl += sm.warp_sum[w];
+        units += sm.warp_sum[w];
+    }
+    long long* const chunk = reinterpret_cast<long long*>(&sm.join);  // the join begins after every warp's search
+    chunk[tid] = incl - mine;
+    __syncthreads();
+
+    // a block has a round of units at least; blocks without any have no piece
+    const long long active = max(1ll, min(static_cast<long long>(gridDim.x), units / kWarps));
+    const long long u0 = blockIdx.x < active ? units * blockIdx.x / active : units;
+    const long long u1 = blockIdx.x < active ? units * (blockIdx.x + 1) / active : units;
+    if (tid < 2) infos[2 * blockIdx.x + tid] = PieceInfo{-1, 0, 0, 0};
+    if (u0 >= u1) return;
+
+    // the warp's first unit
+    Cursor load;
+    {
+        const long long u = u0;  // the block's first; the warp's lies `warp` units on
+        int i = 0;
+        for (int step = kThreads / 2; step > 0; step >>= 1)
+            if (chunk[i + step] <= u) i += step;  // the last chunk that begins at or before u
+        long long rest = u - chunk[i];
+        int b = i * each;
+        Span s = span_of(a, b, group);
+        while (rest >= s.units(a.heads)) {
+            rest -= s.units(a.heads);
+            s = span_of(a, ++b, group);
+        }
+        load.b = b;
+        load.s = s;
+        load.item = static_cast<int>(rest / s.tiles);
+        load.tile = static_cast<int>(rest % s.tiles);
+    }
+    Cursor at = load;  // the block's place: the segment that all its warps are in
+    long long left = u1 - u0;
+    load.tile += warp;
+    settle(a, load, group);
+    long long to_load = left > warp ? (left - warp + kWarps - 1) / kWarps : 0;  // this warp's units
+
+    const int page_size = 1 << a.page_shift;
+    const uint32_t ring = ptx::smem_u32(&sm.ring[warp][0][0][0]);
+    constexpr int kTile = Smem<DP>::kTile;
+    int fill = 0;  // the stage to fill next
+    // the table entries of the unit to load next, read one unit ahead
+    auto entries = [&](const Cursor& c, int2& p) {
+        const int32_t* const row = a.table + c.b * a.stride;
+        const int t0 = c.tile * kTok, t1 = t0 + 16;
+        p.x = t0 < c.s.r.length ? row[t0 >> a.page_shift] : -1;
+        p.y = t1 < c.s.r.length ? row[t1 >> a.page_shift] : -1;
+    };
+    int2 next = make_int2(-1, -1);
+    if (to_load > 0) entries(load, next);
+    // fills a stage with the unit under the cursor; the cursor moves on
+    auto issue = [&]() {
+        if (to_load <= 0) return;
+        int2 p = next;
+        // an entry outside the pool hides its tokens: page 0 is loaded, and not looked at
+        if (p.x < 0 || p.x >= a.pages) p.x = -1;
+        if (p.y < 0 || p.y >= a.pages) p.y = -1;
+        const int head = load.item / load.s.row_tiles;
+        const int t0 = load.tile * kTok;
+        if (lane == 0) {
+            sm.page[warp][fill] = p;
+            const uint32_t bar = ptx::smem_u32(&sm.full[warp][fill]);
+            const uint32_t dst = ring + fill * 2 * kTile;
+            if (p.x < 0 && p.y < 0) {
+                ptx::mbar_arrive(bar);  // nothing to load
+            } else {
+                ptx::mbar_arrive_expect_tx(bar, 2 * kTile);
+                const int off = head * page_size + (t0 & (page_size - 1));
+                const int px = max(p.x, 0);
+                ptx::tma_load_3d(dst, &maps.k, 0, off, px, bar);
+                ptx::tma_load_3d(dst + kTile, &maps.v, 0, off, px, bar);
+                if (page_size == 16) {
+                    const int py = max(p.y, 0);
+                    ptx::tma_load_3d(dst + kTile / 2, &maps.k, 0, off, py, bar);
+                    ptx::tma_load_3d(dst + kTile + kTile / 2, &maps.v, 0, off, py, bar);
+                }
+            }
+        }
+        fill = fill + 1 == kStages ? 0 : fill + 1;
+        --to_load;
+        load.tile += kWarps;
+        settle(a, load, group);
+        if (to_load > 0) entries(load, next);
+    };
+    for (int s = 0; s < kStages; ++s) issue();
+
+    int stage = 0;
+    uint32_t phase = 0;
+    bool ok = true;
+    int turn = warp;  // units until this warp's next one
+    while (left > 0) {
+        // ---- a segment: the rest of this (request, head, row tile), as far as the block's range goes
+        const Request r = at.s.r;
+        const int head = at.item / at.s.row_tiles, row_tile = at.item - head * at.s.row_tiles;
+        const int first = at.tile;
+        const int count = static_cast<int>(min(static_cast<long long>(at.s.tiles - first), left));
+        const int rows_in = min(kRows, r.n * group - row_tile * kRows);
+        const bool upper = rows_in > 8;
+
+        // the thread's two rows of q, scaled to fp16's range
+        uint32_t qf[KS][4];
+        float factor[2];
+        int sees[2];  // positions that the row sees
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            const int rr = row_tile * kRows + g + 8 * half;
+            const bool live = g + 8 * half < rows_in;
+            const int i = live ? rr / group : 0;
+            const int64_t base = (r.row0 + i) * a.q_token_stride +
+                                 static_cast<int64_t>(head * group + (live ? rr % group : 0)) * a.q_head_stride;
+            const uint16_t* const src = static_cast<const uint16_t*>(a.q) + base + q4 * (DP / 4);
+            uint32_t w[DP / 8];
+#pragma unroll
+            for (int c = 0; c < DP / 32; ++c) {  // 8 dimensions
+                uint4 v = make_uint4(0, 0, 0, 0);
+                if (live && q4 * (DP / 4) + c * 8 < a.dim) {
+                    if (q_wide) {
+                        v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+                    } else {
+                        const uint16_t* const s = src + c * 8;
+                        v.x = s[0] | (static_cast<uint32_t>(s[1]) << 16);
+                        v.y = s[2] | (static_cast<uint32_t>(s[3]) << 16);
+                        v.z = s[4] | (static_cast<uint32_t>(s[5]) << 16);
+                        v.w = s[6] | (static_cast<uint32_t>(s[7]) << 16);
+                    }
+                }
+                w[4 * c] = v.x;
+                w[4 * c + 1] = v.y;
+                w[4 * c + 2] = v.z;
+                w[4 * c + 3] = v.w;
+            }
+            float most = 0.0f;
+#pragma unroll
+            for (int c = 0; c < DP / 8; ++c) {
+                const float2 f = widen_q(w[c], bf16);
+                most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+            }
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
+            most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
+            const int shift = row_shift(most);
+#pragma unroll
+            for (int c = 0; c < DP / 8; ++c) {
+                const float2 f = widen_q(w[c], bf16);
+                qf[c >> 1][(c & 1) * 2 + half] = pack_half(scalbnf(f.x, shift), scalbnf(f.y, shift));
+            }
+            factor[half] = scalbnf(a.scale * 1.44269504088896341f, -shift);
+            sees[half] = live ? r.length - r.n + i + 1 : 0;
+        }
+        const int all_see = r.length - r.n + (row_tile * kRows) / group + 1;  // what even the first row sees
+
+        float o[NB][4];
+#pragma unroll
+        for (int j = 0; j < NB; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
+        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        float top_scale = kLeastScale;
+
+        int done = turn;
+        for (; done < count; done += kWarps) {
+            const int t0 = (first + done) * kTok;
+            if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(ptx::smem_u32(&sm.full[warp][stage]), phase, err));
+            const int2 page = sm.page[warp][stage];
+            float ks[2] = {0.0f, 0.0f}, vs[2] = {0.0f, 0.0f};
+            if (page.x >= 0) {
+                ks[0] = a.k_scale[static_cast<int64_t>(page.x) * a.heads + head];
+                vs[0] = a.v_scale[static_cast<int64_t>(page.x) * a.heads + head];
+            }
+            if (page.y >= 0) {
+                ks[1] = a.k_scale[static_cast<int64_t>(page.y) * a.heads + head];
+                vs[1] = a.v_scale[static_cast<int64_t>(page.y) * a.heads + head];
+            }
+            const uint32_t kt = ring + stage * 2 * kTile, vt = kt + kTile;
+            // every row sees every token
+            const bool whole = t0 + kTok <= all_see && page.x >= 0 && page.y >= 0;
+
+            float s[4][4];
+#pragma unroll
+            for (int nb = 0; nb < 4; ++nb) {
+                s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.0f;
+                const int row = nb * 8 + g;
+                uint32_t w[KS];
+#pragma unroll
+                for (int c = 0; c < DP / 64; ++c) {
+                    const uint4 v = lds16(kt + chunk_at<DP>(row, q4 * (DP / 64) + c));
+                    w[4 * c] = v.x;
+                    w[4 * c + 1] = v.y;
+                    w[4 * c + 2] = v.z;
+                    w[4 * c + 3] = v.w;
+                }
+#pragma unroll
+                for (int k = 0; k < KS; ++k)
+                    mma16816(s[nb], qf[k][0], qf[k][1], qf[k][2], qf[k][3], widen2(w[k]), widen2(w[k] >> 16));
+            }
+            // ---- softmax weights, two rows a thread
+            float weight[2];
+            const float before = top_scale;
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+                const float size = fabsf(vs[h]);
+                if (size <= 3.402823466e38f) top_scale = fmaxf(top_scale, size);
+            }
+#pragma unroll
+            for (int h = 0; h < 2; ++h) weight[h] = vs[h] / top_scale * kWeightTop;
+            uint32_t pf[2][4];  // A fragments of the two 16-token steps
+            float keep[2];
+#pragma unroll
+            for (int half = 0; half < 2; ++half) {
+                float z[4][2];
+                float mx = m[half];
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb) {
+                    const float f = factor[half] * ks[nb >> 1];
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float x = s[nb][2 * half + e] * f;
+                        if (!whole) {
+                            const int pos = t0 + nb * 8 + q4 * 2 + e;
+                            const bool seen = pos < sees[half] && (nb < 2 ? page.x : page.y) >= 0;
+                            x = seen ? x : -INFINITY;
+                        }
+                        z[nb][e] = x;
+                        mx = fmaxf(mx, x);
+                    }
+                }
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
+                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
+                const float base = mx == -INFINITY ? 0.0f : mx;
+                keep[half] = exp2_fast(m[half] - base);
+                m[half] = mx;
+                l[half] *= keep[half];
+#pragma unroll
+                for (int nb = 0; nb < 4; ++nb) {
+                    const float p0 = exp2_fast(z[nb][0] - base), p1 = exp2_fast(z[nb][1] - base);
+                    l[half] += p0 + p1;
+                    float w0 = p0 * weight[nb >> 1], w1 = p1 * weight[nb >> 1];
+                    if (!whole) {  // a scale that is not finite does not reach rows that do not see its page
+                        w0 = z[nb][0] == -INFINITY ? 0.0f : w0;
+                        w1 = z[nb][1] == -INFINITY ? 0.0f : w1;
+                    }
+                    pf[nb >> 1][(nb & 1) * 2 + half] = pack_half(w0, w1);
+                }
+                keep[half] *= before / top_scale;
+            }
+            if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+#pragma unroll
+                for (int j = 0; j < NB; ++j) {
+                    o[j][0] *= keep[0];
+                    o[j][1] *= keep[0];
+                    o[j][2] *= keep[1];
+                    o[j][3] *= keep[1];
+                }
+            }
+            // ---- values
+            bool odd = false;  // a NaN code that some row may not see
+#pragma unroll
+            for (int st = 0; st < 2; ++st) {
+                uint32_t v[4][VW];
+#pragma unroll
+                for (int i = 0; i < 4; ++i) {
+                    const int row = st * 16 + q4 * 2 + (i & 1) + (i >> 1) * 8;
+                    if (DP == 128) {
+                        const uint4 x = lds16(vt + chunk_at<DP>(row, g));
+                        v[i][0] = x.x;
+                        v[i][1] = x.y;
+                        v[i][VW - 2] = x.z;
+                        v[i][VW - 1] = x.w;
+                    } else {
+                        const uint2 x = lds8(vt + chunk_at<DP>(row, g >> 1) + (g & 1) * 8);
+                        v[i][0] = x.x;
+                        v[i][1] = x.y;
+                    }
+                    if (!whole) {
+                        // no row's token: its codes may be anything; a token that some rows
+                        // see: its NaN codes are set apart
+                        const bool live = t0 + row < r.length && (st ? page.y : page.x) >= 0;
+#pragma unroll
+                        for (int k = 0; k < VW; ++k) {
+                            const uint32_t nan = __vcmpeq4(v[i][k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                            odd = odd || (live && nan != 0);
+                            v[i][k] = live ? v[i][k] & ~nan : 0u;
+                        }
+                    }
+                }
+#pragma unroll
+                for (int k = 0; k < VW; ++k) {
+                    const uint32_t x01 = __byte_perm(v[0][k], v[1][k], 0x5140), x23 = __byte_perm(v[0][k], v[1][k], 0x7362);
+                    const uint32_t y01 = __byte_perm(v[2][k], v[3][k], 0x5140), y23 = __byte_perm(v[2][k], v[3][k], 0x7362);
+                    mma16816(o[4 * k], pf[st][0], pf[st][1], pf[st][2], pf[st][3], widen2(x01), widen2(y01));
+                    mma16816(o[4 * k + 1], pf[st][0], pf[st][1], pf[st][2], pf[st][3], widen2(x01 >> 16), widen2(y01 >> 16));
+                    mma16816(o[4 * k + 2], pf[st][0], pf[st][1], pf[st][2], pf[st][3], widen2(x23), widen2(y23));
+                    mma16816(o[4 * k + 3], pf[st][0], pf[st][1], pf[st][2], pf[st][3], widen2(x23 >> 16), widen2(y23 >> 16));
+                }
+            }
+            if (!whole && __any_sync(0xffffffffu, odd)) {
+                // the rows that see a NaN code get it, the others do not
+                for (int row = 0; row < kTok; ++row) {
+                    const int pos = t0 + row;
+                    if (pos >= r.length || (row < 16 ? page.x : page.y) < 0) continue;
+#pragma unroll
+                    for (int j = 0; j < NB; ++j) {
+                        // n-block j: the thread's dimensions q4 * DP / 4 + j, + DP / 8
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int d = q4 * (DP / 4) + e * (DP / 8) + j;
+                            uint32_t code;
+                            asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(vt + chunk_at<DP>(row, d >> 4) + (d & 15)));
+                            if ((code & 0x7f) == 0x7f) {
+                                if (pos < sees[0]) o[j][e] = __int_as_float(0x7fffffff);
+                                if (pos < sees[1]) o[j][2 + e] = __int_as_float(0x7fffffff);
+                            }
+                        }
+                    }
+                }
+            }
+            __syncwarp();  // every lane is done with the stage
+            issue();
+            if (++stage == kStages) {
+                stage = 0;
+                phase ^= 1;
+            }
+        }
+        turn = done - count;  // into the next segment
+
+        // ---- the segment's end: the warps' sums are joined, each warp taking two vectors of every lane
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
+            l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
+            if (q4 == 0) {
+                sm.m[warp][g + 8 * half] = m[half];
+                sm.l[warp][g + 8 * half] = l[half];
+            }
+        }
+        __syncthreads();
+        float sum[2], big[2];
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            big[half] = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) big[half] = fmaxf(big[half], sm.m[w][g + 8 * half]);
+            const float base = big[half] == -INFINITY ? 0.0f : big[half];
+            sum[half] = 0.0f;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) {
+                const float lw = sm.l[w][g + 8 * half];
+                // a warp that saw nothing has no part; NaN sums stay NaN
+                sum[half] += lw == 0.0f ? 0.0f : lw * exp2_fast(sm.m[w][g + 8 * half] - base);
+            }
+            const float f = l[half] == 0.0f ? 0.0f : exp2_fast(m[half] - base) * (top_scale / kWeightTop);
+#pragma unroll
+            for (int j = 0; j < NB; ++j) {
+                o[j][2 * half] = l[half] == 0.0f ? 0.0f : o[j][2 * half] * f;
+                o[j][2 * half + 1] = l[half] == 0.0f ? 0.0f : o[j][2 * half + 1] * f;
+            }
+        }
+        const bool begins = first == 0, ends = first + count == at.s.tiles;
+        const bool cut = !(begins && ends);
+        const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
+        constexpr int HV = DP / 16;  // vectors of a row: 8, or 4
+#pragma unroll
+        for (int half = 0; half < 2; ++half) {
+            if (half == 1 && !upper) break;
+            if (half) __syncthreads();
+#pragma unroll
+            for (int k = 0; k < HV; ++k) {
+                // vector k of the row: dimensions 4k .. 4k + 3 of the thread's DP / 4
+                const int j = (4 * k) % NB, e = (4 * k) / NB;
+                sm.join[warp][k][lane] = make_float4(o[j][2 * half + e], o[j + 1][2 * half + e], o[j + 2][2 * half + e],
+                                                     o[j + 3][2 * half + e]);
+            }
+            __syncthreads();
+            if (warp < HV) {
+                float4 x = sm.join[0][warp][lane];
+#pragma unroll
+                for (int w = 1; w < kWarps; ++w) {
+                    const float4 y = sm.join[w][warp][lane];
+                    x.x += y.x;
+                    x.y += y.y;
+                    x.z += y.z;
+                    x.w += y.w;
+                }
+                const int k = half * HV + warp;
+                if (cut) {
+                    pieces[slot].o[k * 32 + lane] = x;
+                } else {
+                    write_vector<DP>(a, r, head, row_tile, group, k, lane, x, sum[half], big[half], out_wide);
+                }
+            }
+        }
+        if (cut) {
+            if (warp == 0 && q4 == 0) {
+#pragma unroll
+                for (int half = 0; half < 2; ++half) {
+                    pieces[slot].m[g + 8 * half] = big[half];
+                    pieces[slot].l[g + 8 * half] = sum[half];
+                }
+            }
+            if (tid == 0) infos[slot] = PieceInfo{at.b, at.item, begins, ends};
+        }
+        __syncthreads();  // sm.join, sm.m and sm.l are free again
+        left -= count;
+        at.tile += count;
+        if (left > 0) settle(a, at, group);
+    }
+}
+
+// One block for each block of the first launch: if a request was cut behind
+// its first tokens there, the block joins all of its pieces, in order.
+template <int DP>
+__global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttentionArgs a, int blocks,
+                                                                  const PieceInfo* infos, const Piece<DP>* pieces,
+                                                                  bool out_wide) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PieceInfo info = infos[2 * blockIdx.x + 1];
+    if (info.request < 0 || info.ends) return;
+    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int group = a.q_heads / a.heads;
+    const Span s = span_of(a, info.request, group);
+    const int head = info.unit / s.row_tiles, row_tile = info.unit - head * s.row_tiles;
+    int last = blockIdx.x + 1;
+    while (last < blocks - 1 && !infos[2 * last].ends) ++last;
+    constexpr int V = 2 * DP / 16;
+    for (int k = warp; k < V; k += kWarps) {
+        int row, dim;
+        vector_place<DP>(k, lane, row, dim);
+        if (row_tile * kRows + row >= s.r.n * group) continue;
+        const Piece<DP>* p = pieces + 2 * blockIdx.x + 1;
+        float m = p->m[row];
+        for (int c = blockIdx.x + 1; c <= last; ++c) m = fmaxf(m, pieces[2 * c].m[row]);
+        const float base = m == -INFINITY ? 0.0f : m;
+        float l = 0.0f;
+        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+        for (int c = blockIdx.x; c <= last; ++c) {
+            p = pieces + (c == static_cast<int>(blockIdx.x) ? 2 * c + 1 : 2 * c);
+            if (p->l[row] == 0.0f) continue;
+            const float f = exp2_fast(p->m[row] - base);
+            const float4 y = p->o[k * 32 + lane];
+            l = fmaf(p->l[row], f, l);
+            x.x = fmaf(y.x, f, x.x);
+            x.y = fmaf(y.y, f, x.y);
+            x.z = fmaf(y.z, f, x.z);
+            x.w = fmaf(y.w, f, x.w);
+        }
+        write_vector<DP>(a, s.r, head, row_tile, group, k, lane, x, l, m, out_wide);
+    }
+}
+
+bool wide_rows(const void* p, int64_t token, int64_t head, int64_t bytes) {
+    return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(token * 2) | static_cast<uintptr_t>(head * 2)) &
+            (bytes - 1)) == 0;
+}
+
+size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
+
+template <int DP>
+cudaError_t launch(const AttentionArgs& a, cudaStream_t stream) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const int blocks = device_info(dev).sm_count;
+    Maps maps;
+    const uint32_t page = 1u << a.page_shift;
+    const uint64_t dims[3] = {static_cast<uint64_t>(a.dim), static_cast<uint64_t>(a.heads) * page,
+                              static_cast<uint64_t>(a.pages > 0 ? a.pages : 1)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(a.dim), static_cast<uint64_t>(a.heads) * page * a.dim};
+    const uint32_t box[3] = {DP, page < kTok ? page : kTok, 1};
+    // a cache without pages: nothing is loaded, but a map needs an address
+    const void* const k = a.pages > 0 ? a.k_cache : a.workspace;
+    const void* const v = a.pages > 0 ? a.v_cache : a.workspace;
+    if (!encode_tmap_bytes(&maps.k, k, dims, strides, box) || !encode_tmap_bytes(&maps.v, v, dims, strides, box))
+        return cudaErrorInvalidValue;
+    uint8_t* const w = static_cast<uint8_t*>(a.workspace);
+    PieceInfo* const infos = reinterpret_cast<PieceInfo*>(w);
+    Piece<DP>* const pieces = reinterpret_cast<Piece<DP>*>(w + round16(sizeof(PieceInfo) * 2 * blocks));
+    const size_t smem = sizeof(Smem<DP>) + 1024;
+    e = cudaFuncSetAttribute(attention_split_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const bool q_wide = wide_rows(a.q, a.q_token_stride, a.q_head_stride, 16);
+    const bool out_wide = wide_rows(a.out, a.out_token_stride, a.out_head_stride, 8);
+    attention_split_kernel<DP><<<blocks, kThreads, smem, stream>>>(a, maps, device_error_word(), infos, pieces, q_wide,
+                                                                   out_wide);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<DP>, a, blocks, static_cast<const PieceInfo*>(infos),
+                              static_cast<const Piece<DP>*>(pieces), out_wide);
+}
+
+}  // namespace
+
+size_t attention_split_workspace(int64_t dim, int sms) {
+    const size_t piece = dim <= 64 ? sizeof(Piece<64>) : sizeof(Piece<128>);
+    return round16(sizeof(PieceInfo) * 2 * sms) + 2 * piece * sms;
+}
+
+cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t stream) {
+    return a.dim <= 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+}
+
+}  // namespace lik

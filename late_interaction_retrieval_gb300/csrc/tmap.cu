@@ -56,4 +56,15 @@ bool encode_tmap_kmajor(CUtensorMap* map, int dtype, const void* base, int rank,
     return r == CUDA_SUCCESS;
 }
 
+bool encode_tmap_bytes(CUtensorMap* map, const void* base, const uint64_t (&dims)[3],
+                       const uint64_t (&strides_bytes)[2], const uint32_t (&box)[3]) {
+    EncodeTiledFn fn = encoder();
+    if (!fn || (box[0] != 64 && box[0] != 128)) return false;
+    const cuuint64_t gdim[3] = {dims[0], dims[1], dims[2]}, gstride[2] = {strides_bytes[0], strides_bytes[1]};
+    const cuuint32_t bdim[3] = {box[0], box[1], box[2]}, estride[3] = {1, 1, 1};
+    return fn(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 3, const_cast<void*>(base), gdim, gstride, bdim, estride,
+              CU_TENSOR_MAP_INTERLEAVE_NONE, box[0] == 64 ? CU_TENSOR_MAP_SWIZZLE_64B : CU_TENSOR_MAP_SWIZZLE_128B,
+              CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
+}
+
 }  // namespace lik
