@@ -42,10 +42,12 @@ __device__ __forceinline__ float exp_scaled(float d, Scale c) {
 }
 
 __device__ __forceinline__ float2 join(float2 x, float2 y, Scale c) {
-    // a NaN stays: comparisons that it fails keep the side that has it
-    const float m = x.x >= y.x ? x.x : (y.x >= x.x ? y.x : x.x + y.x);
-    if (m == -INFINITY) return make_float2(m, 0.0f);
-    return make_float2(m, x.y * exp_scaled(x.x - m, c) + y.y * exp_scaled(y.x - m, c));
+    // the largest is taken without NaN, which stays in the sum: a side's sum is 0 only if it has nothing
+    const float m = fmaxf(x.x, y.x);
+    const float base = m == -INFINITY ? 0.0f : m;
+    const float sx = x.y == 0.0f ? 0.0f : x.y * exp_scaled(x.x - base, c);
+    const float sy = y.y == 0.0f ? 0.0f : y.y * exp_scaled(y.x - base, c);
+    return make_float2(m, sx + sy);
 }
 
 __device__ __forceinline__ float2 warp_join(float2 v, Scale c) {
@@ -57,9 +59,33 @@ __device__ __forceinline__ float2 warp_join(float2 v, Scale c) {
     return v;
 }
 
+// 16 bytes of logits, widened.
+template <typename T>
+struct Vec {
+    static constexpr int n = 16 / sizeof(T);
+    uint4 raw;
+    __device__ __forceinline__ void load(const T* p) { raw = __ldg(reinterpret_cast<const uint4*>(p)); }
+    __device__ __forceinline__ void widen(float (&f)[n]) const {
+        const T* const e = reinterpret_cast<const T*>(&raw);
+#pragma unroll
+        for (int i = 0; i < n; ++i) f[i] = to_f32(e[i]);
+    }
+};
+
+// One logit's (largest, sum): nothing for -inf, a NaN sum for NaN.
+__device__ __forceinline__ float2 one(float z) {
+    return make_float2(z, z == -INFINITY ? 0.0f : (z == z ? 1.0f : z));
+}
+
+// One more value into a running (largest, sum).  A plain product suffices
+// here: a term of 2^-t is off by t * 2^-24 of itself, and its share of the sum
+// is the smaller the larger t is.
+__device__ __forceinline__ float term(float z, float m, Scale c) { return exp2f((z - m) * c.hi); }
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) verify_stats(const VerifyArgs a, const Plan w, Scale c) {
     __shared__ float2 of_warp[kWarps];
+    constexpr int kVec = Vec<T>::n, kUnroll = 32 / kVec;  // 32 columns a thread and turn
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int64_t row = blockIdx.x;
     const int64_t targets = a.drafts + a.requests;
@@ -71,7 +97,42 @@ __global__ void __launch_bounds__(kThreads) verify_stats(const VerifyArgs a, con
     }
     const int64_t c0 = blockIdx.y * w.part, c1 = c0 + w.part < a.cols ? c0 + w.part : a.cols;
     float2 v = make_float2(-INFINITY, 0.0f);
-    for (int64_t k = c0 + tid; k < c1; k += kThreads) v = join(v, make_float2(load_f32(z + k), 1.0f), c);
+    if (c0 < c1) {
+        // columns up to the first 16-byte boundary and behind the last one alone
+        const int64_t to_wide = ((16 - (reinterpret_cast<uintptr_t>(z + c0) & 15)) & 15) / sizeof(T);
+        const int64_t head = to_wide < c1 - c0 ? to_wide : c1 - c0;
+        const int64_t vecs = (c1 - c0 - head) / kVec, tail = c0 + head + vecs * kVec;
+        if (tid < head) v = join(v, one(load_f32(z + c0 + tid)), c);
+        if (tid < c1 - tail) v = join(v, one(load_f32(z + tail + tid)), c);
+        const T* const wide = z + c0 + head;
+        for (int64_t i = tid; i < vecs; i += kUnroll * kThreads) {
+            Vec<T> x[kUnroll];
+            float f[kUnroll][kVec];
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u)
+                if (i + u * kThreads < vecs) x[u].load(wide + (i + u * kThreads) * kVec);
+            float m = v.x;
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (i + u * kThreads < vecs) {
+                    x[u].widen(f[u]);
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) m = fmaxf(m, f[u][e]);
+                }
+            }
+            // all of it -inf so far: 0 stands in, and every term is 0; a NaN makes its own term one
+            const float base = m == -INFINITY ? 0.0f : m;
+            float s = v.y == 0.0f ? 0.0f : v.y * exp_scaled(v.x - base, c);
+#pragma unroll
+            for (int u = 0; u < kUnroll; ++u) {
+                if (i + u * kThreads < vecs) {
+#pragma unroll
+                    for (int e = 0; e < kVec; ++e) s += term(f[u][e], base, c);
+                }
+            }
+            v = make_float2(m, s);
+        }
+    }
     v = warp_join(v, c);
     if (lane == 0) of_warp[warp] = v;
     __syncthreads();
@@ -95,11 +156,22 @@ __device__ __forceinline__ float prob(float z, float2 s, Scale c) {
     return s.y == 0.0f ? 0.0f : exp_scaled(z - s.x, c) / s.y;
 }
 
-__device__ __forceinline__ unsigned long long key_of(float r, float noise, int64_t col) {
-    const float k = r / noise;
-    if (!(k > 0.0f)) return 0;
-    return (static_cast<unsigned long long>(__float_as_uint(k)) << 32) | (0xffffffffu - static_cast<unsigned>(col));
-}
+// A thread's best column: the largest quotient above 0, the first of equals.
+struct Best {
+    float key = 0.0f;
+    int64_t col = 0;
+    __device__ __forceinline__ void offer(float r, float noise, int64_t k) {
+        const float q = __fdividef(r, noise);
+        if (q > key) {
+            key = q;
+            col = k;
+        }
+    }
+    __device__ __forceinline__ unsigned long long packed() const {
+        if (!(key > 0.0f)) return 0;
+        return (static_cast<unsigned long long>(__float_as_uint(key)) << 32) | (0xffffffffu - static_cast<unsigned>(col));
+    }
+};
 
 __device__ __forceinline__ unsigned long long block_max(unsigned long long v, unsigned long long* of_warp) {
 #pragma unroll
@@ -115,7 +187,8 @@ __device__ __forceinline__ unsigned long long block_max(unsigned long long v, un
 }
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads) verify_draw(const VerifyArgs a, const Plan w, Scale c) {
+__global__ void __launch_bounds__(kThreads) verify_draw(const VerifyArgs a, const Plan w, Scale c, bool wide) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ unsigned long long of_warp[kWarps];
     __shared__ int first_fail, is_last;
     __shared__ float2 stat_p, stat_q;
@@ -161,14 +234,37 @@ __global__ void __launch_bounds__(kThreads) verify_draw(const VerifyArgs a, cons
     const int64_t struck = residual && !draft ? a.drafted[dr] : -1;
     const float* const noise = a.noise + b * a.cols;
     const int64_t c0 = blockIdx.x * w.share, c1 = c0 + w.share < a.cols ? c0 + w.share : a.cols;
-    unsigned long long best = 0;
-    for (int64_t k = c0 + tid; k < c1; k += kThreads) {
-        float r = prob(load_f32(z + k), sp, c);
-        if (y) r = fmaxf(r - prob(load_f32(y + k), sq, c), 0.0f);
-        if (k == struck) r = 0.0f;
-        const unsigned long long key = key_of(r, noise[k], k);
-        best = key > best ? key : best;
+    // probabilities by the sums' reciprocals
+    const float ip = sp.y == 0.0f ? 0.0f : 1.0f / sp.y, iq = !y || sq.y == 0.0f ? 0.0f : 1.0f / sq.y;
+    auto left_of = [&](float zp, float zq, int64_t k) {
+        float r = exp_scaled(zp - sp.x, c) * ip;
+        if (y) r = fmaxf(r - exp_scaled(zq - sq.x, c) * iq, 0.0f);
+        return k == struck ? 0.0f : r;
+    };
+    Best mine;
+    if (wide) {
+        constexpr int kVec = Vec<T>::n;
+        for (int64_t k = c0 + tid * kVec; k < c1; k += kThreads * kVec) {
+            Vec<T> xp, xq;
+            float4 e[kVec / 4];
+            xp.load(z + k);
+            if (y) xq.load(y + k);
+            else xq.raw = make_uint4(0, 0, 0, 0);
+#pragma unroll
+            for (int i = 0; i < kVec / 4; ++i) e[i] = __ldg(reinterpret_cast<const float4*>(noise + k) + i);
+            float fp[kVec], fq[kVec];
+            xp.widen(fp);
+            xq.widen(fq);
+#pragma unroll
+            for (int i = 0; i < kVec; ++i)
+                mine.offer(left_of(fp[i], fq[i], k + i), reinterpret_cast<const float*>(e)[i], k + i);
+        }
+    } else {
+#pragma unroll 4
+        for (int64_t k = c0 + tid; k < c1; k += kThreads)
+            mine.offer(left_of(load_f32(z + k), y ? load_f32(y + k) : 0.0f, k), __ldg(noise + k), k);
     }
+    unsigned long long best = mine.packed();
     best = block_max(best, of_warp);
     if (tid == 0) {
         if (best) atomicMax(w.best + b, best);
@@ -180,11 +276,9 @@ __global__ void __launch_bounds__(kThreads) verify_draw(const VerifyArgs a, cons
     if (!is_last) return;
     best = *reinterpret_cast<volatile unsigned long long*>(w.best + b);
     if (best == 0 && residual) {  // nothing is left of the target over the draft: the target itself
-        for (int64_t k = tid; k < a.cols; k += kThreads) {
-            const unsigned long long key = key_of(prob(load_f32(z + k), sp, c), noise[k], k);
-            best = key > best ? key : best;
-        }
-        best = block_max(best, of_warp);
+        Best all;
+        for (int64_t k = tid; k < a.cols; k += kThreads) all.offer(exp_scaled(load_f32(z + k) - sp.x, c) * ip, noise[k], k);
+        best = block_max(all.packed(), of_warp);
     }
     const int token = best ? static_cast<int>(0xffffffffu - static_cast<unsigned>(best)) : -1;
     for (int i = warp; i <= n; i += kWarps) {
@@ -226,8 +320,23 @@ cudaError_t launch(const VerifyArgs& a, const Plan& w, Scale c, cudaStream_t str
     verify_stats<T><<<dim3(static_cast<unsigned>(rows), w.parts), kThreads, 0, stream>>>(a, w, c);
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
-    verify_draw<T><<<dim3(w.races, a.requests), kThreads, 0, stream>>>(a, w, c);
-    return cudaGetLastError();
+    // 16-byte loads from all three rows: every row of each starts on a 16-byte boundary
+    auto whole = [](const void* p, int64_t stride, size_t size) {
+        return ((reinterpret_cast<uintptr_t>(p) | (static_cast<uintptr_t>(stride) * size)) & 15) == 0;
+    };
+    const bool wide = a.cols % Vec<T>::n == 0 && whole(a.target, a.target_stride, sizeof(T)) &&
+                      whole(a.noise, a.cols, 4) && (!a.draft || whole(a.draft, a.draft_stride, sizeof(T)));
+    // its blocks are in place when the first launch ends
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(w.races, a.requests);
+    cfg.blockDim = dim3(kThreads);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, verify_draw<T>, a, w, c, wide);
 }
 
 }  // namespace
@@ -244,9 +353,9 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
     const int sms = device_info(dev).sm_count;
     Plan w;
     w.parts = parts_of(a.drafts + a.requests + (a.draft ? a.drafts : 0), a.cols, sms);
-    w.part = (a.cols + w.parts - 1) / w.parts;
+    w.part = ((a.cols + w.parts - 1) / w.parts + 7) & ~int64_t(7);
     w.races = parts_of(a.requests, a.cols, sms);
-    w.share = (a.cols + w.races - 1) / w.races;
+    w.share = ((a.cols + w.races - 1) / w.races + 7) & ~int64_t(7);
     uint8_t* p = static_cast<uint8_t*>(a.workspace);
     w.stats = reinterpret_cast<float2*>(p);
     p += round16(sizeof(float2) * kMaxParts * static_cast<size_t>(2 * a.drafts + a.requests));
