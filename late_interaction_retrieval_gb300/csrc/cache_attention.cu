@@ -3,15 +3,25 @@
 #include "cache_attention.h"
 
 namespace lik {
+namespace {
 
-size_t cache_attention_workspace(int64_t, int64_t, int64_t, int64_t dim, int64_t, int64_t) {
+// Few rows a key head take the kernel whose tiles have 16 rows.
+bool few_rows(int64_t max_added, int64_t group) { return max_added * group <= 16; }
+
+}  // namespace
+
+size_t cache_attention_workspace(int64_t rows, int64_t q_heads, int64_t heads, int64_t dim, int64_t,
+                                 int64_t max_added) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess) return 0;
-    return attention_split_workspace(dim, device_info(dev).sm_count);
+    const int sms = device_info(dev).sm_count;
+    return few_rows(max_added, q_heads / heads) ? attention_split_workspace(dim, sms)
+                                                : attention_wide_workspace(rows, q_heads / heads, dim, sms);
 }
 
 cudaError_t launch_cache_attention(const AttentionArgs& a, cudaStream_t stream) {
-    return launch_attention_split(a, stream);
+    return few_rows(a.max_added, a.q_heads / a.heads) ? launch_attention_split(a, stream)
+                                                      : launch_attention_wide(a, stream);
 }
 
 }  // namespace lik

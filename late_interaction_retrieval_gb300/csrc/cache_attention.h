@@ -63,5 +63,7 @@ __device__ __forceinline__ uint32_t pack_half(float x, float y) {
 
 cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t stream);
 size_t attention_split_workspace(int64_t dim, int sms);
+cudaError_t launch_attention_wide(const AttentionArgs& a, cudaStream_t stream);
+size_t attention_wide_workspace(int64_t rows, int64_t group, int64_t dim, int sms);
 
 }  // namespace lik

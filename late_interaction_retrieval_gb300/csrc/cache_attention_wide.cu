@@ -1,0 +1,949 @@
+// cache_attention_wide.cu -- attention over the 8-bit cache for many rows a
+// key head (drafts of grouped heads, prompts): the products on tcgen05.
+//
+// A tile is 128 tokens against 128 rows: S = Q K^T in tensor memory, its
+// softmax weights back into tensor memory as fp16, O += P V.  Two tiles are in
+// work at a time, in two streams with a softmax warpgroup, an S/P and an O
+// accumulator each, so that the tensor cores work on one while the other's
+// exponentials are taken.  Where an item has more than 128 rows the streams
+// are its two halves, on the same tokens (the codes are widened once for
+// both); else they are the even and the odd tiles of the same rows, joined at
+// the item's end.
+//
+// The codes become fp16 (exactly) on their way from the TMA ring to the MMA's
+// operand tiles.  K stays token by token.  V is transposed, so that both
+// operands are K-major: a thread takes 8 tokens of 8 dimensions, byte
+// permutes pair the tokens, and every store is 16 bytes.  Those 8 tokens lie
+// 8 apart in a block of 64 (which keeps the loads free of bank conflicts), so
+// the tokens of S's columns are ordered that way: column j of a block holds
+// token (j mod 8) * 8 + j / 8.
+//
+// The weights are 2^7 exp2(z - m) (the page's scale / c), with a maximum m
+// that is only moved when it is exceeded by 2^8 and a scale c that is moved to
+// twice the largest; both moves rescale O, and are rare.  Work is spread as
+// in the kernel for few rows: the batch's tiles end to end, one equal range a
+// block, pieces of cut items joined by a second launch.
+#include "cache_attention.h"
+#include "tmap.h"
+
+namespace lik {
+namespace {
+
+using namespace attn;
+
+constexpr int kThreads = 512;
+constexpr int kTok = 128;
+constexpr int kM = 128;
+constexpr int kItemRows = 256;
+constexpr int kRaw = 8;        // slots of 64 tokens of one operand
+constexpr int kScaleRing = 8;  // tiles whose scales are kept
+constexpr float kHeadroom = 8.0f;
+constexpr float kWeightTop = 128.0f;
+
+// warps
+constexpr int kConvert = 8, kLoad = 12, kMma = 13, kBusy = 14;
+
+constexpr uint32_t kColS = 0, kColO = 256;
+
+struct PieceInfo {
+    int request, head, item;  // request -1: no piece
+    int begins, ends;
+};
+
+template <int DP>
+struct Smem {
+    alignas(1024) uint8_t q[2][DP / 64][kM * 128];
+    uint8_t k[DP / 64][kTok * 128];
+    uint8_t v[2][2][DP * 128];
+    uint8_t raw[kRaw][64 * DP];
+    float2 scale[kScaleRing][8];  // of 16 tokens each: keys', values'
+    uint32_t valid[kScaleRing];
+    uint64_t raw_full[kRaw], raw_empty[kRaw], scale_full[kScaleRing];
+    uint64_t k_full, k_empty, v_full[2], v_empty[2];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t merge_full, merge_empty, exit_bar;
+    uint32_t tmem;
+    int nan_seen;
+    int start[4], end[4];  // request, head, item, tile
+    long long warp_sum[kThreads / 32];
+};
+
+struct Maps {
+    CUtensorMap k, v;
+};
+
+// 256 rows (or what is left) of a request's (token, query head of the key head).
+struct Item {
+    Request r;
+    int b, head, item;
+    int rows;   // of the item
+    int tiles;  // of 128 tokens that any of its rows sees, at least 1
+    bool two;   // more than 128 rows: a stream for each half
+};
+
+__device__ __forceinline__ int items_of(const Request& r, int group) { return (r.n * group + kItemRows - 1) / kItemRows; }
+
+__device__ __forceinline__ void shape(Item& x, int group) {
+    const int all = x.r.n * group, first = x.item * kItemRows;
+    x.rows = min(kItemRows, all - first);
+    x.two = x.rows > kM;
+    const int sees = x.r.length - x.r.n + (first + x.rows - 1) / group + 1;
+    x.tiles = max(1, (sees + kTok - 1) / kTok);
+}
+
+__device__ __forceinline__ long long steps_of(const Request& r, int group, int i) {
+    Item x;
+    x.r = r;
+    x.item = i;
+    shape(x, group);
+    return static_cast<long long>(x.tiles) * (x.two ? 2 : 1);
+}
+
+__device__ long long steps_of_head(const Request& r, int group) {
+    long long s = 0;
+    for (int i = 0; i < items_of(r, group); ++i) s += steps_of(r, group, i);
+    return s;
+}
+
+// Walks a block's segments: an item and a range of its tiles.
+struct Walk {
+    Item x;
+    int t0, t1;
+    bool last;
+    int end[4];
+    __device__ __forceinline__ void place(const AttentionArgs& a, int group, int tile) {
+        shape(x, group);
+        last = x.b == end[0] && x.head == end[1] && x.item == end[2];
+        t0 = tile;
+        t1 = last ? end[3] : x.tiles;
+    }
+    __device__ __forceinline__ void begin(const AttentionArgs& a, int group, const int* from, const int* to) {
+        for (int i = 0; i < 4; ++i) end[i] = to[i];
+        x.b = from[0];
+        x.head = from[1];
+        x.item = from[2];
+        x.r = request_of(a, x.b);
+        place(a, group, from[3]);
+    }
+    __device__ __forceinline__ void next(const AttentionArgs& a, int group) {
+        if (++x.item >= items_of(x.r, group)) {
+            x.item = 0;
+            if (++x.head >= a.heads) {
+                x.head = 0;
+                do {
+                    x.r = request_of(a, ++x.b);
+                } while (x.r.n == 0);  // the end's request has rows
+            }
+        }
+        place(a, group, 0);
+    }
+};
+
+__device__ __forceinline__ uint4 lds16(uint32_t at) {
+    uint4 v;
+    asm volatile("ld.shared.v4.u32 {%0, %1, %2, %3}, [%4];" : "=r"(v.x), "=r"(v.y), "=r"(v.z), "=r"(v.w) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ uint2 lds8(uint32_t at) {
+    uint2 v;
+    asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ void sts16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
+    asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
+}
+// Shared memory written by this thread, before the tensor cores read it.
+__device__ __forceinline__ void fence_operands() { asm volatile("fence.proxy.async.shared::cta;" ::: "memory"); }
+
+// 16-byte chunk c of row r of a raw tile as TMA swizzles it.
+template <int DP>
+__device__ __forceinline__ uint32_t raw_at(int r, int c) {
+    return DP == 128 ? r * 128 + ((c ^ (r & 7)) << 4) : r * 64 + ((c ^ ((r >> 1) & 3)) << 4);
+}
+// 16-byte chunk c of row r of an operand tile with rows of 128 bytes, swizzled.
+__device__ __forceinline__ uint32_t tile_at(int r, int c) { return r * 128 + ((c ^ (r & 7)) << 4); }
+
+// D (+)= A B^T with A (fp16, two to a 32-bit column) in tensor memory.
+__device__ __forceinline__ void mma_f16_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, bool accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d),
+        "r"(a), "l"(b), "r"(idesc), "r"(accumulate ? 1u : 0u)
+        : "memory");
+}
+
+__device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&v)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, "
+        "%12, %13, %14, %15, %16};" ::"r"(taddr),
+        "r"(v[0]), "r"(v[1]), "r"(v[2]), "r"(v[3]), "r"(v[4]), "r"(v[5]), "r"(v[6]), "r"(v[7]), "r"(v[8]),
+        "r"(v[9]), "r"(v[10]), "r"(v[11]), "r"(v[12]), "r"(v[13]), "r"(v[14]), "r"(v[15])
+        : "memory");
+}
+
+// 8 neighbouring dimensions of one row to the output.
+__device__ __forceinline__ void store8(void* out, int64_t at, const float (&f)[8], bool bf16, bool wide) {
+    uint32_t w[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        if (bf16) {
+            const __nv_bfloat162 x = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
+            w[i] = *reinterpret_cast<const uint32_t*>(&x);
+        } else {
+            w[i] = pack_half(f[2 * i], f[2 * i + 1]);
+        }
+    }
+    uint16_t* const p = static_cast<uint16_t*>(out) + at;
+    if (wide) {
+        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    } else {
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            p[2 * i] = static_cast<uint16_t>(w[i]);
+            p[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
+        }
+    }
+}
+
+template <int DP>
+__global__ void __launch_bounds__(kThreads, 1)
+    attention_wide_kernel(const AttentionArgs a, const __grid_constant__ Maps maps, unsigned int* err,
+                          PieceInfo* infos, float* pieces, int piece_rows, bool q_wide, bool out_wide) {
+    extern __shared__ uint8_t raw_smem[];
+    Smem<DP>& sm = *reinterpret_cast<Smem<DP>*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int group = a.q_heads / a.heads;
+    const bool bf16 = a.dtype == kBF16;
+    using ptx::smem_u32;
+
+    if (tid == 0) {
+        for (int i = 0; i < kRaw; ++i) {
+            ptx::mbar_init(smem_u32(&sm.raw_full[i]), 1);
+            ptx::mbar_init(smem_u32(&sm.raw_empty[i]), 4);
+        }
+        for (int i = 0; i < kScaleRing; ++i) ptx::mbar_init(smem_u32(&sm.scale_full[i]), 1);
+        ptx::mbar_init(smem_u32(&sm.k_full), 4);
+        ptx::mbar_init(smem_u32(&sm.k_empty), 1);
+        for (int i = 0; i < 2; ++i) {
+            ptx::mbar_init(smem_u32(&sm.v_full[i]), 4);
+            ptx::mbar_init(smem_u32(&sm.v_empty[i]), 1);
+            ptx::mbar_init(smem_u32(&sm.q_full[i]), 4);
+            ptx::mbar_init(smem_u32(&sm.s_full[i]), 1);
+            ptx::mbar_init(smem_u32(&sm.p_full[i]), 4);
+            ptx::mbar_init(smem_u32(&sm.o_full[i]), 1);
+        }
+        ptx::mbar_init(smem_u32(&sm.merge_full), 4);
+        ptx::mbar_init(smem_u32(&sm.merge_empty), 4);
+        ptx::mbar_init(smem_u32(&sm.exit_bar), kBusy);
+        sm.nan_seen = 0;
+        ptx::fence_mbar_init();
+    }
+    // ---- the block's range of steps (a tile of one stream), from every request's
+    const int B = a.requests, each = (B + kThreads - 1) / kThreads;
+    long long mine = 0;
+    for (int b = min(tid * each, B); b < min(tid * each + each, B); ++b)
+        mine += steps_of_head(request_of(a, b), group) * a.heads;
+    long long incl = mine;
+#pragma unroll
+    for (int d = 1; d < 32; d <<= 1) {
+        const long long o = __shfl_up_sync(0xffffffffu, incl, d);
+        if (lane >= d) incl += o;
+    }
+    if (lane == 31) sm.warp_sum[warp] = incl;
+    __syncthreads();
+    long long all = 0;
+    for (int w = 0; w < kThreads / 32; ++w) {
+        if (w < warp) incl += sm.warp_sum[w];
+        all += sm.warp_sum[w];
+    }
+    const long long excl = incl - mine;
+    // a block has two steps at least
+    const long long active = max(1ll, min(static_cast<long long>(gridDim.x), all / 2));
+    const long long u0 = blockIdx.x < active ? all * blockIdx.x / active : all;
+    const long long u1 = blockIdx.x < active ? all * (blockIdx.x + 1) / active : all;
+    if (tid < 2) infos[2 * blockIdx.x + tid] = PieceInfo{-1, 0, 0, 0, 0};
+    if (u0 >= u1) return;
+    // the tile that holds step u, by the thread whose requests do; a range ends
+    // before the tile of its last bound, or behind the batch's last
+    auto locate = [&](long long u, int* to, int more) {
+        if (u < excl || u >= incl) return;
+        long long rest = u - excl;
+        int b = tid * each;
+        Request r = request_of(a, b);
+        long long per = steps_of_head(r, group);
+        while (rest >= per * a.heads) {
+            rest -= per * a.heads;
+            r = request_of(a, ++b);
+            per = steps_of_head(r, group);
+        }
+        to[0] = b;
+        to[1] = static_cast<int>(rest / per);
+        rest %= per;
+        int i = 0;
+        while (rest >= steps_of(r, group, i)) rest -= steps_of(r, group, i++);
+        Item x;
+        x.r = r;
+        x.item = i;
+        shape(x, group);
+        to[2] = i;
+        to[3] = static_cast<int>(x.two ? rest / 2 : rest) + more;
+    };
+    locate(u0, sm.start, 0);
+    if (u1 < all) locate(u1, sm.end, 0);
+    else locate(all - 1, sm.end, 1);
+    if (warp == kMma) {
+        ptx::tmem_alloc(smem_u32(&sm.tmem), 512);
+        ptx::tmem_relinquish();
+        ptx::tc_fence_before();
+    }
+    __syncthreads();
+    ptx::tc_fence_after();
+    const uint32_t tmem = sm.tmem;
+    if (warp >= kBusy) return;
+
+    Walk w;
+    w.begin(a, group, sm.start, sm.end);
+    bool ok = true;
+    const int page_size = 1 << a.page_shift;
+
+    if (warp == kLoad) {
+        // ------------------------------------------------------- raw tiles --
+        const int box = min(page_size, 64);
+        int slot = 0;
+        uint32_t phase = 1;  // an empty ring
+        int n = 0;           // tiles so far
+        float2 scale = make_float2(0.0f, 0.0f);
+        bool pending = false;  // scales of the tile before that are not written yet
+        auto page_at = [&](const Walk& x, int t) {
+            const int pos = t * kTok + 16 * lane;
+            int p = -1;
+            if (lane < 8 && pos < x.x.r.length) p = a.table[x.x.b * a.stride + (pos >> a.page_shift)];
+            return p >= 0 && p < a.pages ? p : -1;
+        };
+        auto publish = [&](int tile) {
+            if (lane < 8) sm.scale[tile & (kScaleRing - 1)][lane] = scale;
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.scale_full[tile & (kScaleRing - 1)]));
+        };
+        int page = w.t1 > w.t0 ? page_at(w, w.t0) : -1;
+        while (ok) {
+            for (int t = w.t0; ok && t < w.t1; ++t) {
+                const int now = page;
+                const uint32_t live = __ballot_sync(0xffffffffu, now >= 0);
+                for (int part = 0; part < 4; ++part) {  // K 0-63, K 64-127, V 0-63, V 64-127
+                    const int half = part & 1;
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.raw_empty[slot]), phase, err));
+                    if (!ok) break;
+                    const uint32_t bar = smem_u32(&sm.raw_full[slot]);
+                    const bool any = ((live >> (4 * half)) & 15u) != 0;
+                    if (part == 0 && lane == 0) sm.valid[n & (kScaleRing - 1)] = live;
+                    __syncwarp();
+                    if (lane == 0) {
+                        if (any) ptx::mbar_arrive_expect_tx(bar, 64 * DP);
+                        else ptx::mbar_arrive(bar);  // nothing to load
+                    }
+                    __syncwarp();
+                    // a lane loads what begins at its 16 tokens
+                    const int tok = 16 * lane - 64 * half;
+                    if (any && lane < 8 && tok >= 0 && tok < 64 && tok % box == 0) {
+                        const int off = w.x.head * page_size + ((t * kTok + 16 * lane) & (page_size - 1));
+                        ptx::tma_load_3d(smem_u32(&sm.raw[slot][tok * DP]), part < 2 ? &maps.k : &maps.v, 0, off,
+                                         max(now, 0), bar);
+                    }
+                    if (++slot == kRaw) {
+                        slot = 0;
+                        phase ^= 1;
+                    }
+                }
+                if (!ok) break;
+                // the scales are on their way while the next tile's pages are looked up; those of
+                // the tile before have arrived
+                if (pending) publish(n - 1);
+                scale = make_float2(0.0f, 0.0f);
+                if (now >= 0) {
+                    scale.x = a.k_scale[static_cast<int64_t>(now) * a.heads + w.x.head];
+                    scale.y = a.v_scale[static_cast<int64_t>(now) * a.heads + w.x.head];
+                }
+                pending = true;
+                ++n;
+                if (t + 1 < w.t1) page = page_at(w, t + 1);
+            }
+            if (!ok || w.last) break;
+            w.next(a, group);
+            if (w.t1 > w.t0) page = page_at(w, w.t0);
+        }
+        if (ok && pending) publish(n - 1);
+    } else if (warp >= kConvert && warp < kConvert + 4) {
+        // ----------------------------------------------- codes to operands --
+        const int ct = tid - 32 * kConvert;
+        int slot = 0;
+        uint32_t raw_phase = 0;
+        int n = 0;
+        auto release = [&]() {
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.raw_empty[slot]));
+            if (++slot == kRaw) {
+                slot = 0;
+                raw_phase ^= 1;
+            }
+        };
+        while (ok) {
+            // what even the item's first row sees
+            const int all_see = w.x.r.length - w.x.r.n + (w.x.item * kItemRows) / group + 1;
+            for (int t = w.t0; ok && t < w.t1; ++t, ++n) {
+                // K: a thread widens 16 dimensions of a token at a time
+                if (n > 0) ok = ptx::mbar_wait(smem_u32(&sm.k_empty), (n - 1) & 1, err);
+                for (int half = 0; half < 2; ++half) {
+                    if (ok) ok = ptx::mbar_wait(smem_u32(&sm.raw_full[slot]), raw_phase, err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t src = smem_u32(sm.raw[slot]), dst = smem_u32(sm.k[0]);
+                    constexpr int C = DP / 16;  // chunks of a token
+#pragma unroll
+                    for (int i = 0; i < 64 * C / 128; ++i) {
+                        const int item = ct + 128 * i, c = item % C, tok = item / C;
+                        const uint4 x = lds16(src + raw_at<DP>(tok, c));
+                        const int row = half * 64 + (tok & 7) * 8 + (tok >> 3);
+                        const uint32_t at = dst + (c >> 2) * (kTok * 128);
+                        const uint32_t lo = at + tile_at(row, (c & 3) * 2), hi = at + tile_at(row, (c & 3) * 2 + 1);
+                        const uint32_t l0 = widen2(x.x), l1 = widen2(x.x >> 16), l2 = widen2(x.y), l3 = widen2(x.y >> 16);
+                        const uint32_t h0 = widen2(x.z), h1 = widen2(x.z >> 16), h2 = widen2(x.w), h3 = widen2(x.w >> 16);
+                        // the two 64-dimension tiles share their banks: their lanes take turns
+                        if (c & 4) {
+                            sts16(hi, h0, h1, h2, h3);
+                            sts16(lo, l0, l1, l2, l3);
+                        } else {
+                            sts16(lo, l0, l1, l2, l3);
+                            sts16(hi, h0, h1, h2, h3);
+                        }
+                    }
+                    release();
+                }
+                if (!ok) break;
+                fence_operands();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.k_full));
+                // V: 8 tokens, 8 apart, of 8 dimensions, transposed
+                if (n > 1) ok = ptx::mbar_wait(smem_u32(&sm.v_empty[n & 1]), ((n >> 1) - 1) & 1, err);
+                for (int half = 0; half < 2; ++half) {
+                    if (ok) ok = ptx::mbar_wait(smem_u32(&sm.raw_full[slot]), raw_phase, err);
+                    ok = __all_sync(0xffffffffu, ok);
+                    if (!ok) break;
+                    const uint32_t src = smem_u32(sm.raw[slot]), dst = smem_u32(sm.v[n & 1][half]);
+                    const uint32_t valid = sm.valid[n & (kScaleRing - 1)];
+                    const int first = t * kTok + half * 64;
+                    const bool whole = first + 64 <= all_see && ((valid >> (4 * half)) & 15u) == 15u;
+                    const int c8 = ct & 7, d8 = ct >> 3;  // tokens 8 i + c8; dimensions 8 d8 ..
+                    if (d8 < DP / 8) {
+                        uint2 x[8];
+#pragma unroll
+                        for (int i = 0; i < 8; ++i) x[i] = lds8(src + raw_at<DP>(8 * i + c8, d8 >> 1) + (d8 & 1) * 8);
+                        if (!whole) {
+                            bool nan = false;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i) {
+                                const int tok = 8 * i + c8, pos = first + tok;
+                                const bool live = pos < w.x.r.length && ((valid >> (4 * half + (tok >> 4))) & 1u);
+                                // of a token that only some rows see, NaN codes are set apart
+                                const bool some = pos >= all_see;
+                                const uint32_t nx = __vcmpeq4(x[i].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                const uint32_t ny = __vcmpeq4(x[i].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                nan = nan || (live && some && (nx | ny));
+                                x[i].x = live ? (some ? x[i].x & ~nx : x[i].x) : 0u;
+                                x[i].y = live ? (some ? x[i].y & ~ny : x[i].y) : 0u;
+                            }
+                            if (nan) sm.nan_seen = 1;
+                        }
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t p[4][4];  // [dimension][pair of tokens]
+#pragma unroll
+                            for (int i = 0; i < 4; ++i) {
+                                const uint32_t u = h ? x[2 * i].y : x[2 * i].x, v = h ? x[2 * i + 1].y : x[2 * i + 1].x;
+                                const uint32_t a01 = __byte_perm(u, v, 0x5140), a23 = __byte_perm(u, v, 0x7362);
+                                p[0][i] = widen2(a01);
+                                p[1][i] = widen2(a01 >> 16);
+                                p[2][i] = widen2(a23);
+                                p[3][i] = widen2(a23 >> 16);
+                            }
+#pragma unroll
+                            for (int j = 0; j < 4; ++j)
+                                sts16(dst + tile_at(8 * d8 + 4 * h + j, c8), p[j][0], p[j][1], p[j][2], p[j][3]);
+                        }
+                    }
+                    release();
+                }
+                if (!ok) break;
+                fence_operands();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.v_full[n & 1]));
+            }
+            if (!ok || w.last) break;
+            w.next(a, group);
+        }
+    } else if (warp == kMma) {
+        // ------------------------------------------------------------ MMAs --
+        if (lane == 0) {
+            constexpr uint32_t kIdS = ptx::f16_idesc(kM, kTok, false), kIdO = ptx::f16_idesc(kM, DP, false);
+            int n = 0;            // tiles before this segment
+            uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            while (ok) {
+                const int tiles = w.t1 - w.t0, steps = w.x.two ? 2 * tiles : tiles;
+                const bool two = w.x.two;
+                auto issue_s = [&](int u) {
+                    const int s = u & 1, t = two ? u >> 1 : u;
+                    if (u < 2) {
+                        ok = ok && ptx::mbar_wait(smem_u32(&sm.q_full[s]), q_phase[s], err);
+                        q_phase[s] ^= 1;
+                    }
+                    if (!two || s == 0) ok = ok && ptx::mbar_wait(smem_u32(&sm.k_full), (n + t) & 1, err);
+                    if (!ok) return;
+                    ptx::tc_fence_after();
+                    ptx::mma_kchain<DP / 16>(tmem + kColS + 128 * s, smem_u32(sm.q[s][0]), kM * 128, smem_u32(sm.k[0]),
+                                             kTok * 128, DP / 16, kIdS);
+                    ptx::mma_commit(smem_u32(&sm.s_full[s]));
+                    if (!two || s == 1) ptx::mma_commit(smem_u32(&sm.k_empty));
+                };
+                for (int u = 0; ok && u < min(2, steps); ++u) issue_s(u);
+                for (int u = 0; ok && u < steps; ++u) {
+                    const int s = u & 1, t = two ? u >> 1 : u, buf = (n + t) & 1;
+                    if (!two || s == 0) ok = ptx::mbar_wait(smem_u32(&sm.v_full[buf]), ((n + t) >> 1) & 1, err);
+                    ok = ok && ptx::mbar_wait(smem_u32(&sm.p_full[s]), p_phase[s], err);
+                    p_phase[s] ^= 1;
+                    if (!ok) break;
+                    ptx::tc_fence_after();
+                    const uint32_t vb = smem_u32(sm.v[buf][0]);
+#pragma unroll
+                    for (int k = 0; k < kTok / 16; ++k)
+                        mma_f16_ts(tmem + kColO + 128 * s, tmem + kColS + 128 * s + 8 * k,
+                                   ptx::sw128_kmajor_desc(vb + (k >> 2) * (DP * 128) + (k & 3) * 32), kIdO,
+                                   u >= 2 || k != 0);
+                    if (!two || s == 1) ptx::mma_commit(smem_u32(&sm.v_empty[buf]));
+                    if (u + 2 >= steps) ptx::mma_commit(smem_u32(&sm.o_full[s]));
+                    if (u + 2 < steps) issue_s(u + 2);
+                }
+                n += tiles;
+                if (!ok || w.last) break;
+                w.next(a, group);
+            }
+        }
+        __syncwarp();
+    } else {
+        // --------------------------------------------------------- softmax --
+        const int s = warp >> 2, row = tid & 127;
+        const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
+        const uint32_t col_s = tmem + lanes + kColS + 128 * s, col_o = tmem + lanes + kColO + 128 * s;
+        int n = 0;
+        uint32_t s_phase = 0, o_phase = 0, merge_phase = 0;
+        while (ok) {
+            const bool two = w.x.two;
+            const int tiles = w.t1 - w.t0, steps = two ? tiles : (tiles + 1 - s) / 2;
+            const int in_item = (two ? s * kM : 0) + row;
+            const bool live = in_item < w.x.rows;
+            const int rr = w.x.item * kItemRows + in_item;  // of the request's rows
+            const int i = live ? rr / group : 0;
+            const int h = w.x.head * group + (live ? rr % group : 0);
+            const int sees = live ? w.x.r.length - w.x.r.n + i + 1 : 0;
+            const int all_see = w.x.r.length - w.x.r.n + (w.x.item * kItemRows) / group + 1;
+            float factor = 0.0f, mref = -INFINITY, l = 0.0f, cref = 0.0f;
+            if (steps > 0) {
+                // the row of q, scaled to fp16's range
+                const uint16_t* const src = static_cast<const uint16_t*>(a.q) + (w.x.r.row0 + i) * a.q_token_stride +
+                                            h * a.q_head_stride;
+                auto load = [&](int c) {
+                    uint4 v = make_uint4(0, 0, 0, 0);
+                    if (live && c * 8 < a.dim) {
+                        if (q_wide) {
+                            v = __ldg(reinterpret_cast<const uint4*>(src) + c);
+                        } else {
+                            const uint16_t* const e = src + c * 8;
+                            v.x = e[0] | (static_cast<uint32_t>(e[1]) << 16);
+                            v.y = e[2] | (static_cast<uint32_t>(e[3]) << 16);
+                            v.z = e[4] | (static_cast<uint32_t>(e[5]) << 16);
+                            v.w = e[6] | (static_cast<uint32_t>(e[7]) << 16);
+                        }
+                    }
+                    return v;
+                };
+                uint4 x[DP / 8];
+#pragma unroll
+                for (int c = 0; c < DP / 8; ++c) x[c] = load(c);
+                float most = 0.0f;
+#pragma unroll
+                for (int c = 0; c < DP / 8; ++c) {
+                    const uint32_t e[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = widen_q(e[k], bf16);
+                        most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
+                    }
+                }
+                const int shift = row_shift(most);
+#pragma unroll
+                for (int c = 0; c < DP / 8; ++c) {
+                    const uint32_t e[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 f = widen_q(e[k], bf16);
+                        o[k] = pack_half(scalbnf(f.x, shift), scalbnf(f.y, shift));
+                    }
+                    sts16(smem_u32(sm.q[s][c >> 3]) + tile_at(row, c & 7), o[0], o[1], o[2], o[3]);
+                }
+                factor = scalbnf(a.scale * 1.44269504088896341f, -shift);
+                fence_operands();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.q_full[s]));
+            }
+            for (int st = 0; st < steps; ++st) {
+                const int t = two ? st : 2 * st + s;  // of the segment
+                const int at = (n + t) & (kScaleRing - 1), tok0 = (w.t0 + t) * kTok;
+                ok = ptx::mbar_wait(smem_u32(&sm.scale_full[at]), ((n + t) / kScaleRing) & 1, err) &&
+                     ptx::mbar_wait(smem_u32(&sm.s_full[s]), s_phase, err);
+                s_phase ^= 1;
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint32_t valid = sm.valid[at];
+                const bool whole = tok0 + kTok <= all_see && valid == 255u;
+                // a pass for the maximum
+                float mx = -INFINITY;
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32];
+                    ptx::tmem_ld_32(col_s + 32 * c, v);
+                    float fk[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) fk[k] = sm.scale[at][(c >> 1) * 4 + k].x * factor;
+                    if (whole) {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(v[j]) * fk[(j & 7) >> 1]);
+                    } else {
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) {
+                            const int tok = (c >> 1) * 64 + (j & 7) * 8 + (c & 1) * 4 + (j >> 3);
+                            const bool seen = tok0 + tok < sees && ((valid >> (tok >> 4)) & 1u);
+                            mx = fmaxf(mx, seen ? __uint_as_float(v[j]) * fk[(j & 7) >> 1] : -INFINITY);
+                        }
+                    }
+                }
+                float keep = 1.0f;
+                if (mx > mref + kHeadroom || mref == -INFINITY) {
+                    keep = mref == -INFINITY ? 0.0f : exp2_fast(mref - mx);
+                    mref = mx;
+                    l *= keep;
+                }
+                float vmost = 0.0f;
+#pragma unroll
+                for (int k = 0; k < 8; ++k) {
+                    const float size = fabsf(sm.scale[at][k].y);
+                    vmost = size <= 3.402823466e38f ? fmaxf(vmost, size) : vmost;
+                }
+                if (vmost > cref) {
+                    const float to = fminf(2.0f * vmost, 3.402823466e38f);
+                    keep *= cref / to;
+                    cref = to;
+                }
+                // the step's S came after the step before's product: O is at rest
+                if (st > 0 && __any_sync(0xffffffffu, keep != 1.0f)) {
+#pragma unroll
+                    for (int c = 0; c < DP / 32; ++c) {
+                        uint32_t v[32];
+                        ptx::tmem_ld_32(col_o + 32 * c, v);
+#pragma unroll
+                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * keep);
+                        ptx::tmem_st_32(col_o + 32 * c, v);
+                    }
+                }
+                const float base = mref == -INFINITY ? 0.0f : mref;
+                const float inv = cref > 0.0f ? kWeightTop / cref : 0.0f;
+                float sum = 0.0f;
+                // a pass for the weights, which take the place of scores that have been read
+#pragma unroll
+                for (int c = 0; c < 4; ++c) {
+                    uint32_t v[32], p[16];
+                    ptx::tmem_ld_32(col_s + 32 * c, v);
+                    float fk[4], wt[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float2 x = sm.scale[at][(c >> 1) * 4 + k];
+                        fk[k] = x.x * factor;
+                        wt[k] = x.y * inv;
+                    }
+                    float part = 0.0f;
+#pragma unroll
+                    for (int j = 0; j < 32; j += 2) {
+                        const int k = (j & 7) >> 1;
+                        float e0 = exp2_fast(fmaf(__uint_as_float(v[j]), fk[k], -base));
+                        float e1 = exp2_fast(fmaf(__uint_as_float(v[j + 1]), fk[k], -base));
+                        float w0 = e0 * wt[k], w1 = e1 * wt[k];
+                        if (!whole) {
+                            const int tok = (c >> 1) * 64 + (j & 7) * 8 + (c & 1) * 4 + (j >> 3);
+                            const bool page = (valid >> (tok >> 4)) & 1u;
+                            if (!(tok0 + tok < sees && page)) e0 = w0 = 0.0f;
+                            if (!(tok0 + tok + 8 < sees && page)) e1 = w1 = 0.0f;
+                        }
+                        part += e0 + e1;
+                        p[j >> 1] = pack_half(w0, w1);
+                    }
+                    sum += part;
+                    tmem_st_16(col_s + 16 * c, p);
+                }
+                l += sum;
+                ptx::tmem_wait_st();
+                ptx::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.p_full[s]));
+            }
+            if (!ok) break;
+            if (steps > 0) {
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.o_full[s]), o_phase, err));
+                o_phase ^= 1;
+                if (!ok) break;
+                ptx::tc_fence_after();
+            }
+            // ---- the segment's end
+            if (tiles > 0) {
+                const bool begins = w.t0 == 0, ends = w.t1 == w.x.tiles, cut = !(begins && ends);
+                const bool join = !two && tiles > 1;  // the odd tiles' sums go to the even ones'
+                const bool nan = *reinterpret_cast<volatile int*>(&sm.nan_seen) != 0;
+                constexpr int H = DP / 2;  // dimensions that fit the idle q tile of stream 1
+                float* const box = reinterpret_cast<float*>(&sm.q[1][0][0]);
+                // stream 1's maxima and sums, in the other q tile: the last product of stream 1 came after every
+                // S of the item
+                float2* const ml = reinterpret_cast<float2*>(&sm.q[0][0][0]);
+                if (s == 1 && !two) {
+                    if (join) {
+                        const float f = cref / kWeightTop;
+                        for (int part = 0; part < 2; ++part) {
+                            if (part) ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.merge_empty), merge_phase, err));
+                            if (!ok) break;
+                            if (part) merge_phase ^= 1;
+#pragma unroll
+                            for (int c = 0; c < H / 32; ++c) {
+                                uint32_t v[32];
+                                ptx::tmem_ld_32(col_o + part * H + 32 * c, v);
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) box[(32 * c + j) * kM + row] = __uint_as_float(v[j]) * f;
+                            }
+                            if (part == 0) ml[row] = make_float2(mref, l);
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.merge_full));
+                        }
+                        if (!ok) break;
+                        ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.merge_empty), merge_phase, err));
+                        merge_phase ^= 1;
+                        if (!ok) break;
+                    }
+                } else {
+                    float f0 = cref / kWeightTop, f1 = 0.0f, m = mref;
+                    const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
+                    float* const piece = pieces + static_cast<int64_t>(slot) * piece_rows * (DP + 4);
+                    const int64_t t = w.x.r.row0 + i;
+                    for (int part = 0; part < 2; ++part) {
+                        if (join) {
+                            ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.merge_full), merge_phase, err));
+                            merge_phase ^= 1;
+                            if (!ok) break;
+                            if (part == 0) {
+                                const float2 o = ml[row];
+                                m = fmaxf(mref, o.x);
+                                const float base = m == -INFINITY ? 0.0f : m;
+                                const float k0 = exp2_fast(mref - base), k1 = exp2_fast(o.x - base);
+                                // a side without weights has no part; NaN sums stay
+                                f0 = l == 0.0f ? 0.0f : f0 * k0;
+                                f1 = o.y == 0.0f ? 0.0f : k1;
+                                l = (l == 0.0f ? 0.0f : l * k0) + (o.y == 0.0f ? 0.0f : o.y * k1);
+                            }
+                        }
+                        const float g = cut ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+#pragma unroll
+                        for (int c = 0; c < H / 32; ++c) {
+                            uint32_t v[32];
+                            ptx::tmem_ld_32(col_o + part * H + 32 * c, v);
+#pragma unroll
+                            for (int e = 0; e < 4; ++e) {
+                                const int d = part * H + 32 * c + 8 * e;
+                                float f[8];
+#pragma unroll
+                                for (int j = 0; j < 8; ++j) {
+                                    float o = l == 0.0f ? 0.0f : __uint_as_float(v[8 * e + j]) * f0;
+                                    if (join && f1 != 0.0f) o = fmaf(box[(32 * c + 8 * e + j) * kM + row], f1, o);
+                                    f[j] = o * g;
+                                }
+                                if (nan && live) {
+                                    // NaN codes that were set apart: those of tokens that this row sees
+                                    for (int pos = max(all_see, w.t0 * kTok); pos < min(sees, w.t1 * kTok); ++pos) {
+                                        const int pg = a.table[w.x.b * a.stride + (pos >> a.page_shift)];
+                                        if (pg < 0 || pg >= a.pages || d >= a.dim) continue;
+                                        const uint8_t* const code =
+                                            a.v_cache + (((static_cast<int64_t>(pg) * a.heads + w.x.head) << a.page_shift) +
+                                                         (pos & (page_size - 1))) * a.dim + d;
+#pragma unroll
+                                        for (int j = 0; j < 8; ++j)
+                                            if ((code[j] & 0x7f) == 0x7f) f[j] = __int_as_float(0x7fffffff);
+                                    }
+                                }
+                                if (live && cut) {
+                                    float4* const to = reinterpret_cast<float4*>(piece + in_item * DP + d);
+                                    to[0] = make_float4(f[0], f[1], f[2], f[3]);
+                                    to[1] = make_float4(f[4], f[5], f[6], f[7]);
+                                } else if (live && d < a.dim) {
+                                    store8(a.out, t * a.out_token_stride + h * a.out_head_stride + d, f, bf16, out_wide);
+                                }
+                            }
+                        }
+                        if (join) {
+                            __syncwarp();
+                            if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.merge_empty));
+                        }
+                    }
+                    if (!ok) break;
+                    if (live && cut) {
+                        float* const sums = piece + static_cast<int64_t>(piece_rows) * DP + 2 * in_item;
+                        sums[0] = m;
+                        sums[1] = l;
+                    } else if (live && a.lse) {
+                        a.lse[t * a.q_heads + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+                    }
+                    if (cut && row == 0 && s == 0)
+                        infos[slot] = PieceInfo{w.x.b, w.x.head, w.x.item, begins, ends};
+                }
+                ptx::tc_fence_before();
+            }
+            n += tiles;
+            if (w.last) break;
+            w.next(a, group);
+        }
+    }
+
+    // Tensor memory is given back once every warp has done with it.
+    ptx::tc_fence_before();
+    __syncwarp();
+    if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.exit_bar));
+    if (warp == kMma) {
+        __syncwarp();
+        ptx::mbar_wait(smem_u32(&sm.exit_bar), 0, err);
+        ptx::tc_fence_after();
+        ptx::tmem_dealloc(tmem, 512);
+    }
+}
+
+// One block for each block of the first launch: if it left the first piece of
+// an item that goes on, all of the item's pieces are joined here, in order.
+template <int DP>
+__global__ void __launch_bounds__(256) attention_wide_join(const AttentionArgs a, int blocks, const PieceInfo* infos,
+                                                           const float* pieces, int piece_rows, bool out_wide) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const PieceInfo info = infos[2 * blockIdx.x + 1];
+    if (info.request < 0 || info.ends) return;
+    const int group = a.q_heads / a.heads;
+    Item x;
+    x.r = request_of(a, info.request);
+    x.item = info.item;
+    shape(x, group);
+    int last = blockIdx.x + 1;
+    while (last < blocks - 1 && !infos[2 * last].ends) ++last;
+    const int64_t size = static_cast<int64_t>(piece_rows) * (DP + 4), ml_at = static_cast<int64_t>(piece_rows) * DP;
+    const int per_row = a.dim / 8;
+    for (int k = blockIdx.y * 256 + threadIdx.x; k < x.rows * per_row; k += gridDim.y * 256) {
+        const int row = k / per_row, d = (k - row * per_row) * 8;
+        auto piece = [&](int c) { return pieces + (c == static_cast<int>(blockIdx.x) ? 2 * c + 1 : 2 * c) * size; };
+        float m = -INFINITY;
+        for (int c = blockIdx.x; c <= last; ++c) m = fmaxf(m, piece(c)[ml_at + 2 * row]);  // a block has a tile at least
+        const float base = m == -INFINITY ? 0.0f : m;
+        float l = 0.0f, f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        for (int c = blockIdx.x; c <= last; ++c) {
+            const float* const p = piece(c);
+            const float lc = p[ml_at + 2 * row + 1];
+            if (lc == 0.0f) continue;
+            const float g = exp2_fast(p[ml_at + 2 * row] - base);
+            l = fmaf(lc, g, l);
+            const float4 u = *reinterpret_cast<const float4*>(p + row * DP + d);
+            const float4 v = *reinterpret_cast<const float4*>(p + row * DP + d + 4);
+            f[0] = fmaf(u.x, g, f[0]);
+            f[1] = fmaf(u.y, g, f[1]);
+            f[2] = fmaf(u.z, g, f[2]);
+            f[3] = fmaf(u.w, g, f[3]);
+            f[4] = fmaf(v.x, g, f[4]);
+            f[5] = fmaf(v.y, g, f[5]);
+            f[6] = fmaf(v.z, g, f[6]);
+            f[7] = fmaf(v.w, g, f[7]);
+        }
+        const float inv = l == 0.0f ? 0.0f : 1.0f / l;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) f[j] *= inv;
+        const int rr = info.item * kItemRows + row;
+        const int64_t t = x.r.row0 + rr / group;
+        const int h = info.head * group + rr % group;
+        store8(a.out, t * a.out_token_stride + h * a.out_head_stride + d, f, a.dtype == kBF16, out_wide);
+        if (d == 0 && a.lse) a.lse[t * a.q_heads + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
+    }
+}
+
+bool wide_rows(const void* p, int64_t token, int64_t head) {
+    return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(token * 2) | static_cast<uintptr_t>(head * 2)) & 15) == 0;
+}
+
+size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
+
+int piece_rows_of(int64_t rows, int64_t group) {
+    return static_cast<int>(rows * group < kItemRows ? (rows * group + 3) & ~int64_t(3) : kItemRows);
+}
+
+template <int DP>
+cudaError_t launch(const AttentionArgs& a, cudaStream_t stream) {
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const int blocks = device_info(dev).sm_count;
+    Maps maps;
+    const uint32_t page = 1u << a.page_shift;
+    const uint64_t dims[3] = {static_cast<uint64_t>(a.dim), static_cast<uint64_t>(a.heads) * page,
+                              static_cast<uint64_t>(a.pages > 0 ? a.pages : 1)};
+    const uint64_t strides[2] = {static_cast<uint64_t>(a.dim), static_cast<uint64_t>(a.heads) * page * a.dim};
+    const uint32_t box[3] = {DP, page < 64 ? page : 64, 1};
+    // a cache without pages: nothing is loaded, but a map needs an address
+    const void* const k = a.pages > 0 ? a.k_cache : a.workspace;
+    const void* const v = a.pages > 0 ? a.v_cache : a.workspace;
+    if (!encode_tmap_bytes(&maps.k, k, dims, strides, box) || !encode_tmap_bytes(&maps.v, v, dims, strides, box))
+        return cudaErrorInvalidValue;
+    uint8_t* const w = static_cast<uint8_t*>(a.workspace);
+    PieceInfo* const infos = reinterpret_cast<PieceInfo*>(w);
+    float* const pieces = reinterpret_cast<float*>(w + round16(sizeof(PieceInfo) * 2 * blocks));
+    const int piece_rows = piece_rows_of(a.rows, a.q_heads / a.heads);
+    const size_t smem = sizeof(Smem<DP>) + 1024;
+    e = cudaFuncSetAttribute(attention_wide_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             static_cast<int>(smem));
+    if (e != cudaSuccess) return e;
+    const bool q_wide = wide_rows(a.q, a.q_token_stride, a.q_head_stride);
+    const bool out_wide = wide_rows(a.out, a.out_token_stride, a.out_head_stride);
+    attention_wide_kernel<DP><<<blocks, kThreads, smem, stream>>>(a, maps, device_error_word(), infos, pieces,
+                                                                  piece_rows, q_wide, out_wide);
+    if ((e = cudaGetLastError()) != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(blocks, 4);
+    cfg.blockDim = dim3(256);
+    cfg.stream = stream;
+    cudaLaunchAttribute attr;
+    attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &attr;
+    cfg.numAttrs = 1;
+    return cudaLaunchKernelEx(&cfg, attention_wide_join<DP>, a, blocks, static_cast<const PieceInfo*>(infos),
+                              static_cast<const float*>(pieces), piece_rows, out_wide);
+}
+
+}  // namespace
+
+size_t attention_wide_workspace(int64_t rows, int64_t group, int64_t dim, int sms) {
+    return round16(sizeof(PieceInfo) * 2 * sms) +
+           sizeof(float) * 2 * sms * static_cast<size_t>(piece_rows_of(rows, group)) * ((dim <= 64 ? 64 : 128) + 4);
+}
+
+cudaError_t launch_attention_wide(const AttentionArgs& a, cudaStream_t stream) {
+    return a.dim <= 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+}
+
+}  // namespace lik
