@@ -49,6 +49,12 @@ __device__ __forceinline__ int row_shift(float most) {
     return 14 - ilogbf(most);
 }
 
+// 2^shift in two factors, each a normal number for any shift that row_shift gives (or its negative).
+__device__ __forceinline__ float2 power_of_two(int shift) {
+    const int half = shift >> 1;
+    return make_float2(__int_as_float((127 + half) << 23), __int_as_float((127 + shift - half) << 23));
+}
+
 __device__ __forceinline__ float2 widen_q(uint32_t v, bool bf16) {
     if (bf16) return make_float2(__uint_as_float(v << 16), __uint_as_float(v & 0xffff0000u));
     return __half22float2(*reinterpret_cast<const __half2*>(&v));

@@ -353,12 +353,13 @@ __global__ void __launch_bounds__(kThreads, 1)
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 1));
             most = fmaxf(most, __shfl_xor_sync(0xffffffffu, most, 2));
             const int shift = row_shift(most);
+            const float2 up = power_of_two(shift), down = power_of_two(-shift);
 #pragma unroll
             for (int c = 0; c < DP / 8; ++c) {
                 const float2 f = widen_q(w[c], bf16);
-                qf[c >> 1][(c & 1) * 2 + half] = pack_half(scalbnf(f.x, shift), scalbnf(f.y, shift));
+                qf[c >> 1][(c & 1) * 2 + half] = pack_half(f.x * up.x * up.y, f.y * up.x * up.y);
             }
-            factor[half] = scalbnf(a.scale * 1.44269504088896341f, -shift);
+            factor[half] = a.scale * 1.44269504088896341f * down.x * down.y;
             sees[half] = live ? r.length - r.n + i + 1 : 0;
         }
         const int all_see = r.length - r.n + (row_tile * kRows) / group + 1;  // what even the first row sees

@@ -32,16 +32,18 @@ namespace {
 using namespace attn;
 
 constexpr int kThreads = 512;
-constexpr int kTok = 128;
+constexpr int kTok = 64;
 constexpr int kM = 128;
 constexpr int kItemRows = 256;
-constexpr int kRaw = 8;        // slots of 64 tokens of one operand
-constexpr int kScaleRing = 8;  // tiles whose scales are kept
+constexpr int kRaw = 6;         // raw tiles of one operand
+constexpr int kKeys = 3, kValues = 4;  // operand tiles
+constexpr int kAhead = 2;       // steps of a stream whose scores are computed ahead
+constexpr int kScaleRing = 16;  // tiles whose scales are kept
 constexpr float kHeadroom = 8.0f;
-constexpr float kWeightTop = 128.0f;
+constexpr float kWeightTop = 128.0f;  // 2^7 * 2^8 at the scale c: 2^15
 
 // warps
-constexpr int kConvert = 8, kLoad = 12, kMma = 13, kBusy = 14;
+constexpr int kConvert = 8, kLoad = 12, kMma = 13, kBusy = 15;  // an issuer of MMAs for each stream
 
 constexpr uint32_t kColS = 0, kColO = 256;
 
@@ -53,14 +55,15 @@ struct PieceInfo {
 template <int DP>
 struct Smem {
     alignas(1024) uint8_t q[2][DP / 64][kM * 128];
-    uint8_t k[DP / 64][kTok * 128];
-    uint8_t v[2][2][DP * 128];
-    uint8_t raw[kRaw][64 * DP];
-    float2 scale[kScaleRing][8];  // of 16 tokens each: keys', values'
+    uint8_t k[kKeys][DP / 64][kTok * 128];
+    uint8_t v[kValues][DP * 128];
+    uint8_t raw[kRaw][kTok * DP];
+    float2 scale[kScaleRing][4];  // of 16 tokens each: keys', values'
     uint32_t valid[kScaleRing];
     uint64_t raw_full[kRaw], raw_empty[kRaw], scale_full[kScaleRing];
-    uint64_t k_full, k_empty, v_full[2], v_empty[2];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t k_full[kKeys], k_empty[kKeys], v_full[kValues], v_empty[kValues];
+    uint64_t q_full[2], s_full[2][2], p_full[2][2];
+    uint64_t o_step[2], o_full[2];  // a step is in O; an item's last one is
     uint64_t merge_full, merge_empty, exit_bar;
     uint32_t tmem;
     int nan_seen;
@@ -182,6 +185,41 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&v)[1
         : "memory");
 }
 
+// 64 columns of this thread's lane, and their maximum, which the loads take
+// (loads and wait in one statement, so that no use comes before the wait).
+__device__ __forceinline__ void tmem_ldmax_64(uint32_t taddr, uint32_t (&v)[64], float& mx) {
+    float a, b, c, d;
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, %64, [%68];\n\t"
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %65, [%69];\n\t"
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47}, %66, [%70];\n\t"
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, %67, [%71];\n\t"
+        "tcgen05.wait::ld.sync.aligned;"
+        : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
+          "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
+          "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
+          "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]),
+          "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]),
+          "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
+          "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63]),
+          "=f"(a), "=f"(b), "=f"(c), "=f"(d)
+        : "r"(taddr), "r"(taddr + 16), "r"(taddr + 32), "r"(taddr + 48)
+        : "memory");
+    mx = fmaxf(fmaxf(a, b), fmaxf(c, d));
+}
+
+// Registers of a warpgroup's threads: 256 threads of 152 and 256 of 104 are the
+// 512 of 128 that the block is launched with.
+template <int N>
+__device__ __forceinline__ void more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+
 // 8 neighbouring dimensions of one row to the output.
 __device__ __forceinline__ void store8(void* out, int64_t at, const float (&f)[8], bool bf16, bool wide) {
     uint32_t w[4];
@@ -223,15 +261,22 @@ __global__ void __launch_bounds__(kThreads, 1)
             ptx::mbar_init(smem_u32(&sm.raw_empty[i]), 4);
         }
         for (int i = 0; i < kScaleRing; ++i) ptx::mbar_init(smem_u32(&sm.scale_full[i]), 1);
-        ptx::mbar_init(smem_u32(&sm.k_full), 4);
-        ptx::mbar_init(smem_u32(&sm.k_empty), 1);
-        for (int i = 0; i < 2; ++i) {
+        for (int i = 0; i < kKeys; ++i) {
+            ptx::mbar_init(smem_u32(&sm.k_full[i]), 4);
+            ptx::mbar_init(smem_u32(&sm.k_empty[i]), 2);
+        }
+        for (int i = 0; i < kValues; ++i) {
             ptx::mbar_init(smem_u32(&sm.v_full[i]), 4);
-            ptx::mbar_init(smem_u32(&sm.v_empty[i]), 1);
+            ptx::mbar_init(smem_u32(&sm.v_empty[i]), 2);
+        }
+        for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(smem_u32(&sm.q_full[i]), 4);
-            ptx::mbar_init(smem_u32(&sm.s_full[i]), 1);
-            ptx::mbar_init(smem_u32(&sm.p_full[i]), 4);
+            ptx::mbar_init(smem_u32(&sm.o_step[i]), 1);
             ptx::mbar_init(smem_u32(&sm.o_full[i]), 1);
+            for (int b = 0; b < 2; ++b) {
+                ptx::mbar_init(smem_u32(&sm.s_full[i][b]), 1);
+                ptx::mbar_init(smem_u32(&sm.p_full[i][b]), 4);
+            }
         }
         ptx::mbar_init(smem_u32(&sm.merge_full), 4);
         ptx::mbar_init(smem_u32(&sm.merge_empty), 4);
@@ -300,7 +345,10 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    if (warp >= kBusy) return;
+    if (warp >= kBusy) {
+        fewer_registers<104>();
+        return;
+    }
 
     Walk w;
     w.begin(a, group, sm.start, sm.end);
@@ -309,6 +357,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 
     if (warp == kLoad) {
         // ------------------------------------------------------- raw tiles --
+        fewer_registers<104>();
         const int box = min(page_size, 64);
         int slot = 0;
         uint32_t phase = 1;  // an empty ring
@@ -318,11 +367,11 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto page_at = [&](const Walk& x, int t) {
             const int pos = t * kTok + 16 * lane;
             int p = -1;
-            if (lane < 8 && pos < x.x.r.length) p = a.table[x.x.b * a.stride + (pos >> a.page_shift)];
+            if (lane < 4 && pos < x.x.r.length) p = a.table[x.x.b * a.stride + (pos >> a.page_shift)];
             return p >= 0 && p < a.pages ? p : -1;
         };
         auto publish = [&](int tile) {
-            if (lane < 8) sm.scale[tile & (kScaleRing - 1)][lane] = scale;
+            if (lane < 4) sm.scale[tile & (kScaleRing - 1)][lane] = scale;
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.scale_full[tile & (kScaleRing - 1)]));
         };
@@ -331,24 +380,21 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int t = w.t0; ok && t < w.t1; ++t) {
                 const int now = page;
                 const uint32_t live = __ballot_sync(0xffffffffu, now >= 0);
-                for (int part = 0; part < 4; ++part) {  // K 0-63, K 64-127, V 0-63, V 64-127
-                    const int half = part & 1;
+#pragma unroll 1
+                for (int part = 0; part < 2; ++part) {  // keys, values
                     ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.raw_empty[slot]), phase, err));
                     if (!ok) break;
                     const uint32_t bar = smem_u32(&sm.raw_full[slot]);
-                    const bool any = ((live >> (4 * half)) & 15u) != 0;
-                    if (part == 0 && lane == 0) sm.valid[n & (kScaleRing - 1)] = live;
-                    __syncwarp();
                     if (lane == 0) {
-                        if (any) ptx::mbar_arrive_expect_tx(bar, 64 * DP);
+                        sm.valid[n & (kScaleRing - 1)] = live;
+                        if (live) ptx::mbar_arrive_expect_tx(bar, kTok * DP);
                         else ptx::mbar_arrive(bar);  // nothing to load
                     }
                     __syncwarp();
                     // a lane loads what begins at its 16 tokens
-                    const int tok = 16 * lane - 64 * half;
-                    if (any && lane < 8 && tok >= 0 && tok < 64 && tok % box == 0) {
+                    if (live && lane < 4 && 16 * lane % box == 0) {
                         const int off = w.x.head * page_size + ((t * kTok + 16 * lane) & (page_size - 1));
-                        ptx::tma_load_3d(smem_u32(&sm.raw[slot][tok * DP]), part < 2 ? &maps.k : &maps.v, 0, off,
+                        ptx::tma_load_3d(smem_u32(&sm.raw[slot][16 * lane * DP]), part ? &maps.v : &maps.k, 0, off,
                                          max(now, 0), bar);
                     }
                     if (++slot == kRaw) {
@@ -376,6 +422,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && pending) publish(n - 1);
     } else if (warp >= kConvert && warp < kConvert + 4) {
         // ----------------------------------------------- codes to operands --
+        fewer_registers<104>();
         const int ct = tid - 32 * kConvert;
         int slot = 0;
         uint32_t raw_phase = 0;
@@ -388,23 +435,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                 raw_phase ^= 1;
             }
         };
+        int kb = 0;
+        uint32_t k_phase = 1;  // empty buffers
         while (ok) {
             // what even the item's first row sees
             const int all_see = w.x.r.length - w.x.r.n + (w.x.item * kItemRows) / group + 1;
             for (int t = w.t0; ok && t < w.t1; ++t, ++n) {
                 // K: a thread widens 16 dimensions of a token at a time
-                if (n > 0) ok = ptx::mbar_wait(smem_u32(&sm.k_empty), (n - 1) & 1, err);
-                for (int half = 0; half < 2; ++half) {
-                    if (ok) ok = ptx::mbar_wait(smem_u32(&sm.raw_full[slot]), raw_phase, err);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    const uint32_t src = smem_u32(sm.raw[slot]), dst = smem_u32(sm.k[0]);
+                ok = ptx::mbar_wait(smem_u32(&sm.k_empty[kb]), k_phase, err) &&
+                     ptx::mbar_wait(smem_u32(&sm.raw_full[slot]), raw_phase, err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                {
+                    const uint32_t src = smem_u32(sm.raw[slot]), dst = smem_u32(sm.k[kb][0]);
                     constexpr int C = DP / 16;  // chunks of a token
 #pragma unroll
-                    for (int i = 0; i < 64 * C / 128; ++i) {
+                    for (int i = 0; i < kTok * C / 128; ++i) {
                         const int item = ct + 128 * i, c = item % C, tok = item / C;
                         const uint4 x = lds16(src + raw_at<DP>(tok, c));
-                        const int row = half * 64 + (tok & 7) * 8 + (tok >> 3);
+                        const int row = (tok & 7) * 8 + (tok >> 3);
                         const uint32_t at = dst + (c >> 2) * (kTok * 128);
                         const uint32_t lo = at + tile_at(row, (c & 3) * 2), hi = at + tile_at(row, (c & 3) * 2 + 1);
                         const uint32_t l0 = widen2(x.x), l1 = widen2(x.x >> 16), l2 = widen2(x.y), l3 = widen2(x.y >> 16);
@@ -418,22 +467,25 @@ __global__ void __launch_bounds__(kThreads, 1)
                             sts16(hi, h0, h1, h2, h3);
                         }
                     }
-                    release();
                 }
-                if (!ok) break;
                 fence_operands();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.k_full));
+                release();
+                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.k_full[kb]));
+                if (++kb == kKeys) {
+                    kb = 0;
+                    k_phase ^= 1;
+                }
                 // V: 8 tokens, 8 apart, of 8 dimensions, transposed
-                if (n > 1) ok = ptx::mbar_wait(smem_u32(&sm.v_empty[n & 1]), ((n >> 1) - 1) & 1, err);
-                for (int half = 0; half < 2; ++half) {
-                    if (ok) ok = ptx::mbar_wait(smem_u32(&sm.raw_full[slot]), raw_phase, err);
-                    ok = __all_sync(0xffffffffu, ok);
-                    if (!ok) break;
-                    const uint32_t src = smem_u32(sm.raw[slot]), dst = smem_u32(sm.v[n & 1][half]);
+                const int vb = n & (kValues - 1);
+                ok = ptx::mbar_wait(smem_u32(&sm.v_empty[vb]), ((n / kValues) & 1) ^ 1, err) &&
+                     ptx::mbar_wait(smem_u32(&sm.raw_full[slot]), raw_phase, err);
+                ok = __all_sync(0xffffffffu, ok);
+                if (!ok) break;
+                {
+                    const uint32_t src = smem_u32(sm.raw[slot]), dst = smem_u32(sm.v[vb]);
                     const uint32_t valid = sm.valid[n & (kScaleRing - 1)];
-                    const int first = t * kTok + half * 64;
-                    const bool whole = first + 64 <= all_see && ((valid >> (4 * half)) & 15u) == 15u;
+                    const int first = t * kTok;
+                    const bool whole = first + kTok <= all_see && valid == 15u;
                     const int c8 = ct & 7, d8 = ct >> 3;  // tokens 8 i + c8; dimensions 8 d8 ..
                     if (d8 < DP / 8) {
                         uint2 x[8];
@@ -444,7 +496,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                             for (int i = 0; i < 8; ++i) {
                                 const int tok = 8 * i + c8, pos = first + tok;
-                                const bool live = pos < w.x.r.length && ((valid >> (4 * half + (tok >> 4))) & 1u);
+                                const bool live = pos < w.x.r.length && ((valid >> (tok >> 4)) & 1u);
                                 // of a token that only some rows see, NaN codes are set apart
                                 const bool some = pos >= all_see;
                                 const uint32_t nx = __vcmpeq4(x[i].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
@@ -472,56 +524,68 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 sts16(dst + tile_at(8 * d8 + 4 * h + j, c8), p[j][0], p[j][1], p[j][2], p[j][3]);
                         }
                     }
-                    release();
                 }
-                if (!ok) break;
                 fence_operands();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.v_full[n & 1]));
+                release();
+                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.v_full[vb]));
             }
             if (!ok || w.last) break;
             w.next(a, group);
         }
-    } else if (warp == kMma) {
+    } else if (warp >= kMma) {
         // ------------------------------------------------------------ MMAs --
+        fewer_registers<104>();
         if (lane == 0) {
             constexpr uint32_t kIdS = ptx::f16_idesc(kM, kTok, false), kIdO = ptx::f16_idesc(kM, DP, false);
-            int n = 0;            // tiles before this segment
-            uint32_t q_phase[2] = {0, 0}, p_phase[2] = {0, 0};
+            const int s = warp - kMma;
+            const uint32_t col_s = tmem + kColS + 128 * s, col_o = tmem + kColO + 128 * s;
+            int n = 0;                    // tiles before this segment
+            int scored = 0, summed = 0;   // steps of this stream so far
+            uint32_t q_phase = 0;
             while (ok) {
-                const int tiles = w.t1 - w.t0, steps = w.x.two ? 2 * tiles : tiles;
                 const bool two = w.x.two;
-                auto issue_s = [&](int u) {
-                    const int s = u & 1, t = two ? u >> 1 : u;
-                    if (u < 2) {
-                        ok = ok && ptx::mbar_wait(smem_u32(&sm.q_full[s]), q_phase[s], err);
-                        q_phase[s] ^= 1;
-                    }
-                    if (!two || s == 0) ok = ok && ptx::mbar_wait(smem_u32(&sm.k_full), (n + t) & 1, err);
+                const int tiles = w.t1 - w.t0, steps = two ? tiles : (tiles + 1 - s) / 2;
+                // A buffer is empty again when both streams have done with it; a tile of one stream counts twice.
+                auto done = [&](uint64_t* bar) {
+                    ptx::mma_commit(smem_u32(bar));
+                    if (!two) ptx::mma_commit(smem_u32(bar));
+                };
+                // Step i's tile.  Tiles are filled in order, so the other stream's phase between two of this
+                // stream's in one buffer has been completed when this one asks for the second.
+                auto tile_of = [&](int i) { return n + (two ? i : 2 * i + s); };
+                auto score = [&](int i) {
+                    const int t = tile_of(i), kb = t % kKeys, b = scored & 1;
+                    ok = ok && ptx::mbar_wait(smem_u32(&sm.k_full[kb]), (t / kKeys) & 1, err);
                     if (!ok) return;
                     ptx::tc_fence_after();
-                    ptx::mma_kchain<DP / 16>(tmem + kColS + 128 * s, smem_u32(sm.q[s][0]), kM * 128, smem_u32(sm.k[0]),
+                    // the buffer's weights of two steps ago were multiplied by an instruction before this one
+                    ptx::mma_kchain<DP / 16>(col_s + 64 * b, smem_u32(sm.q[s][0]), kM * 128, smem_u32(sm.k[kb][0]),
                                              kTok * 128, DP / 16, kIdS);
-                    ptx::mma_commit(smem_u32(&sm.s_full[s]));
-                    if (!two || s == 1) ptx::mma_commit(smem_u32(&sm.k_empty));
+                    ptx::mma_commit(smem_u32(&sm.s_full[s][b]));
+                    done(&sm.k_empty[kb]);
+                    ++scored;
                 };
-                for (int u = 0; ok && u < min(2, steps); ++u) issue_s(u);
-                for (int u = 0; ok && u < steps; ++u) {
-                    const int s = u & 1, t = two ? u >> 1 : u, buf = (n + t) & 1;
-                    if (!two || s == 0) ok = ptx::mbar_wait(smem_u32(&sm.v_full[buf]), ((n + t) >> 1) & 1, err);
-                    ok = ok && ptx::mbar_wait(smem_u32(&sm.p_full[s]), p_phase[s], err);
-                    p_phase[s] ^= 1;
+                if (steps > 0) {
+                    ok = ptx::mbar_wait(smem_u32(&sm.q_full[s]), q_phase, err);
+                    q_phase ^= 1;
+                }
+                for (int i = 0; ok && i < min(kAhead, steps); ++i) score(i);
+                for (int i = 0; ok && i < steps; ++i) {
+                    const int t = tile_of(i), vb = t & (kValues - 1), b = summed & 1;
+                    ok = ptx::mbar_wait(smem_u32(&sm.v_full[vb]), (t / kValues) & 1, err) &&
+                         ptx::mbar_wait(smem_u32(&sm.p_full[s][b]), (summed >> 1) & 1, err);
                     if (!ok) break;
+                    ++summed;
                     ptx::tc_fence_after();
-                    const uint32_t vb = smem_u32(sm.v[buf][0]);
+                    const uint32_t v0 = smem_u32(sm.v[vb]);
 #pragma unroll
                     for (int k = 0; k < kTok / 16; ++k)
-                        mma_f16_ts(tmem + kColO + 128 * s, tmem + kColS + 128 * s + 8 * k,
-                                   ptx::sw128_kmajor_desc(vb + (k >> 2) * (DP * 128) + (k & 3) * 32), kIdO,
-                                   u >= 2 || k != 0);
-                    if (!two || s == 1) ptx::mma_commit(smem_u32(&sm.v_empty[buf]));
-                    if (u + 2 >= steps) ptx::mma_commit(smem_u32(&sm.o_full[s]));
-                    if (u + 2 < steps) issue_s(u + 2);
+                        mma_f16_ts(col_o, col_s + 64 * b + 8 * k, ptx::sw128_kmajor_desc(v0 + k * 32), kIdO,
+                                   i > 0 || k != 0);
+                    ptx::mma_commit(smem_u32(&sm.o_step[s]));
+                    if (i + 1 == steps) ptx::mma_commit(smem_u32(&sm.o_full[s]));
+                    done(&sm.v_empty[vb]);
+                    if (i + kAhead < steps) score(i + kAhead);
                 }
                 n += tiles;
                 if (!ok || w.last) break;
@@ -531,11 +595,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // --------------------------------------------------------- softmax --
+        more_registers<152>();
         const int s = warp >> 2, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
-        const uint32_t col_s = tmem + lanes + kColS + 128 * s, col_o = tmem + lanes + kColO + 128 * s;
-        int n = 0;
-        uint32_t s_phase = 0, o_phase = 0, merge_phase = 0;
+        const uint32_t col_o = tmem + lanes + kColO + 128 * s;
+        int n = 0, count = 0;  // tiles, and steps of this stream, before
+        uint32_t o_phase = 0, merge_phase = 0;
         while (ok) {
             const bool two = w.x.two;
             const int tiles = w.t1 - w.t0, steps = two ? tiles : (tiles + 1 - s) / 2;
@@ -546,29 +611,29 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int h = w.x.head * group + (live ? rr % group : 0);
             const int sees = live ? w.x.r.length - w.x.r.n + i + 1 : 0;
             const int all_see = w.x.r.length - w.x.r.n + (w.x.item * kItemRows) / group + 1;
+            const bool idle = __ballot_sync(0xffffffffu, live) == 0;  // no row of this warp's: its weights do not matter
             float factor = 0.0f, mref = -INFINITY, l = 0.0f, cref = 0.0f;
             if (steps > 0) {
                 // the row of q, scaled to fp16's range
                 const uint16_t* const src = static_cast<const uint16_t*>(a.q) + (w.x.r.row0 + i) * a.q_token_stride +
                                             h * a.q_head_stride;
-                auto load = [&](int c) {
-                    uint4 v = make_uint4(0, 0, 0, 0);
-                    if (live && c * 8 < a.dim) {
-                        if (q_wide) {
-                            v = __ldg(reinterpret_cast<const uint4*>(src) + c);
-                        } else {
-                            const uint16_t* const e = src + c * 8;
-                            v.x = e[0] | (static_cast<uint32_t>(e[1]) << 16);
-                            v.y = e[2] | (static_cast<uint32_t>(e[3]) << 16);
-                            v.z = e[4] | (static_cast<uint32_t>(e[5]) << 16);
-                            v.w = e[6] | (static_cast<uint32_t>(e[7]) << 16);
-                        }
-                    }
-                    return v;
-                };
                 uint4 x[DP / 8];
+                if (q_wide) {
 #pragma unroll
-                for (int c = 0; c < DP / 8; ++c) x[c] = load(c);
+                    for (int c = 0; c < DP / 8; ++c)
+                        x[c] = live && c * 8 < a.dim ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
+                } else {
+#pragma unroll
+                    for (int c = 0; c < DP / 8; ++c) {
+                        uint32_t e[4] = {0, 0, 0, 0};
+                        if (live && c * 8 < a.dim) {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                e[k] = src[8 * c + 2 * k] | (static_cast<uint32_t>(src[8 * c + 2 * k + 1]) << 16);
+                        }
+                        x[c] = make_uint4(e[0], e[1], e[2], e[3]);
+                    }
+                }
                 float most = 0.0f;
 #pragma unroll
                 for (int c = 0; c < DP / 8; ++c) {
@@ -580,6 +645,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 const int shift = row_shift(most);
+                const float2 up = power_of_two(shift), down = power_of_two(-shift);
 #pragma unroll
                 for (int c = 0; c < DP / 8; ++c) {
                     const uint32_t e[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
@@ -587,11 +653,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
                         const float2 f = widen_q(e[k], bf16);
-                        o[k] = pack_half(scalbnf(f.x, shift), scalbnf(f.y, shift));
+                        o[k] = pack_half(f.x * up.x * up.y, f.y * up.x * up.y);
                     }
                     sts16(smem_u32(sm.q[s][c >> 3]) + tile_at(row, c & 7), o[0], o[1], o[2], o[3]);
                 }
-                factor = scalbnf(a.scale * 1.44269504088896341f, -shift);
+                factor = a.scale * 1.44269504088896341f * down.x * down.y;
                 fence_operands();
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.q_full[s]));
@@ -599,102 +665,127 @@ __global__ void __launch_bounds__(kThreads, 1)
             for (int st = 0; st < steps; ++st) {
                 const int t = two ? st : 2 * st + s;  // of the segment
                 const int at = (n + t) & (kScaleRing - 1), tok0 = (w.t0 + t) * kTok;
+                const int b = count & 1;
+                const uint32_t col_s = tmem + lanes + kColS + 128 * s + 64 * b;
                 ok = ptx::mbar_wait(smem_u32(&sm.scale_full[at]), ((n + t) / kScaleRing) & 1, err) &&
-                     ptx::mbar_wait(smem_u32(&sm.s_full[s]), s_phase, err);
-                s_phase ^= 1;
+                     ptx::mbar_wait(smem_u32(&sm.s_full[s][b]), (count >> 1) & 1, err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
                 ptx::tc_fence_after();
-                const uint32_t valid = sm.valid[at];
-                const bool whole = tok0 + kTok <= all_see && valid == 255u;
-                // a pass for the maximum
-                float mx = -INFINITY;
+                if (!idle) {
+                    const uint32_t valid = sm.valid[at];
+                    const bool whole = tok0 + kTok <= all_see && valid == 15u;
+                    uint32_t v[64];  // the row's scores, as they are
+                    const float2* const scales = sm.scale[at];
+                    // 16 tokens that share their scales: the columns with (j mod 8) / 2 alike.  A factor is never
+                    // 0: a hidden token's score is -inf.
+                    float fk[4], vs[4], mx = -INFINITY, vmost = 0.0f;
+                    if (whole && page_size >= 64) {
+                        // one page, no token hidden: the loads bring the maximum with them
+                        const float2 x = scales[0];
+                        const float f = x.x * factor;
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32];
-                    ptx::tmem_ld_32(col_s + 32 * c, v);
-                    float fk[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) fk[k] = sm.scale[at][(c >> 1) * 4 + k].x * factor;
-                    if (whole) {
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) mx = fmaxf(mx, __uint_as_float(v[j]) * fk[(j & 7) >> 1]);
+                        for (int k = 0; k < 4; ++k) {
+                            fk[k] = f <= 1e-37f ? 1e-37f : f;
+                            vs[k] = x.y;
+                        }
+                        vmost = x.y <= 3.402823466e38f ? fmaxf(0.0f, x.y) : 0.0f;
+                        tmem_ldmax_64(col_s, v, mx);
+                        mx *= fk[0];
                     } else {
+                        ptx::tmem_ld_32x2(col_s, col_s + 32,
+                                          *reinterpret_cast<uint32_t(*)[32]>(v), *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+                        if (!whole) {
 #pragma unroll
-                        for (int j = 0; j < 32; ++j) {
-                            const int tok = (c >> 1) * 64 + (j & 7) * 8 + (c & 1) * 4 + (j >> 3);
-                            const bool seen = tok0 + tok < sees && ((valid >> (tok >> 4)) & 1u);
-                            mx = fmaxf(mx, seen ? __uint_as_float(v[j]) * fk[(j & 7) >> 1] : -INFINITY);
+                            for (int j = 0; j < 64; ++j) {
+                                const int tok = (j & 7) * 8 + (j >> 3);
+                                const bool seen = tok0 + tok < sees && ((valid >> (tok >> 4)) & 1u);
+                                v[j] = seen ? v[j] : 0xff800000u;
+                            }
+                        }
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            // scales that are not finite do not reach rows that see none of their tokens
+                            const float2 x = scales[k];
+                            const bool seen = whole || (tok0 + 16 * k < sees && ((valid >> k) & 1u));
+                            const float f = x.x * factor;
+                            fk[k] = f <= 1e-37f || !seen ? 1e-37f : f;
+                            vs[k] = seen ? x.y : 0.0f;
+                            float g0 = -INFINITY, g1 = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < 8; i += 2) {
+                                const int j = k * 2 + 8 * i;
+                                g0 = fmaxf(fmaxf(g0, __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
+                                g1 = fmaxf(fmaxf(g1, __uint_as_float(v[j + 8])), __uint_as_float(v[j + 9]));
+                            }
+                            mx = fmaxf(mx, fmaxf(g0, g1) * fk[k]);
+                            vmost = x.y <= 3.402823466e38f ? fmaxf(vmost, x.y) : vmost;  // c is the warp's, not the row's
                         }
                     }
-                }
-                float keep = 1.0f;
-                if (mx > mref + kHeadroom || mref == -INFINITY) {
-                    keep = mref == -INFINITY ? 0.0f : exp2_fast(mref - mx);
-                    mref = mx;
-                    l *= keep;
-                }
-                float vmost = 0.0f;
-#pragma unroll
-                for (int k = 0; k < 8; ++k) {
-                    const float size = fabsf(sm.scale[at][k].y);
-                    vmost = size <= 3.402823466e38f ? fmaxf(vmost, size) : vmost;
-                }
-                if (vmost > cref) {
-                    const float to = fminf(2.0f * vmost, 3.402823466e38f);
-                    keep *= cref / to;
-                    cref = to;
-                }
-                // the step's S came after the step before's product: O is at rest
-                if (st > 0 && __any_sync(0xffffffffu, keep != 1.0f)) {
-#pragma unroll
-                    for (int c = 0; c < DP / 32; ++c) {
-                        uint32_t v[32];
-                        ptx::tmem_ld_32(col_o + 32 * c, v);
-#pragma unroll
-                        for (int j = 0; j < 32; ++j) v[j] = __float_as_uint(__uint_as_float(v[j]) * keep);
-                        ptx::tmem_st_32(col_o + 32 * c, v);
+                    // both moves are by powers of two, exact for what has been summed and rounded
+                    float keep = 1.0f;
+                    if (mx > mref + kHeadroom || mref == -INFINITY) {
+                        const float to = ceilf(mx);
+                        keep = mref == -INFINITY ? 0.0f : exp2_fast(mref - to);
+                        mref = to;
+                        l *= keep;
                     }
-                }
-                const float base = mref == -INFINITY ? 0.0f : mref;
-                const float inv = cref > 0.0f ? kWeightTop / cref : 0.0f;
-                float sum = 0.0f;
-                // a pass for the weights, which take the place of scores that have been read
+                    if (vmost > cref) {
+                        const float to = __int_as_float(min((__float_as_int(vmost) & 0x7f800000) + (1 << 23), 0x7f000000));
+                        keep *= cref / to;
+                        cref = to;
+                    }
+                    if (st > 0 && __any_sync(0xffffffffu, keep != 1.0f)) {
+                        // O is at rest once the step before is in it: this step's product waits for its weights.
+                        // (The step before that is: this step's scores came after it.  So the phase is not taken
+                        // for one of two steps ago.)
+                        ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.o_step[s]), (count - 1) & 1, err));
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < DP / 16; ++c) {
+                            uint32_t o[16];
+                            ptx::tmem_ld_16(col_o + 16 * c, o);
 #pragma unroll
-                for (int c = 0; c < 4; ++c) {
-                    uint32_t v[32], p[16];
-                    ptx::tmem_ld_32(col_s + 32 * c, v);
-                    float fk[4], wt[4];
+                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+                            tmem_st_16(col_o + 16 * c, o);
+                        }
+                    }
+                    const float base = mref == -INFINITY ? 0.0f : mref;
+                    const float inv = cref > 0.0f ? kWeightTop / cref : 0.0f;
+                    // a group's weight goes into the exponent, and out of its sum again; 2^-60 stands in for
+                    // smaller ones (the fp16 weights are 0 then)
+                    float minus[4], out_of[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float2 x = sm.scale[at][(c >> 1) * 4 + k];
-                        fk[k] = x.x * factor;
-                        wt[k] = x.y * inv;
+                        const float wt = vs[k] * inv;
+                        const float of = wt <= 8.67361738e-19f ? 8.67361738e-19f : wt;
+                        minus[k] = __log2f(of) - base;
+                        out_of[k] = __frcp_rn(of);
                     }
-                    float part = 0.0f;
+                    // the weights take the place of the scores
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                    for (int j = 0; j < 32; j += 2) {
-                        const int k = (j & 7) >> 1;
-                        float e0 = exp2_fast(fmaf(__uint_as_float(v[j]), fk[k], -base));
-                        float e1 = exp2_fast(fmaf(__uint_as_float(v[j + 1]), fk[k], -base));
-                        float w0 = e0 * wt[k], w1 = e1 * wt[k];
-                        if (!whole) {
-                            const int tok = (c >> 1) * 64 + (j & 7) * 8 + (c & 1) * 4 + (j >> 3);
-                            const bool page = (valid >> (tok >> 4)) & 1u;
-                            if (!(tok0 + tok < sees && page)) e0 = w0 = 0.0f;
-                            if (!(tok0 + tok + 8 < sees && page)) e1 = w1 = 0.0f;
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t p[16];
+#pragma unroll
+                        for (int i = 0; i < 16; ++i) {
+                            const int j = 32 * c + 2 * i, k = i & 3;
+                            const float e0 = exp2_fast(fmaf(__uint_as_float(v[j]), fk[k], minus[k]));
+                            const float e1 = exp2_fast(fmaf(__uint_as_float(v[j + 1]), fk[k], minus[k]));
+                            sum[k] += e0 + e1;
+                            p[i] = pack_half(e0, e1);
                         }
-                        part += e0 + e1;
-                        p[j >> 1] = pack_half(w0, w1);
+                        tmem_st_16(col_s + 16 * c, p);
                     }
-                    sum += part;
-                    tmem_st_16(col_s + 16 * c, p);
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) l = fmaf(sum[k], out_of[k], l);
                 }
-                l += sum;
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.p_full[s]));
+                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.p_full[s][b]));
+                ++count;
             }
             if (!ok) break;
             if (steps > 0) {
@@ -708,98 +799,92 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const bool begins = w.t0 == 0, ends = w.t1 == w.x.tiles, cut = !(begins && ends);
                 const bool join = !two && tiles > 1;  // the odd tiles' sums go to the even ones'
                 const bool nan = *reinterpret_cast<volatile int*>(&sm.nan_seen) != 0;
-                constexpr int H = DP / 2;  // dimensions that fit the idle q tile of stream 1
-                float* const box = reinterpret_cast<float*>(&sm.q[1][0][0]);
-                // stream 1's maxima and sums, in the other q tile: the last product of stream 1 came after every
-                // S of the item
-                float2* const ml = reinterpret_cast<float2*>(&sm.q[0][0][0]);
                 if (s == 1 && !two) {
                     if (join) {
-                        const float f = cref / kWeightTop;
-                        for (int part = 0; part < 2; ++part) {
-                            if (part) ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.merge_empty), merge_phase, err));
-                            if (!ok) break;
-                            if (part) merge_phase ^= 1;
-#pragma unroll
-                            for (int c = 0; c < H / 32; ++c) {
-                                uint32_t v[32];
-                                ptx::tmem_ld_32(col_o + part * H + 32 * c, v);
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) box[(32 * c + j) * kM + row] = __uint_as_float(v[j]) * f;
-                            }
-                            if (part == 0) ml[row] = make_float2(mref, l);
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.merge_full));
-                        }
-                        if (!ok) break;
+                        // stream 0's warp of the same rows reads this stream's O, and beside it, in the columns of
+                        // scores that are no longer needed, its maximum, sum and scale
+                        uint32_t x[16] = {__float_as_uint(mref), __float_as_uint(l), __float_as_uint(cref / kWeightTop)};
+                        tmem_st_16(tmem + lanes + kColS + 128, x);
+                        ptx::tmem_wait_st();
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.merge_full));
                         ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.merge_empty), merge_phase, err));
                         merge_phase ^= 1;
                         if (!ok) break;
+                        ptx::tc_fence_after();
                     }
                 } else {
                     float f0 = cref / kWeightTop, f1 = 0.0f, m = mref;
                     const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
                     float* const piece = pieces + static_cast<int64_t>(slot) * piece_rows * (DP + 4);
                     const int64_t t = w.x.r.row0 + i;
-                    for (int part = 0; part < 2; ++part) {
-                        if (join) {
-                            ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.merge_full), merge_phase, err));
-                            merge_phase ^= 1;
-                            if (!ok) break;
-                            if (part == 0) {
-                                const float2 o = ml[row];
-                                m = fmaxf(mref, o.x);
-                                const float base = m == -INFINITY ? 0.0f : m;
-                                const float k0 = exp2_fast(mref - base), k1 = exp2_fast(o.x - base);
-                                // a side without weights has no part; NaN sums stay
-                                f0 = l == 0.0f ? 0.0f : f0 * k0;
-                                f1 = o.y == 0.0f ? 0.0f : k1;
-                                l = (l == 0.0f ? 0.0f : l * k0) + (o.y == 0.0f ? 0.0f : o.y * k1);
+                    if (join) {
+                        ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.merge_full), merge_phase, err));
+                        merge_phase ^= 1;
+                        if (!ok) break;
+                        ptx::tc_fence_after();
+                        uint32_t x[16];
+                        ptx::tmem_ld_16(tmem + lanes + kColS + 128, x);
+                        const float m1 = __uint_as_float(x[0]), l1 = __uint_as_float(x[1]);
+                        m = fmaxf(mref, m1);
+                        const float base = m == -INFINITY ? 0.0f : m;
+                        const float k0 = exp2_fast(mref - base), k1 = exp2_fast(m1 - base);
+                        // a side without weights has no part; NaN sums stay
+                        f0 = l == 0.0f ? 0.0f : f0 * k0;
+                        f1 = l1 == 0.0f ? 0.0f : __uint_as_float(x[2]) * k1;
+                        l = (l == 0.0f ? 0.0f : l * k0) + (l1 == 0.0f ? 0.0f : l1 * k1);
+                    }
+                    const float g = cut ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+#pragma unroll 1
+                    for (int c = 0; c < DP / 16; ++c) {
+                        uint32_t v[16], y[16];
+                        if (join) ptx::tmem_ld_16x2(col_o + 16 * c, col_o + 128 + 16 * c, v, y);
+                        else ptx::tmem_ld_16(col_o + 16 * c, v);
+#pragma unroll
+                        for (int e = 0; e < 2; ++e) {
+                            const int d = 16 * c + 8 * e;
+                            float f[8];
+#pragma unroll
+                            for (int j = 0; j < 8; ++j) {
+                                float o = f0 == 0.0f ? 0.0f : __uint_as_float(v[8 * e + j]) * f0;
+                                if (join && f1 != 0.0f) o = fmaf(__uint_as_float(y[8 * e + j]), f1, o);
+                                f[j] = o * g;
                             }
-                        }
-                        const float g = cut ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
-#pragma unroll
-                        for (int c = 0; c < H / 32; ++c) {
-                            uint32_t v[32];
-                            ptx::tmem_ld_32(col_o + part * H + 32 * c, v);
-#pragma unroll
-                            for (int e = 0; e < 4; ++e) {
-                                const int d = part * H + 32 * c + 8 * e;
-                                float f[8];
+                            if (nan && live && d < a.dim) {
+                                // NaN codes that were set apart: those of tokens that this row sees
+                                uint32_t hit = 0;
+                                for (int pos = max(all_see, w.t0 * kTok); pos < min(sees, w.t1 * kTok); ++pos) {
+                                    const int pg = a.table[w.x.b * a.stride + (pos >> a.page_shift)];
+                                    if (pg < 0 || pg >= a.pages) continue;
+                                    const uint2 x = *reinterpret_cast<const uint2*>(
+                                        a.v_cache + (((static_cast<int64_t>(pg) * a.heads + w.x.head) << a.page_shift) +
+                                                     (pos & (page_size - 1))) * a.dim + d);
+                                    const uint32_t lo = __vcmpeq4(x.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                    const uint32_t hi = __vcmpeq4(x.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                    hit |= (lo & 0x01020408u) | (hi & 0x10204080u);
+                                }
+                                // bytes of lo: bits 3, 10, 17, 24; of hi: 7, 14, 21, 28 (dimension 0 lowest)
 #pragma unroll
                                 for (int j = 0; j < 8; ++j) {
-                                    float o = l == 0.0f ? 0.0f : __uint_as_float(v[8 * e + j]) * f0;
-                                    if (join && f1 != 0.0f) o = fmaf(box[(32 * c + 8 * e + j) * kM + row], f1, o);
-                                    f[j] = o * g;
-                                }
-                                if (nan && live) {
-                                    // NaN codes that were set apart: those of tokens that this row sees
-                                    for (int pos = max(all_see, w.t0 * kTok); pos < min(sees, w.t1 * kTok); ++pos) {
-                                        const int pg = a.table[w.x.b * a.stride + (pos >> a.page_shift)];
-                                        if (pg < 0 || pg >= a.pages || d >= a.dim) continue;
-                                        const uint8_t* const code =
-                                            a.v_cache + (((static_cast<int64_t>(pg) * a.heads + w.x.head) << a.page_shift) +
-                                                         (pos & (page_size - 1))) * a.dim + d;
-#pragma unroll
-                                        for (int j = 0; j < 8; ++j)
-                                            if ((code[j] & 0x7f) == 0x7f) f[j] = __int_as_float(0x7fffffff);
-                                    }
-                                }
-                                if (live && cut) {
-                                    float4* const to = reinterpret_cast<float4*>(piece + in_item * DP + d);
-                                    to[0] = make_float4(f[0], f[1], f[2], f[3]);
-                                    to[1] = make_float4(f[4], f[5], f[6], f[7]);
-                                } else if (live && d < a.dim) {
-                                    store8(a.out, t * a.out_token_stride + h * a.out_head_stride + d, f, bf16, out_wide);
+                                    const int bit = j < 4 ? 3 + 7 * j : 7 + 7 * (j - 4);
+                                    if ((hit >> bit) & 1u) f[j] = __int_as_float(0x7fffffff);
                                 }
                             }
-                        }
-                        if (join) {
-                            __syncwarp();
-                            if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.merge_empty));
+                            if (live && cut) {
+                                float4* const to = reinterpret_cast<float4*>(piece + in_item * DP + d);
+                                to[0] = make_float4(f[0], f[1], f[2], f[3]);
+                                to[1] = make_float4(f[4], f[5], f[6], f[7]);
+                            } else if (live && d < a.dim) {
+                                store8(a.out, t * a.out_token_stride + h * a.out_head_stride + d, f, bf16, out_wide);
+                            }
                         }
                     }
-                    if (!ok) break;
+                    if (join) {
+                        ptx::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.merge_empty));
+                    }
                     if (live && cut) {
                         float* const sums = piece + static_cast<int64_t>(piece_rows) * DP + 2 * in_item;
                         sums[0] = m;
