@@ -39,8 +39,8 @@ constexpr int kRaw = 6;         // raw tiles of one operand
 constexpr int kKeys = 3, kValues = 4;  // operand tiles
 constexpr int kAhead = 2;       // steps of a stream whose scores are computed ahead
 constexpr int kScaleRing = 16;  // tiles whose scales are kept
-constexpr float kHeadroom = 8.0f;
-constexpr float kWeightTop = 128.0f;  // 2^7 * 2^8 at the scale c: 2^15
+constexpr float kLogTop = 15.0f, kLogStart = 7.0f;  // log2 of the largest weight, and of a maximum's when it is set
+constexpr float kNothing = -1048576.0f;            // a row's reference before it has seen a token
 
 // warps
 constexpr int kConvert = 8, kLoad = 12, kMma = 13, kBusy = 15;  // an issuer of MMAs for each stream
@@ -58,7 +58,7 @@ struct Smem {
     uint8_t k[kKeys][DP / 64][kTok * 128];
     uint8_t v[kValues][DP * 128];
     uint8_t raw[kRaw][kTok * DP];
-    float2 scale[kScaleRing][4];  // of 16 tokens each: keys', values'
+    float4 scale[kScaleRing][4];  // of 16 tokens each: keys', values', log2 and reciprocal of the latter
     uint32_t valid[kScaleRing];
     uint64_t raw_full[kRaw], raw_empty[kRaw], scale_full[kScaleRing];
     uint64_t k_full[kKeys], k_empty[kKeys], v_full[kValues], v_empty[kValues];
@@ -108,25 +108,26 @@ __device__ long long steps_of_head(const Request& r, int group) {
     return s;
 }
 
-// Walks a block's segments: an item and a range of its tiles.
+// Walks a block's segments: an item and a range of its tiles.  The range's end
+// stays in shared memory.
 struct Walk {
     Item x;
     int t0, t1;
     bool last;
-    int end[4];
-    __device__ __forceinline__ void place(const AttentionArgs& a, int group, int tile) {
+    const int* end;
+    __device__ __forceinline__ void place(int group, int tile) {
         shape(x, group);
         last = x.b == end[0] && x.head == end[1] && x.item == end[2];
         t0 = tile;
         t1 = last ? end[3] : x.tiles;
     }
     __device__ __forceinline__ void begin(const AttentionArgs& a, int group, const int* from, const int* to) {
-        for (int i = 0; i < 4; ++i) end[i] = to[i];
+        end = to;
         x.b = from[0];
         x.head = from[1];
         x.item = from[2];
         x.r = request_of(a, x.b);
-        place(a, group, from[3]);
+        place(group, from[3]);
     }
     __device__ __forceinline__ void next(const AttentionArgs& a, int group) {
         if (++x.item >= items_of(x.r, group)) {
@@ -138,7 +139,7 @@ struct Walk {
                 } while (x.r.n == 0);  // the end's request has rows
             }
         }
-        place(a, group, 0);
+        place(group, 0);
     }
 };
 
@@ -151,6 +152,14 @@ __device__ __forceinline__ uint2 lds8(uint32_t at) {
     uint2 v;
     asm volatile("ld.shared.v2.u32 {%0, %1}, [%2];" : "=r"(v.x), "=r"(v.y) : "r"(at));
     return v;
+}
+__device__ __forceinline__ uint32_t lds4(uint32_t at) {
+    uint32_t v;
+    asm volatile("ld.shared.u32 %0, [%1];" : "=r"(v) : "r"(at));
+    return v;
+}
+__device__ __forceinline__ void sts8(uint32_t at, uint32_t x, uint32_t y) {
+    asm volatile("st.shared.v2.u32 [%0], {%1, %2};" ::"r"(at), "r"(x), "r"(y) : "memory");
 }
 __device__ __forceinline__ void sts16(uint32_t at, uint32_t x, uint32_t y, uint32_t z, uint32_t w) {
     asm volatile("st.shared.v4.u32 [%0], {%1, %2, %3, %4};" ::"r"(at), "r"(x), "r"(y), "r"(z), "r"(w) : "memory");
@@ -185,39 +194,21 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&v)[1
         : "memory");
 }
 
-// 64 columns of this thread's lane, and their maximum, which the loads take
+// 32 columns of this thread's lane, and their maximum, which the loads take
 // (loads and wait in one statement, so that no use comes before the wait).
-__device__ __forceinline__ void tmem_ldmax_64(uint32_t taddr, uint32_t (&v)[64], float& mx) {
-    float a, b, c, d;
+__device__ __forceinline__ void tmem_ldmax_32(uint32_t taddr, uint32_t (&v)[32], float& mx) {
+    float a, b;
     asm volatile(
-        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, %64, [%68];\n\t"
-        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %65, [%69];\n\t"
-        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47}, %66, [%70];\n\t"
-        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, %67, [%71];\n\t"
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, %32, [%34];\n\t"
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %33, [%35];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
           "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
-          "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]),
-          "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]),
-          "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
-          "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63]),
-          "=f"(a), "=f"(b), "=f"(c), "=f"(d)
-        : "r"(taddr), "r"(taddr + 16), "r"(taddr + 32), "r"(taddr + 48)
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=f"(a), "=f"(b)
+        : "r"(taddr), "r"(taddr + 16)
         : "memory");
-    mx = fmaxf(fmaxf(a, b), fmaxf(c, d));
-}
-
-// Registers of a warpgroup's threads: 256 threads of 152 and 256 of 104 are the
-// 512 of 128 that the block is launched with.
-template <int N>
-__device__ __forceinline__ void more_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void fewer_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+    mx = fmaxf(a, b);
 }
 
 // 8 neighbouring dimensions of one row to the output.
@@ -345,19 +336,15 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    if (warp >= kBusy) {
-        fewer_registers<104>();
-        return;
-    }
+    if (warp >= kBusy) return;
 
-    Walk w;
-    w.begin(a, group, sm.start, sm.end);
     bool ok = true;
     const int page_size = 1 << a.page_shift;
 
     if (warp == kLoad) {
         // ------------------------------------------------------- raw tiles --
-        fewer_registers<104>();
+        Walk w;
+        w.begin(a, group, sm.start, sm.end);
         const int box = min(page_size, 64);
         int slot = 0;
         uint32_t phase = 1;  // an empty ring
@@ -371,7 +358,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             return p >= 0 && p < a.pages ? p : -1;
         };
         auto publish = [&](int tile) {
-            if (lane < 4) sm.scale[tile & (kScaleRing - 1)][lane] = scale;
+            if (lane < 4)
+                sm.scale[tile & (kScaleRing - 1)][lane] = make_float4(scale.x, scale.y, __log2f(scale.y), __fdividef(1.0f, scale.y));
             __syncwarp();
             if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.scale_full[tile & (kScaleRing - 1)]));
         };
@@ -422,7 +410,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (ok && pending) publish(n - 1);
     } else if (warp >= kConvert && warp < kConvert + 4) {
         // ----------------------------------------------- codes to operands --
-        fewer_registers<104>();
+        Walk w;
+        w.begin(a, group, sm.start, sm.end);
         const int ct = tid - 32 * kConvert;
         int slot = 0;
         uint32_t raw_phase = 0;
@@ -449,7 +438,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 {
                     const uint32_t src = smem_u32(sm.raw[slot]), dst = smem_u32(sm.k[kb][0]);
                     constexpr int C = DP / 16;  // chunks of a token
-#pragma unroll
+#pragma unroll 1
                     for (int i = 0; i < kTok * C / 128; ++i) {
                         const int item = ct + 128 * i, c = item % C, tok = item / C;
                         const uint4 x = lds16(src + raw_at<DP>(tok, c));
@@ -470,6 +459,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 }
                 fence_operands();
                 release();
+                // the tile's scales too are there before its scores
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.scale_full[n & (kScaleRing - 1)]),
+                                                            (n / kScaleRing) & 1, err));
+                if (!ok) break;
                 if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.k_full[kb]));
                 if (++kb == kKeys) {
                     kb = 0;
@@ -485,44 +478,42 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const uint32_t src = smem_u32(sm.raw[slot]), dst = smem_u32(sm.v[vb]);
                     const uint32_t valid = sm.valid[n & (kScaleRing - 1)];
                     const int first = t * kTok;
-                    const bool whole = first + kTok <= all_see && valid == 15u;
                     const int c8 = ct & 7, d8 = ct >> 3;  // tokens 8 i + c8; dimensions 8 d8 ..
-                    if (d8 < DP / 8) {
-                        uint2 x[8];
+                    if (first + kTok > all_see || valid != 15u) {
+                        // tokens that no row sees count as 0; of those that only some rows see, NaN codes are set
+                        // apart.  A thread mends the codes that it will read.
+                        bool nan = false;
+#pragma unroll 1
+                        for (int i = 0; d8 < DP / 8 && i < 8; ++i) {
+                            const int tok = 8 * i + c8, pos = first + tok;
+                            const uint32_t at = src + raw_at<DP>(tok, d8 >> 1) + (d8 & 1) * 8;
+                            const uint2 x = lds8(at);
+                            const bool live = pos < w.x.r.length && ((valid >> (tok >> 4)) & 1u);
+                            const uint32_t some = pos >= all_see ? 0xffffffffu : 0u;
+                            const uint32_t nx = __vcmpeq4(x.x & 0x7f7f7f7fu, 0x7f7f7f7fu) & some;
+                            const uint32_t ny = __vcmpeq4(x.y & 0x7f7f7f7fu, 0x7f7f7f7fu) & some;
+                            nan = nan || (live && (nx | ny));
+                            sts8(at, live ? x.x & ~nx : 0u, live ? x.y & ~ny : 0u);
+                        }
+                        if (nan) sm.nan_seen = 1;
+                    }
+#pragma unroll 1
+                    for (int h = 0; d8 < DP / 8 && h < 2; ++h) {
+                        uint32_t x[8], p[4][4];  // [dimension][pair of tokens]
 #pragma unroll
-                        for (int i = 0; i < 8; ++i) x[i] = lds8(src + raw_at<DP>(8 * i + c8, d8 >> 1) + (d8 & 1) * 8);
-                        if (!whole) {
-                            bool nan = false;
+                        for (int i = 0; i < 8; ++i) x[i] = lds4(src + raw_at<DP>(8 * i + c8, d8 >> 1) + (d8 & 1) * 8 + 4 * h);
 #pragma unroll
-                            for (int i = 0; i < 8; ++i) {
-                                const int tok = 8 * i + c8, pos = first + tok;
-                                const bool live = pos < w.x.r.length && ((valid >> (tok >> 4)) & 1u);
-                                // of a token that only some rows see, NaN codes are set apart
-                                const bool some = pos >= all_see;
-                                const uint32_t nx = __vcmpeq4(x[i].x & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                const uint32_t ny = __vcmpeq4(x[i].y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                nan = nan || (live && some && (nx | ny));
-                                x[i].x = live ? (some ? x[i].x & ~nx : x[i].x) : 0u;
-                                x[i].y = live ? (some ? x[i].y & ~ny : x[i].y) : 0u;
-                            }
-                            if (nan) sm.nan_seen = 1;
+                        for (int i = 0; i < 4; ++i) {
+                            const uint32_t a01 = __byte_perm(x[2 * i], x[2 * i + 1], 0x5140);
+                            const uint32_t a23 = __byte_perm(x[2 * i], x[2 * i + 1], 0x7362);
+                            p[0][i] = widen2(a01);
+                            p[1][i] = widen2(a01 >> 16);
+                            p[2][i] = widen2(a23);
+                            p[3][i] = widen2(a23 >> 16);
                         }
 #pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t p[4][4];  // [dimension][pair of tokens]
-#pragma unroll
-                            for (int i = 0; i < 4; ++i) {
-                                const uint32_t u = h ? x[2 * i].y : x[2 * i].x, v = h ? x[2 * i + 1].y : x[2 * i + 1].x;
-                                const uint32_t a01 = __byte_perm(u, v, 0x5140), a23 = __byte_perm(u, v, 0x7362);
-                                p[0][i] = widen2(a01);
-                                p[1][i] = widen2(a01 >> 16);
-                                p[2][i] = widen2(a23);
-                                p[3][i] = widen2(a23 >> 16);
-                            }
-#pragma unroll
-                            for (int j = 0; j < 4; ++j)
-                                sts16(dst + tile_at(8 * d8 + 4 * h + j, c8), p[j][0], p[j][1], p[j][2], p[j][3]);
-                        }
+                        for (int j = 0; j < 4; ++j)
+                            sts16(dst + tile_at(8 * d8 + 4 * h + j, c8), p[j][0], p[j][1], p[j][2], p[j][3]);
                     }
                 }
                 fence_operands();
@@ -534,7 +525,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
     } else if (warp >= kMma) {
         // ------------------------------------------------------------ MMAs --
-        fewer_registers<104>();
+        Walk w;
+        w.begin(a, group, sm.start, sm.end);
         if (lane == 0) {
             constexpr uint32_t kIdS = ptx::f16_idesc(kM, kTok, false), kIdO = ptx::f16_idesc(kM, DP, false);
             const int s = warp - kMma;
@@ -559,8 +551,16 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) return;
                     ptx::tc_fence_after();
                     // the buffer's weights of two steps ago were multiplied by an instruction before this one
-                    ptx::mma_kchain<DP / 16>(col_s + 64 * b, smem_u32(sm.q[s][0]), kM * 128, smem_u32(sm.k[kb][0]),
-                                             kTok * 128, DP / 16, kIdS);
+                    uint64_t qd = ptx::sw128_kmajor_desc(smem_u32(sm.q[s][0]));
+                    uint64_t kd = ptx::sw128_kmajor_desc(smem_u32(sm.k[kb][0]));
+#pragma unroll 1
+                    for (int atom = 0; atom < DP / 64; ++atom) {  // 64 dimensions: 4 steps of 32 bytes
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            ptx::mma_f16(col_s + 64 * b, qd + 2 * k, kd + 2 * k, kIdS, atom > 0 || k != 0);
+                        qd += kM * 128 / 16;
+                        kd += kTok * 128 / 16;
+                    }
                     ptx::mma_commit(smem_u32(&sm.s_full[s][b]));
                     done(&sm.k_empty[kb]);
                     ++scored;
@@ -577,11 +577,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (!ok) break;
                     ++summed;
                     ptx::tc_fence_after();
-                    const uint32_t v0 = smem_u32(sm.v[vb]);
+                    const uint64_t vd = ptx::sw128_kmajor_desc(smem_u32(sm.v[vb]));
 #pragma unroll
                     for (int k = 0; k < kTok / 16; ++k)
-                        mma_f16_ts(col_o, col_s + 64 * b + 8 * k, ptx::sw128_kmajor_desc(v0 + k * 32), kIdO,
-                                   i > 0 || k != 0);
+                        mma_f16_ts(col_o, col_s + 64 * b + 8 * k, vd + 2 * k, kIdO, i > 0 || k != 0);
                     ptx::mma_commit(smem_u32(&sm.o_step[s]));
                     if (i + 1 == steps) ptx::mma_commit(smem_u32(&sm.o_full[s]));
                     done(&sm.v_empty[vb]);
@@ -595,7 +594,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // --------------------------------------------------------- softmax --
-        more_registers<152>();
+        Walk w;
+        w.begin(a, group, sm.start, sm.end);
         const int s = warp >> 2, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
         const uint32_t col_o = tmem + lanes + kColO + 128 * s;
@@ -612,43 +612,39 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int sees = live ? w.x.r.length - w.x.r.n + i + 1 : 0;
             const int all_see = w.x.r.length - w.x.r.n + (w.x.item * kItemRows) / group + 1;
             const bool idle = __ballot_sync(0xffffffffu, live) == 0;  // no row of this warp's: its weights do not matter
-            float factor = 0.0f, mref = -INFINITY, l = 0.0f, cref = 0.0f;
+            float factor = 0.0f, ref = kNothing, l = 0.0f, cref = 0.0f;
             if (steps > 0) {
                 // the row of q, scaled to fp16's range
                 const uint16_t* const src = static_cast<const uint16_t*>(a.q) + (w.x.r.row0 + i) * a.q_token_stride +
                                             h * a.q_head_stride;
-                uint4 x[DP / 8];
-                if (q_wide) {
+                auto load = [&](int c) {  // 8 dimensions
+                    if (!live || c * 8 >= a.dim) return make_uint4(0, 0, 0, 0);
+                    if (q_wide) return __ldg(reinterpret_cast<const uint4*>(src) + c);
+                    uint32_t e[4];
 #pragma unroll
-                    for (int c = 0; c < DP / 8; ++c)
-                        x[c] = live && c * 8 < a.dim ? __ldg(reinterpret_cast<const uint4*>(src) + c) : make_uint4(0, 0, 0, 0);
-                } else {
-#pragma unroll
-                    for (int c = 0; c < DP / 8; ++c) {
-                        uint32_t e[4] = {0, 0, 0, 0};
-                        if (live && c * 8 < a.dim) {
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                e[k] = src[8 * c + 2 * k] | (static_cast<uint32_t>(src[8 * c + 2 * k + 1]) << 16);
-                        }
-                        x[c] = make_uint4(e[0], e[1], e[2], e[3]);
-                    }
-                }
+                    for (int k = 0; k < 4; ++k)
+                        e[k] = src[8 * c + 2 * k] | (static_cast<uint32_t>(src[8 * c + 2 * k + 1]) << 16);
+                    return make_uint4(e[0], e[1], e[2], e[3]);
+                };
+                // two passes of little code, the second from L1 (code that runs once an item is fetched each time)
                 float most = 0.0f;
+#pragma unroll 1
+                for (int c = 0; c < DP / 8; c += 4) {
+                    uint4 x[4];
 #pragma unroll
-                for (int c = 0; c < DP / 8; ++c) {
-                    const uint32_t e[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+                    for (int k = 0; k < 4; ++k) x[k] = load(c + k);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float2 f = widen_q(e[k], bf16);
+                    for (int k = 0; k < 16; ++k) {
+                        const float2 f = widen_q(reinterpret_cast<const uint32_t*>(x)[k], bf16);
                         most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
                     }
                 }
                 const int shift = row_shift(most);
                 const float2 up = power_of_two(shift), down = power_of_two(-shift);
-#pragma unroll
+#pragma unroll 1
                 for (int c = 0; c < DP / 8; ++c) {
-                    const uint32_t e[4] = {x[c].x, x[c].y, x[c].z, x[c].w};
+                    const uint4 x = load(c);
+                    const uint32_t e[4] = {x.x, x.y, x.z, x.w};
                     uint32_t o[4];
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
@@ -662,124 +658,134 @@ __global__ void __launch_bounds__(kThreads, 1)
                 __syncwarp();
                 if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.q_full[s]));
             }
+            // O times `keep` (1 in rows that need none).  It is at rest once the step before is in it: this step's
+            // product waits for its weights.  (The step before that is: this step's scores came after it.  So the
+            // phase is not taken for one of two steps ago.)
+            auto rescale = [&](float keep) {
+                if (!__all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.o_step[s]), (count - 1) & 1, err))) return false;
+                ptx::tc_fence_after();
+#pragma unroll 1
+                for (int c = 0; c < DP / 16; ++c) {
+                    uint32_t o[16];
+                    ptx::tmem_ld_16(col_o + 16 * c, o);
+#pragma unroll
+                    for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
+                    tmem_st_16(col_o + 16 * c, o);
+                }
+                return true;
+            };
+#pragma unroll 1
             for (int st = 0; st < steps; ++st) {
                 const int t = two ? st : 2 * st + s;  // of the segment
                 const int at = (n + t) & (kScaleRing - 1), tok0 = (w.t0 + t) * kTok;
                 const int b = count & 1;
                 const uint32_t col_s = tmem + lanes + kColS + 128 * s + 64 * b;
-                ok = ptx::mbar_wait(smem_u32(&sm.scale_full[at]), ((n + t) / kScaleRing) & 1, err) &&
-                     ptx::mbar_wait(smem_u32(&sm.s_full[s][b]), (count >> 1) & 1, err);
-                ok = __all_sync(0xffffffffu, ok);
+                ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.s_full[s][b]), (count >> 1) & 1, err));
                 if (!ok) break;
                 ptx::tc_fence_after();
                 if (!idle) {
                     const uint32_t valid = sm.valid[at];
                     const bool whole = tok0 + kTok <= all_see && valid == 15u;
-                    uint32_t v[64];  // the row's scores, as they are
-                    const float2* const scales = sm.scale[at];
-                    // 16 tokens that share their scales: the columns with (j mod 8) / 2 alike.  A factor is never
-                    // 0: a hidden token's score is -inf.
-                    float fk[4], vs[4], mx = -INFINITY, vmost = 0.0f;
-                    if (whole && page_size >= 64) {
-                        // one page, no token hidden: the loads bring the maximum with them
-                        const float2 x = scales[0];
-                        const float f = x.x * factor;
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            fk[k] = f <= 1e-37f ? 1e-37f : f;
-                            vs[k] = x.y;
-                        }
-                        vmost = x.y <= 3.402823466e38f ? fmaxf(0.0f, x.y) : 0.0f;
-                        tmem_ldmax_64(col_s, v, mx);
-                        mx *= fk[0];
-                    } else {
-                        ptx::tmem_ld_32x2(col_s, col_s + 32,
-                                          *reinterpret_cast<uint32_t(*)[32]>(v), *reinterpret_cast<uint32_t(*)[32]>(v + 32));
-                        if (!whole) {
-#pragma unroll
-                            for (int j = 0; j < 64; ++j) {
-                                const int tok = (j & 7) * 8 + (j >> 3);
-                                const bool seen = tok0 + tok < sees && ((valid >> (tok >> 4)) & 1u);
-                                v[j] = seen ? v[j] : 0xff800000u;
-                            }
-                        }
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) {
-                            // scales that are not finite do not reach rows that see none of their tokens
-                            const float2 x = scales[k];
-                            const bool seen = whole || (tok0 + 16 * k < sees && ((valid >> k) & 1u));
-                            const float f = x.x * factor;
-                            fk[k] = f <= 1e-37f || !seen ? 1e-37f : f;
-                            vs[k] = seen ? x.y : 0.0f;
-                            float g0 = -INFINITY, g1 = -INFINITY;
-#pragma unroll
-                            for (int i = 0; i < 8; i += 2) {
-                                const int j = k * 2 + 8 * i;
-                                g0 = fmaxf(fmaxf(g0, __uint_as_float(v[j])), __uint_as_float(v[j + 1]));
-                                g1 = fmaxf(fmaxf(g1, __uint_as_float(v[j + 8])), __uint_as_float(v[j + 9]));
-                            }
-                            mx = fmaxf(mx, fmaxf(g0, g1) * fk[k]);
-                            vmost = x.y <= 3.402823466e38f ? fmaxf(vmost, x.y) : vmost;  // c is the warp's, not the row's
-                        }
-                    }
-                    // both moves are by powers of two, exact for what has been summed and rounded
-                    float keep = 1.0f;
-                    if (mx > mref + kHeadroom || mref == -INFINITY) {
-                        const float to = ceilf(mx);
-                        keep = mref == -INFINITY ? 0.0f : exp2_fast(mref - to);
-                        mref = to;
-                        l *= keep;
-                    }
-                    if (vmost > cref) {
-                        const float to = __int_as_float(min((__float_as_int(vmost) & 0x7f800000) + (1 << 23), 0x7f000000));
-                        keep *= cref / to;
-                        cref = to;
-                    }
-                    if (st > 0 && __any_sync(0xffffffffu, keep != 1.0f)) {
-                        // O is at rest once the step before is in it: this step's product waits for its weights.
-                        // (The step before that is: this step's scores came after it.  So the phase is not taken
-                        // for one of two steps ago.)
-                        ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.o_step[s]), (count - 1) & 1, err));
-                        if (!ok) break;
-                        ptx::tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < DP / 16; ++c) {
-                            uint32_t o[16];
-                            ptx::tmem_ld_16(col_o + 16 * c, o);
-#pragma unroll
-                            for (int j = 0; j < 16; ++j) o[j] = __float_as_uint(__uint_as_float(o[j]) * keep);
-                            tmem_st_16(col_o + 16 * c, o);
-                        }
-                    }
-                    const float base = mref == -INFINITY ? 0.0f : mref;
-                    const float inv = cref > 0.0f ? kWeightTop / cref : 0.0f;
-                    // a group's weight goes into the exponent, and out of its sum again; 2^-60 stands in for
-                    // smaller ones (the fp16 weights are 0 then)
-                    float minus[4], out_of[4];
+                    const bool even = whole && page_size >= 64;  // one page, no token hidden
+                    // 16 tokens that share their scales: the columns with (j mod 8) / 2 alike
+                    float fk[4], lw[4];
+                    float vmost = 0.0f;
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float wt = vs[k] * inv;
-                        const float of = wt <= 8.67361738e-19f ? 8.67361738e-19f : wt;
-                        minus[k] = __log2f(of) - base;
-                        out_of[k] = __frcp_rn(of);
+                        const float vs = sm.scale[at][k].y;
+                        vmost = vs <= 3.402823466e38f ? fmaxf(vmost, vs) : vmost;
                     }
-                    // the weights take the place of the scores
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    if (vmost > cref) {  // the same in every row
+                        const float to = __int_as_float(min((__float_as_int(vmost) & 0x7f800000) + (1 << 23), 0x7f000000));
+                        if (st > 0 && !(ok = rescale(cref / to))) break;
+                        cref = to;
+                    }
+                    // log2 of a group's weight (c: 2^7).  2^-60 of c stands in for smaller scales (their fp16
+                    // weights are 0 then).  A factor is never 0: a hidden token's score is -inf.  Scales that are
+                    // not finite do not reach rows that see none of their tokens.
+                    const float logc = static_cast<float>((__float_as_int(cref) >> 23) - 127);
+                    const float least = cref * 8.67361738e-19f;
 #pragma unroll
+                    for (int k = 0; k < 4; ++k) {
+                        const float4 x = sm.scale[at][k];
+                        const bool seen = whole || (tok0 + 16 * k < sees && ((valid >> k) & 1u));
+                        const float f = x.x * factor;
+                        fk[k] = f <= 1e-37f || !seen ? 1e-37f : f;
+                        lw[k] = x.y <= least || !seen ? kLogStart - 60.0f : x.z + (kLogStart - logc);
+                    }
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                    // 32 columns at a time, in little code: four warps of three roles share an instruction cache
+#pragma unroll 1
                     for (int c = 0; c < 2; ++c) {
-                        uint32_t p[16];
+                        uint32_t v[32], p[16];
+                        float top;
+                        if (even) {
+                            float mx;
+                            tmem_ldmax_32(col_s + 32 * c, v, mx);
+                            top = fmaf(mx, fk[0], lw[0] - ref);
+                        } else {
+                            ptx::tmem_ld_32(col_s + 32 * c, v);
+                            if (!whole) {
+                                const int left = sees - tok0 - 4 * c;
+#pragma unroll
+                                for (int j = 0; j < 32; ++j) {
+                                    const int tok = (j & 7) * 8 + (j >> 3);  // + 4 c
+                                    const bool seen = tok < left && ((valid >> ((j & 7) >> 1)) & 1u);
+                                    v[j] = seen ? v[j] : 0xff800000u;
+                                }
+                            }
+                            top = -INFINITY;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                float g0 = -INFINITY;
+#pragma unroll
+                                for (int i = 0; i < 4; ++i)
+                                    g0 = fmaxf(fmaxf(g0, __uint_as_float(v[2 * k + 8 * i])), __uint_as_float(v[2 * k + 8 * i + 1]));
+                                top = fmaxf(top, fmaf(g0, fk[k], lw[k] - ref));
+                            }
+                        }
+                        // a weight beyond fp16's range: the row's reference moves, by a power of two, exact for
+                        // what has been summed and rounded
+                        if (__any_sync(0xffffffffu, top > kLogTop)) {
+                            float keep = 1.0f;
+                            if (top > kLogTop) {
+                                const float by = ceilf(top) - kLogStart;
+                                keep = exp2_fast(-by);  // 0 for the first tokens that a row sees
+                                ref += by;
+                                l *= keep;
+                            }
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) sum[k] *= keep;
+                            if (st > 0 && !(ok = rescale(keep))) break;
+                            if (c) {
+                                ptx::tmem_wait_st();
+                                ptx::tmem_ld_16(col_s, p);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) {
+                                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[j]));
+                                    p[j] = pack_half(f.x * keep, f.y * keep);
+                                }
+                                tmem_st_16(col_s, p);
+                            }
+                        }
+                        // the weights take the place of the scores
+                        float minus[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) minus[k] = lw[k] - ref;
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const int j = 32 * c + 2 * i, k = i & 3;
-                            const float e0 = exp2_fast(fmaf(__uint_as_float(v[j]), fk[k], minus[k]));
-                            const float e1 = exp2_fast(fmaf(__uint_as_float(v[j + 1]), fk[k], minus[k]));
+                            const int k = i & 3;
+                            const float e0 = exp2_fast(fmaf(__uint_as_float(v[2 * i]), fk[k], minus[k]));
+                            const float e1 = exp2_fast(fmaf(__uint_as_float(v[2 * i + 1]), fk[k], minus[k]));
                             sum[k] += e0 + e1;
                             p[i] = pack_half(e0, e1);
                         }
                         tmem_st_16(col_s + 16 * c, p);
                     }
+                    if (!ok) break;
+                    // the group's weight out of its sum again
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) l = fmaf(sum[k], out_of[k], l);
+                    for (int k = 0; k < 4; ++k) l = fmaf(sum[k], exp2_fast(-lw[k]), l);
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
@@ -803,7 +809,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (join) {
                         // stream 0's warp of the same rows reads this stream's O, and beside it, in the columns of
                         // scores that are no longer needed, its maximum, sum and scale
-                        uint32_t x[16] = {__float_as_uint(mref), __float_as_uint(l), __float_as_uint(cref / kWeightTop)};
+                        uint32_t x[16] = {__float_as_uint(ref), __float_as_uint(l), __float_as_uint(cref * 0.0078125f)};
                         tmem_st_16(tmem + lanes + kColS + 128, x);
                         ptx::tmem_wait_st();
                         ptx::tc_fence_before();
@@ -815,7 +821,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         ptx::tc_fence_after();
                     }
                 } else {
-                    float f0 = cref / kWeightTop, f1 = 0.0f, m = mref;
+                    float f0 = cref * 0.0078125f, f1 = 0.0f, m = ref;  // 2^-7 c
                     const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
                     float* const piece = pieces + static_cast<int64_t>(slot) * piece_rows * (DP + 4);
                     const int64_t t = w.x.r.row0 + i;
@@ -827,9 +833,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         uint32_t x[16];
                         ptx::tmem_ld_16(tmem + lanes + kColS + 128, x);
                         const float m1 = __uint_as_float(x[0]), l1 = __uint_as_float(x[1]);
-                        m = fmaxf(mref, m1);
-                        const float base = m == -INFINITY ? 0.0f : m;
-                        const float k0 = exp2_fast(mref - base), k1 = exp2_fast(m1 - base);
+                        m = fmaxf(ref, m1);
+                        const float k0 = exp2_fast(ref - m), k1 = exp2_fast(m1 - m);
                         // a side without weights has no part; NaN sums stay
                         f0 = l == 0.0f ? 0.0f : f0 * k0;
                         f1 = l1 == 0.0f ? 0.0f : __uint_as_float(x[2]) * k1;
