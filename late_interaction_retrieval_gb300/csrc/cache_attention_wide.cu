@@ -31,7 +31,7 @@ namespace {
 
 using namespace attn;
 
-constexpr int kThreads = 512;
+constexpr int kThreads = 640;
 constexpr int kTok = 64;
 constexpr int kM = 128;
 constexpr int kItemRows = 256;
@@ -43,7 +43,7 @@ constexpr float kLogTop = 15.0f, kLogStart = 7.0f;  // log2 of the largest weigh
 constexpr float kNothing = -1048576.0f;            // a row's reference before it has seen a token
 
 // warps
-constexpr int kConvert = 8, kLoad = 12, kMma = 13, kBusy = 15;  // an issuer of MMAs for each stream
+constexpr int kConvert = 8, kLoad = 16, kMma = 17, kBusy = 19;  // converters of K, of V; an issuer of MMAs a stream
 
 constexpr uint32_t kColS = 0, kColO = 256;
 
@@ -58,7 +58,7 @@ struct Smem {
     uint8_t k[kKeys][DP / 64][kTok * 128];
     uint8_t v[kValues][DP * 128];
     uint8_t raw[kRaw][kTok * DP];
-    float4 scale[kScaleRing][4];  // of 16 tokens each: keys', values', log2 and reciprocal of the latter
+    float4 scale[kScaleRing][4];  // of 16 tokens each: keys', values', log2 of the latter
     uint32_t valid[kScaleRing];
     uint64_t raw_full[kRaw], raw_empty[kRaw], scale_full[kScaleRing];
     uint64_t k_full[kKeys], k_empty[kKeys], v_full[kValues], v_empty[kValues];
@@ -194,22 +194,34 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&v)[1
         : "memory");
 }
 
-// 32 columns of this thread's lane, and their maximum, which the loads take
+// 64 columns of this thread's lane, and their maximum, which the loads take
 // (loads and wait in one statement, so that no use comes before the wait).
-__device__ __forceinline__ void tmem_ldmax_32(uint32_t taddr, uint32_t (&v)[32], float& mx) {
-    float a, b;
+__device__ __forceinline__ void tmem_ldmax_64(uint32_t taddr, uint32_t (&v)[64], float& mx) {
+    float a, b, c, d;
     asm volatile(
-        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, %32, [%34];\n\t"
-        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %33, [%35];\n\t"
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, %64, [%68];\n\t"
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %65, [%69];\n\t"
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47}, %66, [%70];\n\t"
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, %67, [%71];\n\t"
         "tcgen05.wait::ld.sync.aligned;"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
           "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]), "=f"(a), "=f"(b)
-        : "r"(taddr), "r"(taddr + 16)
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
+          "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]),
+          "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]),
+          "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
+          "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63]),
+          "=f"(a), "=f"(b), "=f"(c), "=f"(d)
+        : "r"(taddr), "r"(taddr + 16), "r"(taddr + 32), "r"(taddr + 48)
         : "memory");
-    mx = fmaxf(a, b);
+    mx = fmaxf(fmaxf(a, b), fmaxf(c, d));
 }
+
+// Registers of a warpgroup's threads: 256 threads of 144 and 384 of 64 are the
+// 640 of 96 that the block is launched with.
+__device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 144;"); }
+__device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
 
 // 8 neighbouring dimensions of one row to the output.
 __device__ __forceinline__ void store8(void* out, int64_t at, const float (&f)[8], bool bf16, bool wide) {
@@ -336,45 +348,62 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     ptx::tc_fence_after();
     const uint32_t tmem = sm.tmem;
-    if (warp >= kBusy) return;
+    if (warp >= kBusy) {
+        fewer_registers();
+        return;
+    }
 
     bool ok = true;
     const int page_size = 1 << a.page_shift;
 
     if (warp == kLoad) {
         // ------------------------------------------------------- raw tiles --
+        fewer_registers();
         Walk w;
         w.begin(a, group, sm.start, sm.end);
         const int box = min(page_size, 64);
         int slot = 0;
         uint32_t phase = 1;  // an empty ring
         int n = 0;           // tiles so far
+        // a lane looks up 16 tokens of the next 8 tiles, while the 8 before are on their way
+        int page = -1;
         float2 scale = make_float2(0.0f, 0.0f);
-        bool pending = false;  // scales of the tile before that are not written yet
-        auto page_at = [&](const Walk& x, int t) {
-            const int pos = t * kTok + 16 * lane;
+        auto look_up = [&](int t, int& pg, float2& sc) {
+            const int pos = (t + (lane >> 2)) * kTok + 16 * (lane & 3);
             int p = -1;
-            if (lane < 4 && pos < x.x.r.length) p = a.table[x.x.b * a.stride + (pos >> a.page_shift)];
-            return p >= 0 && p < a.pages ? p : -1;
+            if (t + (lane >> 2) < w.t1 && pos < w.x.r.length) p = a.table[w.x.b * a.stride + (pos >> a.page_shift)];
+            pg = p >= 0 && p < a.pages ? p : -1;
+            sc = make_float2(0.0f, 0.0f);
+            if (pg >= 0) {
+                sc.x = a.k_scale[static_cast<int64_t>(pg) * a.heads + w.x.head];
+                sc.y = a.v_scale[static_cast<int64_t>(pg) * a.heads + w.x.head];
+            }
         };
-        auto publish = [&](int tile) {
-            if (lane < 4)
-                sm.scale[tile & (kScaleRing - 1)][lane] = make_float4(scale.x, scale.y, __log2f(scale.y), __fdividef(1.0f, scale.y));
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.scale_full[tile & (kScaleRing - 1)]));
-        };
-        int page = w.t1 > w.t0 ? page_at(w, w.t0) : -1;
         while (ok) {
-            for (int t = w.t0; ok && t < w.t1; ++t) {
-                const int now = page;
-                const uint32_t live = __ballot_sync(0xffffffffu, now >= 0);
+            int next_page;
+            float2 next_scale;
+            look_up(w.t0, next_page, next_scale);
+            for (int t = w.t0; ok && t < w.t1; ++t, ++n) {
+                const int of = (t - w.t0) & 7;  // of the lanes' tiles
+                if (of == 0) {
+                    page = next_page;
+                    scale = next_scale;
+                    look_up(t + 8, next_page, next_scale);
+                }
+                const int now = __shfl_sync(0xffffffffu, page, 4 * of + (lane & 3));
+                const uint32_t live = __ballot_sync(0xffffffffu, lane < 4 && now >= 0);
+                const int at = n & (kScaleRing - 1);
+                if (lane >> 2 == of)
+                    sm.scale[at][lane & 3] = make_float4(scale.x, scale.y, __log2f(scale.y), 0.0f);
+                if (lane == 0) sm.valid[at] = live;
+                __syncwarp();
+                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.scale_full[at]));
 #pragma unroll 1
                 for (int part = 0; part < 2; ++part) {  // keys, values
                     ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.raw_empty[slot]), phase, err));
                     if (!ok) break;
                     const uint32_t bar = smem_u32(&sm.raw_full[slot]);
                     if (lane == 0) {
-                        sm.valid[n & (kScaleRing - 1)] = live;
                         if (live) ptx::mbar_arrive_expect_tx(bar, kTok * DP);
                         else ptx::mbar_arrive(bar);  // nothing to load
                     }
@@ -390,55 +419,36 @@ __global__ void __launch_bounds__(kThreads, 1)
                         phase ^= 1;
                     }
                 }
-                if (!ok) break;
-                // the scales are on their way while the next tile's pages are looked up; those of
-                // the tile before have arrived
-                if (pending) publish(n - 1);
-                scale = make_float2(0.0f, 0.0f);
-                if (now >= 0) {
-                    scale.x = a.k_scale[static_cast<int64_t>(now) * a.heads + w.x.head];
-                    scale.y = a.v_scale[static_cast<int64_t>(now) * a.heads + w.x.head];
-                }
-                pending = true;
-                ++n;
-                if (t + 1 < w.t1) page = page_at(w, t + 1);
             }
             if (!ok || w.last) break;
             w.next(a, group);
-            if (w.t1 > w.t0) page = page_at(w, w.t0);
         }
-        if (ok && pending) publish(n - 1);
-    } else if (warp >= kConvert && warp < kConvert + 4) {
+    } else if (warp >= kConvert && warp < kConvert + 8) {
         // ----------------------------------------------- codes to operands --
+        fewer_registers();
         Walk w;
         w.begin(a, group, sm.start, sm.end);
-        const int ct = tid - 32 * kConvert;
-        int slot = 0;
-        uint32_t raw_phase = 0;
-        int n = 0;
-        auto release = [&]() {
-            __syncwarp();
-            if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.raw_empty[slot]));
-            if (++slot == kRaw) {
-                slot = 0;
-                raw_phase ^= 1;
-            }
-        };
-        int kb = 0;
-        uint32_t k_phase = 1;  // empty buffers
+        const int ct = tid & 127;
+        const bool keys = warp < kConvert + 4;
+        int n = 0, slot = keys ? 0 : 1, buf = 0;
+        uint32_t raw_phase = 0, phase = 1;  // full raw tiles, empty operand tiles
+        const int buffers = keys ? kKeys : kValues;
+        uint64_t* const empty = keys ? sm.k_empty : sm.v_empty;
         while (ok) {
             // what even the item's first row sees
             const int all_see = w.x.r.length - w.x.r.n + (w.x.item * kItemRows) / group + 1;
-            for (int t = w.t0; ok && t < w.t1; ++t, ++n) {
-                // K: a thread widens 16 dimensions of a token at a time
-                ok = ptx::mbar_wait(smem_u32(&sm.k_empty[kb]), k_phase, err) &&
+#pragma unroll 1
+            for (int t = w.t0; t < w.t1; ++t, ++n) {
+                ok = ptx::mbar_wait(smem_u32(&empty[buf]), phase, err) &&
                      ptx::mbar_wait(smem_u32(&sm.raw_full[slot]), raw_phase, err);
                 ok = __all_sync(0xffffffffu, ok);
                 if (!ok) break;
-                {
-                    const uint32_t src = smem_u32(sm.raw[slot]), dst = smem_u32(sm.k[kb][0]);
+                const uint32_t src = smem_u32(sm.raw[slot]);
+                if (keys) {
+                    // a thread widens 16 dimensions of a token at a time
+                    const uint32_t dst = smem_u32(sm.k[buf][0]);
                     constexpr int C = DP / 16;  // chunks of a token
-#pragma unroll 1
+#pragma unroll 2
                     for (int i = 0; i < kTok * C / 128; ++i) {
                         const int item = ct + 128 * i, c = item % C, tok = item / C;
                         const uint4 x = lds16(src + raw_at<DP>(tok, c));
@@ -456,26 +466,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                             sts16(hi, h0, h1, h2, h3);
                         }
                     }
-                }
-                fence_operands();
-                release();
-                // the tile's scales too are there before its scores
-                ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.scale_full[n & (kScaleRing - 1)]),
-                                                            (n / kScaleRing) & 1, err));
-                if (!ok) break;
-                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.k_full[kb]));
-                if (++kb == kKeys) {
-                    kb = 0;
-                    k_phase ^= 1;
-                }
-                // V: 8 tokens, 8 apart, of 8 dimensions, transposed
-                const int vb = n & (kValues - 1);
-                ok = ptx::mbar_wait(smem_u32(&sm.v_empty[vb]), ((n / kValues) & 1) ^ 1, err) &&
-                     ptx::mbar_wait(smem_u32(&sm.raw_full[slot]), raw_phase, err);
-                ok = __all_sync(0xffffffffu, ok);
-                if (!ok) break;
-                {
-                    const uint32_t src = smem_u32(sm.raw[slot]), dst = smem_u32(sm.v[vb]);
+                } else {
+                    // 8 tokens, 8 apart, of 8 dimensions, transposed
+                    const uint32_t dst = smem_u32(sm.v[buf]);
                     const uint32_t valid = sm.valid[n & (kScaleRing - 1)];
                     const int first = t * kTok;
                     const int c8 = ct & 7, d8 = ct >> 3;  // tokens 8 i + c8; dimensions 8 d8 ..
@@ -517,14 +510,31 @@ __global__ void __launch_bounds__(kThreads, 1)
                     }
                 }
                 fence_operands();
-                release();
-                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.v_full[vb]));
+                if (keys) {  // the tile's scales too are there before its scores
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.scale_full[n & (kScaleRing - 1)]),
+                                                                (n / kScaleRing) & 1, err));
+                    if (!ok) break;
+                }
+                __syncwarp();
+                if (lane == 0) {
+                    ptx::mbar_arrive(smem_u32(&sm.raw_empty[slot]));
+                    ptx::mbar_arrive(smem_u32(keys ? &sm.k_full[buf] : &sm.v_full[buf]));
+                }
+                if ((slot += 2) >= kRaw) {
+                    slot -= kRaw;
+                    raw_phase ^= 1;
+                }
+                if (++buf == buffers) {
+                    buf = 0;
+                    phase ^= 1;
+                }
             }
             if (!ok || w.last) break;
             w.next(a, group);
         }
     } else if (warp >= kMma) {
         // ------------------------------------------------------------ MMAs --
+        fewer_registers();
         Walk w;
         w.begin(a, group, sm.start, sm.end);
         if (lane == 0) {
@@ -594,6 +604,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         __syncwarp();
     } else {
         // --------------------------------------------------------- softmax --
+        more_registers();
         Walk w;
         w.begin(a, group, sm.start, sm.end);
         const int s = warp >> 2, row = tid & 127;
@@ -612,7 +623,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int sees = live ? w.x.r.length - w.x.r.n + i + 1 : 0;
             const int all_see = w.x.r.length - w.x.r.n + (w.x.item * kItemRows) / group + 1;
             const bool idle = __ballot_sync(0xffffffffu, live) == 0;  // no row of this warp's: its weights do not matter
-            float factor = 0.0f, ref = kNothing, l = 0.0f, cref = 0.0f;
+            float factor = 0.0f, ref = kNothing, l = 0.0f, cref = 0.0f, logc = -127.0f;  // logc: log2 of cref
             if (steps > 0) {
                 // the row of q, scaled to fp16's range
                 const uint16_t* const src = static_cast<const uint16_t*>(a.q) + (w.x.r.row0 + i) * a.q_token_stride +
@@ -626,15 +637,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         e[k] = src[8 * c + 2 * k] | (static_cast<uint32_t>(src[8 * c + 2 * k + 1]) << 16);
                     return make_uint4(e[0], e[1], e[2], e[3]);
                 };
-                // two passes of little code, the second from L1 (code that runs once an item is fetched each time)
+                // two passes of little code (what runs once an item is fetched each time), the second from L1
                 float most = 0.0f;
 #pragma unroll 1
-                for (int c = 0; c < DP / 8; c += 4) {
-                    uint4 x[4];
+                for (int c = 0; c < DP / 8; c += 8) {
+                    uint4 x[8];
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) x[k] = load(c + k);
+                    for (int k = 0; k < 8; ++k) x[k] = load(c + k);
 #pragma unroll
-                    for (int k = 0; k < 16; ++k) {
+                    for (int k = 0; k < 32; ++k) {
                         const float2 f = widen_q(reinterpret_cast<const uint32_t*>(x)[k], bf16);
                         most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
                     }
@@ -642,16 +653,21 @@ __global__ void __launch_bounds__(kThreads, 1)
                 const int shift = row_shift(most);
                 const float2 up = power_of_two(shift), down = power_of_two(-shift);
 #pragma unroll 1
-                for (int c = 0; c < DP / 8; ++c) {
-                    const uint4 x = load(c);
-                    const uint32_t e[4] = {x.x, x.y, x.z, x.w};
-                    uint32_t o[4];
+                for (int c = 0; c < DP / 8; c += 4) {
+                    uint4 x[4];
+#pragma unroll
+                    for (int k = 0; k < 4; ++k) x[k] = load(c + k);
 #pragma unroll
                     for (int k = 0; k < 4; ++k) {
-                        const float2 f = widen_q(e[k], bf16);
-                        o[k] = pack_half(f.x * up.x * up.y, f.y * up.x * up.y);
+                        const uint32_t* const e = reinterpret_cast<const uint32_t*>(&x[k]);
+                        uint32_t o[4];
+#pragma unroll
+                        for (int j = 0; j < 4; ++j) {
+                            const float2 f = widen_q(e[j], bf16);
+                            o[j] = pack_half(f.x * up.x * up.y, f.y * up.x * up.y);
+                        }
+                        sts16(smem_u32(sm.q[s][(c + k) >> 3]) + tile_at(row, (c + k) & 7), o[0], o[1], o[2], o[3]);
                     }
-                    sts16(smem_u32(sm.q[s][c >> 3]) + tile_at(row, c & 7), o[0], o[1], o[2], o[3]);
                 }
                 factor = a.scale * 1.44269504088896341f * down.x * down.y;
                 fence_operands();
@@ -688,104 +704,110 @@ __global__ void __launch_bounds__(kThreads, 1)
                     const bool whole = tok0 + kTok <= all_see && valid == 15u;
                     const bool even = whole && page_size >= 64;  // one page, no token hidden
                     // 16 tokens that share their scales: the columns with (j mod 8) / 2 alike
-                    float fk[4], lw[4];
-                    float vmost = 0.0f;
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float vs = sm.scale[at][k].y;
-                        vmost = vs <= 3.402823466e38f ? fmaxf(vmost, vs) : vmost;
-                    }
-                    if (vmost > cref) {  // the same in every row
+                    uint32_t v[64];
+                    float fk[4], lw[4], mx = 0.0f;
+                    // c grows to the scales' range: the same in every row
+                    auto grow = [&](float vmost) {
                         const float to = __int_as_float(min((__float_as_int(vmost) & 0x7f800000) + (1 << 23), 0x7f000000));
-                        if (st > 0 && !(ok = rescale(cref / to))) break;
+                        if (st > 0) ok = rescale(cref / to);
                         cref = to;
-                    }
+                        logc = static_cast<float>((__float_as_int(to) >> 23) - 127);
+                    };
                     // log2 of a group's weight (c: 2^7).  2^-60 of c stands in for smaller scales (their fp16
                     // weights are 0 then).  A factor is never 0: a hidden token's score is -inf.  Scales that are
                     // not finite do not reach rows that see none of their tokens.
-                    const float logc = static_cast<float>((__float_as_int(cref) >> 23) - 127);
-                    const float least = cref * 8.67361738e-19f;
+                    auto weigh = [&](float4 x, bool seen, float& f, float& w) {
+                        f = x.x * factor;
+                        f = f <= 1e-37f || !seen ? 1e-37f : f;
+                        w = x.y <= cref * 8.67361738e-19f || !seen ? kLogStart - 60.0f : x.z + (kLogStart - logc);
+                    };
+                    if (even) {
+                        const float4 x = sm.scale[at][0];
+                        tmem_ldmax_64(col_s, v, mx);
+                        if (x.y > cref && x.y <= 3.402823466e38f) grow(x.y);
+                        weigh(x, true, fk[0], lw[0]);
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const float4 x = sm.scale[at][k];
-                        const bool seen = whole || (tok0 + 16 * k < sees && ((valid >> k) & 1u));
-                        const float f = x.x * factor;
-                        fk[k] = f <= 1e-37f || !seen ? 1e-37f : f;
-                        lw[k] = x.y <= least || !seen ? kLogStart - 60.0f : x.z + (kLogStart - logc);
+                        for (int k = 1; k < 4; ++k) {
+                            fk[k] = fk[0];
+                            lw[k] = lw[0];
+                        }
+                    } else {
+                        float vmost = 0.0f;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float vs = sm.scale[at][k].y;
+                            vmost = vs <= 3.402823466e38f ? fmaxf(vmost, vs) : vmost;
+                        }
+                        if (vmost > cref) grow(vmost);
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            weigh(sm.scale[at][k], whole || (tok0 + 16 * k < sees && ((valid >> k) & 1u)), fk[k], lw[k]);
+                        ptx::tmem_ld_32x2(col_s, col_s + 32, *reinterpret_cast<uint32_t(*)[32]>(v),
+                                          *reinterpret_cast<uint32_t(*)[32]>(v + 32));
+                        if (!whole) {
+                            const int left = sees - tok0;
+#pragma unroll
+                            for (int j = 0; j < 64; ++j) {
+                                const int tok = (j & 7) * 8 + (j >> 3);
+                                const bool seen = tok < left && ((valid >> (tok >> 4)) & 1u);
+                                v[j] = seen ? v[j] : 0xff800000u;
+                            }
+                        }
                     }
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
-                    // 32 columns at a time, in little code: four warps of three roles share an instruction cache
-#pragma unroll 1
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t v[32], p[16];
-                        float top;
-                        if (even) {
-                            float mx;
-                            tmem_ldmax_32(col_s + 32 * c, v, mx);
-                            top = fmaf(mx, fk[0], lw[0] - ref);
-                        } else {
-                            ptx::tmem_ld_32(col_s + 32 * c, v);
-                            if (!whole) {
-                                const int left = sees - tok0 - 4 * c;
-#pragma unroll
-                                for (int j = 0; j < 32; ++j) {
-                                    const int tok = (j & 7) * 8 + (j >> 3);  // + 4 c
-                                    const bool seen = tok < left && ((valid >> ((j & 7) >> 1)) & 1u);
-                                    v[j] = seen ? v[j] : 0xff800000u;
-                                }
-                            }
-                            top = -INFINITY;
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) {
-                                float g0 = -INFINITY;
-#pragma unroll
-                                for (int i = 0; i < 4; ++i)
-                                    g0 = fmaxf(fmaxf(g0, __uint_as_float(v[2 * k + 8 * i])), __uint_as_float(v[2 * k + 8 * i + 1]));
-                                top = fmaxf(top, fmaf(g0, fk[k], lw[k] - ref));
-                            }
-                        }
-                        // a weight beyond fp16's range: the row's reference moves, by a power of two, exact for
-                        // what has been summed and rounded
-                        if (__any_sync(0xffffffffu, top > kLogTop)) {
-                            float keep = 1.0f;
-                            if (top > kLogTop) {
-                                const float by = ceilf(top) - kLogStart;
-                                keep = exp2_fast(-by);  // 0 for the first tokens that a row sees
-                                ref += by;
-                                l *= keep;
-                            }
-#pragma unroll
-                            for (int k = 0; k < 4; ++k) sum[k] *= keep;
-                            if (st > 0 && !(ok = rescale(keep))) break;
-                            if (c) {
-                                ptx::tmem_wait_st();
-                                ptx::tmem_ld_16(col_s, p);
-#pragma unroll
-                                for (int j = 0; j < 16; ++j) {
-                                    const float2 f = __half22float2(*reinterpret_cast<const __half2*>(&p[j]));
-                                    p[j] = pack_half(f.x * keep, f.y * keep);
-                                }
-                                tmem_st_16(col_s, p);
-                            }
-                        }
-                        // the weights take the place of the scores
-                        float minus[4];
+                    if (!ok) break;
+                    float minus[4];
+                    auto limit = [&]() {  // log2 of the largest weight; the groups' terms under the reference
 #pragma unroll
                         for (int k = 0; k < 4; ++k) minus[k] = lw[k] - ref;
+                        if (even) return fmaf(mx, fk[0], minus[0]);
+                        float top = -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            float g = -INFINITY;
+#pragma unroll
+                            for (int i = 0; i < 8; ++i)
+                                g = fmaxf(fmaxf(g, __uint_as_float(v[2 * k + 8 * i])), __uint_as_float(v[2 * k + 8 * i + 1]));
+                            top = fmaxf(top, fmaf(g, fk[k], minus[k]));
+                        }
+                        return top;
+                    };
+                    const float top = limit();
+                    // a weight beyond fp16's range: the row's reference moves, by a power of two, exact for what has
+                    // been summed and rounded
+                    if (__any_sync(0xffffffffu, top > kLogTop)) {
+                        float keep = 1.0f;
+                        if (top > kLogTop) {
+                            const float by = ceilf(top) - kLogStart;
+                            keep = exp2_fast(-by);  // 0 for the first tokens that a row sees
+                            ref += by;
+                            l *= keep;
+                        }
+                        if (st > 0 && !(ok = rescale(keep))) break;
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) minus[k] = lw[k] - ref;
+                    }
+                    // the weights take the place of the scores
+                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+#pragma unroll
+                    for (int c = 0; c < 2; ++c) {
+                        uint32_t p[16];
 #pragma unroll
                         for (int i = 0; i < 16; ++i) {
-                            const int k = i & 3;
-                            const float e0 = exp2_fast(fmaf(__uint_as_float(v[2 * i]), fk[k], minus[k]));
-                            const float e1 = exp2_fast(fmaf(__uint_as_float(v[2 * i + 1]), fk[k], minus[k]));
+                            const int j = 32 * c + 2 * i, k = i & 3;
+                            const float e0 = exp2_fast(fmaf(__uint_as_float(v[j]), fk[k], minus[k]));
+                            const float e1 = exp2_fast(fmaf(__uint_as_float(v[j + 1]), fk[k], minus[k]));
                             sum[k] += e0 + e1;
                             p[i] = pack_half(e0, e1);
                         }
                         tmem_st_16(col_s + 16 * c, p);
                     }
-                    if (!ok) break;
                     // the group's weight out of its sum again
+                    if (even) {
+                        l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), exp2_fast(-lw[0]), l);
+                    } else {
 #pragma unroll
-                    for (int k = 0; k < 4; ++k) l = fmaf(sum[k], exp2_fast(-lw[k]), l);
+                        for (int k = 0; k < 4; ++k) l = fmaf(sum[k], exp2_fast(-lw[k]), l);
+                    }
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
