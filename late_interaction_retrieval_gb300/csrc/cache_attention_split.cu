@@ -1,19 +1,22 @@
 // cache_attention_split.cu -- attention over the 8-bit cache for few rows a
 // key head (single tokens): the cache is read once, at the memory's rate.
 //
-// A unit is 32 tokens of one (request, key head, 16 rows).  The units of the
-// batch, laid end to end, are cut into one equal range a block, so that long
-// and short requests load the chip evenly; a request that is cut leaves
+// A unit is 32 tokens of one (request, key head, 8 or 16 rows).  The units of
+// the batch, laid end to end, are cut into one equal range a block, so that
+// long and short requests load the chip evenly; a request that is cut leaves
 // partial sums, which a second launch joins in the order of the cache.  In a
-// block every warp takes every eighth unit, with a ring of its own that TMA
+// block every warp takes every n-th unit, with a ring of its own that TMA
 // fills: no warp waits for another until a request's end.
 //
-// Products are m16n8k16 with the rows as M.  The codes of 8 bits become fp16
-// in registers on their way from shared memory to the fragments (exactly, one
+// Products are m16n8k16 with the tokens (scores) and the dimensions (output)
+// as M and 8 rows as N, so that no product is spent on rows that are not
+// there: S^T = K Q^T, O^T = V^T P^T.  The codes of 8 bits become fp16 in
+// registers on their way from shared memory to the fragments (exactly, one
 // conversion for two codes), and the order of the dimensions and tokens inside
 // a fragment is chosen so that every load is 16 bytes wide: a thread's K codes
 // are 32 neighbouring dimensions of one token, its V codes 16 neighbouring
-// dimensions of 4 tokens, transposed by byte permutes.
+// dimensions of 4 tokens, transposed by byte permutes.  The weights go from
+// the one product's layout to the other's by an 8x8 transpose in registers.
 //
 // Rows are scaled to fp16's range by a power of two.  The softmax weights are
 // 2^15 * exp(z - max) * (the page's scale / the largest so far), rounded to
@@ -27,30 +30,41 @@ namespace {
 
 using namespace attn;
 
-constexpr int kWarps = 8;
-constexpr int kThreads = 32 * kWarps;
-constexpr int kTok = 32;     // tokens of a unit
-constexpr int kRows = 16;    // rows of a unit
-constexpr int kStages = 3;
+constexpr int kTok = 32;  // tokens of a unit
 constexpr float kWeightTop = 32768.0f;
+
+// Blocks of 8 rows (NR of them), warps of a block and stages of a warp's ring:
+// 16 rows need more registers, so fewer warps with deeper rings.
+template <int NR>
+struct Shape;
+template <>
+struct Shape<1> {
+    static constexpr int kWarps = 12, kStages = 2;
+};
+template <>
+struct Shape<2> {
+    static constexpr int kWarps = 8, kStages = 3;
+};
 
 // Where a block's pieces of cut requests lie, and whose they are.
 struct PieceInfo {
     int request, unit;  // unit: head * row tiles + row tile; request -1: no piece
     int begins, ends;   // whether it holds the first / the last tokens
 };
-template <int DP>
+template <int DP, int NR>
 struct Piece {
-    float m[kRows], l[kRows];
-    float4 o[kRows * DP / 4];
+    float m[8 * NR], l[8 * NR];
+    float4 o[8 * NR * DP / 4];
 };
 
-template <int DP>
+template <int DP, int NR>
 struct Smem {
+    static constexpr int kWarps = Shape<NR>::kWarps, kStages = Shape<NR>::kStages;
     static constexpr int kTile = kTok * DP;  // bytes of one operand's tile
     alignas(1024) uint8_t ring[kWarps][kStages][2][kTile];
-    float4 join[kWarps][DP / 16][32];  // half of every warp's sums
-    float m[kWarps][kRows], l[kWarps][kRows];
+    float4 join[kWarps][4][32];  // 4 vectors of every lane's sums at a time
+    float m[kWarps][8 * NR], l[kWarps][8 * NR];
+    float scale[kWarps][kStages][4];  // keys' and values' of the first 16 tokens, of the last 16
     uint64_t full[kWarps][kStages];
     int2 page[kWarps][kStages];
     long long warp_sum[kWarps];
@@ -69,11 +83,12 @@ struct Span {
     }
 };
 
+template <int NR>
 __device__ __forceinline__ Span span_of(const AttentionArgs& a, int b, int group) {
     Span s;
     s.r = request_of(a, b);
     s.tiles = s.r.n ? max(1, (s.r.length + kTok - 1) / kTok) : 0;
-    s.row_tiles = (s.r.n * group + kRows - 1) / kRows;
+    s.row_tiles = (s.r.n * group + 8 * NR - 1) / (8 * NR);
     return s;
 }
 
@@ -83,6 +98,7 @@ struct Cursor {
     Span s;
 };
 
+template <int NR>
 __device__ __forceinline__ void settle(const AttentionArgs& a, Cursor& c, int group) {
     while (c.tile >= c.s.tiles) {
         c.tile -= c.s.tiles;
@@ -93,7 +109,7 @@ __device__ __forceinline__ void settle(const AttentionArgs& a, Cursor& c, int gr
                     c.s.tiles = INT32_MAX;  // behind the last unit
                     return;
                 }
-                c.s = span_of(a, c.b, group);
+                c.s = span_of<NR>(a, c.b, group);
             } while (c.s.tiles == 0);
         }
     }
@@ -105,6 +121,13 @@ __device__ __forceinline__ void mma16816(float (&d)[4], uint32_t a0, uint32_t a1
         "{%0, %1, %2, %3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+
+// The transpose of an 8x8 matrix of 16-bit elements over the warp.
+__device__ __forceinline__ uint32_t transpose8(uint32_t x) {
+    uint32_t y;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(y) : "r"(x));
+    return y;
 }
 
 __device__ __forceinline__ uint4 lds16(uint32_t at) {
@@ -148,21 +171,21 @@ __device__ __forceinline__ void store4(void* out, int64_t at, float4 v, bool bf1
     }
 }
 
-// Register vector k of a lane: row lane / 4 (+ 8 in the upper half of the
-// vectors), 4 dimensions of the lane's DP / 4.
+// Vector k of a lane's sums: 4 of its DP / 8 dimensions of one of its 2 NR rows.
 template <int DP>
 __device__ __forceinline__ void vector_place(int k, int lane, int& row, int& dim) {
-    constexpr int half = DP / 16;  // vectors of a row
-    row = (lane >> 2) + (k >= half ? 8 : 0);
-    dim = (lane & 3) * (DP / 4) + (k & (half - 1)) * 4;
+    constexpr int per_row = DP / 32;
+    const int e = k / per_row;
+    row = (e >> 1) * 8 + (lane & 3) * 2 + (e & 1);
+    dim = (lane >> 2) * (DP / 8) + (k % per_row) * 4;
 }
 
-template <int DP>
+template <int DP, int NR>
 __device__ __forceinline__ void write_vector(const AttentionArgs& a, const Request& r, int head, int row_tile,
                                              int group, int k, int lane, float4 o, float l, float m, bool wide) {
     int row, dim;
     vector_place<DP>(k, lane, row, dim);
-    const int rr = row_tile * kRows + row;
+    const int rr = row_tile * 8 * NR + row;
     if (rr >= r.n * group) return;
     const int64_t t = r.row0 + rr / group;
     const int h = head * group + rr % group;
@@ -178,15 +201,18 @@ __device__ __forceinline__ void write_vector(const AttentionArgs& a, const Reque
         a.lse[t * a.q_heads + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
 }
 
-template <int DP>
-__global__ void __launch_bounds__(kThreads, 1)
+template <int DP, int NR>
+__global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
     attention_split_kernel(const AttentionArgs a, const __grid_constant__ Maps maps, unsigned int* err,
-                           PieceInfo* infos, Piece<DP>* pieces, bool q_wide, bool out_wide) {
+                           PieceInfo* infos, Piece<DP, NR>* pieces, bool q_wide, bool out_wide) {
+    constexpr int kWarps = Shape<NR>::kWarps, kStages = Shape<NR>::kStages, kThreads = 32 * kWarps, kRows = 8 * NR;
+    constexpr int KS = DP / 16;    // k-steps of a score, words of K codes a thread and token
+    constexpr int MB = DP / 16;    // m-blocks of the output
+    constexpr int VW = DP / 32;    // words of V codes a thread and token
+    constexpr int VR = DP / 32;    // vectors of a row
+    constexpr int kVectors = 2 * NR * VR;
     extern __shared__ uint8_t raw[];
-    Smem<DP>& sm = *reinterpret_cast<Smem<DP>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
-    constexpr int KS = DP / 16;   // k-steps of a score, words of K codes a thread and token
-    constexpr int NB = DP / 8;    // n-blocks of the output
-    constexpr int VW = DP / 32;   // words of V codes a thread and token
+    Smem<DP, NR>& sm = *reinterpret_cast<Smem<DP, NR>*>((reinterpret_cast<uintptr_t>(raw) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int g = lane >> 2, q4 = lane & 3;
     const int group = a.q_heads / a.heads;
@@ -200,7 +226,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     // neighbouring requests
     const int B = a.requests, each = (B + kThreads - 1) / kThreads;
     long long mine = 0;
-    for (int b = min(tid * each, B); b < min(tid * each + each, B); ++b) mine += span_of(a, b, group).units(a.heads);
+    for (int b = min(tid * each, B); b < min(tid * each + each, B); ++b) mine += span_of<NR>(a, b, group).units(a.heads);
     long long incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -218,26 +244,28 @@ __global__ void __launch_bounds__(kThreads, 1)
     chunk[tid] = incl - mine;
     __syncthreads();
 
-    // a block has a round of units at least; blocks without any have no piece
-    const long long active = max(1ll, min(static_cast<long long>(gridDim.x), units / kWarps));
+    // a block has 8 units at least; blocks without any have no piece
+    const long long active = max(1ll, min(static_cast<long long>(gridDim.x), units / 8));
     const long long u0 = blockIdx.x < active ? units * blockIdx.x / active : units;
     const long long u1 = blockIdx.x < active ? units * (blockIdx.x + 1) / active : units;
     if (tid < 2) infos[2 * blockIdx.x + tid] = PieceInfo{-1, 0, 0, 0};
     if (u0 >= u1) return;
 
-    // the warp's first unit
+    // the block's first unit
     Cursor load;
     {
-        const long long u = u0;  // the block's first; the warp's lies `warp` units on
-        int i = 0;
-        for (int step = kThreads / 2; step > 0; step >>= 1)
-            if (chunk[i + step] <= u) i += step;  // the last chunk that begins at or before u
-        long long rest = u - chunk[i];
-        int b = i * each;
-        Span s = span_of(a, b, group);
+        int lo = 0, hi = kThreads;  // the last chunk that begins at or before it
+        while (hi - lo > 1) {
+            const int mid = (lo + hi) >> 1;
+            if (chunk[mid] <= u0) lo = mid;
+            else hi = mid;
+        }
+        long long rest = u0 - chunk[lo];
+        int b = lo * each;
+        Span s = span_of<NR>(a, b, group);
         while (rest >= s.units(a.heads)) {
             rest -= s.units(a.heads);
-            s = span_of(a, ++b, group);
+            s = span_of<NR>(a, ++b, group);
         }
         load.b = b;
         load.s = s;
@@ -247,12 +275,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     Cursor at = load;  // the block's place: the segment that all its warps are in
     long long left = u1 - u0;
     load.tile += warp;
-    settle(a, load, group);
+    settle<NR>(a, load, group);
     long long to_load = left > warp ? (left - warp + kWarps - 1) / kWarps : 0;  // this warp's units
 
     const int page_size = 1 << a.page_shift;
     const uint32_t ring = ptx::smem_u32(&sm.ring[warp][0][0][0]);
-    constexpr int kTile = Smem<DP>::kTile;
+    constexpr int kTile = Smem<DP, NR>::kTile;
     int fill = 0;  // the stage to fill next
     // the table entries of the unit to load next, read one unit ahead
     auto entries = [&](const Cursor& c, int2& p) {
@@ -265,37 +293,49 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (to_load > 0) entries(load, next);
     // fills a stage with the unit under the cursor; the cursor moves on
     auto issue = [&]() {
-        if (to_load <= 0) return;
-        int2 p = next;
-        // an entry outside the pool hides its tokens: page 0 is loaded, and not looked at
-        if (p.x < 0 || p.x >= a.pages) p.x = -1;
-        if (p.y < 0 || p.y >= a.pages) p.y = -1;
-        const int head = load.item / load.s.row_tiles;
-        const int t0 = load.tile * kTok;
-        if (lane == 0) {
-            sm.page[warp][fill] = p;
-            const uint32_t bar = ptx::smem_u32(&sm.full[warp][fill]);
-            const uint32_t dst = ring + fill * 2 * kTile;
-            if (p.x < 0 && p.y < 0) {
-                ptx::mbar_arrive(bar);  // nothing to load
-            } else {
-                ptx::mbar_arrive_expect_tx(bar, 2 * kTile);
-                const int off = head * page_size + (t0 & (page_size - 1));
-                const int px = max(p.x, 0);
-                ptx::tma_load_3d(dst, &maps.k, 0, off, px, bar);
-                ptx::tma_load_3d(dst + kTile, &maps.v, 0, off, px, bar);
-                if (page_size == 16) {
-                    const int py = max(p.y, 0);
-                    ptx::tma_load_3d(dst + kTile / 2, &maps.k, 0, off, py, bar);
-                    ptx::tma_load_3d(dst + kTile + kTile / 2, &maps.v, 0, off, py, bar);
+        if (to_load > 0) {
+            int2 p = next;
+            // an entry outside the pool hides its tokens: page 0 is loaded, and not looked at
+            if (p.x < 0 || p.x >= a.pages) p.x = -1;
+            if (p.y < 0 || p.y >= a.pages) p.y = -1;
+            const int head = load.item / load.s.row_tiles;
+            const int t0 = load.tile * kTok;
+            if (lane < 4) {
+                const int pg = lane < 2 ? p.x : p.y;
+                const uint32_t to = ptx::smem_u32(&sm.scale[warp][fill][lane]);
+                if (pg >= 0) {
+                    const float* const from = (lane & 1 ? a.v_scale : a.k_scale) + static_cast<int64_t>(pg) * a.heads + head;
+                    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(to), "l"(from) : "memory");
+                } else {
+                    sm.scale[warp][fill][lane] = 0.0f;
                 }
             }
+            if (lane == 0) {
+                sm.page[warp][fill] = p;
+                const uint32_t bar = ptx::smem_u32(&sm.full[warp][fill]);
+                const uint32_t dst = ring + fill * 2 * kTile;
+                if (p.x < 0 && p.y < 0) {
+                    ptx::mbar_arrive(bar);  // nothing to load
+                } else {
+                    ptx::mbar_arrive_expect_tx(bar, 2 * kTile);
+                    const int off = head * page_size + (t0 & (page_size - 1));
+                    const int px = max(p.x, 0);
+                    ptx::tma_load_3d(dst, &maps.k, 0, off, px, bar);
+                    ptx::tma_load_3d(dst + kTile, &maps.v, 0, off, px, bar);
+                    if (page_size == 16) {
+                        const int py = max(p.y, 0);
+                        ptx::tma_load_3d(dst + kTile / 2, &maps.k, 0, off, py, bar);
+                        ptx::tma_load_3d(dst + kTile + kTile / 2, &maps.v, 0, off, py, bar);
+                    }
+                }
+            }
+            fill = fill + 1 == kStages ? 0 : fill + 1;
+            --to_load;
+            load.tile += kWarps;
+            settle<NR>(a, load, group);
+            if (to_load > 0) entries(load, next);
         }
-        fill = fill + 1 == kStages ? 0 : fill + 1;
-        --to_load;
-        load.tile += kWarps;
-        settle(a, load, group);
-        if (to_load > 0) entries(load, next);
+        asm volatile("cp.async.commit_group;" ::: "memory");  // one a unit, counted
     };
     for (int s = 0; s < kStages; ++s) issue();
 
@@ -310,20 +350,19 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int first = at.tile;
         const int count = static_cast<int>(min(static_cast<long long>(at.s.tiles - first), left));
         const int rows_in = min(kRows, r.n * group - row_tile * kRows);
-        const bool upper = rows_in > 8;
 
-        // the thread's two rows of q, scaled to fp16's range
-        uint32_t qf[KS][4];
-        float factor[2];
-        int sees[2];  // positions that the row sees
+        // q, scaled to fp16's range: the thread's part (a quarter of the dimensions) of rows g, g + 8
+        uint32_t qf[NR][KS][2];
+        float factor[NR][2];  // of rows 2 q4, 2 q4 + 1 (+ 8)
+        int sees[NR][2];      // positions that those see
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            const int rr = row_tile * kRows + g + 8 * half;
-            const bool live = g + 8 * half < rows_in;
+        for (int nr = 0; nr < NR; ++nr) {
+            const int row = nr * 8 + g, rr = row_tile * kRows + row;
+            const bool live = row < rows_in;
             const int i = live ? rr / group : 0;
-            const int64_t base = (r.row0 + i) * a.q_token_stride +
-                                 static_cast<int64_t>(head * group + (live ? rr % group : 0)) * a.q_head_stride;
-            const uint16_t* const src = static_cast<const uint16_t*>(a.q) + base + q4 * (DP / 4);
+            const uint16_t* const src = static_cast<const uint16_t*>(a.q) + (r.row0 + i) * a.q_token_stride +
+                                        static_cast<int64_t>(head * group + (live ? rr % group : 0)) * a.q_head_stride +
+                                        q4 * (DP / 4);
             uint32_t w[DP / 8];
 #pragma unroll
             for (int c = 0; c < DP / 32; ++c) {  // 8 dimensions
@@ -357,113 +396,138 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
             for (int c = 0; c < DP / 8; ++c) {
                 const float2 f = widen_q(w[c], bf16);
-                qf[c >> 1][(c & 1) * 2 + half] = pack_half(f.x * up.x * up.y, f.y * up.x * up.y);
+                qf[nr][c >> 1][c & 1] = pack_half(f.x * up.x * up.y, f.y * up.x * up.y);
             }
-            factor[half] = a.scale * 1.44269504088896341f * down.x * down.y;
-            sees[half] = live ? r.length - r.n + i + 1 : 0;
+            const float of_row = a.scale * 1.44269504088896341f * down.x * down.y;
+            const int row_sees = live ? r.length - r.n + i + 1 : 0;
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                factor[nr][e] = __shfl_sync(0xffffffffu, of_row, 4 * (2 * q4 + e));
+                sees[nr][e] = __shfl_sync(0xffffffffu, row_sees, 4 * (2 * q4 + e));
+            }
         }
         const int all_see = r.length - r.n + (row_tile * kRows) / group + 1;  // what even the first row sees
 
-        float o[NB][4];
+        float o[MB][NR][4];
 #pragma unroll
-        for (int j = 0; j < NB; ++j) o[j][0] = o[j][1] = o[j][2] = o[j][3] = 0.0f;
-        float m[2] = {-INFINITY, -INFINITY}, l[2] = {0.0f, 0.0f};
+        for (int j = 0; j < MB; ++j)
+#pragma unroll
+            for (int nr = 0; nr < NR; ++nr) o[j][nr][0] = o[j][nr][1] = o[j][nr][2] = o[j][nr][3] = 0.0f;
+        float m[NR][2], l[NR][2];
+#pragma unroll
+        for (int nr = 0; nr < NR; ++nr) {
+            m[nr][0] = m[nr][1] = -INFINITY;
+            l[nr][0] = l[nr][1] = 0.0f;
+        }
         float top_scale = kLeastScale;
 
         int done = turn;
         for (; done < count; done += kWarps) {
             const int t0 = (first + done) * kTok;
             if (ok) ok = __all_sync(0xffffffffu, ptx::mbar_wait(ptx::smem_u32(&sm.full[warp][stage]), phase, err));
+            asm volatile("cp.async.wait_group %0;" ::"n"(kStages - 1) : "memory");
+            __syncwarp();  // the scales that other lanes fetched
             const int2 page = sm.page[warp][stage];
-            float ks[2] = {0.0f, 0.0f}, vs[2] = {0.0f, 0.0f};
-            if (page.x >= 0) {
-                ks[0] = a.k_scale[static_cast<int64_t>(page.x) * a.heads + head];
-                vs[0] = a.v_scale[static_cast<int64_t>(page.x) * a.heads + head];
-            }
-            if (page.y >= 0) {
-                ks[1] = a.k_scale[static_cast<int64_t>(page.y) * a.heads + head];
-                vs[1] = a.v_scale[static_cast<int64_t>(page.y) * a.heads + head];
-            }
+            const float4 sc = *reinterpret_cast<const float4*>(sm.scale[warp][stage]);
+            const float ks[2] = {sc.x, sc.z}, vs[2] = {sc.y, sc.w};
             const uint32_t kt = ring + stage * 2 * kTile, vt = kt + kTile;
             // every row sees every token
             const bool whole = t0 + kTok <= all_see && page.x >= 0 && page.y >= 0;
 
-            float s[4][4];
+            float s[2][NR][4];
 #pragma unroll
-            for (int nb = 0; nb < 4; ++nb) {
-                s[nb][0] = s[nb][1] = s[nb][2] = s[nb][3] = 0.0f;
-                const int row = nb * 8 + g;
-                uint32_t w[KS];
+            for (int mb = 0; mb < 2; ++mb) {
 #pragma unroll
-                for (int c = 0; c < DP / 64; ++c) {
-                    const uint4 v = lds16(kt + chunk_at<DP>(row, q4 * (DP / 64) + c));
-                    w[4 * c] = v.x;
-                    w[4 * c + 1] = v.y;
-                    w[4 * c + 2] = v.z;
-                    w[4 * c + 3] = v.w;
+                for (int nr = 0; nr < NR; ++nr) s[mb][nr][0] = s[mb][nr][1] = s[mb][nr][2] = s[mb][nr][3] = 0.0f;
+                uint32_t w[2][KS];  // codes of tokens g, g + 8
+#pragma unroll
+                for (int h = 0; h < 2; ++h)
+#pragma unroll
+                    for (int c = 0; c < DP / 64; ++c) {
+                        const uint4 v = lds16(kt + chunk_at<DP>(mb * 16 + h * 8 + g, q4 * (DP / 64) + c));
+                        w[h][4 * c] = v.x;
+                        w[h][4 * c + 1] = v.y;
+                        w[h][4 * c + 2] = v.z;
+                        w[h][4 * c + 3] = v.w;
+                    }
+#pragma unroll
+                for (int k = 0; k < KS; ++k) {
+                    const uint32_t a0 = widen2(w[0][k]), a1 = widen2(w[1][k]);
+                    const uint32_t a2 = widen2(w[0][k] >> 16), a3 = widen2(w[1][k] >> 16);
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr) mma16816(s[mb][nr], a0, a1, a2, a3, qf[nr][k][0], qf[nr][k][1]);
                 }
-#pragma unroll
-                for (int k = 0; k < KS; ++k)
-                    mma16816(s[nb], qf[k][0], qf[k][1], qf[k][2], qf[k][3], widen2(w[k]), widen2(w[k] >> 16));
             }
-            // ---- softmax weights, two rows a thread
-            float weight[2];
+            // ---- softmax weights: rows 2 q4, 2 q4 + 1 (+ 8), tokens g, g + 8 of each 16
             const float before = top_scale;
+            float weight[2];
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
                 const float size = fabsf(vs[h]);
                 if (size <= 3.402823466e38f) top_scale = fmaxf(top_scale, size);
             }
 #pragma unroll
-            for (int h = 0; h < 2; ++h) weight[h] = vs[h] / top_scale * kWeightTop;
-            uint32_t pf[2][4];  // A fragments of the two 16-token steps
-            float keep[2];
+            for (int h = 0; h < 2; ++h) weight[h] = __fdividef(vs[h], top_scale) * kWeightTop;
+            uint32_t pf[2][NR][2];  // B fragments of the two 16-token steps
+            float keep[NR][2];
+            bool moved = before != top_scale;
 #pragma unroll
-            for (int half = 0; half < 2; ++half) {
-                float z[4][2];
-                float mx = m[half];
+            for (int nr = 0; nr < NR; ++nr) {
+                float wt[2][2][2];  // [16 tokens][token half][row]
 #pragma unroll
-                for (int nb = 0; nb < 4; ++nb) {
-                    const float f = factor[half] * ks[nb >> 1];
+                for (int e = 0; e < 2; ++e) {
+                    float z[2][2], mx = m[nr][e];
 #pragma unroll
-                    for (int e = 0; e < 2; ++e) {
-                        float x = s[nb][2 * half + e] * f;
-                        if (!whole) {
-                            const int pos = t0 + nb * 8 + q4 * 2 + e;
-                            const bool seen = pos < sees[half] && (nb < 2 ? page.x : page.y) >= 0;
-                            x = seen ? x : -INFINITY;
+                    for (int mb = 0; mb < 2; ++mb) {
+                        const float f = factor[nr][e] * ks[mb];
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            float x = s[mb][nr][2 * h + e] * f;
+                            if (!whole) {
+                                const int pos = t0 + mb * 16 + h * 8 + g;
+                                const bool seen = pos < sees[nr][e] && (mb ? page.y : page.x) >= 0;
+                                x = seen ? x : -INFINITY;
+                            }
+                            z[mb][h] = x;
+                            mx = fmaxf(mx, x);
                         }
-                        z[nb][e] = x;
-                        mx = fmaxf(mx, x);
                     }
-                }
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 1));
-                mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 2));
-                const float base = mx == -INFINITY ? 0.0f : mx;
-                keep[half] = exp2_fast(m[half] - base);
-                m[half] = mx;
-                l[half] *= keep[half];
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
+                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
+                    const float base = mx == -INFINITY ? 0.0f : mx;
+                    keep[nr][e] = exp2_fast(m[nr][e] - base);
+                    moved = moved || m[nr][e] != mx;
+                    m[nr][e] = mx;
+                    l[nr][e] *= keep[nr][e];
 #pragma unroll
-                for (int nb = 0; nb < 4; ++nb) {
-                    const float p0 = exp2_fast(z[nb][0] - base), p1 = exp2_fast(z[nb][1] - base);
-                    l[half] += p0 + p1;
-                    float w0 = p0 * weight[nb >> 1], w1 = p1 * weight[nb >> 1];
-                    if (!whole) {  // a scale that is not finite does not reach rows that do not see its page
-                        w0 = z[nb][0] == -INFINITY ? 0.0f : w0;
-                        w1 = z[nb][1] == -INFINITY ? 0.0f : w1;
-                    }
-                    pf[nb >> 1][(nb & 1) * 2 + half] = pack_half(w0, w1);
+                    for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                        for (int h = 0; h < 2; ++h) {
+                            const float p = exp2_fast(z[mb][h] - base);
+                            l[nr][e] += p;
+                            float x = p * weight[mb];
+                            // a scale that is not finite does not reach rows that do not see its page
+                            if (!whole) x = z[mb][h] == -INFINITY ? 0.0f : x;
+                            wt[mb][h][e] = x;
+                        }
+                    keep[nr][e] *= __fdividef(before, top_scale);
                 }
-                keep[half] *= before / top_scale;
+#pragma unroll
+                for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) pf[mb][nr][h] = transpose8(pack_half(wt[mb][h][0], wt[mb][h][1]));
             }
-            if (__any_sync(0xffffffffu, keep[0] != 1.0f || keep[1] != 1.0f)) {
+            if (__any_sync(0xffffffffu, moved)) {
 #pragma unroll
-                for (int j = 0; j < NB; ++j) {
-                    o[j][0] *= keep[0];
-                    o[j][1] *= keep[0];
-                    o[j][2] *= keep[1];
-                    o[j][3] *= keep[1];
-                }
+                for (int j = 0; j < MB; ++j)
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr) {
+                        o[j][nr][0] *= keep[nr][0];
+                        o[j][nr][1] *= keep[nr][1];
+                        o[j][nr][2] *= keep[nr][0];
+                        o[j][nr][3] *= keep[nr][1];
+                    }
             }
             // ---- values
             bool odd = false;  // a NaN code that some row may not see
@@ -500,28 +564,35 @@ __global__ void __launch_bounds__(kThreads, 1)
                 for (int k = 0; k < VW; ++k) {
                     const uint32_t x01 = __byte_perm(v[0][k], v[1][k], 0x5140), x23 = __byte_perm(v[0][k], v[1][k], 0x7362);
                     const uint32_t y01 = __byte_perm(v[2][k], v[3][k], 0x5140), y23 = __byte_perm(v[2][k], v[3][k], 0x7362);
-                    mma16816(o[4 * k], pf[st][0], pf[st][1], pf[st][2], pf[st][3], widen2(x01), widen2(y01));
-                    mma16816(o[4 * k + 1], pf[st][0], pf[st][1], pf[st][2], pf[st][3], widen2(x01 >> 16), widen2(y01 >> 16));
-                    mma16816(o[4 * k + 2], pf[st][0], pf[st][1], pf[st][2], pf[st][3], widen2(x23), widen2(y23));
-                    mma16816(o[4 * k + 3], pf[st][0], pf[st][1], pf[st][2], pf[st][3], widen2(x23 >> 16), widen2(y23 >> 16));
+                    const uint32_t a0 = widen2(x01), a1 = widen2(x01 >> 16), a2 = widen2(y01), a3 = widen2(y01 >> 16);
+                    const uint32_t b0 = widen2(x23), b1 = widen2(x23 >> 16), b2 = widen2(y23), b3 = widen2(y23 >> 16);
+#pragma unroll
+                    for (int nr = 0; nr < NR; ++nr) {
+                        mma16816(o[2 * k][nr], a0, a1, a2, a3, pf[st][nr][0], pf[st][nr][1]);
+                        mma16816(o[2 * k + 1][nr], b0, b1, b2, b3, pf[st][nr][0], pf[st][nr][1]);
+                    }
                 }
             }
             if (!whole && __any_sync(0xffffffffu, odd)) {
                 // the rows that see a NaN code get it, the others do not
+#pragma unroll 1
                 for (int row = 0; row < kTok; ++row) {
                     const int pos = t0 + row;
                     if (pos >= r.length || (row < 16 ? page.x : page.y) < 0) continue;
 #pragma unroll
-                    for (int j = 0; j < NB; ++j) {
-                        // n-block j: the thread's dimensions q4 * DP / 4 + j, + DP / 8
+                    for (int j = 0; j < MB; ++j) {
+                        // m-block j: the thread's dimensions g * DP / 8 + 2 j, + 1
 #pragma unroll
                         for (int e = 0; e < 2; ++e) {
-                            const int d = q4 * (DP / 4) + e * (DP / 8) + j;
+                            const int d = g * (DP / 8) + 2 * j + e;
                             uint32_t code;
                             asm volatile("ld.shared.u8 %0, [%1];" : "=r"(code) : "r"(vt + chunk_at<DP>(row, d >> 4) + (d & 15)));
                             if ((code & 0x7f) == 0x7f) {
-                                if (pos < sees[0]) o[j][e] = __int_as_float(0x7fffffff);
-                                if (pos < sees[1]) o[j][2 + e] = __int_as_float(0x7fffffff);
+#pragma unroll
+                                for (int nr = 0; nr < NR; ++nr) {
+                                    if (pos < sees[nr][0]) o[j][nr][2 * e] = __int_as_float(0x7fffffff);
+                                    if (pos < sees[nr][1]) o[j][nr][2 * e + 1] = __int_as_float(0x7fffffff);
+                                }
                             }
                         }
                     }
@@ -536,55 +607,62 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         turn = done - count;  // into the next segment
 
-        // ---- the segment's end: the warps' sums are joined, each warp taking two vectors of every lane
+        // ---- the segment's end: the warps' sums are joined, 4 vectors of every lane at a time
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            l[half] += __shfl_xor_sync(0xffffffffu, l[half], 1);
-            l[half] += __shfl_xor_sync(0xffffffffu, l[half], 2);
-            if (q4 == 0) {
-                sm.m[warp][g + 8 * half] = m[half];
-                sm.l[warp][g + 8 * half] = l[half];
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 4);
+                l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 8);
+                l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 16);
+                if (g == 0) {
+                    sm.m[warp][nr * 8 + 2 * q4 + e] = m[nr][e];
+                    sm.l[warp][nr * 8 + 2 * q4 + e] = l[nr][e];
+                }
             }
-        }
         __syncthreads();
-        float sum[2], big[2];
+        // a row's largest maximum and whole sum; a warp that saw nothing has no part, NaN sums stay
+        auto whole_row = [&](int row, float& big, float& sum) {
+            big = -INFINITY;
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            big[half] = -INFINITY;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) big[half] = fmaxf(big[half], sm.m[w][g + 8 * half]);
-            const float base = big[half] == -INFINITY ? 0.0f : big[half];
-            sum[half] = 0.0f;
+            for (int w = 0; w < kWarps; ++w) big = fmaxf(big, sm.m[w][row]);
+            const float base = big == -INFINITY ? 0.0f : big;
+            sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
-                const float lw = sm.l[w][g + 8 * half];
-                // a warp that saw nothing has no part; NaN sums stay NaN
-                sum[half] += lw == 0.0f ? 0.0f : lw * exp2_fast(sm.m[w][g + 8 * half] - base);
+                const float lw = sm.l[w][row];
+                sum += lw == 0.0f ? 0.0f : lw * exp2_fast(sm.m[w][row] - base);
             }
-            const float f = l[half] == 0.0f ? 0.0f : exp2_fast(m[half] - base) * (top_scale / kWeightTop);
+        };
 #pragma unroll
-            for (int j = 0; j < NB; ++j) {
-                o[j][2 * half] = l[half] == 0.0f ? 0.0f : o[j][2 * half] * f;
-                o[j][2 * half + 1] = l[half] == 0.0f ? 0.0f : o[j][2 * half + 1] * f;
+        for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                float big = -INFINITY;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) big = fmaxf(big, sm.m[w][nr * 8 + 2 * q4 + e]);
+                const float base = big == -INFINITY ? 0.0f : big;
+                const float f = l[nr][e] == 0.0f ? 0.0f : exp2_fast(m[nr][e] - base) * (top_scale / kWeightTop);
+#pragma unroll
+                for (int j = 0; j < MB; ++j)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h)
+                        o[j][nr][2 * h + e] = l[nr][e] == 0.0f ? 0.0f : o[j][nr][2 * h + e] * f;
             }
-        }
         const bool begins = first == 0, ends = first + count == at.s.tiles;
         const bool cut = !(begins && ends);
         const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
-        constexpr int HV = DP / 16;  // vectors of a row: 8, or 4
 #pragma unroll
-        for (int half = 0; half < 2; ++half) {
-            if (half == 1 && !upper) break;
-            if (half) __syncthreads();
+        for (int k0 = 0; k0 < kVectors; k0 += 4) {
+            if (k0) __syncthreads();
 #pragma unroll
-            for (int k = 0; k < HV; ++k) {
-                // vector k of the row: dimensions 4k .. 4k + 3 of the thread's DP / 4
-                const int j = (4 * k) % NB, e = (4 * k) / NB;
-                sm.join[warp][k][lane] = make_float4(o[j][2 * half + e], o[j + 1][2 * half + e], o[j + 2][2 * half + e],
-                                                     o[j + 3][2 * half + e]);
+            for (int k = k0; k < k0 + 4; ++k) {
+                const int e = k / VR, i = k % VR, nr = e >> 1, b = e & 1;
+                sm.join[warp][k - k0][lane] =
+                    make_float4(o[2 * i][nr][b], o[2 * i][nr][2 + b], o[2 * i + 1][nr][b], o[2 * i + 1][nr][2 + b]);
             }
             __syncthreads();
-            if (warp < HV) {
+            if (warp < 4) {
                 float4 x = sm.join[0][warp][lane];
 #pragma unroll
                 for (int w = 1; w < kWarps; ++w) {
@@ -594,52 +672,54 @@ __global__ void __launch_bounds__(kThreads, 1)
                     x.z += y.z;
                     x.w += y.w;
                 }
-                const int k = half * HV + warp;
+                const int k = k0 + warp;
                 if (cut) {
                     pieces[slot].o[k * 32 + lane] = x;
                 } else {
-                    write_vector<DP>(a, r, head, row_tile, group, k, lane, x, sum[half], big[half], out_wide);
+                    int row, dim;
+                    vector_place<DP>(k, lane, row, dim);
+                    float big, sum;
+                    whole_row(row, big, sum);
+                    write_vector<DP, NR>(a, r, head, row_tile, group, k, lane, x, sum, big, out_wide);
                 }
             }
         }
         if (cut) {
-            if (warp == 0 && q4 == 0) {
-#pragma unroll
-                for (int half = 0; half < 2; ++half) {
-                    pieces[slot].m[g + 8 * half] = big[half];
-                    pieces[slot].l[g + 8 * half] = sum[half];
-                }
+            if (tid < kRows) {
+                float big, sum;
+                whole_row(tid, big, sum);
+                pieces[slot].m[tid] = big;
+                pieces[slot].l[tid] = sum;
             }
             if (tid == 0) infos[slot] = PieceInfo{at.b, at.item, begins, ends};
         }
         __syncthreads();  // sm.join, sm.m and sm.l are free again
         left -= count;
         at.tile += count;
-        if (left > 0) settle(a, at, group);
+        if (left > 0) settle<NR>(a, at, group);
     }
 }
 
 // One block for each block of the first launch: if a request was cut behind
 // its first tokens there, the block joins all of its pieces, in order.
-template <int DP>
-__global__ void __launch_bounds__(kThreads) attention_join_kernel(const AttentionArgs a, int blocks,
-                                                                  const PieceInfo* infos, const Piece<DP>* pieces,
-                                                                  bool out_wide) {
+template <int DP, int NR>
+__global__ void __launch_bounds__(256) attention_join_kernel(const AttentionArgs a, int blocks, const PieceInfo* infos,
+                                                             const Piece<DP, NR>* pieces, bool out_wide) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PieceInfo info = infos[2 * blockIdx.x + 1];
     if (info.request < 0 || info.ends) return;
     const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
     const int group = a.q_heads / a.heads;
-    const Span s = span_of(a, info.request, group);
+    const Span s = span_of<NR>(a, info.request, group);
     const int head = info.unit / s.row_tiles, row_tile = info.unit - head * s.row_tiles;
     int last = blockIdx.x + 1;
     while (last < blocks - 1 && !infos[2 * last].ends) ++last;
-    constexpr int V = 2 * DP / 16;
-    for (int k = warp; k < V; k += kWarps) {
+    constexpr int V = 2 * NR * DP / 32;
+    for (int k = warp; k < V; k += 8) {
         int row, dim;
         vector_place<DP>(k, lane, row, dim);
-        if (row_tile * kRows + row >= s.r.n * group) continue;
-        const Piece<DP>* p = pieces + 2 * blockIdx.x + 1;
+        if (row_tile * 8 * NR + row >= s.r.n * group) continue;
+        const Piece<DP, NR>* p = pieces + 2 * blockIdx.x + 1;
         float m = p->m[row];
         for (int c = blockIdx.x + 1; c <= last; ++c) m = fmaxf(m, pieces[2 * c].m[row]);
         const float base = m == -INFINITY ? 0.0f : m;
@@ -656,7 +736,7 @@ __global__ void __launch_bounds__(kThreads) attention_join_kernel(const Attentio
             x.z = fmaf(y.z, f, x.z);
             x.w = fmaf(y.w, f, x.w);
         }
-        write_vector<DP>(a, s.r, head, row_tile, group, k, lane, x, l, m, out_wide);
+        write_vector<DP, NR>(a, s.r, head, row_tile, group, k, lane, x, l, m, out_wide);
     }
 }
 
@@ -667,7 +747,7 @@ bool wide_rows(const void* p, int64_t token, int64_t head, int64_t bytes) {
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
 
-template <int DP>
+template <int DP, int NR>
 cudaError_t launch(const AttentionArgs& a, cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -686,38 +766,39 @@ cudaError_t launch(const AttentionArgs& a, cudaStream_t stream) {
         return cudaErrorInvalidValue;
     uint8_t* const w = static_cast<uint8_t*>(a.workspace);
     PieceInfo* const infos = reinterpret_cast<PieceInfo*>(w);
-    Piece<DP>* const pieces = reinterpret_cast<Piece<DP>*>(w + round16(sizeof(PieceInfo) * 2 * blocks));
-    const size_t smem = sizeof(Smem<DP>) + 1024;
-    e = cudaFuncSetAttribute(attention_split_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
+    Piece<DP, NR>* const pieces = reinterpret_cast<Piece<DP, NR>*>(w + round16(sizeof(PieceInfo) * 2 * blocks));
+    const size_t smem = sizeof(Smem<DP, NR>) + 1024;
+    e = cudaFuncSetAttribute(attention_split_kernel<DP, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
                              static_cast<int>(smem));
     if (e != cudaSuccess) return e;
     const bool q_wide = wide_rows(a.q, a.q_token_stride, a.q_head_stride, 16);
     const bool out_wide = wide_rows(a.out, a.out_token_stride, a.out_head_stride, 8);
-    attention_split_kernel<DP><<<blocks, kThreads, smem, stream>>>(a, maps, device_error_word(), infos, pieces, q_wide,
+    attention_split_kernel<DP, NR><<<blocks, 32 * Shape<NR>::kWarps, smem, stream>>>(a, maps, device_error_word(), infos, pieces, q_wide,
                                                                    out_wide);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);
-    cfg.blockDim = dim3(kThreads);
+    cfg.blockDim = dim3(256);
     cfg.stream = stream;
     cudaLaunchAttribute attr;
     attr.id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &attr;
     cfg.numAttrs = 1;
-    return cudaLaunchKernelEx(&cfg, attention_join_kernel<DP>, a, blocks, static_cast<const PieceInfo*>(infos),
-                              static_cast<const Piece<DP>*>(pieces), out_wide);
+    return cudaLaunchKernelEx(&cfg, attention_join_kernel<DP, NR>, a, blocks, static_cast<const PieceInfo*>(infos),
+                              static_cast<const Piece<DP, NR>*>(pieces), out_wide);
 }
 
 }  // namespace
 
 size_t attention_split_workspace(int64_t dim, int sms) {
-    const size_t piece = dim <= 64 ? sizeof(Piece<64>) : sizeof(Piece<128>);
+    const size_t piece = dim <= 64 ? sizeof(Piece<64, 2>) : sizeof(Piece<128, 2>);
     return round16(sizeof(PieceInfo) * 2 * sms) + 2 * piece * sms;
 }
 
 cudaError_t launch_attention_split(const AttentionArgs& a, cudaStream_t stream) {
-    return a.dim <= 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+    if (a.max_added * (a.q_heads / a.heads) <= 8) return a.dim <= 64 ? launch<64, 1>(a, stream) : launch<128, 1>(a, stream);
+    return a.dim <= 64 ? launch<64, 2>(a, stream) : launch<128, 2>(a, stream);
 }
 
 }  // namespace lik
