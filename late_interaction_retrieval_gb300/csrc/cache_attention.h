@@ -12,6 +12,10 @@
 namespace lik {
 namespace attn {
 
+// log2 of the largest weight, and of a row's largest one when its reference is set; the reference before
+// the row has seen a token.
+constexpr float kLogTop = 15.0f, kLogStart = 7.0f, kNothing = -1048576.0f;
+
 // One request as the device has it, clamped to what the buffers hold.
 struct Request {
     int row0, n;   // its rows

@@ -18,10 +18,13 @@
 // dimensions of 4 tokens, transposed by byte permutes.  The weights go from
 // the one product's layout to the other's by an 8x8 transpose in registers.
 //
-// Rows are scaled to fp16's range by a power of two.  The softmax weights are
-// 2^15 * exp(z - max) * (the page's scale / the largest so far), rounded to
-// fp16: 11 bits over 29 binades, below which a weight's share of the sum is
-// under 2^-29.  Statistics, sums and the join are fp32.
+// Rows are scaled to fp16's range by a power of two.  A softmax weight is
+// rounded to fp16 as 2^7 exp(z - ref) * (the page's scale / c): ref is a power
+// of two near the row's largest weight, and moves only where one passes 2^15;
+// c is a power of two not below the scales.  So a unit needs no maximum over
+// the warp, and sums are seldom rescaled, exactly.  11 bits are kept over 20
+// binades below the largest weight, 2^-31 of it is lost.  Statistics, sums and
+// the join are fp32.
 #include "cache_attention.h"
 #include "tmap.h"
 
@@ -31,7 +34,6 @@ namespace {
 using namespace attn;
 
 constexpr int kTok = 32;  // tokens of a unit
-constexpr float kWeightTop = 32768.0f;
 
 // Blocks of 8 rows (NR of them), warps of a block and stages of a warp's ring:
 // 16 rows need more registers, so fewer warps with deeper rings.
@@ -92,9 +94,9 @@ __device__ __forceinline__ Span span_of(const AttentionArgs& a, int b, int group
     return s;
 }
 
-// A place in the order of units.
+// A place in the order of units: requests, key heads, row tiles, tiles.
 struct Cursor {
-    int b, item, tile;  // item: head * row_tiles + row tile
+    int b, head, row_tile, tile;
     Span s;
 };
 
@@ -102,16 +104,17 @@ template <int NR>
 __device__ __forceinline__ void settle(const AttentionArgs& a, Cursor& c, int group) {
     while (c.tile >= c.s.tiles) {
         c.tile -= c.s.tiles;
-        if (++c.item >= c.s.row_tiles * a.heads) {
-            c.item = 0;
-            do {
-                if (++c.b >= a.requests) {
-                    c.s.tiles = INT32_MAX;  // behind the last unit
-                    return;
-                }
-                c.s = span_of<NR>(a, c.b, group);
-            } while (c.s.tiles == 0);
-        }
+        if (++c.row_tile < c.s.row_tiles) continue;
+        c.row_tile = 0;
+        if (++c.head < a.heads) continue;
+        c.head = 0;
+        do {
+            if (++c.b >= a.requests) {
+                c.s.tiles = INT32_MAX;  // behind the last unit
+                return;
+            }
+            c.s = span_of<NR>(a, c.b, group);
+        } while (c.s.tiles == 0);
     }
 }
 
@@ -269,7 +272,9 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
         }
         load.b = b;
         load.s = s;
-        load.item = static_cast<int>(rest / s.tiles);
+        const int item = static_cast<int>(rest / s.tiles);
+        load.head = item / s.row_tiles;
+        load.row_tile = item - load.head * s.row_tiles;
         load.tile = static_cast<int>(rest % s.tiles);
     }
     Cursor at = load;  // the block's place: the segment that all its warps are in
@@ -298,7 +303,7 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
             // an entry outside the pool hides its tokens: page 0 is loaded, and not looked at
             if (p.x < 0 || p.x >= a.pages) p.x = -1;
             if (p.y < 0 || p.y >= a.pages) p.y = -1;
-            const int head = load.item / load.s.row_tiles;
+            const int head = load.head;
             const int t0 = load.tile * kTok;
             if (lane < 4) {
                 const int pg = lane < 2 ? p.x : p.y;
@@ -346,7 +351,7 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
     while (left > 0) {
         // ---- a segment: the rest of this (request, head, row tile), as far as the block's range goes
         const Request r = at.s.r;
-        const int head = at.item / at.s.row_tiles, row_tile = at.item - head * at.s.row_tiles;
+        const int head = at.head, row_tile = at.row_tile;
         const int first = at.tile;
         const int count = static_cast<int>(min(static_cast<long long>(at.s.tiles - first), left));
         const int rows_in = min(kRows, r.n * group - row_tile * kRows);
@@ -413,13 +418,25 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
         for (int j = 0; j < MB; ++j)
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) o[j][nr][0] = o[j][nr][1] = o[j][nr][2] = o[j][nr][3] = 0.0f;
-        float m[NR][2], l[NR][2];
+        float ref[NR][2], l[NR][2];
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-            m[nr][0] = m[nr][1] = -INFINITY;
+            ref[nr][0] = ref[nr][1] = kNothing;
             l[nr][0] = l[nr][1] = 0.0f;
         }
-        float top_scale = kLeastScale;
+        float c = 0.0f, logc = -127.0f;  // and its log2
+        bool some = false;               // whether o holds anything
+        auto rescale = [&](const float (&keep)[NR][2]) {
+#pragma unroll
+            for (int j = 0; j < MB; ++j)
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    o[j][nr][0] *= keep[nr][0];
+                    o[j][nr][1] *= keep[nr][1];
+                    o[j][nr][2] *= keep[nr][0];
+                    o[j][nr][3] *= keep[nr][1];
+                }
+        };
 
         int done = turn;
         for (; done < count; done += kWarps) {
@@ -459,76 +476,91 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
                 }
             }
             // ---- softmax weights: rows 2 q4, 2 q4 + 1 (+ 8), tokens g, g + 8 of each 16
-            const float before = top_scale;
-            float weight[2];
+            float vmost = vs[0] <= 3.402823466e38f ? fmaxf(vs[0], 0.0f) : 0.0f;
+            vmost = vs[1] <= 3.402823466e38f ? fmaxf(vmost, vs[1]) : vmost;
+            if (vmost > c) {  // the same in every lane
+                const float to = __int_as_float(min((__float_as_int(vmost) & 0x7f800000) + (1 << 23), 0x7f000000));
+                if (some) {
+                    float keep[NR][2];
 #pragma unroll
-            for (int h = 0; h < 2; ++h) {
-                const float size = fabsf(vs[h]);
-                if (size <= 3.402823466e38f) top_scale = fmaxf(top_scale, size);
-            }
-#pragma unroll
-            for (int h = 0; h < 2; ++h) weight[h] = __fdividef(vs[h], top_scale) * kWeightTop;
-            uint32_t pf[2][NR][2];  // B fragments of the two 16-token steps
-            float keep[NR][2];
-            bool moved = before != top_scale;
-#pragma unroll
-            for (int nr = 0; nr < NR; ++nr) {
-                float wt[2][2][2];  // [16 tokens][token half][row]
-#pragma unroll
-                for (int e = 0; e < 2; ++e) {
-                    float z[2][2], mx = m[nr][e];
-#pragma unroll
-                    for (int mb = 0; mb < 2; ++mb) {
-                        const float f = factor[nr][e] * ks[mb];
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            float x = s[mb][nr][2 * h + e] * f;
-                            if (!whole) {
-                                const int pos = t0 + mb * 16 + h * 8 + g;
-                                const bool seen = pos < sees[nr][e] && (mb ? page.y : page.x) >= 0;
-                                x = seen ? x : -INFINITY;
-                            }
-                            z[mb][h] = x;
-                            mx = fmaxf(mx, x);
-                        }
-                    }
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 4));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 8));
-                    mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, 16));
-                    const float base = mx == -INFINITY ? 0.0f : mx;
-                    keep[nr][e] = exp2_fast(m[nr][e] - base);
-                    moved = moved || m[nr][e] != mx;
-                    m[nr][e] = mx;
-                    l[nr][e] *= keep[nr][e];
-#pragma unroll
-                    for (int mb = 0; mb < 2; ++mb)
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            const float p = exp2_fast(z[mb][h] - base);
-                            l[nr][e] += p;
-                            float x = p * weight[mb];
-                            // a scale that is not finite does not reach rows that do not see its page
-                            if (!whole) x = z[mb][h] == -INFINITY ? 0.0f : x;
-                            wt[mb][h][e] = x;
-                        }
-                    keep[nr][e] *= __fdividef(before, top_scale);
+                    for (int nr = 0; nr < NR; ++nr) keep[nr][0] = keep[nr][1] = c / to;
+                    rescale(keep);
                 }
+                c = to;
+                logc = static_cast<float>((__float_as_int(to) >> 23) - 127);
+            }
+            some = true;
+            // log2 of the weights' factors; 2^-60 of c stands in for smaller scales (their fp16 weights are 0 then)
+            // and for one that is not finite, whose weights become NaN below: the sums do not depend on it
+            float lw[2], out_of[2];
+            const bool broken = !(vs[0] <= 3.402823466e38f && vs[1] <= 3.402823466e38f);
+#pragma unroll
+            for (int mb = 0; mb < 2; ++mb) {
+                const bool usual = vs[mb] > c * 8.67361738e-19f && vs[mb] <= 3.402823466e38f;
+                lw[mb] = usual ? __log2f(vs[mb]) + (kLogStart - logc) : kLogStart - 60.0f;
+                out_of[mb] = exp2_fast(-lw[mb]);
+            }
+            float z[2][NR][4];  // log2 of the weights
+            auto weigh = [&]() {
+                float top = -INFINITY;
 #pragma unroll
                 for (int mb = 0; mb < 2; ++mb)
 #pragma unroll
-                    for (int h = 0; h < 2; ++h) pf[mb][nr][h] = transpose8(pack_half(wt[mb][h][0], wt[mb][h][1]));
-            }
-            if (__any_sync(0xffffffffu, moved)) {
+                    for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
-                for (int j = 0; j < MB; ++j)
+                        for (int i = 0; i < 4; ++i) {
+                            const int e = i & 1;
+                            float x = fmaf(s[mb][nr][i], factor[nr][e] * ks[mb], lw[mb] - ref[nr][e]);
+                            if (!whole) {
+                                const int pos = t0 + mb * 16 + (i >> 1) * 8 + g;
+                                x = pos < sees[nr][e] && (mb ? page.y : page.x) >= 0 ? x : -INFINITY;
+                            }
+                            z[mb][nr][i] = x;
+                            top = fmaxf(top, x);
+                        }
+                return top;
+            };
+            if (__any_sync(0xffffffffu, weigh() > kLogTop)) {
+                float keep[NR][2];
 #pragma unroll
-                    for (int nr = 0; nr < NR; ++nr) {
-                        o[j][nr][0] *= keep[nr][0];
-                        o[j][nr][1] *= keep[nr][1];
-                        o[j][nr][2] *= keep[nr][0];
-                        o[j][nr][3] *= keep[nr][1];
+                for (int nr = 0; nr < NR; ++nr)
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float top = fmaxf(fmaxf(z[0][nr][e], z[0][nr][2 + e]), fmaxf(z[1][nr][e], z[1][nr][2 + e]));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 4));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
+                        top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
+                        keep[nr][e] = 1.0f;
+                        if (top > kLogTop) {
+                            const float by = ceilf(top) - kLogStart;
+                            keep[nr][e] = exp2_fast(-by);  // 0 for the first tokens that a row sees
+                            ref[nr][e] += by;
+                            l[nr][e] *= keep[nr][e];
+                        }
                     }
+                rescale(keep);
+                weigh();
             }
+            uint32_t pf[2][NR][2];  // B fragments of the two 16-token steps
+#pragma unroll
+            for (int mb = 0; mb < 2; ++mb)
+#pragma unroll
+                for (int nr = 0; nr < NR; ++nr) {
+                    float p[4];
+#pragma unroll
+                    for (int i = 0; i < 4; ++i) p[i] = exp2_fast(z[mb][nr][i]);
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        l[nr][e] = fmaf(p[e] + p[2 + e], out_of[mb], l[nr][e]);
+                    }
+                    if (broken) {
+#pragma unroll
+                        for (int i = 0; i < 4; ++i)
+                            if (!(vs[mb] <= 3.402823466e38f) && z[mb][nr][i] != -INFINITY) p[i] = __int_as_float(0x7fffffff);
+                    }
+                    pf[mb][nr][0] = transpose8(pack_half(p[0], p[1]));
+                    pf[mb][nr][1] = transpose8(pack_half(p[2], p[3]));
+                }
             // ---- values
             bool odd = false;  // a NaN code that some row may not see
 #pragma unroll
@@ -616,33 +648,31 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
                 l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 8);
                 l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 16);
                 if (g == 0) {
-                    sm.m[warp][nr * 8 + 2 * q4 + e] = m[nr][e];
+                    sm.m[warp][nr * 8 + 2 * q4 + e] = ref[nr][e];
                     sm.l[warp][nr * 8 + 2 * q4 + e] = l[nr][e];
                 }
             }
         __syncthreads();
         // a row's largest maximum and whole sum; a warp that saw nothing has no part, NaN sums stay
         auto whole_row = [&](int row, float& big, float& sum) {
-            big = -INFINITY;
+            big = kNothing;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) big = fmaxf(big, sm.m[w][row]);
-            const float base = big == -INFINITY ? 0.0f : big;
             sum = 0.0f;
 #pragma unroll
             for (int w = 0; w < kWarps; ++w) {
                 const float lw = sm.l[w][row];
-                sum += lw == 0.0f ? 0.0f : lw * exp2_fast(sm.m[w][row] - base);
+                sum += lw == 0.0f ? 0.0f : lw * exp2_fast(sm.m[w][row] - big);
             }
         };
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                float big = -INFINITY;
+                float big = kNothing;
 #pragma unroll
                 for (int w = 0; w < kWarps; ++w) big = fmaxf(big, sm.m[w][nr * 8 + 2 * q4 + e]);
-                const float base = big == -INFINITY ? 0.0f : big;
-                const float f = l[nr][e] == 0.0f ? 0.0f : exp2_fast(m[nr][e] - base) * (top_scale / kWeightTop);
+                const float f = l[nr][e] == 0.0f ? 0.0f : exp2_fast(ref[nr][e] - big) * (c * 0.0078125f);  // 2^-7 c
 #pragma unroll
                 for (int j = 0; j < MB; ++j)
 #pragma unroll
@@ -691,7 +721,7 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
                 pieces[slot].m[tid] = big;
                 pieces[slot].l[tid] = sum;
             }
-            if (tid == 0) infos[slot] = PieceInfo{at.b, at.item, begins, ends};
+            if (tid == 0) infos[slot] = PieceInfo{at.b, head * at.s.row_tiles + row_tile, begins, ends};
         }
         __syncthreads();  // sm.join, sm.m and sm.l are free again
         left -= count;
@@ -705,38 +735,74 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
 template <int DP, int NR>
 __global__ void __launch_bounds__(256) attention_join_kernel(const AttentionArgs a, int blocks, const PieceInfo* infos,
                                                              const Piece<DP, NR>* pieces, bool out_wide) {
+    constexpr int kRows = 8 * NR, kMost = 64;  // pieces whose factors are kept at a time
+    __shared__ float factor[kMost][kRows], sum[kMost][kRows];
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PieceInfo info = infos[2 * blockIdx.x + 1];
     if (info.request < 0 || info.ends) return;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int group = a.q_heads / a.heads;
     const Span s = span_of<NR>(a, info.request, group);
     const int head = info.unit / s.row_tiles, row_tile = info.unit - head * s.row_tiles;
-    int last = blockIdx.x + 1;
-    while (last < blocks - 1 && !infos[2 * last].ends) ++last;
-    constexpr int V = 2 * NR * DP / 32;
-    for (int k = warp; k < V; k += 8) {
-        int row, dim;
-        vector_place<DP>(k, lane, row, dim);
-        if (row_tile * 8 * NR + row >= s.r.n * group) continue;
-        const Piece<DP, NR>* p = pieces + 2 * blockIdx.x + 1;
-        float m = p->m[row];
-        for (int c = blockIdx.x + 1; c <= last; ++c) m = fmaxf(m, pieces[2 * c].m[row]);
-        const float base = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f;
-        float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
-        for (int c = blockIdx.x; c <= last; ++c) {
-            p = pieces + (c == static_cast<int>(blockIdx.x) ? 2 * c + 1 : 2 * c);
-            if (p->l[row] == 0.0f) continue;
-            const float f = exp2_fast(p->m[row] - base);
-            const float4 y = p->o[k * 32 + lane];
-            l = fmaf(p->l[row], f, l);
-            x.x = fmaf(y.x, f, x.x);
-            x.y = fmaf(y.y, f, x.y);
-            x.z = fmaf(y.z, f, x.z);
-            x.w = fmaf(y.w, f, x.w);
+    const int first = blockIdx.x;
+    int n = 1;  // pieces: of this block and the blocks behind it
+    while (first + n < blocks) {
+        const int c = first + n + lane;
+        const unsigned ends = __ballot_sync(0xffffffffu, c >= blocks || infos[2 * c].ends);
+        n += ends ? __ffs(ends) : 32;
+        if (ends) break;
+    }
+    n = min(n, blocks - first);
+    auto piece = [&](int i) { return pieces + 2 * (first + i) + (i == 0 ? 1 : 0); };
+    constexpr int V = 2 * NR * DP / 32, kEach = (V + 7) / 8;
+    float m[kEach], l[kEach];
+    float4 x[kEach];
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        m[j] = kNothing;
+        l[j] = 0.0f;
+        x[j] = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+    }
+    for (int i0 = 0; i0 < n; i0 += kMost) {
+        const int some = min(kMost, n - i0);
+        for (int i = tid; i < some * kRows; i += 256) {
+            factor[i / kRows][i % kRows] = piece(i0 + i / kRows)->m[i % kRows];
+            sum[i / kRows][i % kRows] = piece(i0 + i / kRows)->l[i % kRows];
         }
-        write_vector<DP, NR>(a, s.r, head, row_tile, group, k, lane, x, l, m, out_wide);
+        __syncthreads();
+#pragma unroll
+        for (int j = 0; j < kEach; ++j) {
+            const int k = warp + 8 * j;
+            if (k >= V) continue;
+            int row, dim;
+            vector_place<DP>(k, lane, row, dim);
+            float big = m[j];
+            for (int i = 0; i < some; ++i) big = fmaxf(big, factor[i][row]);
+            const float keep = exp2_fast(m[j] - big);
+            m[j] = big;
+            l[j] *= keep;
+            x[j].x *= keep;
+            x[j].y *= keep;
+            x[j].z *= keep;
+            x[j].w *= keep;
+#pragma unroll 8
+            for (int i = 0; i < some; ++i) {
+                const float4 y = piece(i0 + i)->o[k * 32 + lane];
+                const float li = sum[i][row], f = li == 0.0f ? 0.0f : exp2_fast(factor[i][row] - big);
+                // a piece that saw nothing holds zeros
+                l[j] = fmaf(li, f, l[j]);
+                x[j].x = fmaf(y.x, f, x[j].x);
+                x[j].y = fmaf(y.y, f, x[j].y);
+                x[j].z = fmaf(y.z, f, x[j].z);
+                x[j].w = fmaf(y.w, f, x[j].w);
+            }
+        }
+        __syncthreads();
+    }
+#pragma unroll
+    for (int j = 0; j < kEach; ++j) {
+        const int k = warp + 8 * j;
+        if (k < V) write_vector<DP, NR>(a, s.r, head, row_tile, group, k, lane, x[j], l[j], m[j], out_wide);
     }
 }
 

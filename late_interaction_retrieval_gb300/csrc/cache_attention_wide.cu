@@ -39,9 +39,6 @@ constexpr int kRaw = 6;         // raw tiles of one operand
 constexpr int kKeys = 3, kValues = 4;  // operand tiles
 constexpr int kAhead = 2;       // steps of a stream whose scores are computed ahead
 constexpr int kScaleRing = 16;  // tiles whose scales are kept
-constexpr float kLogTop = 15.0f, kLogStart = 7.0f;  // log2 of the largest weight, and of a maximum's when it is set
-constexpr float kNothing = -1048576.0f;            // a row's reference before it has seen a token
-
 // warps
 constexpr int kConvert = 8, kLoad = 16, kMma = 17, kBusy = 19;  // converters of K, of V; an issuer of MMAs a stream
 
@@ -624,6 +621,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int all_see = w.x.r.length - w.x.r.n + (w.x.item * kItemRows) / group + 1;
             const bool idle = __ballot_sync(0xffffffffu, live) == 0;  // no row of this warp's: its weights do not matter
             float factor = 0.0f, ref = kNothing, l = 0.0f, cref = 0.0f, logc = -127.0f;  // logc: log2 of cref
+            bool nan_scale = false;  // the row sees a page whose values' scale is not finite
             if (steps > 0) {
                 // the row of q, scaled to fp16's range
                 const uint16_t* const src = static_cast<const uint16_t*>(a.q) + (w.x.r.row0 + i) * a.q_token_stride +
@@ -714,12 +712,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         logc = static_cast<float>((__float_as_int(to) >> 23) - 127);
                     };
                     // log2 of a group's weight (c: 2^7).  2^-60 of c stands in for smaller scales (their fp16
-                    // weights are 0 then).  A factor is never 0: a hidden token's score is -inf.  Scales that are
-                    // not finite do not reach rows that see none of their tokens.
+                    // weights are 0 then) and for one that is not finite, which makes the whole row's output NaN: the
+                    // sums do not depend on it.  A factor is never 0: a hidden token's score is -inf.  A factor that
+                    // is not finite does not reach rows that see none of its tokens.
                     auto weigh = [&](float4 x, bool seen, float& f, float& w) {
                         f = x.x * factor;
                         f = f <= 1e-37f || !seen ? 1e-37f : f;
-                        w = x.y <= cref * 8.67361738e-19f || !seen ? kLogStart - 60.0f : x.z + (kLogStart - logc);
+                        const bool finite = x.y <= 3.402823466e38f;
+                        nan_scale = nan_scale || (seen && !finite);
+                        w = x.y > cref * 8.67361738e-19f && finite ? x.z + (kLogStart - logc) : kLogStart - 60.0f;
                     };
                     if (even) {
                         const float4 x = sm.scale[at][0];
@@ -831,7 +832,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     if (join) {
                         // stream 0's warp of the same rows reads this stream's O, and beside it, in the columns of
                         // scores that are no longer needed, its maximum, sum and scale
-                        uint32_t x[16] = {__float_as_uint(ref), __float_as_uint(l), __float_as_uint(cref * 0.0078125f)};
+                        uint32_t x[16] = {__float_as_uint(ref), __float_as_uint(l), __float_as_uint(cref * 0.0078125f), nan_scale};
                         tmem_st_16(tmem + lanes + kColS + 128, x);
                         ptx::tmem_wait_st();
                         ptx::tc_fence_before();
@@ -860,6 +861,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         // a side without weights has no part; NaN sums stay
                         f0 = l == 0.0f ? 0.0f : f0 * k0;
                         f1 = l1 == 0.0f ? 0.0f : __uint_as_float(x[2]) * k1;
+                        nan_scale = nan_scale || x[3];
                         l = (l == 0.0f ? 0.0f : l * k0) + (l1 == 0.0f ? 0.0f : l1 * k1);
                     }
                     const float g = cut ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
@@ -876,7 +878,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             for (int j = 0; j < 8; ++j) {
                                 float o = f0 == 0.0f ? 0.0f : __uint_as_float(v[8 * e + j]) * f0;
                                 if (join && f1 != 0.0f) o = fmaf(__uint_as_float(y[8 * e + j]), f1, o);
-                                f[j] = o * g;
+                                f[j] = nan_scale ? __int_as_float(0x7fffffff) : o * g;
                             }
                             if (nan && live && d < a.dim) {
                                 // NaN codes that were set apart: those of tokens that this row sees

@@ -423,8 +423,8 @@ def test_attention_nan_of_tokens_that_a_row_does_not_see():
         got = run_attention(*case, 0.125)
         assert_attention((got[0], None), want)
     # the last token opens a page whose scales are not finite
-    for bad in (NAN, INF):
-        q, kc, vc, ks, vs, table, offsets, lengths = case = _requests(_gen(8), [33, 12], [2, 1], 1, 2, 64, 16, "f16")
+    for bad, group in ((NAN, 2), (INF, 2), (NAN, 20), (INF, 20)):
+        q, kc, vc, ks, vs, table, offsets, lengths = case = _requests(_gen(8), [33, 12], [2, 1], 1, group, 64, 16, "f16")
         vs[int(table[0, 2]), 0] = bad
         got = run_attention(*case, 0.125)
         want = ref.attention(*case, 0.125)
