@@ -65,7 +65,7 @@ struct Smem {
     static constexpr int kTile = kTok * DP;  // bytes of one operand's tile
     alignas(1024) uint8_t ring[kWarps][kStages][2][kTile];
     float4 join[kWarps][4][32];  // 4 vectors of every lane's sums at a time
-    float m[kWarps][8 * NR], l[kWarps][8 * NR];
+    float m[kWarps][8 * NR], l[kWarps][8 * NR], c[kWarps];
     float scale[kWarps][kStages][4];  // keys' and values' of the first 16 tokens, of the last 16
     uint64_t full[kWarps][kStages];
     int2 page[kWarps][kStages];
@@ -639,7 +639,7 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
         }
         turn = done - count;  // into the next segment
 
-        // ---- the segment's end: the warps' sums are joined, 4 vectors of every lane at a time
+        // ---- the segment's end: the warps' sums are joined, 4 vectors of every lane at a time, each by one warp
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -652,33 +652,7 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
                     sm.l[warp][nr * 8 + 2 * q4 + e] = l[nr][e];
                 }
             }
-        __syncthreads();
-        // a row's largest maximum and whole sum; a warp that saw nothing has no part, NaN sums stay
-        auto whole_row = [&](int row, float& big, float& sum) {
-            big = kNothing;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) big = fmaxf(big, sm.m[w][row]);
-            sum = 0.0f;
-#pragma unroll
-            for (int w = 0; w < kWarps; ++w) {
-                const float lw = sm.l[w][row];
-                sum += lw == 0.0f ? 0.0f : lw * exp2_fast(sm.m[w][row] - big);
-            }
-        };
-#pragma unroll
-        for (int nr = 0; nr < NR; ++nr)
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                float big = kNothing;
-#pragma unroll
-                for (int w = 0; w < kWarps; ++w) big = fmaxf(big, sm.m[w][nr * 8 + 2 * q4 + e]);
-                const float f = l[nr][e] == 0.0f ? 0.0f : exp2_fast(ref[nr][e] - big) * (c * 0.0078125f);  // 2^-7 c
-#pragma unroll
-                for (int j = 0; j < MB; ++j)
-#pragma unroll
-                    for (int h = 0; h < 2; ++h)
-                        o[j][nr][2 * h + e] = l[nr][e] == 0.0f ? 0.0f : o[j][nr][2 * h + e] * f;
-            }
+        if (lane == 0) sm.c[warp] = c * 0.0078125f;  // 2^-7 c: what a weight of 1 stands for
         const bool begins = first == 0, ends = first + count == at.s.tiles;
         const bool cut = !(begins && ends);
         const int slot = 2 * blockIdx.x + (begins ? 1 : 0);
@@ -693,36 +667,37 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
             }
             __syncthreads();
             if (warp < 4) {
-                float4 x = sm.join[0][warp][lane];
-#pragma unroll
-                for (int w = 1; w < kWarps; ++w) {
-                    const float4 y = sm.join[w][warp][lane];
-                    x.x += y.x;
-                    x.y += y.y;
-                    x.z += y.z;
-                    x.w += y.w;
-                }
                 const int k = k0 + warp;
+                int row, dim;
+                vector_place<DP>(k, lane, row, dim);
+                float big = kNothing, sum = 0.0f;
+#pragma unroll
+                for (int w = 0; w < kWarps; ++w) big = fmaxf(big, sm.m[w][row]);
+                float4 x = make_float4(0.0f, 0.0f, 0.0f, 0.0f);
+#pragma unroll 4
+                for (int w = 0; w < kWarps; ++w) {
+                    const float lw = sm.l[w][row];
+                    if (lw == 0.0f) continue;  // a warp that saw nothing has no part, NaN sums stay
+                    const float f = exp2_fast(sm.m[w][row] - big), fc = f * sm.c[w];
+                    const float4 y = sm.join[w][warp][lane];
+                    sum = fmaf(lw, f, sum);
+                    x.x = fmaf(y.x, fc, x.x);
+                    x.y = fmaf(y.y, fc, x.y);
+                    x.z = fmaf(y.z, fc, x.z);
+                    x.w = fmaf(y.w, fc, x.w);
+                }
                 if (cut) {
                     pieces[slot].o[k * 32 + lane] = x;
+                    if (dim == 0) {
+                        pieces[slot].m[row] = big;
+                        pieces[slot].l[row] = sum;
+                    }
                 } else {
-                    int row, dim;
-                    vector_place<DP>(k, lane, row, dim);
-                    float big, sum;
-                    whole_row(row, big, sum);
                     write_vector<DP, NR>(a, r, head, row_tile, group, k, lane, x, sum, big, out_wide);
                 }
             }
         }
-        if (cut) {
-            if (tid < kRows) {
-                float big, sum;
-                whole_row(tid, big, sum);
-                pieces[slot].m[tid] = big;
-                pieces[slot].l[tid] = sum;
-            }
-            if (tid == 0) infos[slot] = PieceInfo{at.b, head * at.s.row_tiles + row_tile, begins, ends};
-        }
+        if (cut && tid == 0) infos[slot] = PieceInfo{at.b, head * at.s.row_tiles + row_tile, begins, ends};
         __syncthreads();  // sm.join, sm.m and sm.l are free again
         left -= count;
         at.tile += count;
