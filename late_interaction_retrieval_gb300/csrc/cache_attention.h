@@ -34,10 +34,16 @@ __device__ __forceinline__ Request request_of(const AttentionArgs& a, int b) {
     return r;
 }
 
-// Two e4m3 codes (low byte first) as fp16: exact, NaN stays NaN.
-__device__ __forceinline__ uint32_t widen2(uint32_t codes) {
+// Two e4m3 codes (low byte first) of a word's lower or upper half as fp16:
+// exact, NaN stays NaN.
+__device__ __forceinline__ uint32_t widen_low(uint32_t codes) {
     uint32_t h;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(h) : "h"(static_cast<unsigned short>(codes)));
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, lo;\n\t}" : "=r"(h) : "r"(codes));
+    return h;
+}
+__device__ __forceinline__ uint32_t widen_high(uint32_t codes) {
+    uint32_t h;
+    asm("{\n\t.reg .b16 lo, hi;\n\tmov.b32 {lo, hi}, %1;\n\tcvt.rn.f16x2.e4m3x2 %0, hi;\n\t}" : "=r"(h) : "r"(codes));
     return h;
 }
 

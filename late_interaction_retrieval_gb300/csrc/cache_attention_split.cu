@@ -66,7 +66,7 @@ struct Smem {
     alignas(1024) uint8_t ring[kWarps][kStages][2][kTile];
     float4 join[kWarps][4][32];  // 4 vectors of every lane's sums at a time
     float m[kWarps][8 * NR], l[kWarps][8 * NR], c[kWarps];
-    float scale[kWarps][kStages][4];  // keys' and values' of the first 16 tokens, of the last 16
+    alignas(16) float scale[kWarps][kStages][4];  // keys' and values' of the first 16 tokens, of the last 16
     uint64_t full[kWarps][kStages];
     int2 page[kWarps][kStages];
     long long warp_sum[kWarps];
@@ -469,8 +469,8 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
                     }
 #pragma unroll
                 for (int k = 0; k < KS; ++k) {
-                    const uint32_t a0 = widen2(w[0][k]), a1 = widen2(w[1][k]);
-                    const uint32_t a2 = widen2(w[0][k] >> 16), a3 = widen2(w[1][k] >> 16);
+                    const uint32_t a0 = widen_low(w[0][k]), a1 = widen_low(w[1][k]);
+                    const uint32_t a2 = widen_high(w[0][k]), a3 = widen_high(w[1][k]);
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr) mma16816(s[mb][nr], a0, a1, a2, a3, qf[nr][k][0], qf[nr][k][1]);
                 }
@@ -596,8 +596,8 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
                 for (int k = 0; k < VW; ++k) {
                     const uint32_t x01 = __byte_perm(v[0][k], v[1][k], 0x5140), x23 = __byte_perm(v[0][k], v[1][k], 0x7362);
                     const uint32_t y01 = __byte_perm(v[2][k], v[3][k], 0x5140), y23 = __byte_perm(v[2][k], v[3][k], 0x7362);
-                    const uint32_t a0 = widen2(x01), a1 = widen2(x01 >> 16), a2 = widen2(y01), a3 = widen2(y01 >> 16);
-                    const uint32_t b0 = widen2(x23), b1 = widen2(x23 >> 16), b2 = widen2(y23), b3 = widen2(y23 >> 16);
+                    const uint32_t a0 = widen_low(x01), a1 = widen_high(x01), a2 = widen_low(y01), a3 = widen_high(y01);
+                    const uint32_t b0 = widen_low(x23), b1 = widen_high(x23), b2 = widen_low(y23), b3 = widen_high(y23);
 #pragma unroll
                     for (int nr = 0; nr < NR; ++nr) {
                         mma16816(o[2 * k][nr], a0, a1, a2, a3, pf[st][nr][0], pf[st][nr][1]);

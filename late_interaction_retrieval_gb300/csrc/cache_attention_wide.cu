@@ -452,8 +452,8 @@ __global__ void __launch_bounds__(kThreads, 1)
                         const int row = (tok & 7) * 8 + (tok >> 3);
                         const uint32_t at = dst + (c >> 2) * (kTok * 128);
                         const uint32_t lo = at + tile_at(row, (c & 3) * 2), hi = at + tile_at(row, (c & 3) * 2 + 1);
-                        const uint32_t l0 = widen2(x.x), l1 = widen2(x.x >> 16), l2 = widen2(x.y), l3 = widen2(x.y >> 16);
-                        const uint32_t h0 = widen2(x.z), h1 = widen2(x.z >> 16), h2 = widen2(x.w), h3 = widen2(x.w >> 16);
+                        const uint32_t l0 = widen_low(x.x), l1 = widen_high(x.x), l2 = widen_low(x.y), l3 = widen_high(x.y);
+                        const uint32_t h0 = widen_low(x.z), h1 = widen_high(x.z), h2 = widen_low(x.w), h3 = widen_high(x.w);
                         // the two 64-dimension tiles share their banks: their lanes take turns
                         if (c & 4) {
                             sts16(hi, h0, h1, h2, h3);
@@ -496,10 +496,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int i = 0; i < 4; ++i) {
                             const uint32_t a01 = __byte_perm(x[2 * i], x[2 * i + 1], 0x5140);
                             const uint32_t a23 = __byte_perm(x[2 * i], x[2 * i + 1], 0x7362);
-                            p[0][i] = widen2(a01);
-                            p[1][i] = widen2(a01 >> 16);
-                            p[2][i] = widen2(a23);
-                            p[3][i] = widen2(a23 >> 16);
+                            p[0][i] = widen_low(a01);
+                            p[1][i] = widen_high(a01);
+                            p[2][i] = widen_low(a23);
+                            p[3][i] = widen_high(a23);
                         }
 #pragma unroll
                         for (int j = 0; j < 4; ++j)
