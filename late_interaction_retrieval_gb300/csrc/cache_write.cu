@@ -3,11 +3,13 @@
 //
 // A run (rows of consecutive slots in one page) of one head has to be seen
 // whole before its first value can be rounded: its largest value gives the
-// page's scale.  It is kept in registers between the two, so that it is read
-// once: a long run by a block, a short one (a decoded token, a few drafts) by
-// a warp of it.  The largest value is taken over the values' bits, two 16-bit
-// ones at a time, which also shows whether any is not finite; only then each
-// is looked at.
+// page's scale.  A long run is a block's work and waits in shared memory
+// between the two, read from memory once; what is on its way to shared memory
+// takes no registers, so that a dozen blocks an SM keep enough of it under way.
+// A short run (a decoded token, a few drafts) is a warp's, and is read again
+// from L1.  The largest value is taken over the values' bits, two 16-bit ones
+// at a time, which also shows whether any is not finite; only then each is
+// looked at.
 #include <cuda_fp8.h>
 #include <cuda_runtime.h>
 
@@ -20,8 +22,10 @@ namespace {
 
 constexpr int kThreads = 128;
 constexpr int kWarps = kThreads / 32;
-constexpr int kKept = 8;         // vectors of 8 values that a thread of a block keeps
-constexpr int kKeptByWarp = 2;   // of a warp; longer runs are a block's
+constexpr int kShort = 128;        // vectors of 8 values of the longest run that is a warp's
+constexpr int kMostStage = 32768;  // bytes of a run that wait in shared memory
+constexpr int kMostChunk = 64;     // rows that a block looks at for runs that begin there
+constexpr int kWords = (kMostChunk + 256) / 32;
 
 template <typename T>
 struct Bits;
@@ -37,6 +41,12 @@ template <>
 struct Bits<__nv_bfloat16> {
     static constexpr uint32_t kInf = 0x7f80u;
 };
+
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
 
 // 8 values as they lie in memory.
 template <typename T>
@@ -65,13 +75,24 @@ struct Eight {
             for (int i = 0; i < kWords; ++i) w[i] = s[2 * i] | (static_cast<uint32_t>(s[2 * i + 1]) << 16);
         }
     }
+    __device__ __forceinline__ void load_shared(const T* p) {
+        const uint4* const s = reinterpret_cast<const uint4*>(p);
+#pragma unroll
+        for (int i = 0; i < kWords / 4; ++i) {
+            const uint4 v = s[i];
+            w[4 * i] = v.x;
+            w[4 * i + 1] = v.y;
+            w[4 * i + 2] = v.z;
+            w[4 * i + 3] = v.w;
+        }
+    }
     __device__ __forceinline__ float at(int i) const;
     // The largest of the sizes' bits so far and these; of 16-bit values two at
     // a time, each in its half of `most`.
     __device__ __forceinline__ uint32_t largest(uint32_t most) const {
 #pragma unroll
         for (int i = 0; i < kWords; ++i)
-            most = sizeof(T) == 4 ? max(most, w[i] & 0x7fffffffu) : __vmaxu2(most, w[i] & 0x7fff7fffu);
+            most = sizeof(T) == 4 ? max(most, w[i] & 0x7fffffffu) : max_halves(most, w[i] & 0x7fff7fffu);
         return most;
     }
 };
@@ -106,7 +127,9 @@ __device__ __forceinline__ float size_of_bits<__nv_bfloat16>(uint32_t b) {
 __device__ __forceinline__ bool is_finite(float x) { return fabsf(x) <= 3.402823466e38f; }
 
 __device__ __forceinline__ uint32_t code2(float x, float y) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(x, y), __NV_SATFINITE, __NV_E4M3);
+    unsigned short h;
+    asm("cvt.rn.satfinite.e4m3x2.f32 %0, %1, %2;" : "=h"(h) : "f"(y), "f"(x));
+    return h;
 }
 // NaN for what is not finite (the conversion alone turns an infinity into the largest value).
 __device__ __forceinline__ float nan_unless_finite(float x) { return is_finite(x) ? x : __int_as_float(0x7fffffff); }
@@ -116,19 +139,19 @@ __device__ __forceinline__ float decode(uint32_t code) {
 }
 
 // 8 values in units of their scale, as codes.
-template <typename T>
-__device__ __forceinline__ uint2 encode8(const Eight<T>& v, float inverse, bool all_finite) {
+template <bool kFinite, typename T>
+__device__ __forceinline__ uint2 encode8(const Eight<T>& v, float inverse) {
     uint32_t h[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         float x = v.at(2 * i), y = v.at(2 * i + 1);
-        if (!all_finite) {
+        if (!kFinite) {
             x = nan_unless_finite(x);
             y = nan_unless_finite(y);
         }
         h[i] = code2(x * inverse, y * inverse);
     }
-    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+    return make_uint2(__byte_perm(h[0], h[1], 0x5410), __byte_perm(h[2], h[3], 0x5410));
 }
 
 // Keys or values.
@@ -148,34 +171,64 @@ struct Run {
     int offset, n;
 };
 
+__device__ __forceinline__ void copy16(uint32_t to, const void* from) {
+    asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(to), "l"(from) : "memory");
+}
+
 // One run of one head, by kGroup threads (a warp or the block) of which this
-// is number `tid`.
-template <typename T, int kGroup, int kHeld>
-__device__ __forceinline__ void write_run(const Side<T>& a, const Run& r, int tid, uint32_t* of_warp) {
+// is number `tid`.  stage: shared memory for `room` vectors (a block's), or 0.
+template <typename T, int kGroup>
+__device__ __forceinline__ void write_run(const Side<T>& a, const Run& r, int tid, uint32_t* of_warp, T* stage, int room) {
     const T* const x = a.x + r.row * a.token_stride;
-    const int64_t token_stride = a.token_stride;
-    const bool wide = a.wide;
     const int per_row = a.dim / 8, vectors = r.n * per_row;
-    const float inv_row = 1.0f / static_cast<float>(per_row);
     float* const scale_at = a.scale + r.page * a.heads + a.head;
     const float old = r.offset ? *scale_at : 0.0f;
-    // vector i of the run lies in its row i / per_row (i < 2^12, exact in fp32)
-    auto from = [&](int i) {
-        const int row = static_cast<int>((static_cast<float>(i) + 0.5f) * inv_row);
-        return x + row * token_stride + (i - row * per_row) * 8;
+    // The thread's vectors i = tid, tid + kGroup, ...: vector i lies in the run's row i / per_row.
+    const int row0 = tid / per_row, d0 = tid - row0 * per_row, rows_on = kGroup / per_row, d_on = kGroup - rows_on * per_row;
+    const int64_t on = rows_on * a.token_stride + d_on * 8, wrap = a.token_stride - a.dim;
+    const bool staged = a.wide && vectors <= room;
+    // body(vector of 8, its number)
+    auto each = [&](auto body) {
+        if (staged) {
+#pragma unroll 2
+            for (int i = tid; i < vectors; i += kGroup) {
+                Eight<T> v;
+                v.load_shared(stage + i * 8);
+                body(v, i);
+            }
+            return;
+        }
+        const T* at = x + row0 * a.token_stride + d0 * 8;
+        int d = d0;
+#pragma unroll 2
+        for (int i = tid; i < vectors; i += kGroup) {
+            Eight<T> v;
+            v.load(at, a.wide);
+            body(v, i);
+            d += d_on;
+            at += on;
+            if (d >= per_row) {
+                d -= per_row;
+                at += wrap;
+            }
+        }
     };
-    Eight<T> kept[kHeld];
-    uint32_t bits = 0;
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-        if (tid + j * kGroup < vectors) kept[j].load(from(tid + j * kGroup), wide);
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j)
-        if (tid + j * kGroup < vectors) bits = kept[j].largest(bits);
-    for (int i = tid + kHeld * kGroup; i < vectors; i += kGroup) {
-        Eight<T> v;
-        v.load(from(i), wide);
-        bits = v.largest(bits);
+    if (staged) {  // a thread waits for what it fetched itself: it reads nothing else
+        const T* at = x + row0 * a.token_stride + d0 * 8;
+        int d = d0;
+        uint32_t to = static_cast<uint32_t>(__cvta_generic_to_shared(stage + tid * 8));
+#pragma unroll 4
+        for (int i = tid; i < vectors; i += kGroup, to += kGroup * 8 * sizeof(T)) {
+            copy16(to, at);
+            if (sizeof(T) == 4) copy16(to + 16, at + 4);
+            d += d_on;
+            at += on;
+            if (d >= per_row) {
+                d -= per_row;
+                at += wrap;
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
     }
     auto join = [&](uint32_t b) {
         if (sizeof(T) == 2) b = max(b & 0xffffu, b >> 16);
@@ -189,13 +242,13 @@ __device__ __forceinline__ void write_run(const Side<T>& a, const Run& r, int ti
         }
         return b;
     };
+    uint32_t bits = 0;
+    each([&](const Eight<T>& v, int) { bits = v.largest(bits); });
     bits = join(bits);
     const bool all_finite = bits < Bits<T>::kInf;
     if (!all_finite) {  // the largest of those that are finite
         bits = 0;
-        for (int i = tid; i < vectors; i += kGroup) {
-            Eight<T> v;
-            v.load(from(i), wide);
+        each([&](const Eight<T>& v, int) {
 #pragma unroll
             for (int e = 0; e < Eight<T>::kWords; ++e) {
                 const uint32_t lo = sizeof(T) == 4 ? v.w[e] & 0x7fffffffu : v.w[e] & 0x7fffu;
@@ -203,7 +256,7 @@ __device__ __forceinline__ void write_run(const Side<T>& a, const Run& r, int ti
                 bits = max(bits, lo < Bits<T>::kInf ? lo : 0u);
                 bits = max(bits, hi < Bits<T>::kInf ? hi : 0u);
             }
-        }
+        });
         bits = join(bits);
     }
     const float fresh = fmaxf(__fdiv_rn(size_of_bits<T>(bits), kCodeMax), kLeastScale);
@@ -213,6 +266,7 @@ __device__ __forceinline__ void write_run(const Side<T>& a, const Run& r, int ti
     if (r.offset && scale > old) {
         const float ratio = old * inverse;
         uint4* const held = reinterpret_cast<uint4*>(tile);
+#pragma unroll 1
         for (int i = tid; i < r.offset * a.dim / 16; i += kGroup) {
             uint4 c = held[i];
             uint32_t* const w = reinterpret_cast<uint32_t*>(&c);
@@ -226,26 +280,39 @@ __device__ __forceinline__ void write_run(const Side<T>& a, const Run& r, int ti
             held[i] = c;
         }
     }
-    uint8_t* const to = tile + r.offset * a.dim;
-#pragma unroll
-    for (int j = 0; j < kHeld; ++j) {
-        const int i = tid + j * kGroup;
-        if (i < vectors) *reinterpret_cast<uint2*>(to + i * 8) = encode8(kept[j], inverse, all_finite);
-    }
-    for (int i = tid + kHeld * kGroup; i < vectors; i += kGroup) {
-        Eight<T> v;
-        v.load(from(i), wide);
-        *reinterpret_cast<uint2*>(to + i * 8) = encode8(v, inverse, all_finite);
-    }
+    uint2* const to = reinterpret_cast<uint2*>(tile + r.offset * a.dim);
+    if (all_finite) each([&](const Eight<T>& v, int i) { to[i] = encode8<true>(v, inverse); });
+    else each([&](const Eight<T>& v, int i) { to[i] = encode8<false>(v, inverse); });
     __syncwarp();  // every lane has read the old scale (every warp has: it did before the join)
     if (tid == 0) *scale_at = scale;
 }
 
+// Blocks are (chunk, keys or values, head), heads next to one another: blocks that run together read whole rows and
+// write whole pages.
 template <typename T>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteArgs a, int chunk, bool wide_k, bool wide_v) {
+__global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteArgs a, int chunk, int room, bool wide_k, bool wide_v) {
+    extern __shared__ __align__(16) uint8_t stage[];
     __shared__ uint32_t of_warp[kWarps];
+    __shared__ unsigned on_of[kWords], begins_of[kMostChunk / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int head = blockIdx.y, which = blockIdx.z;
+    const int head = static_cast<int>(blockIdx.x % a.heads), which = blockIdx.y;
+    const int64_t t0 = static_cast<int64_t>(blockIdx.x / a.heads) * chunk;
+    const int page_size = 1 << a.page_shift, words = (chunk + page_size + 31) / 32;
+    // Rows t0, t0 + 1, ...: those of the chunk, and as many behind it as a run that begins there may have.  Bit l of
+    // word k: row t0 + 32 k + l goes on with the run of the row before; a run begins there.
+    const int64_t n_slots = a.pages << a.page_shift;
+    for (int k = warp; k < words; k += kWarps) {
+        const int64_t r = t0 + 32 * k + lane;
+        const int64_t slot = r < a.rows ? a.slots[r] : -1, before = r < a.rows && r > 0 ? a.slots[r - 1] : -1;
+        const bool valid = slot >= 0 && slot < n_slots;
+        const bool goes_on = valid && (slot & (page_size - 1)) != 0 && before >= 0 && before + 1 == slot;
+        const unsigned on = __ballot_sync(0xffffffffu, goes_on);
+        const unsigned begins = __ballot_sync(0xffffffffu, valid && !goes_on && 32 * k + lane < chunk);
+        if (lane == 0) {
+            on_of[k] = on;
+            if (k < kMostChunk / 32) begins_of[k] = begins;
+        }
+    }
     Side<T> side;
     side.x = static_cast<const T*>(which ? a.x[1] : a.x[0]) + head * (which ? a.head_stride[1] : a.head_stride[0]);
     side.token_stride = which ? a.token_stride[1] : a.token_stride[0];
@@ -256,49 +323,28 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteArgs a
     side.dim = a.dim;
     side.page_shift = a.page_shift;
     side.wide = which ? wide_v : wide_k;
-    const int64_t t0 = static_cast<int64_t>(blockIdx.x) * chunk;
-    const int page_size = 1 << a.page_shift;
-    const int64_t n_slots = a.pages << a.page_shift;
-
-    // lane l looks at row t0 + l: does a run begin there, and if not, does one go on?
-    const int64_t t = t0 + lane;
-    const bool looked = lane < chunk && t < a.rows;
-    const int64_t slot = looked ? a.slots[t] : -1;
-    const int64_t before = looked && t > 0 ? a.slots[t - 1] : -1;
-    const bool valid = slot >= 0 && slot < n_slots;
-    const int offset = static_cast<int>(slot & (page_size - 1));
-    const bool goes_on = valid && offset != 0 && before >= 0 && before + 1 == slot;
-    const unsigned begins = __ballot_sync(0xffffffffu, valid && !goes_on);
-    const unsigned on = __ballot_sync(0xffffffffu, goes_on);
-
-    const int short_rows = kKeptByWarp * 32 / (a.dim / 8);  // of a run that a warp keeps
-    int number = 0;
-    for (unsigned rest = begins; rest; rest &= rest - 1) {
-        const int l = __ffs(rest) - 1;
-        Run r;
-        r.row = t0 + l;
-        const int64_t s = __shfl_sync(0xffffffffu, slot, l);
-        r.page = s >> a.page_shift;
-        r.offset = static_cast<int>(s & (page_size - 1));
-        // rows of the chunk behind it that go on; the run may pass the chunk
-        const unsigned behind = l == 31 ? 0u : ~(on >> (l + 1));
-        const int in_chunk = chunk - 1 - l;
-        int n = l == 31 ? 0 : (behind ? __ffs(behind) - 1 : 31);
-        n = n < in_chunk ? n : in_chunk;
-        if (n == in_chunk) {
-            for (int base = n + 1; r.offset + base < page_size; base += 32) {
-                const int64_t k = r.row + base + lane;
-                const bool more = r.offset + base + lane < page_size && k < a.rows && a.slots[k] == s + base + lane;
-                const unsigned stop = ~__ballot_sync(0xffffffffu, more);
-                n = base - 1 + (stop ? __ffs(stop) - 1 : 32);
-                if (stop) break;
+    const int short_rows = kShort / (a.dim / 8);
+    int shorts = 0;
+    __syncthreads();
+#pragma unroll 1
+    for (int k = 0; k < kMostChunk / 32 && 32 * k < chunk; ++k) {
+#pragma unroll 1
+        for (unsigned rest = begins_of[k]; rest; rest &= rest - 1) {
+            const int l = __ffs(rest) - 1;
+            Run r;
+            r.row = t0 + 32 * k + l;
+            const int64_t slot = a.slots[r.row];
+            r.page = slot >> a.page_shift;
+            r.offset = static_cast<int>(slot & (page_size - 1));
+            // rows behind it that go on: the run ends in its page, so within the words
+            const unsigned off = l == 31 ? 0u : ~on_of[k] >> (l + 1);
+            r.n = 1 + (off ? min(__ffs(off) - 1, 31 - l) : 31 - l);
+            for (int j = k + 1; r.n == 32 * (j - k) - l && j < words; ++j) r.n += on_of[j] == 0xffffffffu ? 32 : __ffs(~on_of[j]) - 1;
+            if (r.n <= short_rows) {
+                if (shorts++ % kWarps == warp) write_run<T, 32>(side, r, lane, of_warp, nullptr, 0);
+            } else {
+                write_run<T, kThreads>(side, r, tid, of_warp, reinterpret_cast<T*>(stage), room);
             }
-        }
-        r.n = n + 1;
-        if (r.n <= short_rows) {
-            if (number++ % kWarps == warp) write_run<T, 32, kKeptByWarp>(side, r, lane, of_warp);
-        } else {
-            write_run<T, kThreads, kKept>(side, r, tid, of_warp);
         }
     }
 }
@@ -306,13 +352,19 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteArgs a
 template <typename T>
 cudaError_t launch(const WriteArgs& a, cudaStream_t stream) {
     // rows that a block looks at; a run may go on behind them
-    const int chunk = a.rows <= 512 ? 1 : (a.rows <= 8192 ? 8 : 32);
+    const int chunk = a.rows <= 512 ? 1 : (a.rows <= 8192 ? 8 : kMostChunk);
     bool wide[2];
     for (int i = 0; i < 2; ++i)
         wide[i] = ((reinterpret_cast<uintptr_t>(a.x[i]) | (a.token_stride[i] * sizeof(T)) |
                     (a.head_stride[i] * sizeof(T))) & 15) == 0;
-    const dim3 grid(static_cast<unsigned>((a.rows + chunk - 1) / chunk), static_cast<unsigned>(a.heads), 2);
-    cache_write_kernel<T><<<grid, kThreads, 0, stream>>>(a, chunk, wide[0], wide[1]);
+    // shared memory for the longest run there can be, or kMostStage of it; longer runs are read twice
+    const int64_t most = a.rows, page = int64_t(1) << a.page_shift;
+    const int64_t longest = (most < page ? most : page) * (a.dim / 8), space = kMostStage / (8 * sizeof(T));
+    const int room = static_cast<int>(longest < space ? longest : space);
+    const int64_t blocks = (a.rows + chunk - 1) / chunk * a.heads;
+    if (blocks > INT32_MAX) return cudaErrorInvalidValue;
+    cache_write_kernel<T><<<dim3(static_cast<unsigned>(blocks), 2), kThreads, room * 8 * sizeof(T), stream>>>(
+        a, chunk, room, wide[0], wide[1]);
     return cudaGetLastError();
 }
 
