@@ -33,12 +33,17 @@ struct Plan {
 struct Scale {
     float hi, lo;  // scale * log2(e) in two parts
 };
+__device__ __forceinline__ float exp2_fast(float x) {
+    float y;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(x));
+    return y;
+}
 __device__ __forceinline__ float exp_scaled(float d, Scale c) {
     const float t = d * c.hi;
-    if (t < -200.0f) return 0.0f;  // below every fp32 value; the product may have overflowed
     const float rest = fmaf(d, c.lo, fmaf(d, c.hi, -t));
-    const float e = exp2f(t);
-    return fmaf(e, rest * kLn2, e);
+    const float e = exp2_fast(t);
+    // below every fp32 value the product may have overflowed, and `rest` with it
+    return t < -200.0f ? 0.0f : fmaf(e, rest * kLn2, e);
 }
 
 __device__ __forceinline__ float2 join(float2 x, float2 y, Scale c) {
@@ -65,6 +70,8 @@ struct Vec {
     static constexpr int n = 16 / sizeof(T);
     uint4 raw;
     __device__ __forceinline__ void load(const T* p) { raw = __ldg(reinterpret_cast<const uint4*>(p)); }
+    // The largest (a NaN is passed over): of 16-bit logits two at a time, before they are widened.
+    __device__ __forceinline__ float largest() const;
     __device__ __forceinline__ void widen(float (&f)[n]) const {
         const T* const e = reinterpret_cast<const T*>(&raw);
 #pragma unroll
@@ -72,15 +79,27 @@ struct Vec {
     }
 };
 
+template <>
+__device__ __forceinline__ float Vec<float>::largest() const {
+    return fmaxf(fmaxf(__uint_as_float(raw.x), __uint_as_float(raw.y)), fmaxf(__uint_as_float(raw.z), __uint_as_float(raw.w)));
+}
+template <>
+__device__ __forceinline__ float Vec<__half>::largest() const {
+    const __half2* const h = reinterpret_cast<const __half2*>(&raw);
+    const __half2 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+template <>
+__device__ __forceinline__ float Vec<__nv_bfloat16>::largest() const {
+    const __nv_bfloat162* const h = reinterpret_cast<const __nv_bfloat162*>(&raw);
+    const __nv_bfloat162 m = __hmax2(__hmax2(h[0], h[1]), __hmax2(h[2], h[3]));
+    return fmaxf(__low2float(m), __high2float(m));
+}
+
 // One logit's (largest, sum): nothing for -inf, a NaN sum for NaN.
 __device__ __forceinline__ float2 one(float z) {
     return make_float2(z, z == -INFINITY ? 0.0f : (z == z ? 1.0f : z));
 }
-
-// One more value into a running (largest, sum).  A plain product suffices
-// here: a term of 2^-t is off by t * 2^-24 of itself, and its share of the sum
-// is the smaller the larger t is.
-__device__ __forceinline__ float term(float z, float m, Scale c) { return exp2f((z - m) * c.hi); }
 
 template <typename T>
 __global__ void __launch_bounds__(kThreads) verify_stats(const VerifyArgs a, const Plan w, Scale c) {
@@ -105,32 +124,43 @@ __global__ void __launch_bounds__(kThreads) verify_stats(const VerifyArgs a, con
         if (tid < head) v = join(v, one(load_f32(z + c0 + tid)), c);
         if (tid < c1 - tail) v = join(v, one(load_f32(z + tail + tid)), c);
         const T* const wide = z + c0 + head;
-        for (int64_t i = tid; i < vecs; i += kUnroll * kThreads) {
-            Vec<T> x[kUnroll];
-            float f[kUnroll][kVec];
+        // the next turn's loads are on their way while this one's exponentials are taken
+        Vec<T> x[kUnroll];
+        auto fetch = [&](int64_t i) {
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u)
                 if (i + u * kThreads < vecs) x[u].load(wide + (i + u * kThreads) * kVec);
+        };
+        fetch(tid);
+        for (int64_t i = tid; i < vecs; i += kUnroll * kThreads) {
+            Vec<T> now[kUnroll];
             float m = v.x;
+            int have = 0;  // of the turn's vectors
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
+                now[u] = x[u];
                 if (i + u * kThreads < vecs) {
-                    x[u].widen(f[u]);
-#pragma unroll
-                    for (int e = 0; e < kVec; ++e) m = fmaxf(m, f[u][e]);
+                    m = fmaxf(m, now[u].largest());
+                    have = u + 1;
                 }
             }
-            // all of it -inf so far: 0 stands in, and every term is 0; a NaN makes its own term one
+            fetch(i + kUnroll * kThreads);
+            // All of it -inf so far: 0 stands in, and every term is 0.  A NaN makes its own term one.  The product of
+            // the maximum is rounded once for the turn, and what that takes from every term is put back into the sum.
             const float base = m == -INFINITY ? 0.0f : m;
-            float s = v.y == 0.0f ? 0.0f : v.y * exp_scaled(v.x - base, c);
+            const float minus = -base * c.hi, off = fmaf(base, c.hi, minus);
+            float s[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
             for (int u = 0; u < kUnroll; ++u) {
-                if (i + u * kThreads < vecs) {
+                if (u >= have) continue;
+                float f[kVec];
+                now[u].widen(f);
 #pragma unroll
-                    for (int e = 0; e < kVec; ++e) s += term(f[u][e], base, c);
-                }
+                for (int e = 0; e < kVec; ++e) s[e & 3] += exp2_fast(fmaf(f[e], c.hi, minus));
             }
-            v = make_float2(m, s);
+            const float turn = (s[0] + s[1]) + (s[2] + s[3]);
+            const float kept = v.y == 0.0f ? 0.0f : v.y * exp_scaled(v.x - base, c);
+            v = make_float2(m, kept + fmaf(turn, -off * kLn2, turn));
         }
     }
     v = warp_join(v, c);
@@ -186,12 +216,14 @@ __device__ __forceinline__ unsigned long long block_max(unsigned long long v, un
     return v;
 }
 
+// Drafts whose rows' statistics a block keeps.
+constexpr int kKept = 64;
+
 template <typename T>
 __global__ void __launch_bounds__(kThreads) verify_draw(const VerifyArgs a, const Plan w, Scale c, bool wide) {
-    asm volatile("griddepcontrol.wait;" ::: "memory");
     __shared__ unsigned long long of_warp[kWarps];
     __shared__ int first_fail, is_last;
-    __shared__ float2 stat_p, stat_q;
+    __shared__ float2 stat_p[kKept], stat_q[kKept];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, b = blockIdx.y;
     const int64_t targets = a.drafts + a.requests;
     int64_t lo = a.offsets[b], hi = a.offsets[b + 1];
@@ -200,35 +232,60 @@ __global__ void __launch_bounds__(kThreads) verify_draw(const VerifyArgs a, cons
     const int n = static_cast<int>(hi - lo);
     const T* const target = static_cast<const T*>(a.target);
     const T* const draft = static_cast<const T*>(a.draft);
+    const bool writes = blockIdx.x == 0;  // the tokens that pass; the drawn one is the last block's
     if (tid == 0) first_fail = n;
     __syncthreads();
-    for (int i = warp; i < n; i += kWarps) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    // a warp takes a draft at a time, and the row behind the last (which always "passes")
+    for (int i = warp; i <= n; i += kWarps) {
         // one lane's view of what other warps write, so that the warp stays whole
         if (__shfl_sync(0xffffffffu, *reinterpret_cast<volatile int*>(&first_fail), 0) < i) break;
         const int64_t row = lo + i, tr = row + b;
-        const int x = a.drafted[row];
-        bool pass = x >= 0 && x < a.cols;
-        if (pass) {
-            const float p = prob(load_f32(target + tr * a.target_stride + x), row_stats(w, tr, c), c);
-            const float q = draft ? prob(load_f32(draft + row * a.draft_stride + x), row_stats(w, targets + row, c), c)
-                                  : 1.0f;
-            pass = static_cast<double>(a.uniform[row]) * q < static_cast<double>(p);
+        const int x = i < n ? a.drafted[row] : -1;
+        const float u = i < n ? a.uniform[row] : 0.0f;
+        const bool inside = x >= 0 && x < a.cols;
+        const float zp = inside ? load_f32(target + tr * a.target_stride + x) : 0.0f;
+        const float zq = inside && draft ? load_f32(draft + row * a.draft_stride + x) : 0.0f;
+        const float2 sp = row_stats(w, tr, c);
+        const float2 sq = i < n && draft ? row_stats(w, targets + row, c) : make_float2(0.0f, 0.0f);
+        if (lane == 0) {
+            if (i < kKept) {
+                stat_p[i] = sp;
+                stat_q[i] = sq;
+            }
+            const float p = prob(zp, sp, c), q = draft ? prob(zq, sq, c) : 1.0f;
+            if (i < n && !(inside && static_cast<double>(u) * q < static_cast<double>(p))) atomicMin(&first_fail, i);
+            if (writes && i < n) {
+                a.tokens[tr] = x;
+                a.logp[tr] = a.scale * (zp - sp.x) - logf(sp.y);
+            }
         }
-        if (!pass && lane == 0) atomicMin(&first_fail, i);
     }
     __syncthreads();
     const int kept = first_fail;
     const int64_t tr = lo + b + kept, dr = lo + kept;
     const bool residual = kept < n;
-    if (warp == 0) {
-        const float2 s = row_stats(w, tr, c);
-        if (lane == 0) stat_p = s;
-    } else if (warp == 1) {
-        const float2 s = residual && draft ? row_stats(w, targets + dr, c) : make_float2(0.0f, 0.0f);
-        if (lane == 0) stat_q = s;
+    if (writes) {  // behind what passed there is nothing (but the token that is drawn)
+        for (int i = kept + 1 + tid; i <= n; i += kThreads) {
+            a.tokens[lo + b + i] = -1;
+            a.logp[lo + b + i] = 0.0f;
+        }
+        if (tid == 0) a.accepted[b] = kept;
+        if (b == a.requests - 1) {  // rows behind the last request's
+            for (int64_t r = hi + b + 1 + tid; r < targets; r += kThreads) {
+                a.tokens[r] = -1;
+                a.logp[r] = 0.0f;
+            }
+        }
     }
-    __syncthreads();
-    const float2 sp = stat_p, sq = stat_q;
+    float2 sp, sq;
+    if (kept < kKept) {
+        sp = stat_p[kept];
+        sq = stat_q[kept];
+    } else {
+        sp = row_stats(w, tr, c);
+        sq = residual && draft ? row_stats(w, targets + dr, c) : make_float2(0.0f, 0.0f);
+    }
     const T* const z = target + tr * a.target_stride;
     const T* const y = residual && draft ? draft + dr * a.draft_stride : nullptr;
     const int64_t struck = residual && !draft ? a.drafted[dr] : -1;
@@ -243,29 +300,50 @@ __global__ void __launch_bounds__(kThreads) verify_draw(const VerifyArgs a, cons
     };
     Best mine;
     if (wide) {
-        constexpr int kVec = Vec<T>::n;
-        for (int64_t k = c0 + tid * kVec; k < c1; k += kThreads * kVec) {
-            Vec<T> xp, xq;
-            float4 e[kVec / 4];
-            xp.load(z + k);
-            if (y) xq.load(y + k);
-            else xq.raw = make_uint4(0, 0, 0, 0);
+        constexpr int kVec = Vec<T>::n, kTurn = 16 / kVec;  // 16 columns a thread and turn
+        for (int64_t k0 = c0 + tid * kVec; k0 < c1; k0 += kThreads * kVec * kTurn) {
+            Vec<T> xp[kTurn], xq[kTurn];
+            float4 e[kTurn][kVec / 4];
 #pragma unroll
-            for (int i = 0; i < kVec / 4; ++i) e[i] = __ldg(reinterpret_cast<const float4*>(noise + k) + i);
-            float fp[kVec], fq[kVec];
-            xp.widen(fp);
-            xq.widen(fq);
+            for (int t = 0; t < kTurn; ++t) {
+                const int64_t k = k0 + t * kThreads * kVec;
+                if (k < c1) {
+                    xp[t].load(z + k);
+                    if (y) xq[t].load(y + k);
+                    else xq[t].raw = make_uint4(0, 0, 0, 0);
 #pragma unroll
-            for (int i = 0; i < kVec; ++i)
-                mine.offer(left_of(fp[i], fq[i], k + i), reinterpret_cast<const float*>(e)[i], k + i);
+                    for (int i = 0; i < kVec / 4; ++i) e[t][i] = __ldg(reinterpret_cast<const float4*>(noise + k) + i);
+                }
+            }
+#pragma unroll
+            for (int t = 0; t < kTurn; ++t) {
+                const int64_t k = k0 + t * kThreads * kVec;
+                if (k < c1) {
+                    float fp[kVec], fq[kVec];
+                    xp[t].widen(fp);
+                    xq[t].widen(fq);
+#pragma unroll
+                    for (int i = 0; i < kVec; ++i)
+                        mine.offer(left_of(fp[i], fq[i], k + i), reinterpret_cast<const float*>(e[t])[i], k + i);
+                }
+            }
         }
     } else {
-#pragma unroll 4
-        for (int64_t k = c0 + tid; k < c1; k += kThreads)
-            mine.offer(left_of(load_f32(z + k), y ? load_f32(y + k) : 0.0f, k), __ldg(noise + k), k);
+        constexpr int kTurn = 8;
+        for (int64_t k0 = c0 + tid; k0 < c1; k0 += kThreads * kTurn) {
+            float fp[kTurn], fq[kTurn], e[kTurn];
+#pragma unroll
+            for (int t = 0; t < kTurn; ++t) {
+                const int64_t k = k0 + t * kThreads;
+                fp[t] = k < c1 ? load_f32(z + k) : -INFINITY;
+                fq[t] = y && k < c1 ? load_f32(y + k) : 0.0f;
+                e[t] = k < c1 ? __ldg(noise + k) : INFINITY;
+            }
+#pragma unroll
+            for (int t = 0; t < kTurn; ++t) mine.offer(left_of(fp[t], fq[t], k0 + t * kThreads), e[t], k0 + t * kThreads);
+        }
     }
-    unsigned long long best = mine.packed();
-    best = block_max(best, of_warp);
+    unsigned long long best = block_max(mine.packed(), of_warp);
     if (tid == 0) {
         if (best) atomicMax(w.best + b, best);
         __threadfence();
@@ -280,33 +358,18 @@ __global__ void __launch_bounds__(kThreads) verify_draw(const VerifyArgs a, cons
         for (int64_t k = tid; k < a.cols; k += kThreads) all.offer(exp_scaled(load_f32(z + k) - sp.x, c) * ip, noise[k], k);
         best = block_max(all.packed(), of_warp);
     }
-    const int token = best ? static_cast<int>(0xffffffffu - static_cast<unsigned>(best)) : -1;
-    for (int i = warp; i <= n; i += kWarps) {
-        const int64_t r = lo + b + i;
-        const int t = i < kept ? a.drafted[lo + i] : (i == kept ? token : -1);
-        float lp = 0.0f;
-        if (t >= 0) {
-            const float2 s = row_stats(w, r, c);
-            // in natural logarithms: scale * (z - max) - log(sum)
-            lp = a.scale * (load_f32(target + r * a.target_stride + t) - s.x) - logf(s.y);
-        }
-        if (lane == 0) {
-            a.tokens[r] = t;
-            a.logp[r] = lp;
-        }
-    }
-    if (tid == 0) a.accepted[b] = kept;
-    if (b == a.requests - 1) {  // rows behind the last request's
-        for (int64_t r = hi + b + 1 + tid; r < targets; r += kThreads) {
-            a.tokens[r] = -1;
-            a.logp[r] = 0.0f;
-        }
+    if (tid == 0) {
+        const int token = best ? static_cast<int>(0xffffffffu - static_cast<unsigned>(best)) : -1;
+        a.tokens[tr] = token;
+        // in natural logarithms: scale * (z - max) - log(sum)
+        a.logp[tr] = token >= 0 ? a.scale * (load_f32(z + token) - sp.x) - logf(sp.y) : 0.0f;
     }
 }
 
-int parts_of(int64_t rows, int64_t cols, int sms) {
-    // 4 blocks for each SM, of 4096 columns at least
-    int64_t p = (4 * static_cast<int64_t>(sms) + rows - 1) / (rows > 0 ? rows : 1);
+// Parts of each of `rows` rows: as many as fill the chip once, of 4096 columns
+// at least.
+int parts_of(int64_t rows, int64_t cols, int64_t blocks) {
+    int64_t p = blocks / (rows > 0 ? rows : 1);
     const int64_t most = (cols + 4095) / 4096;
     p = p < most ? p : most;
     return static_cast<int>(p < 1 ? 1 : (p < kMaxParts ? p : kMaxParts));
@@ -352,9 +415,9 @@ cudaError_t launch_verify(const VerifyArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const int sms = device_info(dev).sm_count;
     Plan w;
-    w.parts = parts_of(a.drafts + a.requests + (a.draft ? a.drafts : 0), a.cols, sms);
+    w.parts = parts_of(a.drafts + a.requests + (a.draft ? a.drafts : 0), a.cols, 4 * sms);
     w.part = ((a.cols + w.parts - 1) / w.parts + 7) & ~int64_t(7);
-    w.races = parts_of(a.requests, a.cols, sms);
+    w.races = parts_of(a.requests, a.cols, 3 * sms);
     w.share = ((a.cols + w.races - 1) / w.races + 7) & ~int64_t(7);
     uint8_t* p = static_cast<uint8_t*>(a.workspace);
     w.stats = reinterpret_cast<float2*>(p);
