@@ -5,7 +5,8 @@
 // else: a token's request is found in the first, a new page's request in the
 // second.  Every block sums all requests for itself into its shared memory
 // (12 bytes a request, from L2) and then fills its share of the slots and the
-// table, so that one launch does it with no block waiting for another.
+// table, so that one launch does it with no block waiting for another.  What
+// bounds it is the chain of a token's lookups, so a thread has 4 on their way.
 #include <cuda_runtime.h>
 
 #include "lik_internal.h"
@@ -49,9 +50,12 @@ __device__ __forceinline__ int find(const int* prefix, int n, int t) {
 }
 
 __global__ void __launch_bounds__(kThreads) cache_slots_kernel(const SlotsArgs a) {
-    extern __shared__ int prefix[];  // new tokens [requests + 1], new pages [requests + 1]; both held under 2^31
+    // new tokens and new pages before a request [requests + 1], both held under 2^31; what it had [requests]
+    extern __shared__ int prefix[];
     int* const tokens = prefix;
-    int* const pages = prefix + a.requests + 1;
+    int* const pages = tokens + a.requests + 1;
+    int* const had = pages + a.requests + 1;
+    int* const held = had + a.requests;
     __shared__ int64_t warp_tokens[kWarps], warp_pages[kWarps];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, B = a.requests;
 
@@ -97,6 +101,8 @@ __global__ void __launch_bounds__(kThreads) cache_slots_kernel(const SlotsArgs a
         const Request r = request_of(a, b);
         tokens[b] = clamp_top(it);
         pages[b] = clamp_top(ip);
+        had[b] = static_cast<int>(r.cached);
+        held[b] = static_cast<int>(r.held);
         if (first) {
             const int64_t left = count - ip;
             const int64_t got = left <= 0 ? 0 : (r.need < left ? r.need : left);
@@ -123,34 +129,45 @@ __global__ void __launch_bounds__(kThreads) cache_slots_kernel(const SlotsArgs a
     const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
     // slots; a token's page is one that its request held, or one of this call's,
     // taken from the list itself: no block reads what another writes
-    int b = -1;
-    for (int64_t t = blockIdx.x * static_cast<int64_t>(kThreads) + tid; t < a.capacity; t += step) {
-        int64_t slot = -1;
-        if (t < n_tokens) {
-            const int ti = static_cast<int>(t);
-            if (b < 0 || ti >= tokens[b + 1]) b = find(tokens, B, ti);
-            const int64_t pos = static_cast<int64_t>(max(a.cached[b], 0)) + ti - tokens[b];
-            const int64_t col = pos >> a.page_shift;
-            if (col < a.cols) {
-                const int64_t held = min(static_cast<int64_t>(max(a.held[b], 0)), a.cols);
-                int64_t page;
-                if (col < held) {
-                    page = a.table[b * a.stride + col];
-                } else {
-                    const int64_t at = count - 1 - pages[b] - (col - held);
-                    page = at >= 0 ? a.free_pages[at] : -1;
+    // A warp takes 32 * kTurn tokens, of which most are a prompt's: the request before is looked at first.
+    constexpr int kTurn = 4;
+    const int cols = static_cast<int>(a.cols);
+    for (int64_t t0 = (blockIdx.x * static_cast<int64_t>(kThreads) + (tid & ~31)) * kTurn + lane; t0 < a.capacity;
+         t0 += kTurn * step) {
+        const int32_t* from[kTurn];
+        uint32_t inside[kTurn];
+        int32_t page[kTurn];
+        int b = -1;
+#pragma unroll
+        for (int u = 0; u < kTurn; ++u) {
+            from[u] = nullptr;
+            inside[u] = 0;
+            if (t0 + 32 * u < n_tokens) {
+                const int t = static_cast<int>(t0) + 32 * u;
+                if (b < 0 || tokens[b + 1] <= t) b = find(tokens, B, t);
+                const uint32_t pos = static_cast<uint32_t>(had[b]) + static_cast<uint32_t>(t - tokens[b]);
+                const int col = static_cast<int>(pos >> a.page_shift), own = held[b];
+                inside[u] = pos & ((1u << a.page_shift) - 1);
+                if (col < own) {
+                    from[u] = a.table + b * a.stride + col;
+                } else if (col < cols) {
+                    const int64_t at = count - 1 - pages[b] - (col - own);
+                    if (at >= 0) from[u] = a.free_pages + at;
                 }
-                if (page >= 0) slot = (page << a.page_shift) + (pos & ((int64_t(1) << a.page_shift) - 1));
             }
         }
-        a.slots[t] = slot;
+#pragma unroll
+        for (int u = 0; u < kTurn; ++u) page[u] = from[u] ? *from[u] : -1;
+#pragma unroll
+        for (int u = 0; u < kTurn; ++u)
+            if (t0 + 32 * u < a.capacity)
+                a.slots[t0 + 32 * u] = page[u] >= 0 ? (static_cast<int64_t>(page[u]) << a.page_shift) + inside[u] : -1;
     }
     for (int64_t r = blockIdx.x * static_cast<int64_t>(kThreads) + tid; r < n_pages; r += step) {
         const int ri = static_cast<int>(r);
         const int q = find(pages, B, ri);
-        const int64_t held = min(static_cast<int64_t>(max(a.held[q], 0)), a.cols);
         const int64_t at = count - 1 - r;
-        a.table[q * a.stride + held + (ri - pages[q])] = at >= 0 ? a.free_pages[at] : -1;
+        a.table[q * a.stride + held[q] + (ri - pages[q])] = at >= 0 ? a.free_pages[at] : -1;
     }
 }
 
@@ -164,10 +181,12 @@ cudaError_t launch_cache_slots(const SlotsArgs& a, cudaStream_t stream) {
     const int64_t most = 2 * device_info(dev).sm_count;
     int64_t blocks = (work + 4 * kThreads - 1) / (4 * kThreads);
     blocks = blocks < 1 ? 1 : (blocks < most ? blocks : most);
-    const size_t smem = 2 * sizeof(int) * (static_cast<size_t>(a.requests) + 1);
-    e = cudaFuncSetAttribute(cache_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             2 * sizeof(int) * (kMaxRequests + 1));
-    if (e != cudaSuccess) return e;
+    const size_t smem = sizeof(int) * (4 * static_cast<size_t>(a.requests) + 2);
+    if (smem > 48 * 1024) {
+        e = cudaFuncSetAttribute(cache_slots_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize,
+                                 sizeof(int) * (4 * kMaxRequests + 2));
+        if (e != cudaSuccess) return e;
+    }
     cache_slots_kernel<<<static_cast<unsigned>(blocks), kThreads, smem, stream>>>(a);
     return cudaGetLastError();
 }
