@@ -1,6 +1,8 @@
 // cache_attention.h -- what the kernels of attention over the 8-bit cache share.
 #pragma once
 
+#include <atomic>
+
 #include <cuda.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
@@ -73,6 +75,17 @@ __device__ __forceinline__ float2 widen_q(uint32_t v, bool bf16) {
 __device__ __forceinline__ uint32_t pack_half(float x, float y) {
     const __half2 h = __floats2half2_rn(x, y);
     return *reinterpret_cast<const uint32_t*>(&h);
+}
+
+// Sets a kernel's shared-memory limit once for each device (`done`: one bit a device, of the kernel's own).
+template <typename Kernel>
+inline cudaError_t allow_shared(Kernel kernel, size_t bytes, int device, std::atomic<uint64_t>& done) {
+    const uint64_t bit = uint64_t(1) << (device & 63);
+    if (device < 64 && (done.load(std::memory_order_acquire) & bit)) return cudaSuccess;
+    const cudaError_t e =
+        cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, static_cast<int>(bytes));
+    if (e == cudaSuccess && device < 64) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 }  // namespace attn

@@ -809,8 +809,8 @@ cudaError_t launch(const AttentionArgs& a, cudaStream_t stream) {
     PieceInfo* const infos = reinterpret_cast<PieceInfo*>(w);
     Piece<DP, NR>* const pieces = reinterpret_cast<Piece<DP, NR>*>(w + round16(sizeof(PieceInfo) * 2 * blocks));
     const size_t smem = sizeof(Smem<DP, NR>) + 1024;
-    e = cudaFuncSetAttribute(attention_split_kernel<DP, NR>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
+    static std::atomic<uint64_t> allowed{0};
+    e = allow_shared(attention_split_kernel<DP, NR>, smem, dev, allowed);
     if (e != cudaSuccess) return e;
     const bool q_wide = wide_rows(a.q, a.q_token_stride, a.q_head_stride, 16);
     const bool out_wide = wide_rows(a.out, a.out_token_stride, a.out_head_stride, 8);

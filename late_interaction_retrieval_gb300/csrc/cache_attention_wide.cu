@@ -1028,8 +1028,8 @@ cudaError_t launch(const AttentionArgs& a, cudaStream_t stream) {
     float* const pieces = reinterpret_cast<float*>(w + round16(sizeof(PieceInfo) * 2 * blocks));
     const int piece_rows = piece_rows_of(a.rows, a.q_heads / a.heads);
     const size_t smem = sizeof(Smem<DP>) + 1024;
-    e = cudaFuncSetAttribute(attention_wide_kernel<DP>, cudaFuncAttributeMaxDynamicSharedMemorySize,
-                             static_cast<int>(smem));
+    static std::atomic<uint64_t> allowed{0};
+    e = allow_shared(attention_wide_kernel<DP>, smem, dev, allowed);
     if (e != cudaSuccess) return e;
     const bool q_wide = wide_rows(a.q, a.q_token_stride, a.q_head_stride);
     const bool out_wide = wide_rows(a.out, a.out_token_stride, a.out_head_stride);
