@@ -5,7 +5,8 @@ score(q, d) = sum over valid query tokens i of max over valid document
 tokens j of Q_i . D_j, in three layouts (all-pairs, pairwise, per-query
 candidates) with a backward for each; and training objectives over rows of
 logits (distillation from a teacher's top logits, a clipped policy loss, a
-preference loss), each with its gradient.  All arithmetic runs in the CUDA
+preference loss), each with its gradient; and a serving step of an answer model
+over a cache in 8 bits (``serving``).  All arithmetic runs in the CUDA
 library ``liblik`` (C ABI in ``include/lik.h``); this package only builds it,
 loads it and marshals torch tensors into its calls.
 
@@ -15,9 +16,10 @@ when it is missing.
 """
 import importlib
 
-__all__ = ["binding", "layers", "workloads", "MaxSim", "MaxSimPairwise", "MaxSimKD",
+__all__ = ["binding", "layers", "serving", "workloads", "MaxSim", "MaxSimPairwise", "MaxSimKD",
            "maxsim", "maxsim_pairwise", "maxsim_kd", "DistillTopK", "PolicyLoss", "PreferenceLoss",
-           "distill_topk", "policy_loss", "preference_loss", "LIKError"]
+           "distill_topk", "policy_loss", "preference_loss", "TokenCache",
+           "cache_slots", "cache_write", "cache_attention", "verify_drafts", "LIKError"]
 
 _LAZY = {
     "binding": ("late_interaction_retrieval_gb300.binding", None),
@@ -34,6 +36,12 @@ _LAZY = {
     "distill_topk": ("late_interaction_retrieval_gb300.layers", "distill_topk"),
     "policy_loss": ("late_interaction_retrieval_gb300.layers", "policy_loss"),
     "preference_loss": ("late_interaction_retrieval_gb300.layers", "preference_loss"),
+    "serving": ("late_interaction_retrieval_gb300.serving", None),
+    "TokenCache": ("late_interaction_retrieval_gb300.serving", "TokenCache"),
+    "cache_slots": ("late_interaction_retrieval_gb300.serving", "cache_slots"),
+    "cache_write": ("late_interaction_retrieval_gb300.serving", "cache_write"),
+    "cache_attention": ("late_interaction_retrieval_gb300.serving", "cache_attention"),
+    "verify_drafts": ("late_interaction_retrieval_gb300.serving", "verify_drafts"),
     "LIKError": ("late_interaction_retrieval_gb300.binding", "LIKError"),
 }
 

@@ -1,3 +1,4 @@
+import gc
 import os
 import sys
 
@@ -28,3 +29,11 @@ def pytest_collection_modifyitems(config, items):
     for item in items:
         if "gpu" in item.keywords:
             item.add_marker(skip)
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _no_garbage_left():
+    """Device memory that only cycles hold (a caught error's frames) goes with
+    its module: freed later, it would upset another's count of allocated bytes."""
+    yield
+    gc.collect()
