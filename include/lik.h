@@ -569,18 +569,19 @@ lik_status lik_preference_loss_step(const void* logits, lik_dtype dtype, int64_t
  *     k_cache, v_cache  [pages, heads, page_size, dim], codes of 8 bits (e4m3:
  *                       1 sign, 4 exponent, 3 fraction bits, largest 448),
  *                       contiguous, 16-byte aligned
- *     k_scale, v_scale  [pages, heads] fp32: a code c stands for c * scale
+ *     k_scale, v_scale  [pages, heads] fp32, not negative: a code c stands for
+ *                       c * scale
  * A token's slot is page * page_size + its offset in the page (int64).  A
  * request's tokens 0, 1, ... lie in the pages block_table[b][0], [1], ...;
  * several layers share one table.  A batch has `requests` requests of which
  * request b adds the rows offsets[b] .. offsets[b + 1] - 1 of a packed batch
- * (offsets [requests + 1] int32, device, not falling); they are its last
- * tokens.  Rows behind offsets[requests] are padding: a batch that a graph
+ * (offsets [requests + 1] int32, device, from 0, not falling); they are its
+ * last tokens.  Rows behind offsets[requests] are padding: a batch that a graph
  * was captured with stays as large as it was.  Sizes that only the device
  * knows are never read back; values outside their range are clamped, so that
  * nothing outside a buffer is read or written.
- * Outputs must not overlap inputs, but for what is updated in place (said
- * so).  requests <= 8192.
+ * Outputs must not overlap inputs, nor lie between their rows, but for what
+ * is updated in place (said so).  requests <= 8192.
  */
 
 /*
@@ -649,13 +650,17 @@ lik_status lik_cache_write(const void* k, const void* v, lik_dtype dtype, int64_
  * A row that sees nothing has out 0 and lse -inf.  What a row does not see
  * does not matter to it, whatever it holds (NaN codes, scales of pages that
  * are not its own).  Rows that belong to no request are left as they are.
- * Sums and softmax statistics are fp32; the products' operands are fp16 (q
- * brought into its range by a power of two, the softmax weights rounded to 11
- * bits, codes exact).  Results do not depend on the run.
+ * Sums and softmax statistics are fp32; the products' operands are fp16: codes
+ * exact, q brought into its range by a power of two, and the softmax weights
+ * rounded to 11 bits over the 20 binades below a row's largest one (what is
+ * smaller keeps fewer bits, and below 2^-31 of it none).  Results do not depend
+ * on the run.  A scale of a seen page that is not finite makes its tokens'
+ * scores (k_scale) or the row's output (v_scale) not finite.
  *   q, out [rows, q_heads, dim], fp16 or bf16, element (t, h, d) at t *
  *   token_stride + h * head_stride + d; lse [rows, q_heads] fp32 or NULL;
  *   block_table [requests, table_cols] int32, row b at b * table_stride;
- *   1e-30 <= scale <= 1e30.
+ *   1e-30 <= scale <= 1e30.  lengths are clamped to [0, table_cols *
+ *   page_size], offsets to [0, rows].
  *   max_added: the most tokens that a request adds, as the host knows it: it
  *   chooses the kernel.  A wrong value costs time, not results.
  *   workspace: 16-byte aligned, of lik_cache_attention_workspace_bytes bytes
@@ -693,7 +698,8 @@ lik_status lik_cache_attention(const void* q, lik_dtype dtype, int64_t rows, int
  * With uniform in [0, 1) and noise from the exponential distribution, y is
  * drawn from r's distribution.  A column of -inf has probability 0.  A target
  * row with a NaN or +inf logit, or of -inf alone, passes nothing and draws -1;
- * a drafted token outside [0, cols) does not pass.  Probabilities are fp32,
+ * a draft whose own row has one does not pass and is replaced from p; a
+ * drafted token outside [0, cols) does not pass.  Probabilities are fp32,
  * sums fp32 or wider.
  *   target_logits [drafts + requests, cols], draft_logits [drafts, cols] of
  *   one dtype (fp32, fp16, bf16), row r at element r * stride; drafted

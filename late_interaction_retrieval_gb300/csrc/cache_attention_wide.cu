@@ -1,14 +1,13 @@
 // cache_attention_wide.cu -- attention over the 8-bit cache for many rows a
 // key head (drafts of grouped heads, prompts): the products on tcgen05.
 //
-// A tile is 128 tokens against 128 rows: S = Q K^T in tensor memory, its
-// softmax weights back into tensor memory as fp16, O += P V.  Two tiles are in
-// work at a time, in two streams with a softmax warpgroup, an S/P and an O
-// accumulator each, so that the tensor cores work on one while the other's
-// exponentials are taken.  Where an item has more than 128 rows the streams
-// are its two halves, on the same tokens (the codes are widened once for
-// both); else they are the even and the odd tiles of the same rows, joined at
-// the item's end.
+// A tile is 64 tokens against 128 rows: S = Q K^T in tensor memory, its
+// softmax weights back into tensor memory as fp16, O += P V.  There are two
+// streams with a softmax warpgroup, two S/P and an O accumulator each, so that
+// the tensor cores work on one while the other's exponentials are taken.
+// Where an item has more than 128 rows the streams are its two halves, on the
+// same tokens (the codes are widened once for both); else they are the even
+// and the odd tiles of the same rows, joined at the item's end.
 //
 // The codes become fp16 (exactly) on their way from the TMA ring to the MMA's
 // operand tiles.  K stays token by token.  V is transposed, so that both
@@ -18,11 +17,16 @@
 // the tokens of S's columns are ordered that way: column j of a block holds
 // token (j mod 8) * 8 + j / 8.
 //
-// The weights are 2^7 exp2(z - m) (the page's scale / c), with a maximum m
-// that is only moved when it is exceeded by 2^8 and a scale c that is moved to
-// twice the largest; both moves rescale O, and are rare.  Work is spread as
-// in the kernel for few rows: the batch's tiles end to end, one equal range a
-// block, pieces of cut items joined by a second launch.
+// The weights are 2^7 exp2(z - ref) (the page's scale / c) in fp16.  ref is a
+// power of two near the row's largest weight and c one not below the scales;
+// either moves only when a weight leaves fp16's range, which its sum shows (no
+// maximum is taken on the way), and its move rescales O, exactly.  Work is
+// spread by costs in closed form, the batch's items end to end, one equal
+// range a block; pieces of cut items are joined by a second launch.
+//
+// What bounds it: neither memory nor the tensor cores but the chain weights ->
+// O and next scores -> weights of a stream (2000 clocks a tile, of which the
+// tensor cores take 620), and 14000 clocks at an item's start and end.
 #include "cache_attention.h"
 #include "tmap.h"
 
@@ -41,6 +45,9 @@ constexpr int kAhead = 2;       // steps of a stream whose scores are computed a
 constexpr int kScaleRing = 16;  // tiles whose scales are kept
 // warps
 constexpr int kConvert = 8, kLoad = 16, kMma = 17, kBusy = 19;  // converters of K, of V; an issuer of MMAs a stream
+
+constexpr float kHalfMost = 65504.0f;  // the largest finite fp16
+constexpr float kLogLimit = 9.5f;      // 64 weights of 2^9.5 are below it together
 
 constexpr uint32_t kColS = 0, kColO = 256;
 
@@ -91,18 +98,28 @@ __device__ __forceinline__ void shape(Item& x, int group) {
     x.tiles = max(1, (sees + kTok - 1) / kTok);
 }
 
-__device__ __forceinline__ long long steps_of(const Request& r, int group, int i) {
-    Item x;
-    x.r = r;
-    x.item = i;
-    shape(x, group);
-    return static_cast<long long>(x.tiles) * (x.two ? 2 : 1);
-}
+// What items cost, in closed form, so that a block finds its range without a walk over the batch.  The unit is a token
+// of one stream and one row group of a stream's 128: an item of both streams costs 2 group (tokens that its last row
+// sees + kItemCost), 256 rows being 256 / group tokens, which is counted group times and so stays whole; one of a
+// single stream's rows, whose tiles the streams share, half of that and as much again for its start and end.
+constexpr int kItemCost = 416;  // tokens: q, the output, and the rest of the last tile (14000 clocks, a tile 2000)
 
-__device__ long long steps_of_head(const Request& r, int group) {
-    long long s = 0;
-    for (int i = 0; i < items_of(r, group); ++i) s += steps_of(r, group, i);
-    return s;
+struct Costs {
+    long long each, last;  // 2 group (tokens before the request's new ones + kItemCost); the last item's
+    int items;
+    // of the items before item i
+    __device__ __forceinline__ long long before(int i) const { return i * each + static_cast<long long>(kItemRows) * i * (i + 1); }
+    __device__ __forceinline__ long long all() const { return before(items - 1) + last; }  // of a key head
+};
+
+__device__ __forceinline__ Costs costs_of(const Request& r, int group) {
+    Costs c;
+    c.items = items_of(r, group);
+    const long long base = max(r.length - r.n, 0);
+    const int rows = r.n * group - (c.items - 1) * kItemRows;
+    c.each = 2 * group * (base + kItemCost);
+    c.last = rows > kM ? c.each + 2ll * r.n * group : group * (base + 2 * kItemCost) + r.n * group;
+    return c;
 }
 
 // Walks a block's segments: an item and a range of its tiles.  The range's end
@@ -191,28 +208,64 @@ __device__ __forceinline__ void tmem_st_16(uint32_t taddr, const uint32_t (&v)[1
         : "memory");
 }
 
-// 64 columns of this thread's lane, and their maximum, which the loads take
-// (loads and wait in one statement, so that no use comes before the wait).
-__device__ __forceinline__ void tmem_ldmax_64(uint32_t taddr, uint32_t (&v)[64], float& mx) {
-    float a, b, c, d;
+// 32 columns of this thread's lane, on their way: fence_loaded() before they are used.
+__device__ __forceinline__ void tmem_ld_32(uint32_t taddr, uint32_t (&v)[32]) {
     asm volatile(
-        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15}, %64, [%68];\n\t"
-        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, %65, [%69];\n\t"
-        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%32, %33, %34, %35, %36, %37, %38, %39, %40, %41, %42, %43, %44, %45, %46, %47}, %66, [%70];\n\t"
-        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%48, %49, %50, %51, %52, %53, %54, %55, %56, %57, %58, %59, %60, %61, %62, %63}, %67, [%71];\n\t"
-        "tcgen05.wait::ld.sync.aligned;"
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0, %1, %2, %3, %4, %5, %6, %7, %8, %9, %10, %11, %12, %13, %14, %15, "
+        "%16, %17, %18, %19, %20, %21, %22, %23, %24, %25, %26, %27, %28, %29, %30, %31}, [%32];"
         : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]), "=r"(v[4]), "=r"(v[5]), "=r"(v[6]), "=r"(v[7]),
           "=r"(v[8]), "=r"(v[9]), "=r"(v[10]), "=r"(v[11]), "=r"(v[12]), "=r"(v[13]), "=r"(v[14]), "=r"(v[15]),
           "=r"(v[16]), "=r"(v[17]), "=r"(v[18]), "=r"(v[19]), "=r"(v[20]), "=r"(v[21]), "=r"(v[22]), "=r"(v[23]),
-          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31]),
-          "=r"(v[32]), "=r"(v[33]), "=r"(v[34]), "=r"(v[35]), "=r"(v[36]), "=r"(v[37]), "=r"(v[38]), "=r"(v[39]),
-          "=r"(v[40]), "=r"(v[41]), "=r"(v[42]), "=r"(v[43]), "=r"(v[44]), "=r"(v[45]), "=r"(v[46]), "=r"(v[47]),
-          "=r"(v[48]), "=r"(v[49]), "=r"(v[50]), "=r"(v[51]), "=r"(v[52]), "=r"(v[53]), "=r"(v[54]), "=r"(v[55]),
-          "=r"(v[56]), "=r"(v[57]), "=r"(v[58]), "=r"(v[59]), "=r"(v[60]), "=r"(v[61]), "=r"(v[62]), "=r"(v[63]),
-          "=f"(a), "=f"(b), "=f"(c), "=f"(d)
-        : "r"(taddr), "r"(taddr + 16), "r"(taddr + 32), "r"(taddr + 48)
+          "=r"(v[24]), "=r"(v[25]), "=r"(v[26]), "=r"(v[27]), "=r"(v[28]), "=r"(v[29]), "=r"(v[30]), "=r"(v[31])
+        : "r"(taddr)
         : "memory");
-    mx = fmaxf(fmaxf(a, b), fmaxf(c, d));
+}
+// Waits for the loads; every use of v comes behind it.
+__device__ __forceinline__ void fence_loaded(uint32_t (&v)[32]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(v[0]), "+r"(v[1]), "+r"(v[2]), "+r"(v[3]), "+r"(v[4]), "+r"(v[5]), "+r"(v[6]), "+r"(v[7]),
+                   "+r"(v[8]), "+r"(v[9]), "+r"(v[10]), "+r"(v[11]), "+r"(v[12]), "+r"(v[13]), "+r"(v[14]), "+r"(v[15]),
+                   "+r"(v[16]), "+r"(v[17]), "+r"(v[18]), "+r"(v[19]), "+r"(v[20]), "+r"(v[21]), "+r"(v[22]),
+                   "+r"(v[23]), "+r"(v[24]), "+r"(v[25]), "+r"(v[26]), "+r"(v[27]), "+r"(v[28]), "+r"(v[29]),
+                   "+r"(v[30]), "+r"(v[31])
+                 :
+                 : "memory");
+}
+
+// Two fp32 numbers in one register pair, for one instruction on both.
+__device__ __forceinline__ uint64_t both(float x, float y) {
+    uint64_t d;
+    asm("mov.b64 %0, {%1, %2};" : "=l"(d) : "f"(x), "f"(y));
+    return d;
+}
+__device__ __forceinline__ float2 each_of(uint64_t v) {
+    float2 r;
+    asm("mov.b64 {%0, %1}, %2;" : "=f"(r.x), "=f"(r.y) : "l"(v));
+    return r;
+}
+__device__ __forceinline__ uint64_t fma_both(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+__device__ __forceinline__ uint64_t add_both(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+
+// The larger of either half's 16 bits.
+__device__ __forceinline__ uint32_t max_halves(uint32_t a, uint32_t b) {
+    uint32_t d;
+    asm("max.u16x2 %0, %1, %2;" : "=r"(d) : "r"(a), "r"(b));
+    return d;
+}
+
+// One thread of the warp.
+__device__ __forceinline__ bool elect() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+    return p != 0;
 }
 
 // Registers of a warpgroup's threads: 256 threads of 144 and 384 of 64 are the
@@ -220,24 +273,31 @@ __device__ __forceinline__ void tmem_ldmax_64(uint32_t taddr, uint32_t (&v)[64],
 __device__ __forceinline__ void more_registers() { asm volatile("setmaxnreg.inc.sync.aligned.u32 144;"); }
 __device__ __forceinline__ void fewer_registers() { asm volatile("setmaxnreg.dec.sync.aligned.u32 64;"); }
 
-// 8 neighbouring dimensions of one row to the output.
-__device__ __forceinline__ void store8(void* out, int64_t at, const float (&f)[8], bool bf16, bool wide) {
-    uint32_t w[4];
+__device__ __forceinline__ uint32_t pack_out(float x, float y, bool bf16) {
+    if (!bf16) return pack_half(x, y);
+    const __nv_bfloat162 v = __floats2bfloat162_rn(x, y);
+    return *reinterpret_cast<const uint32_t*>(&v);
+}
+
+// N neighbouring dimensions of one row to the output; wide: the bytes that its rows are aligned to (32: a sector in
+// one store).
+template <int N>
+__device__ __forceinline__ void store(void* out, int64_t at, const float (&f)[N], bool bf16, int wide) {
+    uint32_t w[N / 2];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        if (bf16) {
-            const __nv_bfloat162 x = __floats2bfloat162_rn(f[2 * i], f[2 * i + 1]);
-            w[i] = *reinterpret_cast<const uint32_t*>(&x);
-        } else {
-            w[i] = pack_half(f[2 * i], f[2 * i + 1]);
-        }
-    }
+    for (int i = 0; i < N / 2; ++i) w[i] = pack_out(f[2 * i], f[2 * i + 1], bf16);
     uint16_t* const p = static_cast<uint16_t*>(out) + at;
-    if (wide) {
-        *reinterpret_cast<uint4*>(p) = make_uint4(w[0], w[1], w[2], w[3]);
+    if (N == 16 && wide >= 32) {
+        asm volatile("st.global.v8.b32 [%0], {%1, %2, %3, %4, %5, %6, %7, %8};" ::"l"(p), "r"(w[0]), "r"(w[1]), "r"(w[2]),
+                     "r"(w[3]), "r"(w[N / 2 - 4]), "r"(w[N / 2 - 3]), "r"(w[N / 2 - 2]), "r"(w[N / 2 - 1])
+                     : "memory");
+    } else if (wide >= 16) {
+#pragma unroll
+        for (int i = 0; i < N / 8; ++i)
+            reinterpret_cast<uint4*>(p)[i] = make_uint4(w[4 * i], w[4 * i + 1], w[4 * i + 2], w[4 * i + 3]);
     } else {
 #pragma unroll
-        for (int i = 0; i < 4; ++i) {
+        for (int i = 0; i < N / 2; ++i) {
             p[2 * i] = static_cast<uint16_t>(w[i]);
             p[2 * i + 1] = static_cast<uint16_t>(w[i] >> 16);
         }
@@ -247,7 +307,7 @@ __device__ __forceinline__ void store8(void* out, int64_t at, const float (&f)[8
 template <int DP>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_wide_kernel(const AttentionArgs a, const __grid_constant__ Maps maps, unsigned int* err,
-                          PieceInfo* infos, float* pieces, int piece_rows, bool q_wide, bool out_wide) {
+                          PieceInfo* infos, float* pieces, int piece_rows, bool q_wide, int out_wide) {
     extern __shared__ uint8_t raw_smem[];
     Smem<DP>& sm = *reinterpret_cast<Smem<DP>*>((reinterpret_cast<uintptr_t>(raw_smem) + 1023) & ~uintptr_t(1023));
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -284,11 +344,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         sm.nan_seen = 0;
         ptx::fence_mbar_init();
     }
-    // ---- the block's range of steps (a tile of one stream), from every request's
+    // ---- the block's range of the batch, by costs, from every request's
     const int B = a.requests, each = (B + kThreads - 1) / kThreads;
+    auto cost_of = [&](int b) {
+        const Request r = request_of(a, b);
+        return r.n > 0 ? costs_of(r, group).all() * a.heads : 0ll;
+    };
     long long mine = 0;
-    for (int b = min(tid * each, B); b < min(tid * each + each, B); ++b)
-        mine += steps_of_head(request_of(a, b), group) * a.heads;
+    for (int b = min(tid * each, B); b < min(tid * each + each, B); ++b) mine += cost_of(b);
     long long incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -303,40 +366,40 @@ __global__ void __launch_bounds__(kThreads, 1)
         all += sm.warp_sum[w];
     }
     const long long excl = incl - mine;
-    // a block has two steps at least
-    const long long active = max(1ll, min(static_cast<long long>(gridDim.x), all / 2));
-    const long long u0 = blockIdx.x < active ? all * blockIdx.x / active : all;
-    const long long u1 = blockIdx.x < active ? all * (blockIdx.x + 1) / active : all;
     if (tid < 2) infos[2 * blockIdx.x + tid] = PieceInfo{-1, 0, 0, 0, 0};
-    if (u0 >= u1) return;
-    // the tile that holds step u, by the thread whose requests do; a range ends
-    // before the tile of its last bound, or behind the batch's last
-    auto locate = [&](long long u, int* to, int more) {
+    // a block has two steps (a tile of one stream) at least, or thereabouts
+    const long long active = max(1ll, min(static_cast<long long>(gridDim.x), all / (2 * kTok * group)));
+    if (all == 0 || blockIdx.x >= active) return;
+    auto bound = [&](long long k) { return all / active * k + all % active * k / active; };
+    // the tile that a cost u falls on, by the thread whose requests do; the batch's end comes behind its last tile
+    auto locate = [&](long long u, int* to) {
+        const bool behind = u == all;
+        u -= behind;
         if (u < excl || u >= incl) return;
         long long rest = u - excl;
         int b = tid * each;
-        Request r = request_of(a, b);
-        long long per = steps_of_head(r, group);
-        while (rest >= per * a.heads) {
-            rest -= per * a.heads;
-            r = request_of(a, ++b);
-            per = steps_of_head(r, group);
-        }
+        while (rest >= cost_of(b)) rest -= cost_of(b++);
+        const Request r = request_of(a, b);
+        const Costs c = costs_of(r, group);
         to[0] = b;
-        to[1] = static_cast<int>(rest / per);
-        rest %= per;
-        int i = 0;
-        while (rest >= steps_of(r, group, i)) rest -= steps_of(r, group, i++);
+        to[1] = static_cast<int>(rest / c.all());
+        rest %= c.all();
+        int i = 0;  // the last item that begins at or before it
+        for (int step = 1 << (31 - __clz(c.items)); step; step >>= 1)
+            if (i + step < c.items && c.before(i + step) <= rest) i += step;
         Item x;
         x.r = r;
         x.item = i;
         shape(x, group);
+        const double cost = static_cast<double>(i + 1 < c.items ? c.before(i + 1) - c.before(i) : c.last);
         to[2] = i;
-        to[3] = static_cast<int>(x.two ? rest / 2 : rest) + more;
+        to[3] = behind ? x.tiles : min(x.tiles - 1, static_cast<int>(static_cast<double>(rest - c.before(i)) / cost * x.tiles));
     };
-    locate(u0, sm.start, 0);
-    if (u1 < all) locate(u1, sm.end, 0);
-    else locate(all - 1, sm.end, 1);
+    locate(bound(blockIdx.x), sm.start);
+    locate(bound(blockIdx.x + 1), sm.end);
+    __syncthreads();
+    if (sm.start[0] == sm.end[0] && sm.start[1] == sm.end[1] && sm.start[2] == sm.end[2] && sm.start[3] == sm.end[3])
+        return;  // both bounds fall on one tile
     if (warp == kMma) {
         ptx::tmem_alloc(smem_u32(&sm.tmem), 512);
         ptx::tmem_relinquish();
@@ -534,69 +597,90 @@ __global__ void __launch_bounds__(kThreads, 1)
         fewer_registers();
         Walk w;
         w.begin(a, group, sm.start, sm.end);
-        if (lane == 0) {
-            constexpr uint32_t kIdS = ptx::f16_idesc(kM, kTok, false), kIdO = ptx::f16_idesc(kM, DP, false);
-            const int s = warp - kMma;
-            const uint32_t col_s = tmem + kColS + 128 * s, col_o = tmem + kColO + 128 * s;
-            int n = 0;                    // tiles before this segment
-            int scored = 0, summed = 0;   // steps of this stream so far
-            uint32_t q_phase = 0;
-            while (ok) {
-                const bool two = w.x.two;
-                const int tiles = w.t1 - w.t0, steps = two ? tiles : (tiles + 1 - s) / 2;
-                // A buffer is empty again when both streams have done with it; a tile of one stream counts twice.
-                auto done = [&](uint64_t* bar) {
-                    ptx::mma_commit(smem_u32(bar));
-                    if (!two) ptx::mma_commit(smem_u32(bar));
-                };
-                // Step i's tile.  Tiles are filled in order, so the other stream's phase between two of this
-                // stream's in one buffer has been completed when this one asks for the second.
-                auto tile_of = [&](int i) { return n + (two ? i : 2 * i + s); };
-                auto score = [&](int i) {
-                    const int t = tile_of(i), kb = t % kKeys, b = scored & 1;
-                    ok = ok && ptx::mbar_wait(smem_u32(&sm.k_full[kb]), (t / kKeys) & 1, err);
-                    if (!ok) return;
-                    ptx::tc_fence_after();
-                    // the buffer's weights of two steps ago were multiplied by an instruction before this one
-                    uint64_t qd = ptx::sw128_kmajor_desc(smem_u32(sm.q[s][0]));
-                    uint64_t kd = ptx::sw128_kmajor_desc(smem_u32(sm.k[kb][0]));
-#pragma unroll 1
-                    for (int atom = 0; atom < DP / 64; ++atom) {  // 64 dimensions: 4 steps of 32 bytes
+        // The warp goes through it together, one thread of it issues: so the operands are uniform, and an instruction is
+        // issued in a third of the clocks that it takes in a branch of one lane.
+        constexpr uint32_t kIdS = ptx::f16_idesc(kM, kTok, false), kIdO = ptx::f16_idesc(kM, DP, false);
+        const bool leader = elect();
+        const int s = warp - kMma;
+        const uint32_t col_s = tmem + kColS + 128 * s, col_o = tmem + kColO + 128 * s;
+        // descriptors count addresses in 16 bytes
+        const uint64_t q0 = ptx::sw128_kmajor_desc(smem_u32(sm.q[s][0])), k0 = ptx::sw128_kmajor_desc(smem_u32(sm.k[0][0])),
+                       v0 = ptx::sw128_kmajor_desc(smem_u32(sm.v[0]));
+        int n = 0;        // tiles before this segment
+        uint32_t sb = 0;  // the buffer of the next scores
+        uint32_t ob = 0, p_phase = 0, q_phase = 0;
+        auto wait = [&](uint64_t& bar, uint32_t phase) {
+            ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&bar), phase, err));
+        };
+        while (ok) {
+            const bool two = w.x.two;
+            const int tiles = w.t1 - w.t0, steps = two ? tiles : (tiles + 1 - s) / 2;
+            // A buffer is empty again when both streams have done with it; a tile of one stream counts twice.
+            auto done = [&](uint64_t* bar) {
+                ptx::mma_commit(smem_u32(bar));
+                if (!two) ptx::mma_commit(smem_u32(bar));
+            };
+            // This stream's tiles: all of the segment's, or every second one.  Tiles are filled in order, so the other
+            // stream's phase between two of this stream's in one buffer has been completed when this one asks for the
+            // second.
+            const int first = n + (two ? 0 : s), by = two ? 1 : 2;
+            int kb = first % kKeys, vb = first % kValues;
+            uint32_t k_phase = (first / kKeys) & 1, v_phase = (first / kValues) & 1;
+            // The scores of the next tile.  The weights of two steps ago in their place were multiplied by an
+            // instruction before these.
+            auto score = [&]() {
+                wait(sm.k_full[kb], k_phase);
+                if (!ok) return;
+                ptx::tc_fence_after();
+                const uint64_t kd = k0 + kb * (DP / 64 * kTok * 128 / 16);
+                const uint32_t d = col_s + 64 * sb;
+                if (leader) {
 #pragma unroll
-                        for (int k = 0; k < 4; ++k)
-                            ptx::mma_f16(col_s + 64 * b, qd + 2 * k, kd + 2 * k, kIdS, atom > 0 || k != 0);
-                        qd += kM * 128 / 16;
-                        kd += kTok * 128 / 16;
-                    }
-                    ptx::mma_commit(smem_u32(&sm.s_full[s][b]));
+                    for (int k = 0; k < DP / 16; ++k)  // 64 dimensions a swizzle atom: 4 steps of 32 bytes
+                        ptx::mma_f16(d, q0 + (k >> 2) * (kM * 128 / 16) + 2 * (k & 3),
+                                     kd + (k >> 2) * (kTok * 128 / 16) + 2 * (k & 3), kIdS, k != 0);
+                    ptx::mma_commit(smem_u32(&sm.s_full[s][sb]));
                     done(&sm.k_empty[kb]);
-                    ++scored;
-                };
-                if (steps > 0) {
-                    ok = ptx::mbar_wait(smem_u32(&sm.q_full[s]), q_phase, err);
-                    q_phase ^= 1;
                 }
-                for (int i = 0; ok && i < min(kAhead, steps); ++i) score(i);
-                for (int i = 0; ok && i < steps; ++i) {
-                    const int t = tile_of(i), vb = t & (kValues - 1), b = summed & 1;
-                    ok = ptx::mbar_wait(smem_u32(&sm.v_full[vb]), (t / kValues) & 1, err) &&
-                         ptx::mbar_wait(smem_u32(&sm.p_full[s][b]), (summed >> 1) & 1, err);
-                    if (!ok) break;
-                    ++summed;
-                    ptx::tc_fence_after();
-                    const uint64_t vd = ptx::sw128_kmajor_desc(smem_u32(sm.v[vb]));
+                sb ^= 1;
+                if ((kb += by) >= kKeys) {
+                    kb -= kKeys;
+                    k_phase ^= 1;
+                }
+            };
+            if (steps > 0) {
+                wait(sm.q_full[s], q_phase);
+                q_phase ^= 1;
+            }
+            for (int i = 0; ok && i < min(kAhead, steps); ++i) score();
+            for (int i = 0; ok && i < steps; ++i) {
+                wait(sm.v_full[vb], v_phase);
+                wait(sm.p_full[s][ob], p_phase);
+                if (!ok) break;
+                ptx::tc_fence_after();
+                const uint64_t vd = v0 + vb * (DP * 128 / 16);
+                if (leader) {
 #pragma unroll
                     for (int k = 0; k < kTok / 16; ++k)
-                        mma_f16_ts(col_o, col_s + 64 * b + 8 * k, vd + 2 * k, kIdO, i > 0 || k != 0);
+                        mma_f16_ts(col_o, col_s + 64 * ob + 8 * k, vd + 2 * k, kIdO, i > 0 || k != 0);
+                }
+                // the next scores first: the softmax waits for them
+                if (i + kAhead < steps) score();
+                if (leader) {
                     ptx::mma_commit(smem_u32(&sm.o_step[s]));
                     if (i + 1 == steps) ptx::mma_commit(smem_u32(&sm.o_full[s]));
                     done(&sm.v_empty[vb]);
-                    if (i + kAhead < steps) score(i + kAhead);
                 }
-                n += tiles;
-                if (!ok || w.last) break;
-                w.next(a, group);
+                p_phase ^= ob;
+                ob ^= 1;
+                if ((vb += by) >= kValues) {
+                    vb -= kValues;
+                    v_phase ^= 1;
+                }
             }
+            n += tiles;
+            if (!ok || w.last) break;
+            w.next(a, group);
         }
         __syncwarp();
     } else {
@@ -607,11 +691,82 @@ __global__ void __launch_bounds__(kThreads, 1)
         const int s = warp >> 2, row = tid & 127;
         const uint32_t lanes = static_cast<uint32_t>(warp & 3) << 21;  // the warp's 32 lanes of tensor memory
         const uint32_t col_o = tmem + lanes + kColO + 128 * s;
+        const uint32_t q_tile = smem_u32(sm.q[s][0]);
+        auto steps_here = [&](const Walk& x) { return x.x.two ? x.t1 - x.t0 : (x.t1 - x.t0 + 1 - s) / 2; };
+        // The warp's rows of x's q on their way into the operand tile, as they are: the lanes of a row's chunks next to
+        // one another, so that whole rows are read.
+        auto fetch = [&](const Walk& x) {
+            if (steps_here(x) <= 0) return false;
+            const int in_item = (x.x.two ? s * kM : 0) + row;
+            const bool live = in_item < x.x.rows;
+            const int rr = live ? x.x.item * kItemRows + in_item : 0;
+            const int i = rr / group, h = x.x.head * group + (rr - i * group);
+            const uint16_t* const src = static_cast<const uint16_t*>(a.q) + (x.x.r.row0 + i) * a.q_token_stride + h * a.q_head_stride;
+            if (q_wide) {
+                constexpr int C = DP / 8, R = 32 / C;  // chunks of a row, rows at a time
+                const int c = lane % C;
+                const uint32_t to = q_tile + (c >> 3) * (kM * 128);
+#pragma unroll 4
+                for (int r = lane / C; r < 32; r += R) {
+                    const uint16_t* const from = reinterpret_cast<const uint16_t*>(
+                        __shfl_sync(0xffffffffu, reinterpret_cast<unsigned long long>(live ? src : nullptr), r));
+                    const uint32_t at = to + tile_at((warp & 3) * 32 + r, c & 7);
+                    if (from && c * 8 < a.dim)
+                        asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(at), "l"(from + c * 8) : "memory");
+                    else
+                        sts16(at, 0, 0, 0, 0);
+                }
+            } else {
+#pragma unroll 1
+                for (int c = 0; c < DP / 8; ++c) {
+                    uint32_t e[4] = {0, 0, 0, 0};
+                    if (live && c * 8 < a.dim) {
+#pragma unroll
+                        for (int k = 0; k < 4; ++k)
+                            e[k] = src[8 * c + 2 * k] | (static_cast<uint32_t>(src[8 * c + 2 * k + 1]) << 16);
+                    }
+                    sts16(q_tile + (c >> 3) * (kM * 128) + tile_at(row, c & 7), e[0], e[1], e[2], e[3]);
+                }
+            }
+            return true;
+        };
+        // The thread's row, scaled to fp16's range in its place; the factor of its scores.
+        auto convert = [&]() {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+            uint32_t sizes = 0;  // the largest size's bits of either half
+#pragma unroll 4
+            for (int c = 0; c < DP / 8; ++c) {
+                const uint4 e = lds16(q_tile + (c >> 3) * (kM * 128) + tile_at(row, c & 7));
+                sizes = max_halves(max_halves(sizes, e.x & 0x7fff7fffu), e.y & 0x7fff7fffu);
+                sizes = max_halves(max_halves(sizes, e.z & 0x7fff7fffu), e.w & 0x7fff7fffu);
+            }
+            const int shift = row_shift(widen_q(max(sizes & 0xffffu, sizes >> 16), bf16).x);
+            const float2 up = power_of_two(shift), down = power_of_two(-shift);
+#pragma unroll 2
+            for (int c = 0; c < DP / 8; ++c) {
+                const uint32_t at = q_tile + (c >> 3) * (kM * 128) + tile_at(row, c & 7);
+                const uint4 v = lds16(at);
+                const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+                uint32_t o[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    const float2 f = widen_q(e[j], bf16);
+                    o[j] = pack_half(f.x * up.x * up.y, f.y * up.x * up.y);
+                }
+                sts16(at, o[0], o[1], o[2], o[3]);
+            }
+            fence_operands();
+            __syncwarp();
+            if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.q_full[s]));
+            return a.scale * 1.44269504088896341f * down.x * down.y;
+        };
         int n = 0, count = 0;  // tiles, and steps of this stream, before
         uint32_t o_phase = 0, merge_phase = 0;
+        float factor = fetch(w) ? convert() : 0.0f;
         while (ok) {
             const bool two = w.x.two;
-            const int tiles = w.t1 - w.t0, steps = two ? tiles : (tiles + 1 - s) / 2;
+            const int tiles = w.t1 - w.t0, steps = steps_here(w);
             const int in_item = (two ? s * kM : 0) + row;
             const bool live = in_item < w.x.rows;
             const int rr = w.x.item * kItemRows + in_item;  // of the request's rows
@@ -620,58 +775,18 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int sees = live ? w.x.r.length - w.x.r.n + i + 1 : 0;
             const int all_see = w.x.r.length - w.x.r.n + (w.x.item * kItemRows) / group + 1;
             const bool idle = __ballot_sync(0xffffffffu, live) == 0;  // no row of this warp's: its weights do not matter
-            float factor = 0.0f, ref = kNothing, l = 0.0f, cref = 0.0f, logc = -127.0f;  // logc: log2 of cref
+            float ref = kNothing, l = 0.0f, cref = 0.0f, logc = -127.0f;  // logc: log2 of cref
             bool nan_scale = false;  // the row sees a page whose values' scale is not finite
-            if (steps > 0) {
-                // the row of q, scaled to fp16's range
-                const uint16_t* const src = static_cast<const uint16_t*>(a.q) + (w.x.r.row0 + i) * a.q_token_stride +
-                                            h * a.q_head_stride;
-                auto load = [&](int c) {  // 8 dimensions
-                    if (!live || c * 8 >= a.dim) return make_uint4(0, 0, 0, 0);
-                    if (q_wide) return __ldg(reinterpret_cast<const uint4*>(src) + c);
-                    uint32_t e[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k)
-                        e[k] = src[8 * c + 2 * k] | (static_cast<uint32_t>(src[8 * c + 2 * k + 1]) << 16);
-                    return make_uint4(e[0], e[1], e[2], e[3]);
-                };
-                // two passes of little code (what runs once an item is fetched each time), the second from L1
-                float most = 0.0f;
-#pragma unroll 1
-                for (int c = 0; c < DP / 8; c += 8) {
-                    uint4 x[8];
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) x[k] = load(c + k);
-#pragma unroll
-                    for (int k = 0; k < 32; ++k) {
-                        const float2 f = widen_q(reinterpret_cast<const uint32_t*>(x)[k], bf16);
-                        most = fmaxf(most, fmaxf(fabsf(f.x), fabsf(f.y)));
-                    }
-                }
-                const int shift = row_shift(most);
-                const float2 up = power_of_two(shift), down = power_of_two(-shift);
-#pragma unroll 1
-                for (int c = 0; c < DP / 8; c += 4) {
-                    uint4 x[4];
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) x[k] = load(c + k);
-#pragma unroll
-                    for (int k = 0; k < 4; ++k) {
-                        const uint32_t* const e = reinterpret_cast<const uint32_t*>(&x[k]);
-                        uint32_t o[4];
-#pragma unroll
-                        for (int j = 0; j < 4; ++j) {
-                            const float2 f = widen_q(e[j], bf16);
-                            o[j] = pack_half(f.x * up.x * up.y, f.y * up.x * up.y);
-                        }
-                        sts16(smem_u32(sm.q[s][(c + k) >> 3]) + tile_at(row, (c + k) & 7), o[0], o[1], o[2], o[3]);
-                    }
-                }
-                factor = a.scale * 1.44269504088896341f * down.x * down.y;
-                fence_operands();
-                __syncwarp();
-                if (lane == 0) ptx::mbar_arrive(smem_u32(&sm.q_full[s]));
-            }
+            // The next item's q is fetched once this one's last scores are there, and is an operand before this one's
+            // output is written.
+            bool more = false;  // it has tiles of this stream
+            auto fetch_next = [&]() {
+                if (w.last) return;
+                Walk x = w;
+                x.next(a, group);
+                more = fetch(x);
+            };
+            if (steps == 0) fetch_next();
             // O times `keep` (1 in rows that need none).  It is at rest once the step before is in it: this step's
             // product waits for its weights.  (The step before that is: this step's scores came after it.  So the
             // phase is not taken for one of two steps ago.)
@@ -697,20 +812,13 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.s_full[s][b]), (count >> 1) & 1, err));
                 if (!ok) break;
                 ptx::tc_fence_after();
+                if (st + 1 == steps) fetch_next();
                 if (!idle) {
                     const uint32_t valid = sm.valid[at];
                     const bool whole = tok0 + kTok <= all_see && valid == 15u;
                     const bool even = whole && page_size >= 64;  // one page, no token hidden
                     // 16 tokens that share their scales: the columns with (j mod 8) / 2 alike
-                    uint32_t v[64];
-                    float fk[4], lw[4], mx = 0.0f;
-                    // c grows to the scales' range: the same in every row
-                    auto grow = [&](float vmost) {
-                        const float to = __int_as_float(min((__float_as_int(vmost) & 0x7f800000) + (1 << 23), 0x7f000000));
-                        if (st > 0) ok = rescale(cref / to);
-                        cref = to;
-                        logc = static_cast<float>((__float_as_int(to) >> 23) - 127);
-                    };
+                    float fk[4], lw[4], minus[4];
                     // log2 of a group's weight (c: 2^7).  2^-60 of c stands in for smaller scales (their fp16
                     // weights are 0 then) and for one that is not finite, which makes the whole row's output NaN: the
                     // sums do not depend on it.  A factor is never 0: a hidden token's score is -inf.  A factor that
@@ -722,24 +830,88 @@ __global__ void __launch_bounds__(kThreads, 1)
                         nan_scale = nan_scale || (seen && !finite);
                         w = x.y > cref * 8.67361738e-19f && finite ? x.z + (kLogStart - logc) : kLogStart - 60.0f;
                     };
-                    if (even) {
-                        const float4 x = sm.scale[at][0];
-                        tmem_ldmax_64(col_s, v, mx);
-                        if (x.y > cref && x.y <= 3.402823466e38f) grow(x.y);
-                        weigh(x, true, fk[0], lw[0]);
+                    // A tile that every row sees whole, under the reference as it is: no maximum is taken.  A weight
+                    // beyond fp16's range shows in the sum, and the weights are only stored if there is none.
+                    bool fits = false;
+                    if (whole) {
+                        uint32_t x[32], y[32], p[16], r[16];
+                        tmem_ld_32(col_s, x);
+                        float vmost = 0.0f;
+                        if (even) {
+                            const float4 sc = sm.scale[at][0];
+                            weigh(sc, true, fk[0], lw[0]);
+                            vmost = sc.y;
 #pragma unroll
-                        for (int k = 1; k < 4; ++k) {
-                            fk[k] = fk[0];
-                            lw[k] = lw[0];
+                            for (int k = 1; k < 4; ++k) {
+                                fk[k] = fk[0];
+                                lw[k] = lw[0];
+                            }
+                        } else {
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) {
+                                const float4 sc = sm.scale[at][k];
+                                weigh(sc, true, fk[k], lw[k]);
+                                vmost = sc.y <= vmost ? vmost : sc.y;  // a NaN stays
+                            }
                         }
-                    } else {
+                        uint64_t f2[4], m2[4], s2[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            f2[k] = both(fk[k], fk[k]);
+                            m2[k] = both(lw[k] - ref, lw[k] - ref);
+                            s2[k] = 0;
+                        }
+                        auto weights = [&](const uint32_t (&v)[32], uint32_t (&to)[16]) {
+#pragma unroll
+                            for (int i = 0; i < 16; ++i) {
+                                const int k = i & 3;
+                                const float2 z = each_of(fma_both(both(__uint_as_float(v[2 * i]), __uint_as_float(v[2 * i + 1])),
+                                                                  f2[k], m2[k]));
+                                const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
+                                s2[k] = add_both(s2[k], both(e0, e1));
+                                to[i] = pack_half(e0, e1);
+                            }
+                        };
+                        fence_loaded(x);
+                        tmem_ld_32(col_s + 32, y);
+                        weights(x, p);
+                        fence_loaded(y);
+                        weights(y, r);
+                        float sum[4];
+#pragma unroll
+                        for (int k = 0; k < 4; ++k) {
+                            const float2 h = each_of(s2[k]);
+                            sum[k] = h.x + h.y;
+                        }
+                        const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+                        fits = __all_sync(0xffffffffu, total <= kHalfMost && vmost <= cref);
+                        if (fits) {
+                            tmem_st_16(col_s, p);
+                            tmem_st_16(col_s + 16, r);
+                            // the group's weight out of its sum again
+                            if (even) {
+                                l = fmaf(total, exp2_fast(-lw[0]), l);
+                            } else {
+#pragma unroll
+                                for (int k = 0; k < 4; ++k) l = fmaf(sum[k], exp2_fast(-lw[k]), l);
+                            }
+                        }
+                    }
+                    if (__builtin_expect(!fits, 0)) {
+                        uint32_t v[64];
+                        // c grows to the scales' range: the same in every row
                         float vmost = 0.0f;
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
                             const float vs = sm.scale[at][k].y;
                             vmost = vs <= 3.402823466e38f ? fmaxf(vmost, vs) : vmost;
                         }
-                        if (vmost > cref) grow(vmost);
+                        if (vmost > cref) {
+                            const float to = __int_as_float(min((__float_as_int(vmost) & 0x7f800000) + (1 << 23), 0x7f000000));
+                            if (st > 0 && !(ok = rescale(cref / to))) break;
+                            cref = to;
+                            logc = static_cast<float>((__float_as_int(to) >> 23) - 127);
+                        }
 #pragma unroll
                         for (int k = 0; k < 4; ++k)
                             weigh(sm.scale[at][k], whole || (tok0 + 16 * k < sees && ((valid >> k) & 1u)), fk[k], lw[k]);
@@ -754,58 +926,44 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 v[j] = seen ? v[j] : 0xff800000u;
                             }
                         }
-                    }
-                    if (!ok) break;
-                    float minus[4];
-                    auto limit = [&]() {  // log2 of the largest weight; the groups' terms under the reference
-#pragma unroll
-                        for (int k = 0; k < 4; ++k) minus[k] = lw[k] - ref;
-                        if (even) return fmaf(mx, fk[0], minus[0]);
-                        float top = -INFINITY;
+                        float top = -INFINITY;  // log2 of the largest weight
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
+                            minus[k] = lw[k] - ref;
                             float g = -INFINITY;
 #pragma unroll
                             for (int i = 0; i < 8; ++i)
                                 g = fmaxf(fmaxf(g, __uint_as_float(v[2 * k + 8 * i])), __uint_as_float(v[2 * k + 8 * i + 1]));
                             top = fmaxf(top, fmaf(g, fk[k], minus[k]));
                         }
-                        return top;
-                    };
-                    const float top = limit();
-                    // a weight beyond fp16's range: the row's reference moves, by a power of two, exact for what has
-                    // been summed and rounded
-                    if (__any_sync(0xffffffffu, top > kLogTop)) {
-                        float keep = 1.0f;
-                        if (top > kLogTop) {
-                            const float by = ceilf(top) - kLogStart;
-                            keep = exp2_fast(-by);  // 0 for the first tokens that a row sees
-                            ref += by;
-                            l *= keep;
+                        // a weight near the end of fp16's range: the row's reference moves, by a power of two, exact
+                        // for what has been summed and rounded (64 weights below the limit fit together)
+                        if (__any_sync(0xffffffffu, top > kLogLimit)) {
+                            float keep = 1.0f;
+                            if (top > kLogLimit) {
+                                const float by = ceilf(top) - kLogStart;
+                                keep = exp2_fast(-by);  // 0 for the first tokens that a row sees
+                                ref += by;
+                                l *= keep;
+                            }
+                            if (st > 0 && !(ok = rescale(keep))) break;
+#pragma unroll
+                            for (int k = 0; k < 4; ++k) minus[k] = lw[k] - ref;
                         }
-                        if (st > 0 && !(ok = rescale(keep))) break;
+                        float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
-                        for (int k = 0; k < 4; ++k) minus[k] = lw[k] - ref;
-                    }
-                    // the weights take the place of the scores
-                    float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
+                        for (int c = 0; c < 2; ++c) {
+                            uint32_t p[16];
 #pragma unroll
-                    for (int c = 0; c < 2; ++c) {
-                        uint32_t p[16];
-#pragma unroll
-                        for (int i = 0; i < 16; ++i) {
-                            const int j = 32 * c + 2 * i, k = i & 3;
-                            const float e0 = exp2_fast(fmaf(__uint_as_float(v[j]), fk[k], minus[k]));
-                            const float e1 = exp2_fast(fmaf(__uint_as_float(v[j + 1]), fk[k], minus[k]));
-                            sum[k] += e0 + e1;
-                            p[i] = pack_half(e0, e1);
+                            for (int i = 0; i < 16; ++i) {
+                                const int j = 32 * c + 2 * i, k = i & 3;
+                                const float e0 = exp2_fast(fmaf(__uint_as_float(v[j]), fk[k], minus[k]));
+                                const float e1 = exp2_fast(fmaf(__uint_as_float(v[j + 1]), fk[k], minus[k]));
+                                sum[k] += e0 + e1;
+                                p[i] = pack_half(e0, e1);
+                            }
+                            tmem_st_16(col_s + 16 * c, p);
                         }
-                        tmem_st_16(col_s + 16 * c, p);
-                    }
-                    // the group's weight out of its sum again
-                    if (even) {
-                        l = fmaf((sum[0] + sum[1]) + (sum[2] + sum[3]), exp2_fast(-lw[0]), l);
-                    } else {
 #pragma unroll
                         for (int k = 0; k < 4; ++k) l = fmaf(sum[k], exp2_fast(-lw[k]), l);
                     }
@@ -817,6 +975,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                 ++count;
             }
             if (!ok) break;
+            // the odd tiles' sums go to the even ones', through columns of stream 1's scores: its next ones wait
+            const bool join = !two && tiles > 1;
+            float next_factor = 0.0f;
+            if (more && !(join && s == 1)) next_factor = convert();
             if (steps > 0) {
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.o_full[s]), o_phase, err));
                 o_phase ^= 1;
@@ -826,7 +988,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             // ---- the segment's end
             if (tiles > 0) {
                 const bool begins = w.t0 == 0, ends = w.t1 == w.x.tiles, cut = !(begins && ends);
-                const bool join = !two && tiles > 1;  // the odd tiles' sums go to the even ones'
                 const bool nan = *reinterpret_cast<volatile int*>(&sm.nan_seen) != 0;
                 if (s == 1 && !two) {
                     if (join) {
@@ -865,48 +1026,70 @@ __global__ void __launch_bounds__(kThreads, 1)
                         l = (l == 0.0f ? 0.0f : l * k0) + (l1 == 0.0f ? 0.0f : l1 * k1);
                     }
                     const float g = cut ? 1.0f : (l == 0.0f ? 0.0f : 1.0f / l);
+                    if (__all_sync(0xffffffffu, !live || (l != 0.0f && !nan_scale)) && !nan) {
+                        // nothing special in any row (what runs once an item costs its instructions' fetch: few of them)
+                        const float g0 = f0 * g, g1 = f1 * g;
+#pragma unroll 1
+                        for (int c = 0; c < DP / 16; ++c) {
+                            uint32_t v[16], y[16];
+                            float f[16];
+                            if (join) {
+                                ptx::tmem_ld_16x2(col_o + 16 * c, col_o + 128 + 16 * c, v, y);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) f[j] = fmaf(__uint_as_float(y[j]), g1, __uint_as_float(v[j]) * g0);
+                            } else {
+                                ptx::tmem_ld_16(col_o + 16 * c, v);
+#pragma unroll
+                                for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]) * g0;
+                            }
+                            if (live && cut) {
+                                float4* const to = reinterpret_cast<float4*>(piece + in_item * DP + 16 * c);
+#pragma unroll
+                                for (int j = 0; j < 4; ++j) to[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                            } else if (live && 16 * c < a.dim) {
+                                store(a.out, t * a.out_token_stride + h * a.out_head_stride + 16 * c, f, bf16, out_wide);
+                            }
+                        }
+                    } else
 #pragma unroll 1
                     for (int c = 0; c < DP / 16; ++c) {
                         uint32_t v[16], y[16];
                         if (join) ptx::tmem_ld_16x2(col_o + 16 * c, col_o + 128 + 16 * c, v, y);
                         else ptx::tmem_ld_16(col_o + 16 * c, v);
+                        const int d = 16 * c;
+                        float f[16];
 #pragma unroll
-                        for (int e = 0; e < 2; ++e) {
-                            const int d = 16 * c + 8 * e;
-                            float f[8];
+                        for (int j = 0; j < 16; ++j) {
+                            float o = f0 == 0.0f ? 0.0f : __uint_as_float(v[j]) * f0;
+                            if (join && f1 != 0.0f) o = fmaf(__uint_as_float(y[j]), f1, o);
+                            f[j] = nan_scale ? __int_as_float(0x7fffffff) : o * g;
+                        }
+                        if (nan && live && d < a.dim) {
+                            // NaN codes that were set apart: those of tokens that this row sees
+                            uint32_t hit = 0;
+                            for (int pos = max(all_see, w.t0 * kTok); pos < min(sees, w.t1 * kTok); ++pos) {
+                                const int pg = a.table[w.x.b * a.stride + (pos >> a.page_shift)];
+                                if (pg < 0 || pg >= a.pages) continue;
+                                const uint4 x = *reinterpret_cast<const uint4*>(
+                                    a.v_cache + (((static_cast<int64_t>(pg) * a.heads + w.x.head) << a.page_shift) +
+                                                 (pos & (page_size - 1))) * a.dim + d);
+                                const uint32_t e[4] = {x.x, x.y, x.z, x.w};
 #pragma unroll
-                            for (int j = 0; j < 8; ++j) {
-                                float o = f0 == 0.0f ? 0.0f : __uint_as_float(v[8 * e + j]) * f0;
-                                if (join && f1 != 0.0f) o = fmaf(__uint_as_float(y[8 * e + j]), f1, o);
-                                f[j] = nan_scale ? __int_as_float(0x7fffffff) : o * g;
-                            }
-                            if (nan && live && d < a.dim) {
-                                // NaN codes that were set apart: those of tokens that this row sees
-                                uint32_t hit = 0;
-                                for (int pos = max(all_see, w.t0 * kTok); pos < min(sees, w.t1 * kTok); ++pos) {
-                                    const int pg = a.table[w.x.b * a.stride + (pos >> a.page_shift)];
-                                    if (pg < 0 || pg >= a.pages) continue;
-                                    const uint2 x = *reinterpret_cast<const uint2*>(
-                                        a.v_cache + (((static_cast<int64_t>(pg) * a.heads + w.x.head) << a.page_shift) +
-                                                     (pos & (page_size - 1))) * a.dim + d);
-                                    const uint32_t lo = __vcmpeq4(x.x & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                    const uint32_t hi = __vcmpeq4(x.y & 0x7f7f7f7fu, 0x7f7f7f7fu);
-                                    hit |= (lo & 0x01020408u) | (hi & 0x10204080u);
-                                }
-                                // bytes of lo: bits 3, 10, 17, 24; of hi: 7, 14, 21, 28 (dimension 0 lowest)
-#pragma unroll
-                                for (int j = 0; j < 8; ++j) {
-                                    const int bit = j < 4 ? 3 + 7 * j : 7 + 7 * (j - 4);
-                                    if ((hit >> bit) & 1u) f[j] = __int_as_float(0x7fffffff);
+                                for (int k = 0; k < 4; ++k) {
+                                    const uint32_t is = __vcmpeq4(e[k] & 0x7f7f7f7fu, 0x7f7f7f7fu);
+                                    hit |= ((is & 1u) | ((is >> 7) & 2u) | ((is >> 14) & 4u) | ((is >> 21) & 8u)) << (4 * k);
                                 }
                             }
-                            if (live && cut) {
-                                float4* const to = reinterpret_cast<float4*>(piece + in_item * DP + d);
-                                to[0] = make_float4(f[0], f[1], f[2], f[3]);
-                                to[1] = make_float4(f[4], f[5], f[6], f[7]);
-                            } else if (live && d < a.dim) {
-                                store8(a.out, t * a.out_token_stride + h * a.out_head_stride + d, f, bf16, out_wide);
-                            }
+#pragma unroll
+                            for (int j = 0; j < 16; ++j)
+                                if ((hit >> j) & 1u) f[j] = __int_as_float(0x7fffffff);
+                        }
+                        if (live && cut) {
+                            float4* const to = reinterpret_cast<float4*>(piece + in_item * DP + d);
+#pragma unroll
+                            for (int j = 0; j < 4; ++j) to[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                        } else if (live && d < a.dim) {
+                            store(a.out, t * a.out_token_stride + h * a.out_head_stride + d, f, bf16, out_wide);
                         }
                     }
                     if (join) {
@@ -928,6 +1111,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             }
             n += tiles;
             if (w.last) break;
+            if (more && join && s == 1) next_factor = convert();
+            factor = next_factor;
             w.next(a, group);
         }
     }
@@ -948,7 +1133,7 @@ __global__ void __launch_bounds__(kThreads, 1)
 // an item that goes on, all of the item's pieces are joined here, in order.
 template <int DP>
 __global__ void __launch_bounds__(256) attention_wide_join(const AttentionArgs a, int blocks, const PieceInfo* infos,
-                                                           const float* pieces, int piece_rows, bool out_wide) {
+                                                           const float* pieces, int piece_rows, int out_wide) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     const PieceInfo info = infos[2 * blockIdx.x + 1];
     if (info.request < 0 || info.ends) return;
@@ -965,10 +1150,13 @@ __global__ void __launch_bounds__(256) attention_wide_join(const AttentionArgs a
         const int row = k / per_row, d = (k - row * per_row) * 8;
         auto piece = [&](int c) { return pieces + (c == static_cast<int>(blockIdx.x) ? 2 * c + 1 : 2 * c) * size; };
         float m = -INFINITY;
-        for (int c = blockIdx.x; c <= last; ++c) m = fmaxf(m, piece(c)[ml_at + 2 * row]);  // a block has a tile at least
+        auto holds = [&](int c) { return c == static_cast<int>(blockIdx.x) || infos[2 * c].request >= 0; };
+        for (int c = blockIdx.x; c <= last; ++c)
+            if (holds(c)) m = fmaxf(m, piece(c)[ml_at + 2 * row]);
         const float base = m == -INFINITY ? 0.0f : m;
         float l = 0.0f, f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
         for (int c = blockIdx.x; c <= last; ++c) {
+            if (!holds(c)) continue;
             const float* const p = piece(c);
             const float lc = p[ml_at + 2 * row + 1];
             if (lc == 0.0f) continue;
@@ -991,13 +1179,15 @@ __global__ void __launch_bounds__(256) attention_wide_join(const AttentionArgs a
         const int rr = info.item * kItemRows + row;
         const int64_t t = x.r.row0 + rr / group;
         const int h = info.head * group + rr % group;
-        store8(a.out, t * a.out_token_stride + h * a.out_head_stride + d, f, a.dtype == kBF16, out_wide);
+        store(a.out, t * a.out_token_stride + h * a.out_head_stride + d, f, a.dtype == kBF16, out_wide);
         if (d == 0 && a.lse) a.lse[t * a.q_heads + h] = l == 0.0f ? -INFINITY : (m + log2f(l)) * 0.693147180559945309f;
     }
 }
 
-bool wide_rows(const void* p, int64_t token, int64_t head) {
-    return ((reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(token * 2) | static_cast<uintptr_t>(head * 2)) & 15) == 0;
+// The bytes that every row begins at a multiple of: 32, 16, or 2 for anything else.
+int wide_rows(const void* p, int64_t token, int64_t head) {
+    const uintptr_t all = reinterpret_cast<uintptr_t>(p) | static_cast<uintptr_t>(token * 2) | static_cast<uintptr_t>(head * 2);
+    return all % 32 == 0 ? 32 : all % 16 == 0 ? 16 : 2;
 }
 
 size_t round16(size_t n) { return (n + 15) & ~static_cast<size_t>(15); }
@@ -1031,8 +1221,8 @@ cudaError_t launch(const AttentionArgs& a, cudaStream_t stream) {
     static std::atomic<uint64_t> allowed{0};
     e = allow_shared(attention_wide_kernel<DP>, smem, dev, allowed);
     if (e != cudaSuccess) return e;
-    const bool q_wide = wide_rows(a.q, a.q_token_stride, a.q_head_stride);
-    const bool out_wide = wide_rows(a.out, a.out_token_stride, a.out_head_stride);
+    const bool q_wide = wide_rows(a.q, a.q_token_stride, a.q_head_stride) >= 16;
+    const int out_wide = wide_rows(a.out, a.out_token_stride, a.out_head_stride);
     attention_wide_kernel<DP><<<blocks, kThreads, smem, stream>>>(a, maps, device_error_word(), infos, pieces,
                                                                   piece_rows, q_wide, out_wide);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
