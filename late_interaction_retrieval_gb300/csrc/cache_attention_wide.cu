@@ -508,7 +508,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // a thread widens 16 dimensions of a token at a time
                     const uint32_t dst = smem_u32(sm.k[buf][0]);
                     constexpr int C = DP / 16;  // chunks of a token
-#pragma unroll 2
+#pragma unroll 4
                     for (int i = 0; i < kTok * C / 128; ++i) {
                         const int item = ct + 128 * i, c = item % C, tok = item / C;
                         const uint4 x = lds16(src + raw_at<DP>(tok, c));
@@ -734,27 +734,31 @@ __global__ void __launch_bounds__(kThreads, 1)
         auto convert = [&]() {
             asm volatile("cp.async.wait_all;" ::: "memory");
             __syncwarp();
-            uint32_t sizes = 0;  // the largest size's bits of either half
+            float2 down = make_float2(1.0f, 1.0f);
+            if (bf16) {
+                uint32_t sizes = 0;  // the largest size's bits of either half
 #pragma unroll 4
-            for (int c = 0; c < DP / 8; ++c) {
-                const uint4 e = lds16(q_tile + (c >> 3) * (kM * 128) + tile_at(row, c & 7));
-                sizes = max_halves(max_halves(sizes, e.x & 0x7fff7fffu), e.y & 0x7fff7fffu);
-                sizes = max_halves(max_halves(sizes, e.z & 0x7fff7fffu), e.w & 0x7fff7fffu);
-            }
-            const int shift = row_shift(widen_q(max(sizes & 0xffffu, sizes >> 16), bf16).x);
-            const float2 up = power_of_two(shift), down = power_of_two(-shift);
-#pragma unroll 2
-            for (int c = 0; c < DP / 8; ++c) {
-                const uint32_t at = q_tile + (c >> 3) * (kM * 128) + tile_at(row, c & 7);
-                const uint4 v = lds16(at);
-                const uint32_t e[4] = {v.x, v.y, v.z, v.w};
-                uint32_t o[4];
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const float2 f = widen_q(e[j], bf16);
-                    o[j] = pack_half(f.x * up.x * up.y, f.y * up.x * up.y);
+                for (int c = 0; c < DP / 8; ++c) {
+                    const uint4 e = lds16(q_tile + (c >> 3) * (kM * 128) + tile_at(row, c & 7));
+                    sizes = max_halves(max_halves(sizes, e.x & 0x7fff7fffu), e.y & 0x7fff7fffu);
+                    sizes = max_halves(max_halves(sizes, e.z & 0x7fff7fffu), e.w & 0x7fff7fffu);
                 }
-                sts16(at, o[0], o[1], o[2], o[3]);
+                const int shift = row_shift(widen_q(max(sizes & 0xffffu, sizes >> 16), true).x);
+                const float2 up = power_of_two(shift);
+                down = power_of_two(-shift);
+#pragma unroll 2
+                for (int c = 0; c < DP / 8; ++c) {
+                    const uint32_t at = q_tile + (c >> 3) * (kM * 128) + tile_at(row, c & 7);
+                    const uint4 v = lds16(at);
+                    const uint32_t e[4] = {v.x, v.y, v.z, v.w};
+                    uint32_t o[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j) {
+                        const float2 f = widen_q(e[j], true);
+                        o[j] = pack_half(f.x * up.x * up.y, f.y * up.x * up.y);
+                    }
+                    sts16(at, o[0], o[1], o[2], o[3]);
+                }
             }
             fence_operands();
             __syncwarp();
