@@ -77,6 +77,14 @@ __device__ __forceinline__ uint32_t pack_half(float x, float y) {
     return *reinterpret_cast<const uint32_t*>(&h);
 }
 
+// What the rounding to the two halves of h left of x and y.  An fp16 output holds 11 bits itself, so its weights' 11
+// bits would show in it (half as much again as its own rounding): there a second product adds what is left.  A bf16
+// output's 8 bits hide it.
+__device__ __forceinline__ uint32_t left_of(uint32_t h, float x, float y) {
+    const float2 got = __half22float2(*reinterpret_cast<const __half2*>(&h));
+    return pack_half(x - got.x, y - got.y);
+}
+
 // Sets a kernel's shared-memory limit once for each device (`done`: one bit a device, of the kernel's own).
 template <typename Kernel>
 inline cudaError_t allow_shared(Kernel kernel, size_t bytes, int device, std::atomic<uint64_t>& done) {

@@ -20,7 +20,9 @@
 // The weights are 2^7 exp2(z - ref) (the page's scale / c) in fp16.  ref is a
 // power of two near the row's largest weight and c one not below the scales;
 // either moves only when a weight leaves fp16's range, which its sum shows (no
-// maximum is taken on the way), and its move rescales O, exactly.  Work is
+// maximum is taken on the way), and its move rescales O, exactly.  For fp16
+// outputs, where 11 bits of a weight would show, what their rounding left is
+// multiplied too, from the columns of S that the weights leave free.  Work is
 // spread by costs in closed form, the batch's items end to end, one equal
 // range a block; pieces of cut items are joined by a second launch.
 //
@@ -304,7 +306,7 @@ __device__ __forceinline__ void store(void* out, int64_t at, const float (&f)[N]
     }
 }
 
-template <int DP>
+template <int DP, bool kFine>
 __global__ void __launch_bounds__(kThreads, 1)
     attention_wide_kernel(const AttentionArgs a, const __grid_constant__ Maps maps, unsigned int* err,
                           PieceInfo* infos, float* pieces, int piece_rows, bool q_wide, int out_wide) {
@@ -663,6 +665,9 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                     for (int k = 0; k < kTok / 16; ++k)
                         mma_f16_ts(col_o, col_s + 64 * ob + 8 * k, vd + 2 * k, kIdO, i > 0 || k != 0);
+#pragma unroll
+                    for (int k = 0; kFine && k < kTok / 16; ++k)
+                        mma_f16_ts(col_o, col_s + 64 * ob + 32 + 8 * k, vd + 2 * k, kIdO, true);
                 }
                 // the next scores first: the softmax waits for them
                 if (i + kAhead < steps) score();
@@ -838,7 +843,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                     // beyond fp16's range shows in the sum, and the weights are only stored if there is none.
                     bool fits = false;
                     if (whole) {
-                        uint32_t x[32], y[32], p[16], r[16];
+                        uint32_t x[32], y[32], p[16], r[16], p_rest[16], r_rest[16];
                         tmem_ld_32(col_s, x);
                         float vmost = 0.0f;
                         if (even) {
@@ -865,7 +870,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             m2[k] = both(lw[k] - ref, lw[k] - ref);
                             s2[k] = 0;
                         }
-                        auto weights = [&](const uint32_t (&v)[32], uint32_t (&to)[16]) {
+                        auto weights = [&](const uint32_t (&v)[32], uint32_t (&to)[16], uint32_t (&rest)[16]) {
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 const int k = i & 3;
@@ -874,13 +879,14 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const float e0 = exp2_fast(z.x), e1 = exp2_fast(z.y);
                                 s2[k] = add_both(s2[k], both(e0, e1));
                                 to[i] = pack_half(e0, e1);
+                                if (kFine) rest[i] = left_of(to[i], e0, e1);
                             }
                         };
                         fence_loaded(x);
                         tmem_ld_32(col_s + 32, y);
-                        weights(x, p);
+                        weights(x, p, p_rest);
                         fence_loaded(y);
-                        weights(y, r);
+                        weights(y, r, r_rest);
                         float sum[4];
 #pragma unroll
                         for (int k = 0; k < 4; ++k) {
@@ -892,6 +898,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (fits) {
                             tmem_st_16(col_s, p);
                             tmem_st_16(col_s + 16, r);
+                            if (kFine) {
+                                tmem_st_16(col_s + 32, p_rest);
+                                tmem_st_16(col_s + 48, r_rest);
+                            }
                             // the group's weight out of its sum again
                             if (even) {
                                 l = fmaf(total, exp2_fast(-lw[0]), l);
@@ -957,7 +967,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         float sum[4] = {0.0f, 0.0f, 0.0f, 0.0f};
 #pragma unroll
                         for (int c = 0; c < 2; ++c) {
-                            uint32_t p[16];
+                            uint32_t p[16], rest[16];
 #pragma unroll
                             for (int i = 0; i < 16; ++i) {
                                 const int j = 32 * c + 2 * i, k = i & 3;
@@ -965,8 +975,10 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 const float e1 = exp2_fast(fmaf(__uint_as_float(v[j + 1]), fk[k], minus[k]));
                                 sum[k] += e0 + e1;
                                 p[i] = pack_half(e0, e1);
+                                if (kFine) rest[i] = left_of(p[i], e0, e1);
                             }
                             tmem_st_16(col_s + 16 * c, p);
+                            if (kFine) tmem_st_16(col_s + 32 + 16 * c, rest);
                         }
 #pragma unroll
                         for (int k = 0; k < 4; ++k) l = fmaf(sum[k], exp2_fast(-lw[k]), l);
@@ -1200,7 +1212,7 @@ int piece_rows_of(int64_t rows, int64_t group) {
     return static_cast<int>(rows * group < kItemRows ? (rows * group + 3) & ~int64_t(3) : kItemRows);
 }
 
-template <int DP>
+template <int DP, bool kFine>
 cudaError_t launch(const AttentionArgs& a, cudaStream_t stream) {
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
@@ -1223,11 +1235,11 @@ cudaError_t launch(const AttentionArgs& a, cudaStream_t stream) {
     const int piece_rows = piece_rows_of(a.rows, a.q_heads / a.heads);
     const size_t smem = sizeof(Smem<DP>) + 1024;
     static std::atomic<uint64_t> allowed{0};
-    e = allow_shared(attention_wide_kernel<DP>, smem, dev, allowed);
+    e = allow_shared(attention_wide_kernel<DP, kFine>, smem, dev, allowed);
     if (e != cudaSuccess) return e;
     const bool q_wide = wide_rows(a.q, a.q_token_stride, a.q_head_stride) >= 16;
     const int out_wide = wide_rows(a.out, a.out_token_stride, a.out_head_stride);
-    attention_wide_kernel<DP><<<blocks, kThreads, smem, stream>>>(a, maps, device_error_word(), infos, pieces,
+    attention_wide_kernel<DP, kFine><<<blocks, kThreads, smem, stream>>>(a, maps, device_error_word(), infos, pieces,
                                                                   piece_rows, q_wide, out_wide);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
@@ -1251,7 +1263,8 @@ size_t attention_wide_workspace(int64_t rows, int64_t group, int64_t dim, int sm
 }
 
 cudaError_t launch_attention_wide(const AttentionArgs& a, cudaStream_t stream) {
-    return a.dim <= 64 ? launch<64>(a, stream) : launch<128>(a, stream);
+    if (a.dtype == kBF16) return a.dim <= 64 ? launch<64, false>(a, stream) : launch<128, false>(a, stream);
+    return a.dim <= 64 ? launch<64, true>(a, stream) : launch<128, true>(a, stream);
 }
 
 }  // namespace lik
