@@ -26,9 +26,12 @@
 // spread by costs in closed form, the batch's items end to end, one equal
 // range a block; pieces of cut items are joined by a second launch.
 //
-// What bounds it: neither memory nor the tensor cores but the chain weights ->
-// O and next scores -> weights of a stream (2000 clocks a tile, of which the
-// tensor cores take 620), and 14000 clocks at an item's start and end.
+// What bounds it: neither memory nor the tensor cores (41% busy) but the chain
+// weights -> O and next scores -> weights of a stream (2000 clocks a tile, of
+// which the tensor cores take 620), 14000 clocks at an item's start and end,
+// and with one stream's rows the widening of the codes.  8191 new tokens over
+// 16381, 32 heads, bf16: 513 us, 804 TFLOP/s; 48 requests of 5 drafts over
+// 150001 tokens, 64 heads, fp16: 183 us.
 #include "cache_attention.h"
 #include "tmap.h"
 
