@@ -269,6 +269,16 @@ def test_prompts_of_many_rows(dtype, heads, group, dim, page, lengths, added):
     one.check_attention(one._requests(gen, lengths, added, heads, group, dim, page, dtype))
 
 
+@pytest.mark.parametrize("seed,dtype", [(0, "bf16"), (1, "f16"), (2, "bf16")])
+def test_ragged_batches(seed, dtype):
+    """Prompts, drafts, single and no tokens in one batch, which no two blocks cut alike."""
+    gen = torch.Generator().manual_seed(100 + seed)
+    heads, group, dim, page = [(2, 5, 64, 64), (1, 7, 128, 32), (3, 2, 48, 128)][seed]
+    added = [int(x) for x in torch.randint(0, 70, (11,), generator=gen)] + [1, 0, 1, 5]
+    lengths = [a + int(x) for a, x in zip(added, torch.randint(0, 400, (15,), generator=gen))]
+    one.check_attention(one._requests(gen, lengths, added, heads, group, dim, page, dtype))
+
+
 @pytest.mark.parametrize("dtype,heads,dim,page", [("f32", 1, 128, 256), ("f32", 2, 80, 128), ("bf16", 1, 128, 256),
                                                   ("f16", 1, 112, 256)])
 @pytest.mark.parametrize("apart", [False, True])
