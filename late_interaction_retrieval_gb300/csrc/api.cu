@@ -12,6 +12,8 @@
 #include <cstdio>
 #include <mutex>
 
+#include <cuda.h>
+
 #include "lik.h"
 #include "lik_internal.h"
 #include "validate.h"
@@ -147,13 +149,38 @@ lik_status check_common(lik_dtype dtype, int64_t n_query, int64_t n_doc, int64_t
 
 }  // namespace
 
+namespace {
+
+// The bounds of the allocation that holds p, from the driver (resolved through the runtime, so that the library links
+// against that alone); [0, 0) where there is no answer.
+void allocation_of(const void* p, uintptr_t* lo, uintptr_t* hi) {
+    typedef CUresult (*AddressRangeFn)(CUdeviceptr*, size_t*, CUdeviceptr);
+    static const AddressRangeFn range = [] {
+        void* fn = nullptr;
+        cudaDriverEntryPointQueryResult q;
+        const cudaError_t e = cudaGetDriverEntryPointByVersion("cuMemGetAddressRange", &fn, 12000, cudaEnableDefault, &q);
+        return e == cudaSuccess && q == cudaDriverEntryPointSuccess ? reinterpret_cast<AddressRangeFn>(fn) : nullptr;
+    }();
+    CUdeviceptr base = 0;
+    size_t bytes = 0;
+    const bool known = range && range(&base, &bytes, reinterpret_cast<CUdeviceptr>(p)) == CUDA_SUCCESS;
+    *lo = known ? static_cast<uintptr_t>(base) : 0;
+    *hi = known ? static_cast<uintptr_t>(base) + bytes : 0;
+}
+
+}  // namespace
+
 lik_status check_buffers(int dev, const Spec* specs, int n) {
+    // Small buffers mostly share an allocation (a caching allocator's block), which is asked for once a call.
+    uintptr_t lo = 0, hi = 0;
     for (int k = 0; k < n; ++k) {
         const Spec& s = specs[k];
         if (s.required && s.elems > 0 && !s.ptr) return fail(LIK_ERR_INVALID_ARG, "%s is NULL", s.name);
-        if (s.elems > 0) {
+        const uintptr_t at = reinterpret_cast<uintptr_t>(s.ptr);
+        if (s.elems > 0 && s.ptr && !(at >= lo && at < hi)) {
             lik_status st = check_pointer(s.ptr, dev, s.name);
             if (st != LIK_OK) return st;
+            if (k + 2 < n) allocation_of(s.ptr, &lo, &hi);
         }
     }
     return LIK_OK;
