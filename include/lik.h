@@ -659,7 +659,8 @@ lik_status lik_cache_write(const void* k, const void* v, lik_dtype dtype, int64_
  *   q, out [rows, q_heads, dim], fp16 or bf16, element (t, h, d) at t *
  *   token_stride + h * head_stride + d; lse [rows, q_heads] fp32 or NULL;
  *   block_table [requests, table_cols] int32, row b at b * table_stride;
- *   1e-30 <= scale <= 1e30.  lengths are clamped to [0, table_cols *
+ *   1e-30 <= scale <= 1e30; q_heads is 1 to 128 times heads (at most 1024),
+ *   rows * q_heads <= 2^30.  lengths are clamped to [0, table_cols *
  *   page_size], offsets to [0, rows].
  *   max_added: the most tokens that a request adds, as the host knows it: it
  *   chooses the kernel.  A wrong value costs time, not results.

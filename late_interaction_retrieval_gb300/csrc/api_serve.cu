@@ -43,7 +43,8 @@ lik_status check_table(int64_t requests, int64_t cols, int64_t stride) {
 // rows x heads x dim with heads and dim of a cache
 lik_status check_rows(int64_t rows, int64_t heads, int64_t dim) {
     if (rows < 0 || heads < 0) return fail(LIK_ERR_INVALID_ARG, "negative size");
-    if (heads < 1 || heads > 1024) return fail(LIK_ERR_UNSUPPORTED, "heads must lie in [1, 1024] (got %lld)", static_cast<ll>(heads));
+    if (heads < 1 || heads > 1024)
+        return fail(LIK_ERR_UNSUPPORTED, "heads must lie in [1, 1024] (got %lld)", static_cast<ll>(heads));
     if (dim < 16 || dim > kMaxHeadDim || dim % 16)
         return fail(LIK_ERR_UNSUPPORTED, "dim must be a multiple of 16 in [16, %d] (got %lld)", kMaxHeadDim,
                     static_cast<ll>(dim));
@@ -116,8 +117,9 @@ lik_status check_attention(int64_t rows, int64_t q_heads, int64_t heads, int64_t
     if (q_heads < 1 || q_heads % heads || q_heads / heads > 128)
         return fail(LIK_ERR_UNSUPPORTED, "q_heads %lld must be 1 to 128 times heads %lld", static_cast<ll>(q_heads),
                     static_cast<ll>(heads));
-    if (rows > INT32_MAX || rows * q_heads > INT32_MAX)
-        return fail(LIK_ERR_UNSUPPORTED, "rows * q_heads > 2^31 - 1");
+    // the kernels count a request's rows of all heads, rounded up to an item, in 32 bits
+    if (rows > INT32_MAX || rows * q_heads > (int64_t(1) << 30))
+        return fail(LIK_ERR_UNSUPPORTED, "rows * q_heads > 2^30");
     if (table_cols < 0 || max_added < 0) return fail(LIK_ERR_INVALID_ARG, "negative size");
     if (table_cols * page_size > INT32_MAX)
         return fail(LIK_ERR_UNSUPPORTED, "a table row of more than 2^31 - 1 tokens");

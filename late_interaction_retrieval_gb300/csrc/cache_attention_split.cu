@@ -828,8 +828,8 @@ cudaError_t launch(const AttentionArgs& a, cudaStream_t stream) {
     if (e != cudaSuccess) return e;
     const bool q_wide = wide_rows(a.q, a.q_token_stride, a.q_head_stride, 16);
     const bool out_wide = wide_rows(a.out, a.out_token_stride, a.out_head_stride, 8);
-    attention_split_kernel<DP, NR, kFine><<<blocks, 32 * Shape<NR>::kWarps, smem, stream>>>(a, maps, device_error_word(), infos, pieces, q_wide,
-                                                                   out_wide);
+    attention_split_kernel<DP, NR, kFine><<<blocks, 32 * Shape<NR>::kWarps, smem, stream>>>(
+        a, maps, device_error_word(), infos, pieces, q_wide, out_wide);
     if ((e = cudaGetLastError()) != cudaSuccess) return e;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(blocks);

@@ -709,7 +709,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const bool live = in_item < x.x.rows;
             const int rr = live ? x.x.item * kItemRows + in_item : 0;
             const int i = rr / group, h = x.x.head * group + (rr - i * group);
-            const uint16_t* const src = static_cast<const uint16_t*>(a.q) + (x.x.r.row0 + i) * a.q_token_stride + h * a.q_head_stride;
+            const uint16_t* const src =
+                static_cast<const uint16_t*>(a.q) + (x.x.r.row0 + i) * a.q_token_stride + h * a.q_head_stride;
             if (q_wide) {
                 constexpr int C = DP / 8, R = 32 / C;  // chunks of a row, rows at a time
                 const int c = lane % C;

@@ -344,7 +344,8 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const WriteArgs a
             // rows behind it that go on: the run ends in its page, so within the words
             const unsigned off = l == 31 ? 0u : ~on_of[k] >> (l + 1);
             r.n = 1 + (off ? min(__ffs(off) - 1, 31 - l) : 31 - l);
-            for (int j = k + 1; r.n == 32 * (j - k) - l && j < words; ++j) r.n += on_of[j] == 0xffffffffu ? 32 : __ffs(~on_of[j]) - 1;
+            for (int j = k + 1; r.n == 32 * (j - k) - l && j < words; ++j)
+                r.n += on_of[j] == 0xffffffffu ? 32 : __ffs(~on_of[j]) - 1;
             if (r.n <= short_rows) {
                 if (shorts++ % kWarps == warp) write_run<T, 32>(side, r, lane, of_warp, nullptr, 0);
             } else {

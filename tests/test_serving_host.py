@@ -58,7 +58,7 @@ def test_write_refusals(lib, bad, status):
 
 @pytest.mark.parametrize("bad,status", POOL + HEADS + [
     (dict(dtype=0), 2), (dict(dtype=9), 1), (dict(q_heads=3), 2), (dict(q_heads=0), 2), (dict(q_heads=258), 2),
-    (dict(rows=2 ** 29, q_heads=4), 2), (dict(requests=-1), 1), (dict(requests=8193), 2), (dict(cols=-1), 1),
+    (dict(rows=2 ** 29, q_heads=4), 2), (dict(rows=2 ** 28 + 1, q_heads=4), 2), (dict(requests=-1), 1), (dict(requests=8193), 2), (dict(cols=-1), 1),
     (dict(cols=2 ** 27, stride=2 ** 27), 2), (dict(cols=8, stride=7), 1), (dict(stride=BIG + 1), 2),
     (dict(added=-1), 1), (dict(q=(-1, 32)), 1), (dict(out=(128, -1)), 1), (dict(q=(128, 2 ** 32 + 1)), 2),
     (dict(scale=0.0), 1), (dict(scale=-1.0), 1), (dict(scale=math.nan), 1), (dict(scale=math.inf), 1),
