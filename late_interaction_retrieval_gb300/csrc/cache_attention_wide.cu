@@ -350,13 +350,16 @@ __global__ void __launch_bounds__(kThreads, 1)
         ptx::fence_mbar_init();
     }
     // ---- the block's range of the batch, by costs, from every request's
-    const int B = a.requests, each = (B + kThreads - 1) / kThreads;
+    // Either half of the block sums all requests, and finds one of the range's bounds.
+    constexpr int kHalf = kThreads / 2;
+    const int half = tid >= kHalf, part = tid - half * kHalf;
+    const int B = a.requests, each = (B + kHalf - 1) / kHalf;
     auto cost_of = [&](int b) {
         const Request r = request_of(a, b);
         return r.n > 0 ? costs_of(r, group).all() * a.heads : 0ll;
     };
     long long mine = 0;
-    for (int b = min(tid * each, B); b < min(tid * each + each, B); ++b) mine += cost_of(b);
+    for (int b = min(part * each, B); b < min(part * each + each, B); ++b) mine += cost_of(b);
     long long incl = mine;
 #pragma unroll
     for (int d = 1; d < 32; d <<= 1) {
@@ -366,7 +369,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (lane == 31) sm.warp_sum[warp] = incl;
     __syncthreads();
     long long all = 0;
-    for (int w = 0; w < kThreads / 32; ++w) {
+    for (int w = half * (kHalf / 32); w < (half + 1) * (kHalf / 32); ++w) {
         if (w < warp) incl += sm.warp_sum[w];
         all += sm.warp_sum[w];
     }
@@ -382,13 +385,14 @@ __global__ void __launch_bounds__(kThreads, 1)
         u -= behind;
         if (u < excl || u >= incl) return;
         long long rest = u - excl;
-        int b = tid * each;
-        while (rest >= cost_of(b)) rest -= cost_of(b++);
+        int b = part * each;
+        for (long long c = cost_of(b); rest >= c; c = cost_of(++b)) rest -= c;
         const Request r = request_of(a, b);
         const Costs c = costs_of(r, group);
         to[0] = b;
-        to[1] = static_cast<int>(rest / c.all());
-        rest %= c.all();
+        const long long per_head = c.all();
+        to[1] = static_cast<int>(rest / per_head);
+        rest -= to[1] * per_head;
         int i = 0;  // the last item that begins at or before it
         for (int step = 1 << (31 - __clz(c.items)); step; step >>= 1)
             if (i + step < c.items && c.before(i + step) <= rest) i += step;
@@ -396,12 +400,12 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.r = r;
         x.item = i;
         shape(x, group);
-        const double cost = static_cast<double>(i + 1 < c.items ? c.before(i + 1) - c.before(i) : c.last);
+        // the same rounding for the block that ends here and the one that begins
+        const float cost = static_cast<float>(i + 1 < c.items ? c.before(i + 1) - c.before(i) : c.last);
         to[2] = i;
-        to[3] = behind ? x.tiles : min(x.tiles - 1, static_cast<int>(static_cast<double>(rest - c.before(i)) / cost * x.tiles));
+        to[3] = behind ? x.tiles : min(x.tiles - 1, static_cast<int>(static_cast<float>(rest - c.before(i)) / cost * x.tiles));
     };
-    locate(bound(blockIdx.x), sm.start);
-    locate(bound(blockIdx.x + 1), sm.end);
+    locate(bound(blockIdx.x + half), half ? sm.end : sm.start);
     __syncthreads();
     if (sm.start[0] == sm.end[0] && sm.start[1] == sm.end[1] && sm.start[2] == sm.end[2] && sm.start[3] == sm.end[3])
         return;  // both bounds fall on one tile
@@ -843,10 +847,11 @@ __global__ void __launch_bounds__(kThreads, 1)
                         nan_scale = nan_scale || (seen && !finite);
                         w = x.y > cref * 8.67361738e-19f && finite ? x.z + (kLogStart - logc) : kLogStart - 60.0f;
                     };
-                    // A tile that every row sees whole, under the reference as it is: no maximum is taken.  A weight
-                    // beyond fp16's range shows in the sum, and the weights are only stored if there is none.
+                    // A tile that every row sees whole, under the reference as it is (the first has none): no maximum is
+                    // taken.  A weight beyond fp16's range shows in the sum, and the weights are only stored if there
+                    // is none.
                     bool fits = false;
-                    if (whole) {
+                    if (whole && st > 0) {
                         uint32_t x[32], y[32], p[16], r[16], p_rest[16], r_rest[16];
                         tmem_ld_32(col_s, x);
                         float vmost = 0.0f;
@@ -1063,9 +1068,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 for (int j = 0; j < 16; ++j) f[j] = __uint_as_float(v[j]) * g0;
                             }
                             if (live && cut) {
-                                float4* const to = reinterpret_cast<float4*>(piece + in_item * DP + 16 * c);
+                                float4* const to = reinterpret_cast<float4*>(piece) + 4 * c * piece_rows + in_item;
 #pragma unroll
-                                for (int j = 0; j < 4; ++j) to[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                                for (int j = 0; j < 4; ++j) to[j * piece_rows] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
                             } else if (live && 16 * c < a.dim) {
                                 store(a.out, t * a.out_token_stride + h * a.out_head_stride + 16 * c, f, bf16, out_wide);
                             }
@@ -1105,9 +1110,9 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 if ((hit >> j) & 1u) f[j] = __int_as_float(0x7fffffff);
                         }
                         if (live && cut) {
-                            float4* const to = reinterpret_cast<float4*>(piece + in_item * DP + d);
+                            float4* const to = reinterpret_cast<float4*>(piece) + 4 * c * piece_rows + in_item;
 #pragma unroll
-                            for (int j = 0; j < 4; ++j) to[j] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
+                            for (int j = 0; j < 4; ++j) to[j * piece_rows] = make_float4(f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]);
                         } else if (live && d < a.dim) {
                             store(a.out, t * a.out_token_stride + h * a.out_head_stride + d, f, bf16, out_wide);
                         }
@@ -1165,16 +1170,15 @@ __global__ void __launch_bounds__(256) attention_wide_join(const AttentionArgs a
     int last = blockIdx.x + 1;
     while (last < blocks - 1 && !infos[2 * last].ends) ++last;
     const int64_t size = static_cast<int64_t>(piece_rows) * (DP + 4), ml_at = static_cast<int64_t>(piece_rows) * DP;
-    const int per_row = a.dim / 8;
-    for (int k = blockIdx.y * 256 + threadIdx.x; k < x.rows * per_row; k += gridDim.y * 256) {
-        const int row = k / per_row, d = (k - row * per_row) * 8;
+    for (int k = blockIdx.y * 256 + threadIdx.x; k < x.rows * (a.dim / 16); k += gridDim.y * 256) {
+        const int d = k / x.rows * 16, row = k - d / 16 * x.rows;  // neighbouring threads: neighbouring rows
         auto piece = [&](int c) { return pieces + (c == static_cast<int>(blockIdx.x) ? 2 * c + 1 : 2 * c) * size; };
-        float m = -INFINITY;
         auto holds = [&](int c) { return c == static_cast<int>(blockIdx.x) || infos[2 * c].request >= 0; };
+        float m = -INFINITY;
         for (int c = blockIdx.x; c <= last; ++c)
             if (holds(c)) m = fmaxf(m, piece(c)[ml_at + 2 * row]);
         const float base = m == -INFINITY ? 0.0f : m;
-        float l = 0.0f, f[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        float l = 0.0f, f[16] = {};
         for (int c = blockIdx.x; c <= last; ++c) {
             if (!holds(c)) continue;
             const float* const p = piece(c);
@@ -1182,20 +1186,18 @@ __global__ void __launch_bounds__(256) attention_wide_join(const AttentionArgs a
             if (lc == 0.0f) continue;
             const float g = exp2_fast(p[ml_at + 2 * row] - base);
             l = fmaf(lc, g, l);
-            const float4 u = *reinterpret_cast<const float4*>(p + row * DP + d);
-            const float4 v = *reinterpret_cast<const float4*>(p + row * DP + d + 4);
-            f[0] = fmaf(u.x, g, f[0]);
-            f[1] = fmaf(u.y, g, f[1]);
-            f[2] = fmaf(u.z, g, f[2]);
-            f[3] = fmaf(u.w, g, f[3]);
-            f[4] = fmaf(v.x, g, f[4]);
-            f[5] = fmaf(v.y, g, f[5]);
-            f[6] = fmaf(v.z, g, f[6]);
-            f[7] = fmaf(v.w, g, f[7]);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float4 u = reinterpret_cast<const float4*>(p)[(d / 4 + j) * piece_rows + row];
+                f[4 * j] = fmaf(u.x, g, f[4 * j]);
+                f[4 * j + 1] = fmaf(u.y, g, f[4 * j + 1]);
+                f[4 * j + 2] = fmaf(u.z, g, f[4 * j + 2]);
+                f[4 * j + 3] = fmaf(u.w, g, f[4 * j + 3]);
+            }
         }
         const float inv = l == 0.0f ? 0.0f : 1.0f / l;
 #pragma unroll
-        for (int j = 0; j < 8; ++j) f[j] *= inv;
+        for (int j = 0; j < 16; ++j) f[j] *= inv;
         const int rr = info.item * kItemRows + row;
         const int64_t t = x.r.row0 + rr / group;
         const int h = info.head * group + rr % group;
