@@ -699,7 +699,7 @@ lik_status lik_cache_attention(const void* q, lik_dtype dtype, int64_t rows, int
  * With uniform in [0, 1) and noise from the exponential distribution, y is
  * drawn from r's distribution.  A column of -inf has probability 0.  A target
  * row with a NaN or +inf logit, or of -inf alone, passes nothing and draws -1;
- * a draft whose own row has one does not pass and is replaced from p; a
+ * a draft whose own row is such a row does not pass and is replaced from p; a
  * drafted token outside [0, cols) does not pass.  Probabilities are fp32,
  * sums fp32 or wider.
  *   target_logits [drafts + requests, cols], draft_logits [drafts, cols] of

@@ -285,7 +285,8 @@ __global__ void __launch_bounds__(kThreads) verify_draw(const VerifyArgs a, cons
                 stat_p[i] = sp;
                 stat_q[i] = sq;
             }
-            const float p = prob(zp, sp, c), q = draft ? prob(zq, sq, c) : 1.0f;
+            // a draft row without mass is no distribution: as with a NaN in it, its draft does not pass
+            const float p = prob(zp, sp, c), q = !draft ? 1.0f : sq.y == 0.0f ? NAN : prob(zq, sq, c);
             if (i < n && !(inside && static_cast<double>(u) * q < static_cast<double>(p))) atomicMin(&first_fail, i);
             if (writes && i < n) {
                 a.tokens[tr] = x;

@@ -141,3 +141,23 @@ def test_logits_far_from_zero(dtype, shift):
         case = (target, draft, _drawn(gen, draft, 1.0), offsets, uniform, noise)
         check(case)
         check(case, 0.25)
+
+
+# -------------------------------------------------------- draft rows without mass --
+
+@pytest.mark.parametrize("bad", [-INF, NAN, INF])
+@pytest.mark.parametrize("cols", [100, 4096])
+def test_draft_rows_that_are_no_distribution(bad, cols):
+    """A draft row of -inf alone, or with a NaN or +inf logit: its draft does not pass, and p replaces it."""
+    target, draft, drafted, offsets, _, noise = one._drafts(one._gen(cols), [3, 2, 1, 0], cols, "f32")
+    uniform = torch.zeros(6)
+    broken, none = draft.clone(), draft.clone()
+    for r in (0, 4, 5):
+        none[r] = NAN
+        if bad == -INF:
+            broken[r] = bad
+        else:
+            broken[r, (int(drafted[r]) + 7) % cols] = bad
+    want = definition(target, none, drafted, offsets, uniform, noise)
+    _, accepted = check((target, broken, drafted, offsets, uniform, noise), want=want)
+    assert accepted == [0, 1, 0, 0]
