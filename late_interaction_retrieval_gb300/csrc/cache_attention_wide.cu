@@ -72,7 +72,7 @@ struct Smem {
     uint64_t raw_full[kRaw], raw_empty[kRaw], scale_full[kScaleRing];
     uint64_t k_full[kKeys], k_empty[kKeys], v_full[kValues], v_empty[kValues];
     uint64_t q_full[2], s_full[2][2], p_full[2][2];
-    uint64_t o_step[2], o_full[2];  // a step is in O; an item's last one is
+    uint64_t o_most[2], o_full[2];  // all of an item's steps but the last are in O; all are
     uint64_t merge_full, merge_empty, exit_bar;
     uint32_t tmem;
     int nan_seen;
@@ -336,7 +336,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int i = 0; i < 2; ++i) {
             ptx::mbar_init(smem_u32(&sm.q_full[i]), 4);
-            ptx::mbar_init(smem_u32(&sm.o_step[i]), 1);
+            ptx::mbar_init(smem_u32(&sm.o_most[i]), 1);
             ptx::mbar_init(smem_u32(&sm.o_full[i]), 1);
             for (int b = 0; b < 2; ++b) {
                 ptx::mbar_init(smem_u32(&sm.s_full[i][b]), 1);
@@ -679,7 +679,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                 // the next scores first: the softmax waits for them
                 if (i + kAhead < steps) score();
                 if (leader) {
-                    ptx::mma_commit(smem_u32(&sm.o_step[s]));
+                    if (i + 2 == steps) ptx::mma_commit(smem_u32(&sm.o_most[s]));
                     if (i + 1 == steps) ptx::mma_commit(smem_u32(&sm.o_full[s]));
                     done(&sm.v_empty[vb]);
                 }
@@ -779,7 +779,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             return a.scale * 1.44269504088896341f * down.x * down.y;
         };
         int n = 0, count = 0;  // tiles, and steps of this stream, before
-        uint32_t o_phase = 0, merge_phase = 0;
+        uint32_t most_phase = 0, o_phase = 0, merge_phase = 0;
         float factor = fetch(w) ? convert() : 0.0f;
         while (ok) {
             const bool two = w.x.two;
@@ -804,11 +804,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                 more = fetch(x);
             };
             if (steps == 0) fetch_next();
-            // O times `keep` (1 in rows that need none).  It is at rest once the step before is in it: this step's
-            // product waits for its weights.  (The step before that is: this step's scores came after it.  So the
-            // phase is not taken for one of two steps ago.)
-            auto rescale = [&](float keep) {
-                if (!__all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.o_step[s]), (count - 1) & 1, err))) return false;
+            // O times `keep` (1 in rows that need none) in step st > 0.  It is at rest once the step before is in it:
+            // this step's product waits for its weights.  The next step's scores are issued behind the product of the
+            // step before, and their commit covers it; they wait for nothing of this step.  An item's last step has none
+            // behind it: its barrier is waited for in every item, before the weights are handed over.  So either barrier
+            // is waited for in each of its phases, and is at most one ahead.
+            auto rescale = [&](bool last, float keep) {
+                const int next = count + 1;
+                const uint32_t bar = smem_u32(last ? &sm.o_most[s] : &sm.s_full[s][next & 1]);
+                if (!__all_sync(0xffffffffu, ptx::mbar_wait(bar, last ? most_phase : (next >> 1) & 1, err))) return false;
                 ptx::tc_fence_after();
 #pragma unroll 1
                 for (int c = 0; c < DP / 16; ++c) {
@@ -931,7 +935,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         if (vmost > cref) {
                             const float to = __int_as_float(min((__float_as_int(vmost) & 0x7f800000) + (1 << 23), 0x7f000000));
-                            if (st > 0 && !(ok = rescale(cref / to))) break;
+                            if (st > 0 && !(ok = rescale(st + 1 == steps, cref / to))) break;
                             cref = to;
                             logc = static_cast<float>((__float_as_int(to) >> 23) - 127);
                         }
@@ -969,7 +973,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                                 ref += by;
                                 l *= keep;
                             }
-                            if (st > 0 && !(ok = rescale(keep))) break;
+                            if (st > 0 && !(ok = rescale(st + 1 == steps, keep))) break;
 #pragma unroll
                             for (int k = 0; k < 4; ++k) minus[k] = lw[k] - ref;
                         }
@@ -992,6 +996,11 @@ __global__ void __launch_bounds__(kThreads, 1)
 #pragma unroll
                         for (int k = 0; k < 4; ++k) l = fmaf(sum[k], exp2_fast(-lw[k]), l);
                     }
+                }
+                if (st > 0 && st + 1 == steps) {
+                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.o_most[s]), most_phase, err));
+                    if (!ok) break;
+                    most_phase ^= 1;
                 }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
