@@ -249,7 +249,7 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
         if (w < warp) incl += sm.warp_sum[w];
         units += sm.warp_sum[w];
     }
-    long long* const chunk = reinterpret_cast<long long*>(&sm.join);  // the join begins after every warp's search
+    long long* const chunk = reinterpret_cast<long long*>(&sm.join);
     chunk[tid] = incl - mine;
     __syncthreads();
 
@@ -286,6 +286,7 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
         load.row_tile = item - load.head * s.row_tiles;
         load.tile = static_cast<int>(rest % s.tiles);
     }
+    __syncthreads();  // every warp has searched: sm.join is free, also for a warp that has no unit before the first join
     Cursor at = load;  // the block's place: the segment that all its warps are in
     long long left = u1 - u0;
     load.tile += warp;

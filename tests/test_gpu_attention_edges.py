@@ -1,5 +1,5 @@
 """Attention over the 8-bit cache (GPU) at the ends of its range: references
-that move at every tile.  Definitions and bars: serving_reference.py."""
+that move at every tile, many short requests.  Definitions and bars: serving_reference.py."""
 import pytest
 import torch
 
@@ -36,3 +36,19 @@ def test_references_that_move_at_every_tile(dtype, added, group):
     unit = ref.attention(*case[:2], torch.ones(vc.shape).to(F8), *case[3:], 0.125)[0]
     bar = bar + 2.0 ** -31 * 448 * max(lengths) * unit
     one.assert_attention([t[some] for t in got], [t[some] for t in (out, lse, bar, lse_bar)])
+
+
+# -------------------------------------------------------- many short requests --
+
+@pytest.mark.parametrize("group", [2, 10])
+def test_many_short_requests(group):
+    """More requests than a block has warps' chunks for, of a unit or two each: the same bits in every run."""
+    gen = one._gen(group)
+    n = 700
+    lengths = [int(x) for x in torch.randint(1, 40, (n,), generator=gen)]
+    added = [int(i % 5 != 0) for i in range(n)]
+    case = one._requests(gen, lengths, added, 1, group, 16, 16, "bf16")
+    got = one.check_attention(case)
+    for _ in range(40):
+        again = one.run_attention(*case, 0.25)
+        assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
