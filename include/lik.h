@@ -654,7 +654,9 @@ lik_status lik_cache_write(const void* k, const void* v, lik_dtype dtype, int64_
  * exact, q brought into its range by a power of two, and the softmax weights
  * rounded to 11 bits (for fp16 outputs in two parts, 22 bits) over the 20
  * binades below a row's largest one; what is smaller keeps fewer bits, and
- * below 2^-31 of it none.  Results do not depend on the run.  A scale of a seen page that is not finite makes its tokens'
+ * below 2^-31 of it none.  Scores are fp32 numbers: off by up to 2^-21 of
+ * their size, and of at most 2^27 (a row with a larger one is not defined).
+ * Results do not depend on the run.  A scale of a seen page that is not finite makes its tokens'
  * scores (k_scale) or the row's output (v_scale) not finite.
  *   q, out [rows, q_heads, dim], fp16 or bf16, element (t, h, d) at t *
  *   token_stride + h * head_stride + d; lse [rows, q_heads] fp32 or NULL;

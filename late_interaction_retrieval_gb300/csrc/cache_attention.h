@@ -14,9 +14,9 @@
 namespace lik {
 namespace attn {
 
-// log2 of the largest weight, and of a row's largest one when its reference is set; the reference before
-// the row has seen a token.
-constexpr float kLogTop = 15.0f, kLogStart = 7.0f, kNothing = -1048576.0f;
+// log2 of the largest weight, and of a row's largest one when its reference is set; the reference that a row
+// which has seen nothing has where sums are joined (below any other; its own sum is 0).
+constexpr float kLogTop = 15.0f, kLogStart = 7.0f, kNothing = -1.70141183e38f;
 
 // One request as the device has it, clamped to what the buffers hold.
 struct Request {

@@ -428,10 +428,14 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
         for (int j = 0; j < MB; ++j)
 #pragma unroll
             for (int nr = 0; nr < NR; ++nr) o[j][nr][0] = o[j][nr][1] = o[j][nr][2] = o[j][nr][3] = 0.0f;
-        float ref[NR][2], l[NR][2];
+        // A row's first reference comes from its first token, whatever its score: until then 0 stands in, and its bit in
+        // `have` is clear.  A unit's weights are looked at again where one is above `limit`: in every unit until all rows
+        // that see anything have a reference.
+        float ref[NR][2], l[NR][2], limit = -INFINITY;
+        uint32_t have = 0;
 #pragma unroll
         for (int nr = 0; nr < NR; ++nr) {
-            ref[nr][0] = ref[nr][1] = kNothing;
+            ref[nr][0] = ref[nr][1] = 0.0f;
             l[nr][0] = l[nr][1] = 0.0f;
         }
         float c = 0.0f, logc = -127.0f;  // and its log2
@@ -530,8 +534,13 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
                         }
                 return top;
             };
-            if (__any_sync(0xffffffffu, weigh() > kLogTop)) {
+            // (Written as a loop, the weights' code is there once: 2% of a batch of single tokens.)
+            float most = limit;
+#pragma unroll 1
+            for (int turn = 0; __any_sync(0xffffffffu, weigh() > most) && turn < 2; ++turn) {
                 float keep[NR][2];
+                bool all = true;
+                most = kLogTop;
 #pragma unroll
                 for (int nr = 0; nr < NR; ++nr)
 #pragma unroll
@@ -541,15 +550,18 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 8));
                         top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 16));
                         keep[nr][e] = 1.0f;
-                        if (top > kLogTop) {
-                            const float by = ceilf(top) - kLogStart;
-                            keep[nr][e] = exp2_fast(-by);  // 0 for the first tokens that a row sees
-                            ref[nr][e] += by;
+                        const uint32_t bit = 1u << (2 * nr + e);
+                        if (top > (have & bit ? kLogTop : -INFINITY)) {
+                            const float to = ref[nr][e] + (ceilf(top) - kLogStart);
+                            keep[nr][e] = have & bit ? exp2_fast(ref[nr][e] - to) : 0.0f;
+                            ref[nr][e] = to;
                             l[nr][e] *= keep[nr][e];
+                            have |= bit;
                         }
+                        all = all && ((have & bit) || sees[nr][e] <= 0);
                     }
+                limit = __all_sync(0xffffffffu, all) ? kLogTop : -INFINITY;
                 rescale(keep);
-                weigh();
             }
             uint32_t pf[2][NR][2], pl[2][NR][2];  // B fragments of the two 16-token steps; what their rounding left
 #pragma unroll
@@ -666,7 +678,7 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
                 l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 8);
                 l[nr][e] += __shfl_xor_sync(0xffffffffu, l[nr][e], 16);
                 if (g == 0) {
-                    sm.m[warp][nr * 8 + 2 * q4 + e] = ref[nr][e];
+                    sm.m[warp][nr * 8 + 2 * q4 + e] = l[nr][e] == 0.0f ? kNothing : ref[nr][e];
                     sm.l[warp][nr * 8 + 2 * q4 + e] = l[nr][e];
                 }
             }

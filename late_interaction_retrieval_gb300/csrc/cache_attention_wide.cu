@@ -792,7 +792,9 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int sees = live ? w.x.r.length - w.x.r.n + i + 1 : 0;
             const int all_see = w.x.r.length - w.x.r.n + (w.x.item * kItemRows) / group + 1;
             const bool idle = __ballot_sync(0xffffffffu, live) == 0;  // no row of this warp's: its weights do not matter
-            float ref = kNothing, l = 0.0f, cref = 0.0f, logc = -127.0f;  // logc: log2 of cref
+            // have: the row has a reference, from its first token's score, whatever that is; 0 stands in before
+            float ref = 0.0f, l = 0.0f, cref = 0.0f, logc = -127.0f;  // logc: log2 of cref
+            bool have = false;
             bool nan_scale = false;  // the row sees a page whose values' scale is not finite
             // The next item's q is fetched once this one's last scores are there, and is an operand before this one's
             // output is written.
@@ -907,7 +909,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                             sum[k] = h.x + h.y;
                         }
                         const float total = (sum[0] + sum[1]) + (sum[2] + sum[3]);
-                        fits = __all_sync(0xffffffffu, total <= kHalfMost && vmost <= cref);
+                        fits = __all_sync(0xffffffffu, total <= kHalfMost && vmost <= cref && (have || !live));
                         if (fits) {
                             tmem_st_16(col_s, p);
                             tmem_st_16(col_s + 16, r);
@@ -965,13 +967,15 @@ __global__ void __launch_bounds__(kThreads, 1)
                         }
                         // a weight near the end of fp16's range: the row's reference moves, by a power of two, exact
                         // for what has been summed and rounded (64 weights below the limit fit together)
-                        if (__any_sync(0xffffffffu, top > kLogLimit)) {
+                        const bool moves = top > (have ? kLogLimit : -INFINITY);
+                        if (__any_sync(0xffffffffu, moves)) {
                             float keep = 1.0f;
-                            if (top > kLogLimit) {
-                                const float by = ceilf(top) - kLogStart;
-                                keep = exp2_fast(-by);  // 0 for the first tokens that a row sees
-                                ref += by;
+                            if (moves) {
+                                const float to = ref + (ceilf(top) - kLogStart);
+                                keep = have ? exp2_fast(ref - to) : 0.0f;
+                                ref = to;
                                 l *= keep;
+                                have = true;
                             }
                             if (st > 0 && !(ok = rescale(st + 1 == steps, keep))) break;
 #pragma unroll
@@ -1023,6 +1027,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (tiles > 0) {
                 const bool begins = w.t0 == 0, ends = w.t1 == w.x.tiles, cut = !(begins && ends);
                 const bool nan = *reinterpret_cast<volatile int*>(&sm.nan_seen) != 0;
+                if (l == 0.0f) ref = kNothing;
                 if (s == 1 && !two) {
                     if (join) {
                         // stream 0's warp of the same rows reads this stream's O, and beside it, in the columns of

@@ -1,5 +1,5 @@
-"""Attention over the 8-bit cache (GPU) at the ends of its range: references
-that move at every tile, many short requests.  Definitions and bars: serving_reference.py."""
+"""Attention over the 8-bit cache (GPU) at the ends of its range: scores far
+from 0, references that move at every tile, many short requests.  Definitions and bars: serving_reference.py."""
 import pytest
 import torch
 
@@ -8,7 +8,78 @@ import test_gpu_serving as one
 
 pytestmark = pytest.mark.gpu
 
-F8 = torch.float8_e4m3fn
+F8, NAN = torch.float8_e4m3fn, float("nan")
+
+
+# ----------------------------------------------------------- scores far from 0 --
+
+FAR = 12  # dimensions that make a score far from 0
+
+
+def _far(seed, lengths, added, heads, group, dim, page, dtype, levels):
+    """Scores of whole numbers: `levels` (one a page, in turn) times 256 * 448 * FAR, and a few units.
+
+    They are exact in 32 bits (below 2^24, of whole numbers), and so are their differences; the values' scales are
+    powers of two.  What is left of the bars: a weight's 2^-11, the factor scale * log2(e) (off by 2^-22 of itself at
+    most), which scales the differences of scores, up to `span`, and the log-sum-exp's own 2^-21.  And the step of the
+    smallest weights: 2^-24 in fp16, half of it 2^-25, where a row's largest weight is at least 2^6 (with its page's
+    scale in it), so that each of its tokens is off by up to 2^-31 of the largest weight times its own code: 448 at
+    most, of scales up to 2^-5.  A dimension in which the likely tokens are 0 shows it."""
+    gen = one._gen(seed)
+    q, kc, vc, ks, vs, table, offsets, lengths = one._requests(gen, lengths, added, heads, group, dim, page, dtype)
+    pages = kc.shape[0]
+    unused = ks[:, 0].isnan()
+    small = torch.randint(-2, 3, kc.shape, generator=gen).float()
+    level = torch.zeros(pages)
+    for row in table:
+        for j, p in enumerate(row.tolist()):
+            if p >= 0:
+                level[p] = levels[j % len(levels)]
+    small[..., :FAR] = 448.0 * level[:, None, None, None]
+    hidden = (kc.view(torch.uint8) & 0x7F) == 0x7F
+    kc = torch.where(hidden, kc.float(), small).to(F8)
+    q = torch.randint(-2, 3, q.shape, generator=gen).to(q.dtype)
+    q[..., :FAR] = 256.0
+    ks, vs = torch.ones_like(ks), 2.0 ** torch.randint(-9, -4, vs.shape, generator=gen).float()
+    ks[unused], vs[unused] = NAN, NAN
+    return q, kc, vc, ks, vs, table, offsets, lengths
+
+
+def _check_far(case, span=8 * 128.0, **kw):
+    out, lse, _, _ = ref.attention(*case, 1.0)
+    q, _, vc, _, vs, table, offsets, lengths = case
+    # sum p |v|: the same attention over the values' sizes
+    size = ref.attention(*case[:2], vc.float().abs().to(F8), *case[3:], 1.0)[0]
+    bar = (2.0 ** -11 + 2.0 ** -20 + 2.0 ** -21 * span) * size + (ref.HALF_STEP[q.dtype] * out.abs()).clamp(
+        min=ref.LEAST_HALF_STEP[q.dtype]) + 2.0 ** -31 * 2.0 ** -5 * 448 * max(lengths)
+    got = one.run_attention(*case, 1.0, **kw)
+    one.assert_attention(got, (out, lse, bar, 2.0 ** -18 + 2.0 ** -21 * lse.abs()))
+
+
+BATCHES = [([40, 300], [1, 1], 4), ([700], [1], 1), ([33, 90], [2, 1], 8), ([300, 70], [5, 3], 8), ([260, 3], [130, 3], 4),
+           ([600], [300], 2)]
+# 12 * 256 * 448 = 1376256 below and above 0 (1985508 in powers of two), in all pages or some
+LEVELS = [[-1.0], [1.0], [-1.0, -0.625], [-0.625, -1.0], [-1.0, 0.0], [0.0, -1.0], [-1.0, -1.0, -1.0, 1.0], [1.0, -1.0]]
+
+
+@pytest.mark.parametrize("dtype", ["f16", "bf16"])
+@pytest.mark.parametrize("levels", LEVELS)
+def test_scores_far_from_zero(dtype, levels):
+    for i, (lengths, added, group) in enumerate(BATCHES):
+        for page in (16, 64):
+            _check_far(_far(i, lengths, added, 1, group, 64, page, dtype, levels))
+    _check_far(_far(9, [300, 40], [5, 1], 2, 4, 128, 32, dtype, levels))
+
+
+@pytest.mark.parametrize("levels", [[-1.0], [-1.0, -0.625]])
+def test_scores_far_from_zero_split_along_the_cache(levels):
+    """Pieces whose rows have seen such scores only, and pieces that have seen nothing, joined."""
+    case = _far(3, [20011], [1], 1, 4, 16, 64, "bf16", levels)
+    case[5][0, 40:100] = -1
+    _check_far(case)
+    case = _far(4, [9000], [40], 1, 4, 64, 64, "f16", levels)
+    case[5][0, :70] = -1
+    _check_far(case)
 
 
 # -------------------------------------------- references that move at every tile --
