@@ -643,7 +643,8 @@ lik_status lik_cache_write(const void* k, const void* v, lik_dtype dtype, int64_
  * which adds n = offsets[b + 1] - offsets[b] tokens and has lengths[b] of them
  * in the cache, the new ones included, sees the positions j with
  *     j < lengths[b] - n + i + 1     (its own and all before it)
- * whose page is in the table (an entry outside [0, pages) hides its tokens):
+ * whose page is in the table (an entry outside [0, pages) hides its tokens, and
+ * a table of too few columns those behind it):
  *     z_j    = scale * (q . k_j)
  *     out    = sum_j exp(z_j) v_j / sum_j exp(z_j)
  *     lse[t, h] = log sum_j exp(z_j)
@@ -662,8 +663,8 @@ lik_status lik_cache_write(const void* k, const void* v, lik_dtype dtype, int64_
  *   token_stride + h * head_stride + d; lse [rows, q_heads] fp32 or NULL;
  *   block_table [requests, table_cols] int32, row b at b * table_stride;
  *   1e-30 <= scale <= 1e30; q_heads is 1 to 128 times heads (at most 1024),
- *   rows * q_heads <= 2^30.  lengths are clamped to [0, table_cols *
- *   page_size], offsets to [0, rows].
+ *   rows * q_heads <= 2^30.  Negative lengths count as 0, offsets are
+ *   clamped to [0, rows].
  *   max_added: the most tokens that a request adds, as the host knows it: it
  *   chooses the kernel.  A wrong value costs time, not results.
  *   workspace: 16-byte aligned, of lik_cache_attention_workspace_bytes bytes

@@ -21,7 +21,8 @@ constexpr float kLogTop = 15.0f, kLogStart = 7.0f, kNothing = -1.70141183e38f;
 // One request as the device has it, clamped to what the buffers hold.
 struct Request {
     int row0, n;   // its rows
-    int length;    // its tokens in the cache
+    int length;    // its tokens in the cache, as far as its table goes
+    int before;    // its tokens before the first row's, wherever they are: row i sees before + i + 1
 };
 
 __device__ __forceinline__ Request request_of(const AttentionArgs& a, int b) {
@@ -32,7 +33,10 @@ __device__ __forceinline__ Request request_of(const AttentionArgs& a, int b) {
     hi = min(max(hi, lo), rows);
     r.row0 = lo;
     r.n = hi - lo;
-    r.length = min(max(a.lengths[b], 0), static_cast<int>(a.cols << a.page_shift));
+    // A request that is longer than its table: the tokens behind it are hidden, and the rows stay where they are.
+    const int all = max(a.lengths[b], 0);
+    r.length = min(all, static_cast<int>(a.cols << a.page_shift));
+    r.before = all - r.n;
     return r;
 }
 

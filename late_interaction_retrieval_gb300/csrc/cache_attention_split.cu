@@ -414,14 +414,14 @@ __global__ void __launch_bounds__(32 * Shape<NR>::kWarps, 1)
                 qf[nr][c >> 1][c & 1] = pack_half(f.x * up.x * up.y, f.y * up.x * up.y);
             }
             const float of_row = a.scale * 1.44269504088896341f * down.x * down.y;
-            const int row_sees = live ? r.length - r.n + i + 1 : 0;
+            const int row_sees = live ? r.before + i + 1 : 0;
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
                 factor[nr][e] = __shfl_sync(0xffffffffu, of_row, 4 * (2 * q4 + e));
                 sees[nr][e] = __shfl_sync(0xffffffffu, row_sees, 4 * (2 * q4 + e));
             }
         }
-        const int all_see = r.length - r.n + (row_tile * kRows) / group + 1;  // what even the first row sees
+        const int all_see = r.before + (row_tile * kRows) / group + 1;  // what even the first row sees
 
         float o[MB][NR][4];
 #pragma unroll

@@ -99,7 +99,7 @@ __device__ __forceinline__ void shape(Item& x, int group) {
     const int all = x.r.n * group, first = x.item * kItemRows;
     x.rows = min(kItemRows, all - first);
     x.two = x.rows > kM;
-    const int sees = x.r.length - x.r.n + (first + x.rows - 1) / group + 1;
+    const int sees = min(x.r.before + (first + x.rows - 1) / group + 1, x.r.length);
     x.tiles = max(1, (sees + kTok - 1) / kTok);
 }
 
@@ -505,7 +505,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         uint64_t* const empty = keys ? sm.k_empty : sm.v_empty;
         while (ok) {
             // what even the item's first row sees
-            const int all_see = w.x.r.length - w.x.r.n + (w.x.item * kItemRows) / group + 1;
+            const int all_see = w.x.r.before + (w.x.item * kItemRows) / group + 1;
 #pragma unroll 1
             for (int t = w.t0; t < w.t1; ++t, ++n) {
                 ok = ptx::mbar_wait(smem_u32(&empty[buf]), phase, err) &&
@@ -789,8 +789,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             const int rr = w.x.item * kItemRows + in_item;  // of the request's rows
             const int i = live ? rr / group : 0;
             const int h = w.x.head * group + (live ? rr % group : 0);
-            const int sees = live ? w.x.r.length - w.x.r.n + i + 1 : 0;
-            const int all_see = w.x.r.length - w.x.r.n + (w.x.item * kItemRows) / group + 1;
+            const int sees = live ? w.x.r.before + i + 1 : 0;
+            const int all_see = w.x.r.before + (w.x.item * kItemRows) / group + 1;
             const bool idle = __ballot_sync(0xffffffffu, live) == 0;  // no row of this warp's: its weights do not matter
             // have: the row has a reference, from its first token's score, whatever that is; 0 stands in before
             float ref = 0.0f, l = 0.0f, cref = 0.0f, logc = -127.0f;  // logc: log2 of cref
@@ -1106,7 +1106,7 @@ __global__ void __launch_bounds__(kThreads, 1)
                         if (nan && live && d < a.dim) {
                             // NaN codes that were set apart: those of tokens that this row sees
                             uint32_t hit = 0;
-                            for (int pos = max(all_see, w.t0 * kTok); pos < min(sees, w.t1 * kTok); ++pos) {
+                            for (int pos = max(all_see, w.t0 * kTok); pos < min(min(sees, w.x.r.length), w.t1 * kTok); ++pos) {
                                 const int pg = a.table[w.x.b * a.stride + (pos >> a.page_shift)];
                                 if (pg < 0 || pg >= a.pages) continue;
                                 const uint4 x = *reinterpret_cast<const uint4*>(

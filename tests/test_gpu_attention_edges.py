@@ -1,5 +1,8 @@
 """Attention over the 8-bit cache (GPU) at the ends of its range: scores far
-from 0, references that move at every tile, many short requests.  Definitions and bars: serving_reference.py."""
+from 0, references that move at every tile, many short requests, requests that
+are longer than their table.  Definitions and bars: serving_reference.py."""
+import math
+
 import pytest
 import torch
 
@@ -123,3 +126,38 @@ def test_many_short_requests(group):
     for _ in range(40):
         again = one.run_attention(*case, 0.25)
         assert torch.equal(got[0], again[0]) and torch.equal(got[1], again[1])
+
+
+# ----------------------------------------------- requests longer than their table --
+
+def _cut(case, cols):
+    """The same batch with tables of `cols` columns, and with tables whose further entries are no pages."""
+    q, kc, vc, ks, vs, table, offsets, lengths = case
+    wide = table.clone()
+    wide[:, cols:] = -1
+    return (q, kc, vc, ks, vs, table[:, :cols].contiguous(), offsets, lengths), (q, kc, vc, ks, vs, wide, offsets, lengths)
+
+
+@pytest.mark.parametrize("page,group", [(16, 1), (16, 4), (64, 8), (128, 2)])
+def test_requests_that_pass_their_table(page, group):
+    """A row sees what it would with a longer table, without the tokens that have no place in it."""
+    for seed, (lengths, added) in enumerate([([3 * page + 3, 7], [5, 2]), ([3 * page + 1, 4 * page], [1, 1]),
+                                             ([4 * page, 3 * page + 9], [page + 4, 12]), ([5 * page, 2 * page], [page, 3])]):
+        case = one._requests(one._gen(seed), lengths, added, 2, group, 64, page, "bf16")
+        for cols in (3, 1):
+            narrow, wide = _cut(case, cols)
+            for hint in (1, 1000):  # both kernels
+                got = one.run_attention(*narrow, 0.125, max_added=hint)
+                one.assert_attention(got, ref.attention(*wide, 0.125))
+
+
+def test_lengths_out_of_range():
+    """The largest and negative lengths: all of the table is seen, or nothing."""
+    case = one._requests(one._gen(5), [48, 48, 48], [3, 2, 1], 1, 2, 32, 16, "f16")
+    narrow, wide = _cut(case, 3)
+    q, kc, vc, ks, vs, table, offsets, _ = narrow
+    for hint in (1, 1000):
+        out, lse = one.run_attention(q, kc, vc, ks, vs, table, offsets, [2 ** 31 - 1, -7, 2 ** 31 - 1], 0.2, max_added=hint)
+        want = ref.attention(q, kc, vc, ks, vs, wide[5], offsets, [51, 0, 49], 0.2)
+        one.assert_attention((out, lse), want)
+        assert bool((out[3:5] == 0).all()) and bool((lse[3:5] == -math.inf).all())
