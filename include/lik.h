@@ -605,7 +605,10 @@ lik_status lik_preference_loss_step(const void* logits, lik_dtype dtype, int64_t
  *   free_pages [free_capacity]; free_count, free_left [1]; block_table
  *   [requests, table_cols], row b at element b * table_stride, updated in
  *   place; all int32, device.  slots [slot_capacity] int64; tokens behind
- *   slot_capacity are left out (offsets end there).
+ *   slot_capacity are left out: offsets end there, lengths and pages count
+ *   them.  Before the rows that are there go on to lik_cache_attention, which
+ *   takes them for their requests' last tokens, lengths[b] has to become
+ *   max(cached[b], 0) + offsets[b + 1] - offsets[b].
  *   Negative lengths count as 0; held is clamped to [0, table_cols],
  *   free_count to [0, free_capacity].
  */

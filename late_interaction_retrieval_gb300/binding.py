@@ -714,7 +714,8 @@ def lik_cache_slots(cached, added, held, free_pages, free_count, block_table, he
                     free_left, page_size, stream=None):
     """Block tables (new entries, in place) and slot maps of a batch from its
     requests' lengths: request b holds held[b] pages with cached[b] tokens and
-    gets added[b] more.  Pages come from the end of free_pages[:free_count]."""
+    gets added[b] more.  Pages come from the end of free_pages[:free_count].
+    lengths count tokens behind the last slot too (serving.cache_slots does not)."""
     if cached.dim() != 1 or free_pages.dim() != 1 or slots.dim() != 1:
         raise ValueError("cached, free_pages and slots must have one dimension")
     if not cached.is_cuda:

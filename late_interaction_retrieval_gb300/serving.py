@@ -34,7 +34,8 @@ def cache_slots(cached, added, held, free_pages, free_count, block_table, page_s
     all int32, block_table [requests, most pages] gets its new entries in
     place.  Pages come from the end of free_pages[:free_count]; free_left below
     zero says how many were missing.  slots [rows] (int64, -1: none) says where
-    each row's token goes; lengths are the requests' tokens with the new ones."""
+    each row's token goes; lengths are the requests' tokens with the new ones
+    that have a row: where `rows` are too few, the last tokens are left out."""
     def int32(n):
         return torch.empty(n, dtype=torch.int32, device=cached.device)
 
@@ -43,6 +44,8 @@ def cache_slots(cached, added, held, free_pages, free_count, block_table, page_s
     slots = torch.empty(rows, dtype=torch.int64, device=cached.device)
     binding.lik_cache_slots(cached, added, held, free_pages, free_count, block_table, held_out, lengths, offsets, slots,
                             left, page_size)
+    # the binding's lengths count tokens without a row too; attention takes a request's rows for its last tokens
+    lengths = torch.minimum(lengths, cached.clamp(min=0) + (offsets[1:] - offsets[:-1]))
     return held_out, lengths, offsets, slots, left
 
 

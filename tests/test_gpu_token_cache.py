@@ -1,0 +1,39 @@
+"""Batches (GPU) that do not go as planned: steps that do not fit into the rows."""
+import pytest
+import torch
+
+import serving_reference as ref
+import test_gpu_serving as one
+import test_gpu_serving_step as steps
+from late_interaction_retrieval_gb300 import binding, serving
+
+pytestmark = pytest.mark.gpu
+
+_dev = steps._dev
+
+
+# ------------------------------------------------------------ steps that do not fit --
+
+@pytest.mark.parametrize("most", [1, 40])
+def test_rows_that_are_left_out_shift_nobody(most):
+    """More new tokens than rows: those that have a row see what they would have seen."""
+    gen = one._gen(most)
+    heads, dim, page = 2, 64, 16
+    cached, added, rows = [40, 9, 3], [5, 30, 4], 12
+    case = one._requests(gen, cached, [0] * 3, heads, 4, dim, page, "bf16", spare=12)
+    _, kc, vc, ks, vs, table, _, _ = case
+    used = set(table[table >= 0].tolist())
+    free = _dev([p for p in range(kc.shape[0]) if p not in used])
+    table = torch.cat([table, torch.full((3, 4), -1, dtype=torch.int32)], 1).cuda()
+    held = _dev([-(-c // page) for c in cached])
+    kc, vc, ks, vs = (t.cuda() for t in (kc, vc, ks, vs))
+    held, lengths, offsets, slots, _ = serving.cache_slots(_dev(cached), _dev(added), held, free, _dev([free.shape[0]]), table,
+                                                           page, rows)
+    assert offsets.tolist() == [0, 5, 12, 12] and lengths.tolist() == [45, 16, 3]
+    x, y = (torch.randn(rows, heads, dim, generator=gen).bfloat16().cuda() for _ in range(2))
+    serving.cache_write(x, y, slots, kc, vc, ks, vs)
+    q = torch.randn(rows, 4 * heads, dim, generator=gen).bfloat16().cuda()
+    got = serving.cache_attention(q, kc, vc, ks, vs, table, offsets, lengths, return_lse=True, max_added=most)
+    binding.lik_check_device_error()
+    want = ref.attention(q.cpu(), kc.cpu(), vc.cpu(), ks.cpu(), vs.cpu(), table.cpu(), [0, 5, 12, 12], [45, 16, 3], dim ** -0.5)
+    one.assert_attention(got, want)
