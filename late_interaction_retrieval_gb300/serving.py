@@ -151,8 +151,10 @@ class TokenCache:
                                self.block_table, self.offsets, self.lengths, **options)
 
     def keep(self, tokens):
-        """The first tokens[b] (device, or one number for all) of request b's planned ones stay."""
-        self.cached.add_(tokens)
+        """The first tokens[b] (device, or one number for all) of request b's planned ones stay: no more than were
+        planned, and none in a place without a request, which planned none."""
+        planned = self.offsets[1:] - self.offsets[:-1]
+        self.cached.add_(torch.minimum(planned, tokens) if torch.is_tensor(tokens) else planned.clamp(max=tokens))
 
     def release(self, request):
         """Request number `request` has ended: its pages are free, its place is empty."""

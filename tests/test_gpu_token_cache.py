@@ -1,15 +1,38 @@
-"""Batches (GPU) that do not go as planned: steps that do not fit into the rows."""
+"""TokenCache (GPU) where a batch does not go as planned: places without a
+request, steps that do not fit into the rows."""
 import pytest
 import torch
 
 import serving_reference as ref
 import test_gpu_serving as one
 import test_gpu_serving_step as steps
-from late_interaction_retrieval_gb300 import binding, serving
+from late_interaction_retrieval_gb300 import TokenCache, binding, serving
 
 pytestmark = pytest.mark.gpu
 
 _dev = steps._dev
+
+
+def _cache(pages=8, requests=2, max_tokens=64, heads=1, dim=16, page_size=16):
+    return TokenCache(1, heads, dim, pages=pages, requests=requests, max_tokens=max_tokens, page_size=page_size)
+
+
+# ------------------------------------------------------ places without a request --
+
+@pytest.mark.parametrize("kept", [[4, 1], 4, [9, 9], 9])
+def test_keep_takes_no_more_than_was_planned(kept):
+    """An idle place (no new token) keeps none, whatever the verification of its neighbours' drafts gave it."""
+    cache = _cache()
+    cache.plan(_dev([4, 0]), 6)
+    cache.keep(_dev(kept) if isinstance(kept, list) else kept)
+    assert cache.cached.tolist() == [4, 0]
+    cache.plan(_dev([2, 0]), 6)
+    cache.keep(torch.tensor([1, 1], device="cuda"))  # of 64 bits
+    assert cache.cached.tolist() == [5, 0] and cache.held.tolist() == [1, 0]
+    cache.release(0)
+    cache.plan(_dev([0, 3]), 6)
+    cache.keep(_dev([1, 2]))
+    assert cache.cached.tolist() == [0, 2]
 
 
 # ------------------------------------------------------------ steps that do not fit --
