@@ -114,7 +114,7 @@ class TokenCache:
     stream at a time.  All lengths stay on the device and every buffer where it
     is: a captured step can be replayed.  missing [1] (int32, device) is how
     many pages the last plan wanted beyond those that were free: tokens without
-    a page are neither written nor seen, and such a step is not to be kept.
+    a page are neither written nor seen, and keep() keeps nothing of such a step.
     """
 
     def __init__(self, layers, heads, dim, pages, requests, max_tokens, page_size=64, device="cuda"):
@@ -152,9 +152,11 @@ class TokenCache:
 
     def keep(self, tokens):
         """The first tokens[b] (device, or one number for all) of request b's planned ones stay: no more than were
-        planned, and none in a place without a request, which planned none."""
+        planned, and none in a place without a request, which planned none.  Of a step that lacked pages nothing does:
+        `missing` says so, also behind a captured step, which can be run again once pages are free."""
         planned = self.offsets[1:] - self.offsets[:-1]
-        self.cached.add_(torch.minimum(planned, tokens) if torch.is_tensor(tokens) else planned.clamp(max=tokens))
+        kept = torch.minimum(planned, tokens) if torch.is_tensor(tokens) else planned.clamp(max=tokens)
+        self.cached.add_(kept * (self.missing == 0))
 
     def release(self, request):
         """Request number `request` has ended: its pages are free, its place is empty."""

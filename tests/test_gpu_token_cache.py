@@ -1,5 +1,5 @@
 """TokenCache (GPU) where a batch does not go as planned: places without a
-request, steps that do not fit into the rows."""
+request, steps that do not fit into the pages or the rows."""
 import pytest
 import torch
 
@@ -36,6 +36,25 @@ def test_keep_takes_no_more_than_was_planned(kept):
 
 
 # ------------------------------------------------------------ steps that do not fit --
+
+def _same_state(cache, state):
+    assert cache.cached.tolist() == state
+
+
+def test_a_step_without_pages_is_not_kept():
+    cache = _cache(pages=3)
+    cache.plan(_dev([20, 5]), 25)
+    assert int(cache.missing) == 0
+    cache.keep(_dev([20, 5]))
+    cache.plan(_dev([14, 2]), 25)
+    assert int(cache.missing) == 1
+    cache.keep(_dev([14, 2]))
+    _same_state(cache, [20, 5])
+    cache.plan(_dev([12, 11]), 25)  # the same pages hold these
+    assert int(cache.missing) == 0
+    cache.keep(_dev([12, 11]))
+    _same_state(cache, [32, 16])
+
 
 @pytest.mark.parametrize("most", [1, 40])
 def test_rows_that_are_left_out_shift_nobody(most):
