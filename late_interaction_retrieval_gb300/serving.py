@@ -113,8 +113,10 @@ class TokenCache:
     A step is one plan, each layer's write and attention, one keep, on one
     stream at a time.  All lengths stay on the device and every buffer where it
     is: a captured step can be replayed.  missing [1] (int32, device) is how
-    many pages the last plan wanted beyond those that were free: tokens without
-    a page are neither written nor seen, and keep() keeps nothing of such a step.
+    many pages the last plan lacked: beyond those that were free, behind the
+    table's columns (max_tokens), or for tokens beyond its rows.  0: the step
+    fits.  Tokens without a place are neither written nor seen, and keep() keeps
+    nothing of a step that does not fit.
     """
 
     def __init__(self, layers, heads, dim, pages, requests, max_tokens, page_size=64, device="cuda"):
@@ -138,8 +140,10 @@ class TokenCache:
             self.cached, added, self.held, self._free[:self.pages], self.free_count, self.block_table, self.page_size,
             rows)
         self.held.copy_(held)
-        self.free_count.copy_(left.clamp(min=0))
-        self.missing.copy_(left.neg().clamp(min=0))
+        torch.clamp(left, min=0, out=self.free_count)
+        # tokens without a place, whatever they lacked; the pages that were not free are those of each request, rounded up
+        lost = added.clamp(min=0).sum() - (self.slots >= 0).sum()
+        self.missing.copy_(torch.maximum(left.neg(), (lost + self.page_size - 1) // self.page_size))
         return self.lengths, self.offsets, self.slots
 
     def write(self, layer, k, v):
@@ -152,8 +156,8 @@ class TokenCache:
 
     def keep(self, tokens):
         """The first tokens[b] (device, or one number for all) of request b's planned ones stay: no more than were
-        planned, and none in a place without a request, which planned none.  Of a step that lacked pages nothing does:
-        `missing` says so, also behind a captured step, which can be run again once pages are free."""
+        planned, and none in a place without a request, which planned none.  Of a step that did not fit nothing does:
+        `missing` says so, also behind a captured step, which can be run again once there is room."""
         planned = self.offsets[1:] - self.offsets[:-1]
         kept = torch.minimum(planned, tokens) if torch.is_tensor(tokens) else planned.clamp(max=tokens)
         self.cached.add_(kept * (self.missing == 0))

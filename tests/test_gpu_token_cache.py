@@ -1,5 +1,5 @@
 """TokenCache (GPU) where a batch does not go as planned: places without a
-request, steps that do not fit into the pages or the rows."""
+request, steps that do not fit into the pages, the table or the rows."""
 import pytest
 import torch
 
@@ -54,6 +54,59 @@ def test_a_step_without_pages_is_not_kept():
     assert int(cache.missing) == 0
     cache.keep(_dev([12, 11]))
     _same_state(cache, [32, 16])
+
+
+def test_a_request_that_outgrows_its_table_is_missing_pages():
+    """max_tokens is passed although pages are free: counted, and not kept."""
+    cache = _cache(pages=8, max_tokens=32)
+    cache.plan(_dev([33, 4]), 40)
+    assert int(cache.missing) == 1 and int(cache.free_count) == 5
+    assert cache.slots.tolist()[32] == -1 and min(cache.slots.tolist()[33:37]) >= 0
+    cache.keep(_dev([33, 4]))
+    _same_state(cache, [0, 0])
+    cache.plan(_dev([32, 0]), 40)
+    assert int(cache.missing) == 0
+    cache.keep(32)
+    _same_state(cache, [32, 0])
+    cache.plan(_dev([60, 40]), 100)  # 4 and 1 pages behind the tables
+    assert int(cache.missing) == 5
+    cache.keep(60)
+    _same_state(cache, [32, 0])
+
+
+def test_a_step_of_more_tokens_than_rows_is_not_kept():
+    cache = _cache()
+    cache.plan(_dev([6, 7]), 10)
+    assert int(cache.missing) > 0 and cache.offsets.tolist() == [0, 6, 10]
+    cache.keep(_dev([6, 4]))
+    _same_state(cache, [0, 0])
+    cache.plan(_dev([6, 4]), 10)
+    assert int(cache.missing) == 0
+    cache.keep(_dev([6, 4]))
+    _same_state(cache, [6, 4])
+
+
+def test_a_captured_step_that_does_not_fit_is_not_kept():
+    """Nobody can look between the plan and the keep of a captured step: it looks itself."""
+    cache, added, tokens = _cache(pages=4, max_tokens=48), _dev([1, 1]), _dev([1, 1])
+    cache.plan(added, 40)
+    cache.keep(tokens)
+    cache.release(0)
+    cache.release(1)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        cache.plan(added, 40)
+        cache.keep(tokens)
+    state = [0, 0]
+    # pages held, of 4 in all and 3 a request: 2 and 1; 3 (the one that was left) and 1, where 2 were wanted; so it stays
+    for n, fits in (([20, 3], True), ([20, 17], False), ([0, 30], False), ([9, 0], True), ([8, 12], True), ([1, 0], True),
+                    ([0, 0], True), ([30, 20], False)):
+        added.copy_(_dev(n))
+        tokens.copy_(_dev(n))
+        graph.replay()
+        if fits:
+            state = [s + a for s, a in zip(state, n)]
+        assert cache.cached.tolist() == state and (int(cache.missing) == 0) == fits, n
 
 
 @pytest.mark.parametrize("most", [1, 40])
