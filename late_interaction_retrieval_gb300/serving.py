@@ -107,15 +107,17 @@ class TokenCache:
       plan(added, rows)     a step's new tokens: lengths, offsets and slots
       write(layer, k, v)    their keys and values
       attention(layer, q)   their attention over the cache
+      verify_rows(drafts, total)  the rows and offsets that verify_drafts wants of them
       keep(tokens)          so many of them stay; drafts that were turned down leave
       release(request)      a finished request's pages go back
 
     A step is one plan, each layer's write and attention, one keep, on one
-    stream at a time.  All lengths stay on the device and every buffer where it
-    is: a captured step can be replayed.  missing [1] (int32, device) is how
-    many pages the last plan lacked: beyond those that were free, behind the
-    table's columns (max_tokens), or for tokens beyond its rows.  0: the step
-    fits.  Tokens without a place are neither written nor seen, and keep() keeps
+    stream at a time.  A place without a request (none yet, or released) plans
+    no token.  All lengths stay on the device and every buffer where it is: a
+    captured step can be replayed.  missing [1] (int32, device) is how many
+    pages the last plan lacked: beyond those that were free, behind the table's
+    columns (max_tokens), or for tokens beyond its rows.  0: the step fits.
+    Tokens without a place are neither written nor seen, and keep() keeps
     nothing of a step that does not fit.
     """
 
@@ -153,6 +155,22 @@ class TokenCache:
         """cache_attention of the planned tokens' rows q [rows, q_heads, dim]."""
         return cache_attention(q, self.k[layer], self.v[layer], self.k_scale[layer], self.v_scale[layer],
                                self.block_table, self.offsets, self.lengths, **options)
+
+    def verify_rows(self, drafts, total):
+        """(rows, offsets) with which verify_drafts follows a plan whose request b's last drafts[b] (int32 [requests],
+        device) tokens are drafts, at most `total` together; 0 for a prompt, of which the last row is wanted.  rows
+        [total + requests] (int64) are the batch's rows that target_logits is made of: verify_drafts has one more than
+        drafts for every request.  A place without a request has one too, of no meaning, and so are the token that is
+        drawn there and the rows behind the last: offsets count drafts alone and are not the plan's."""
+        ends = self.offsets[1:]
+        drafts = torch.minimum(drafts, ends - self.offsets[:-1] - 1).clamp(min=0)
+        offsets = torch.zeros_like(self.offsets)
+        torch.cumsum(drafts, 0, dtype=torch.int32, out=offsets[1:])
+        first = offsets[:-1] + torch.arange(drafts.shape[0], dtype=torch.int32, device=offsets.device)
+        at = torch.arange(total + drafts.shape[0], dtype=torch.int32, device=offsets.device)
+        b = torch.searchsorted(first, at, right=True) - 1
+        rows = (ends - 1 - drafts - first)[b] + at
+        return rows.clamp(min=0, max=max(self.slots.shape[0] - 1, 0)).long(), offsets
 
     def keep(self, tokens):
         """The first tokens[b] (device, or one number for all) of request b's planned ones stay: no more than were

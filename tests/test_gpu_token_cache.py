@@ -1,5 +1,6 @@
 """TokenCache (GPU) where a batch does not go as planned: places without a
-request, steps that do not fit into the pages, the table or the rows."""
+request, steps that do not fit into the pages, the table or the rows, and a
+whole step of requests that come and go, as the documentation shows it."""
 import pytest
 import torch
 
@@ -132,3 +133,112 @@ def test_rows_that_are_left_out_shift_nobody(most):
     binding.lik_check_device_error()
     want = ref.attention(q.cpu(), kc.cpu(), vc.cpu(), ks.cpu(), vs.cpu(), table.cpu(), [0, 5, 12, 12], [45, 16, 3], dim ** -0.5)
     one.assert_attention(got, want)
+
+
+# ------------------------------------------------- requests that come and go --
+
+def test_rows_of_the_logits():
+    """Which rows of a step a verification wants: the newest token's and the drafts' of a request that decodes, the last
+    of a prompt; a place without a request has a row of no meaning."""
+    cache = _cache(pages=40, requests=5, max_tokens=64)
+    cache.plan(_dev([3, 0, 20, 1, 0]), 30)
+    rows, offsets = cache.verify_rows(_dev([2, 0, 0, 0, 0]), 4)
+    assert rows.dtype == torch.int64 and offsets.dtype == torch.int32
+    assert offsets.tolist() == [0, 2, 2, 2, 2, 2] and rows.shape == (9,)
+    got = rows.tolist()
+    assert got[:3] == [0, 1, 2] and got[4:6] == [22, 23]
+    assert all(0 <= r < 30 for r in got)
+    # more drafts than a request planned: what it planned but for its newest token
+    rows, offsets = cache.verify_rows(_dev([9, 4, 2, 1, -1]), 6)
+    assert offsets.tolist() == [0, 2, 2, 4, 4, 4] and rows.tolist()[:3] == [0, 1, 2] and rows.tolist()[4:8] == [20 + 0, 21, 22, 23]
+
+
+@pytest.mark.parametrize("captured", [False, True])
+def test_requests_come_and_go(captured):
+    """The documented step over places of which some are empty: each request's rows, tokens and cache are those that it
+    would have alone."""
+    gen = one._gen(4)
+    model = steps.Model(gen, heads=2, group=2, dim=32, cols=97)
+    places, rows, total = 3, 24, 9
+    cache = TokenCache(1, 2, 32, pages=30, requests=places, max_tokens=96, page_size=16)
+    i32 = dict(dtype=torch.int32, device="cuda")
+    b = dict(tokens=torch.zeros(rows, **i32), added=torch.zeros(places, **i32), drafts=torch.zeros(places, **i32),
+             drafted=torch.zeros(total, **i32), uniform=torch.zeros(total, device="cuda"),
+             noise=torch.ones(places, 97, device="cuda"))
+
+    def step():
+        q, k, v = model.qkv(b["tokens"])
+        cache.plan(b["added"], rows)
+        cache.write(0, k, v)
+        x = cache.attention(0, q, max_added=4, out=torch.zeros_like(q))
+        logits = model.logits(x)
+        at, offsets = cache.verify_rows(b["drafts"], total)
+        got = serving.verify_drafts(logits[at], b["drafted"], offsets, b["uniform"], b["noise"])
+        cache.keep(b["added"] - b["drafts"] + got[1])
+        return q, k, v, x, logits, got
+
+    if captured:
+        step()  # nobody is there yet
+        assert cache.cached.tolist() == [0, 0, 0] and cache.held.tolist() == [0, 0, 0]
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            held = step()
+    place, alone, prompt, newest = [None] * places, {}, {}, {}
+    # what happens before each step: a request's name in its place, "-" where one ends
+    for event in ({0: "a"}, {2: "b"}, {}, {0: "-"}, {1: "c"}, {2: "-", 0: "d"}, {}, {1: "-"}, {}):
+        for p, name in event.items():
+            if name == "-":
+                cache.release(p)
+                place[p] = None
+                continue
+            place[p] = name
+            prompt[name] = torch.randint(0, 97, (int(torch.randint(1, 9, (1,), generator=gen)),), generator=gen).tolist()
+            alone[name] = TokenCache(1, 2, 32, pages=6, requests=1, max_tokens=96, page_size=16)
+        packed, added, drafts, drafted = [], [], [], []
+        for name in place:
+            d = []
+            if name in newest:  # the newest token and what a draft model adds to it
+                d = torch.randint(0, 97, (int(torch.randint(0, 4, (1,), generator=gen)),), generator=gen).tolist()
+            new = [] if name is None else [newest[name]] + d if name in newest else prompt[name]
+            packed, drafted = packed + new, drafted + d
+            added.append(len(new))
+            drafts.append(len(d))
+        uniform = torch.rand(total, generator=gen) * 0.05
+        noise = torch.empty(places, 97).exponential_(generator=gen)
+        for key, value in (("tokens", packed + [5] * (rows - len(packed))), ("added", added), ("drafts", drafts),
+                           ("drafted", drafted + [3] * (total - len(drafted)))):
+            b[key].copy_(torch.tensor(value, dtype=torch.int32))
+        b["uniform"].copy_(uniform)
+        b["noise"].copy_(noise)
+        if captured:
+            graph.replay()
+            q, k, v, x, logits, (tokens, accepted, logp) = held
+        else:
+            q, k, v, x, logits, (tokens, accepted, logp) = step()
+        assert int(cache.missing) == 0
+        first = cut = 0
+        for p, name in enumerate(place):
+            if name is None:
+                assert int(cache.cached[p]) == 0 and int(cache.held[p]) == 0
+                continue
+            own, end, d = alone[name], first + added[p], drafts[p]
+            own.plan(_dev([added[p]]), added[p])
+            own.write(0, k[first:end], v[first:end])
+            y = own.attention(0, q[first:end], max_added=4)
+            # either is off by half a step of bf16 and 2^-11 of the values' sizes
+            size = float(own.v_scale.max()) * 448
+            assert float((y.float() - x[first:end].float()).abs().max()) <= 2 * (2.0 ** -8 + 2.0 ** -11 + 2.0 ** -14) * size
+            want = ref.verify(logits[end - d - 1:end].cpu(), None, torch.tensor(drafted[cut:cut + d]), [0, d],
+                              uniform[cut:cut + d], noise[p:p + 1], 1.0)
+            assert tokens[cut + p:cut + p + d + 1].tolist() == want[0] and int(accepted[p]) == want[1][0]
+            own.keep(added[p] - d + want[1][0])
+            n = int(own.cached)
+            assert int(cache.cached[p]) == n and int(cache.held[p]) == int(own.held)
+            here, there = ([c.block_table[r][:int(c.held[r])].long() for c, r in ((cache, p), (own, 0))])
+            assert torch.equal(cache.k_scale[0][here], own.k_scale[0][there])
+            for codes, same in ((cache.k, own.k), (cache.v, own.v)):
+                a, c = (t.view(torch.uint8)[0][at].transpose(1, 2).flatten(0, 1)[:n] for t, at in ((codes, here), (same, there)))
+                assert torch.equal(a, c)
+            newest[name] = want[0][want[1][0]]
+            first, cut = end, cut + d
+    binding.lik_check_device_error()
