@@ -1,6 +1,8 @@
 """TokenCache (GPU) where a batch does not go as planned: places without a
 request, steps that do not fit into the pages, the table or the rows, and a
 whole step of requests that come and go, as the documentation shows it."""
+import os
+
 import pytest
 import torch
 
@@ -242,3 +244,39 @@ def test_requests_come_and_go(captured):
             newest[name] = want[0][want[1][0]]
             first, cut = end, cut + d
     binding.lik_check_device_error()
+
+
+# ---------------------------------------------------------- as it is documented --
+
+def test_the_documented_step():
+    """README's step, as it stands there, on a small model: a request with drafts, an empty place, a prompt."""
+    with open(os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "README.md")) as f:
+        text = f.read()
+    code = text[text.index("**A serving step.**"):]
+    code = code[code.index("```python\n") + 10:]
+    gen = one._gen(6)
+    model = [steps.Model(gen, heads=2, group=2, dim=128, cols=83) for _ in range(2)]
+    caches = []
+
+    class Layer:
+        def __init__(self, weights):
+            self.project, self.finish = weights.qkv, lambda out: weights.logits(out).argmax(1)
+
+    def small(**sizes):
+        caches.append(TokenCache(**dict(sizes, layers=2, heads=2, pages=12, requests=3, max_tokens=64)))
+        return caches[0]
+
+    added, drafts, drafted = [3, 0, 6], [2, 0, 0], [7, 11]
+    target, draft = one._logits(gen, 12, 83, "f32"), one._logits(gen, 2, 83, "f32")
+    uniform, noise = torch.full((2,), 1e-6), torch.empty(3, 83).exponential_(generator=gen)
+    seen = []
+    names = dict(TokenCache=small, verify_drafts=serving.verify_drafts, model=[Layer(m) for m in model], rows=12, total=2,
+                 x=torch.randint(0, 83, (12,), generator=gen).cuda(), added=_dev(added), drafts=_dev(drafts),
+                 drafted=_dev(drafted), uniform=uniform.cuda(), noise=noise.cuda(), draft_logits=draft.cuda(),
+                 head=lambda x: seen.append(x) or target.cuda()[:5])
+    exec(code[:code.index("```")], names)
+    # verify_drafts has 2 + 1 rows of the first request, one of the empty place, one of the prompt
+    assert seen[0].shape == (5,) and torch.equal(seen[0][[0, 1, 2, 4]], names["x"][[0, 1, 2, 8]])
+    want = ref.verify(target[:5], draft, torch.tensor(drafted), [0, 2, 2, 2], uniform, noise, 1.0)
+    assert names["tokens"].tolist() == want[0] and names["accepted"].tolist() == want[1]
+    assert caches[0].cached.tolist() == [1 + want[1][0], 0, 6] and int(caches[0].missing) == 0
