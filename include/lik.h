@@ -663,7 +663,8 @@ lik_status lik_cache_write(const void* k, const void* v, lik_dtype dtype, int64_
  * Results do not depend on the run.  A scale of a seen page that is not finite makes its tokens'
  * scores (k_scale) or the row's output (v_scale) not finite.
  *   q, out [rows, q_heads, dim], fp16 or bf16, element (t, h, d) at t *
- *   token_stride + h * head_stride + d; lse [rows, q_heads] fp32 or NULL;
+ *   token_stride + h * head_stride + d, those of out without overlaps; lse
+ *   [rows, q_heads] fp32 or NULL;
  *   block_table [requests, table_cols] int32, row b at b * table_stride;
  *   1e-30 <= scale <= 1e30; q_heads is 1 to 128 times heads (at most 1024),
  *   rows * q_heads <= 2^30.  Negative lengths count as 0, offsets are

@@ -59,6 +59,17 @@ lik_status check_strides(int64_t rows, int64_t heads, int64_t token, int64_t hea
     return LIK_OK;
 }
 
+// An output whose rows of dim elements do not overlap: heads inside tokens or tokens inside heads, whichever are
+// further apart (a single one may have any stride).
+lik_status check_spread(int64_t rows, int64_t heads, int64_t dim, int64_t token, int64_t head, const char* name) {
+    const bool one_row = rows <= 1, one_head = heads <= 1;
+    const bool inside = (one_head || head >= dim) && (one_row || token >= (one_head ? 0 : (heads - 1) * head) + dim);
+    const bool across = (one_row || token >= dim) && (one_head || head >= (one_row ? 0 : (rows - 1) * token) + dim);
+    if (inside || across) return LIK_OK;
+    return fail(LIK_ERR_INVALID_ARG, "%s has rows that overlap (strides %lld and %lld)", name, static_cast<ll>(token),
+                static_cast<ll>(head));
+}
+
 int64_t span(int64_t rows, int64_t token, int64_t heads, int64_t head, int64_t dim) {
     return rows > 0 && heads > 0 ? (rows - 1) * token + (heads - 1) * head + dim : 0;
 }
@@ -287,6 +298,7 @@ extern "C" lik_status lik_cache_attention(const void* q, lik_dtype dtype, int64_
     if (st == LIK_OK) st = check_table(requests, table_cols, table_stride);
     if (st == LIK_OK) st = check_strides(rows, q_heads, q_token_stride, q_head_stride, "q");
     if (st == LIK_OK) st = check_strides(rows, q_heads, out_token_stride, out_head_stride, "out");
+    if (st == LIK_OK) st = check_spread(rows, q_heads, dim, out_token_stride, out_head_stride, "out");
     if (st == LIK_OK) st = check_scale(scale);
     if (st != LIK_OK) return st;
     int dev = 0;
