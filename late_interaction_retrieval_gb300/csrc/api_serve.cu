@@ -62,6 +62,7 @@ lik_status check_strides(int64_t rows, int64_t heads, int64_t token, int64_t hea
 // An output whose rows of dim elements do not overlap: heads inside tokens or tokens inside heads, whichever are
 // further apart (a single one may have any stride).
 lik_status check_spread(int64_t rows, int64_t heads, int64_t dim, int64_t token, int64_t head, const char* name) {
+    if (rows == 0) return LIK_OK;
     const bool one_row = rows <= 1, one_head = heads <= 1;
     const bool inside = (one_head || head >= dim) && (one_row || token >= (one_head ? 0 : (heads - 1) * head) + dim);
     const bool across = (one_row || token >= dim) && (one_head || head >= (one_row ? 0 : (rows - 1) * token) + dim);
