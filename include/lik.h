@@ -667,8 +667,8 @@ lik_status lik_cache_write(const void* k, const void* v, lik_dtype dtype, int64_
  *   [rows, q_heads] fp32 or NULL;
  *   block_table [requests, table_cols] int32, row b at b * table_stride;
  *   1e-30 <= scale <= 1e30; q_heads is 1 to 128 times heads (at most 1024),
- *   rows * q_heads <= 2^30.  Negative lengths count as 0, offsets are
- *   clamped to [0, rows].
+ *   rows * q_heads <= 2^30; table_cols * page_size <= 2^31 - 4096.  Negative
+ *   lengths count as 0, offsets are clamped to [0, rows].
  *   max_added: the most tokens that a request adds, as the host knows it: it
  *   chooses the kernel.  A wrong value costs time, not results.
  *   workspace: 16-byte aligned, of lik_cache_attention_workspace_bytes bytes

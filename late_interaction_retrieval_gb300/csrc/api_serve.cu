@@ -133,8 +133,9 @@ lik_status check_attention(int64_t rows, int64_t q_heads, int64_t heads, int64_t
     if (rows > INT32_MAX || rows * q_heads > (int64_t(1) << 30))
         return fail(LIK_ERR_UNSUPPORTED, "rows * q_heads > 2^30");
     if (table_cols < 0 || max_added < 0) return fail(LIK_ERR_INVALID_ARG, "negative size");
-    if (table_cols * page_size > INT32_MAX)
-        return fail(LIK_ERR_UNSUPPORTED, "a table row of more than 2^31 - 1 tokens");
+    // positions are counted in 32 bits, and looked up to 16 tiles of 64 tokens ahead
+    if (table_cols * page_size > INT32_MAX - 4095)
+        return fail(LIK_ERR_UNSUPPORTED, "a table row of more than 2^31 - 4096 tokens");
     return LIK_OK;
 }
 

@@ -37,3 +37,12 @@ def test_layouts_that_do_not_overlap(lib, changed):
     """Rows or heads first, gaps, a single row or head, and inputs that repeat: no refusal of the layout."""
     attention(lib, **changed)
     assert b"overlap" not in lib.lik_last_error_message()
+
+
+@pytest.mark.parametrize("cols,page,status", [(2 ** 27 - 1, 16, 2), (2 ** 23 - 1, 256, 2), (2 ** 27 - 255, 16, 2)])
+def test_tables_whose_positions_pass_31_bits(lib, cols, page, status):
+    """Positions are counted in 32 bits, a tile or a few ahead of the last."""
+    assert attention(lib, cols=cols, stride=cols, page_size=page) == status
+    assert lib.lik_last_error_message()
+    size = binding.ctypes.c_size_t(7)
+    assert lib.lik_cache_attention_workspace_bytes(3, 4, 2, 32, 2, page, cols, 2, binding.ctypes.byref(size)) == status
