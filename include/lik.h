@@ -606,9 +606,8 @@ lik_status lik_preference_loss_step(const void* logits, lik_dtype dtype, int64_t
  *   [requests, table_cols], row b at element b * table_stride, updated in
  *   place; all int32, device.  slots [slot_capacity] int64; tokens behind
  *   slot_capacity are left out: offsets end there, lengths and pages count
- *   them.  Before the rows that are there go on to lik_cache_attention, which
- *   takes them for their requests' last tokens, lengths[b] has to become
- *   max(cached[b], 0) + offsets[b + 1] - offsets[b].
+ *   them (lik_cache_attention takes a request's rows for its last tokens: give
+ *   it the lengths of lik_cache_slots_fit where that can happen).
  *   Negative lengths count as 0; held is clamped to [0, table_cols],
  *   free_count to [0, free_capacity].
  */
@@ -617,6 +616,24 @@ lik_status lik_cache_slots(const int32_t* cached, const int32_t* added, const in
                            const int32_t* free_count, int32_t* block_table, int64_t table_cols, int64_t table_stride,
                            int32_t* held_out, int32_t* lengths, int32_t* offsets, int64_t* slots,
                            int64_t slot_capacity, int32_t* free_left, cudaStream_t stream);
+
+/*
+ * The same for a batch that may not fit, and what becomes of it:
+ *     lengths[b]  counts the new tokens that have a row alone
+ *     missing [1] 0 if every new token has its row and its page; else the pages
+ *                 that were not free, or those that the tokens without a place
+ *                 would fill, whichever is more (behind the table's columns, or
+ *                 without a row)
+ *     most[b]     what request b may have in the cache after the step: lengths[b]
+ *                 if missing is 0, else what it had
+ *   most [requests], missing [1] int32, device.
+ */
+lik_status lik_cache_slots_fit(const int32_t* cached, const int32_t* added, const int32_t* held, int64_t requests,
+                               int64_t page_size, const int32_t* free_pages, int64_t free_capacity,
+                               const int32_t* free_count, int32_t* block_table, int64_t table_cols,
+                               int64_t table_stride, int32_t* held_out, int32_t* lengths, int32_t* offsets,
+                               int64_t* slots, int64_t slot_capacity, int32_t* free_left, int32_t* most,
+                               int32_t* missing, cudaStream_t stream);
 
 /*
  * New keys and values into the cache.  Rows t, t + 1, ... whose slots follow

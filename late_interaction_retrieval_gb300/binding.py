@@ -63,6 +63,8 @@ SIGNATURES = {
     "lik_preference_loss_step": (_I32, _LOGITS + [_P, _P, _I64, _P, _P] + [_F] * 3 + [_I32, _F] + [_P] * 5
                                  + [_I64, _P]),
     "lik_cache_slots": (_I32, [_P] * 3 + [_I64] * 2 + [_P, _I64, _P, _P] + [_I64] * 2 + [_P] * 4 + [_I64, _P, _P]),
+    "lik_cache_slots_fit": (_I32, [_P] * 3 + [_I64] * 2 + [_P, _I64, _P, _P] + [_I64] * 2 + [_P] * 4 + [_I64]
+                            + [_P] * 4),
     "lik_cache_write": (_I32, [_P, _P, _I32] + [_I64] * 7 + [_P] * 5 + [_I64] * 2 + [_P]),
     "lik_cache_attention_workspace_bytes": (_I32, [_I64] * 8 + [_P]),
     "lik_cache_attention": (_I32, [_P, _I32] + [_I64] * 5 + [_P] * 4 + [_I64] * 3 + [_P] + [_I64] * 2 + [_P] * 2
@@ -710,25 +712,41 @@ def _pool(k_cache, v_cache, k_scale, v_scale, heads, dim, dev):
             _vector(v_scale, "v_scale", (pages, h), f32, dev)), pages, h, page
 
 
-def lik_cache_slots(cached, added, held, free_pages, free_count, block_table, held_out, lengths, offsets, slots,
-                    free_left, page_size, stream=None):
-    """Block tables (new entries, in place) and slot maps of a batch from its
-    requests' lengths: request b holds held[b] pages with cached[b] tokens and
-    gets added[b] more.  Pages come from the end of free_pages[:free_count].
-    lengths count tokens behind the last slot too (serving.cache_slots does not)."""
+def _cache_slots(name, cached, added, held, free_pages, free_count, block_table, held_out, lengths, offsets, slots,
+                 free_left, page_size, stream, *fit):
     if cached.dim() != 1 or free_pages.dim() != 1 or slots.dim() != 1:
         raise ValueError("cached, free_pages and slots must have one dimension")
     if not cached.is_cuda:
         raise ValueError("cached must be a CUDA tensor")
     dev, i32, n = cached.device, torch.int32, cached.shape[0]
     table, _, cols, stride = _table(block_table, dev, n)
-    _call("lik_cache_slots", _vector(cached, "cached", (n,), i32, dev), _vector(added, "added", (n,), i32, dev),
+    fit = [_vector(t, what, (size,), i32, dev) for t, what, size in zip(fit, ("most", "missing"), (n, 1))]
+    _call(name, _vector(cached, "cached", (n,), i32, dev), _vector(added, "added", (n,), i32, dev),
           _vector(held, "held", (n,), i32, dev), n, page_size,
           _vector(free_pages, "free_pages", free_pages.shape, i32, dev), free_pages.shape[0],
           _vector(free_count, "free_count", (1,), i32, dev), table, cols, stride,
           _vector(held_out, "held_out", (n,), i32, dev), _vector(lengths, "lengths", (n,), i32, dev),
           _vector(offsets, "offsets", (n + 1,), i32, dev), _vector(slots, "slots", slots.shape, torch.int64, dev),
-          slots.shape[0], _vector(free_left, "free_left", (1,), i32, dev), _stream(dev, stream))
+          slots.shape[0], _vector(free_left, "free_left", (1,), i32, dev), *fit, _stream(dev, stream))
+
+
+def lik_cache_slots(cached, added, held, free_pages, free_count, block_table, held_out, lengths, offsets, slots,
+                    free_left, page_size, stream=None):
+    """Block tables (new entries, in place) and slot maps of a batch from its
+    requests' lengths: request b holds held[b] pages with cached[b] tokens and
+    gets added[b] more.  Pages come from the end of free_pages[:free_count].
+    lengths count tokens behind the last slot too."""
+    _cache_slots("lik_cache_slots", cached, added, held, free_pages, free_count, block_table, held_out, lengths, offsets,
+                 slots, free_left, page_size, stream)
+
+
+def lik_cache_slots_fit(cached, added, held, free_pages, free_count, block_table, held_out, lengths, offsets, slots,
+                        free_left, most, missing, page_size, stream=None):
+    """The same where the batch may not fit: lengths count the tokens that have
+    a row; missing [1] is 0 if all have their place; most [requests] is what a
+    request may have after the step."""
+    _cache_slots("lik_cache_slots_fit", cached, added, held, free_pages, free_count, block_table, held_out, lengths,
+                 offsets, slots, free_left, page_size, stream, most, missing)
 
 
 def lik_cache_write(k, v, slots, k_cache, v_cache, k_scale, v_scale, stream=None):

@@ -144,12 +144,13 @@ lik_status check_attention(int64_t rows, int64_t q_heads, int64_t heads, int64_t
 
 using namespace lik;
 
-extern "C" lik_status lik_cache_slots(const int32_t* cached, const int32_t* added, const int32_t* held,
-                                      int64_t requests, int64_t page_size, const int32_t* free_pages,
-                                      int64_t free_capacity, const int32_t* free_count, int32_t* block_table,
-                                      int64_t table_cols, int64_t table_stride, int32_t* held_out, int32_t* lengths,
-                                      int32_t* offsets, int64_t* slots, int64_t slot_capacity, int32_t* free_left,
-                                      cudaStream_t stream) {
+// fit: whether most and missing are wanted too
+static lik_status cache_slots(const int32_t* cached, const int32_t* added, const int32_t* held, int64_t requests,
+                              int64_t page_size, const int32_t* free_pages, int64_t free_capacity,
+                              const int32_t* free_count, int32_t* block_table, int64_t table_cols,
+                              int64_t table_stride, int32_t* held_out, int32_t* lengths, int32_t* offsets,
+                              int64_t* slots, int64_t slot_capacity, int32_t* free_left, bool fit, int32_t* most,
+                              int32_t* missing, cudaStream_t stream) {
     clear_message();
     SlotsArgs a{};
     lik_status st = check_page_size(page_size, &a.page_shift);
@@ -174,8 +175,10 @@ extern "C" lik_status lik_cache_slots(const int32_t* cached, const int32_t* adde
         {"offsets", offsets, true, B + 1},
         {"free_left", free_left, true, 1},
         {"slots", slots, true, slot_capacity},
+        {"most", most, fit, B},
+        {"missing", missing, fit, 1},
     };
-    if ((st = check_buffers(dev, specs, 11)) != LIK_OK) return st;
+    if ((st = check_buffers(dev, specs, fit ? 13 : 11)) != LIK_OK) return st;
     for (const Spec& s : specs)
         if ((st = check_aligned(s.ptr, s.ptr == slots ? 8 : 4, s.name)) != LIK_OK) return st;
     const Bytes ins[] = {{"cached", cached, 4 * B},         {"added", added, 4 * B},
@@ -183,8 +186,9 @@ extern "C" lik_status lik_cache_slots(const int32_t* cached, const int32_t* adde
                          {"free_count", free_count, 4}};
     const Bytes outs[] = {{"block_table", block_table, 4 * specs[5].elems}, {"held_out", held_out, 4 * B},
                           {"lengths", lengths, 4 * B},                      {"offsets", offsets, 4 * (B + 1)},
-                          {"slots", slots, 8 * slot_capacity},              {"free_left", free_left, 4}};
-    if ((st = check_apart(outs, 6, ins, 5)) != LIK_OK) return st;
+                          {"slots", slots, 8 * slot_capacity},              {"free_left", free_left, 4},
+                          {"most", most, 4 * B},                            {"missing", missing, 4}};
+    if ((st = check_apart(outs, 8, ins, 5)) != LIK_OK) return st;
     a.cached = cached;
     a.added = added;
     a.held = held;
@@ -201,8 +205,32 @@ extern "C" lik_status lik_cache_slots(const int32_t* cached, const int32_t* adde
     a.slots = slots;
     a.capacity = slot_capacity;
     a.free_left = free_left;
+    a.most = most;
+    a.missing = missing;
     const cudaError_t e = launch_cache_slots(a, stream);
     return e == cudaSuccess ? LIK_OK : cuda_fail(e, "slot map launch");
+}
+
+extern "C" lik_status lik_cache_slots(const int32_t* cached, const int32_t* added, const int32_t* held,
+                                      int64_t requests, int64_t page_size, const int32_t* free_pages,
+                                      int64_t free_capacity, const int32_t* free_count, int32_t* block_table,
+                                      int64_t table_cols, int64_t table_stride, int32_t* held_out, int32_t* lengths,
+                                      int32_t* offsets, int64_t* slots, int64_t slot_capacity, int32_t* free_left,
+                                      cudaStream_t stream) {
+    return cache_slots(cached, added, held, requests, page_size, free_pages, free_capacity, free_count, block_table,
+                       table_cols, table_stride, held_out, lengths, offsets, slots, slot_capacity, free_left, false,
+                       nullptr, nullptr, stream);
+}
+
+extern "C" lik_status lik_cache_slots_fit(const int32_t* cached, const int32_t* added, const int32_t* held,
+                                          int64_t requests, int64_t page_size, const int32_t* free_pages,
+                                          int64_t free_capacity, const int32_t* free_count, int32_t* block_table,
+                                          int64_t table_cols, int64_t table_stride, int32_t* held_out,
+                                          int32_t* lengths, int32_t* offsets, int64_t* slots, int64_t slot_capacity,
+                                          int32_t* free_left, int32_t* most, int32_t* missing, cudaStream_t stream) {
+    return cache_slots(cached, added, held, requests, page_size, free_pages, free_capacity, free_count, block_table,
+                       table_cols, table_stride, held_out, lengths, offsets, slots, slot_capacity, free_left, true,
+                       most, missing, stream);
 }
 
 extern "C" lik_status lik_cache_write(const void* k, const void* v, lik_dtype dtype, int64_t rows, int64_t heads,

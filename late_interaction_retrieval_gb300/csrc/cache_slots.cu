@@ -99,6 +99,7 @@ __global__ void __launch_bounds__(kThreads) cache_slots_kernel(const SlotsArgs a
     int64_t count = *a.free_count;
     count = count < 0 ? 0 : (count < a.free_capacity ? count : a.free_capacity);
     const bool first = blockIdx.x == 0;
+    int64_t lost = 0;  // new tokens without a row or a page
     for (int b = b0; b < b1; ++b) {
         const Request r = request_of(a, b);
         tokens[b] = clamp_top(it);
@@ -109,8 +110,17 @@ __global__ void __launch_bounds__(kThreads) cache_slots_kernel(const SlotsArgs a
             const int64_t left = count - ip;
             const int64_t got = left <= 0 ? 0 : (r.need < left ? r.need : left);
             a.held_out[b] = static_cast<int>(r.held + got);
-            a.lengths[b] = clamp_top(r.cached + r.added);
-            a.offsets[b] = clamp_top(it < a.capacity ? it : a.capacity);
+            const int64_t row0 = it < a.capacity ? it : a.capacity;
+            a.offsets[b] = clamp_top(row0);
+            int64_t kept = r.added;
+            if (a.missing) {
+                const int64_t row1 = it + r.added < a.capacity ? it + r.added : a.capacity;
+                kept = row1 - row0;
+                const int64_t room = ((r.held + got) << a.page_shift) - r.cached;
+                const int64_t placed = kept < room ? kept : room;
+                lost += r.added - (placed > 0 ? placed : 0);
+            }
+            a.lengths[b] = clamp_top(r.cached + kept);
         }
         it += r.added;
         ip += r.need;
@@ -127,6 +137,19 @@ __global__ void __launch_bounds__(kThreads) cache_slots_kernel(const SlotsArgs a
         }
     }
     __syncthreads();
+    if (first && a.missing) {  // the block's sums of tokens are no longer needed
+#pragma unroll
+        for (int d = 16; d > 0; d >>= 1) lost += __shfl_xor_sync(0xffffffffu, lost, d);
+        if (lane == 0) warp_tokens[warp] = lost;
+        __syncthreads();
+        int64_t missing = all_pages - count, pages_lost = 0;
+#pragma unroll
+        for (int w = 0; w < kWarps; ++w) pages_lost += warp_tokens[w];
+        pages_lost = (pages_lost + (int64_t(1) << a.page_shift) - 1) >> a.page_shift;
+        missing = missing > pages_lost ? missing : pages_lost;
+        if (tid == 0) *a.missing = clamp_top(missing);
+        for (int b = b0; b < b1; ++b) a.most[b] = missing ? had[b] : a.lengths[b];  // its own writes
+    }
 
     const int64_t step = static_cast<int64_t>(gridDim.x) * kThreads;
     // slots; a token's page is one that its request held, or one of this call's,

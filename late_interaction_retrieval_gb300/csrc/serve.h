@@ -28,6 +28,7 @@ struct SlotsArgs {
     int64_t* slots;
     int64_t capacity;
     int32_t* free_left;
+    int32_t *most, *missing;  // whether the step fits: both, or neither
 };
 cudaError_t launch_cache_slots(const SlotsArgs& a, cudaStream_t stream);
 

@@ -36,16 +36,20 @@ def cache_slots(cached, added, held, free_pages, free_count, block_table, page_s
     zero says how many were missing.  slots [rows] (int64, -1: none) says where
     each row's token goes; lengths are the requests' tokens with the new ones
     that have a row: where `rows` are too few, the last tokens are left out."""
+    return _slots(cached, added, held, free_pages, free_count, block_table, page_size, rows,
+                  *torch.empty((2, cached.shape[0] + 1), dtype=torch.int32, device=cached.device))
+
+
+def _slots(cached, added, held, free_pages, free_count, block_table, page_size, rows, most, missing):
+    """cache_slots, with the buffers (at least as long) for whether the step fits."""
     def int32(n):
         return torch.empty(n, dtype=torch.int32, device=cached.device)
 
     n = cached.shape[0]
     held_out, lengths, offsets, left = int32(n), int32(n), int32(n + 1), int32(1)
     slots = torch.empty(rows, dtype=torch.int64, device=cached.device)
-    binding.lik_cache_slots(cached, added, held, free_pages, free_count, block_table, held_out, lengths, offsets, slots,
-                            left, page_size)
-    # the binding's lengths count tokens without a row too; attention takes a request's rows for its last tokens
-    lengths = torch.minimum(lengths, cached.clamp(min=0) + (offsets[1:] - offsets[:-1]))
+    binding.lik_cache_slots_fit(cached, added, held, free_pages, free_count, block_table, held_out, lengths, offsets,
+                                slots, left, most[:n], missing[:1], page_size)
     return held_out, lengths, offsets, slots, left
 
 
@@ -134,18 +138,16 @@ class TokenCache:
         # one entry behind the pages, where release() puts what is no page
         self._free = torch.arange(pages + 1, dtype=torch.int32, device=device)
         self.free_count, self.missing = full((1,), pages), full((1,), 0)
+        self._most = full((requests,), 0)  # what a request may have after the step that was planned last
         self.lengths = self.offsets = self.slots = None
 
     def plan(self, added, rows):
         """Places for added[b] (int32 [requests], device) new tokens of request b, at most `rows` together."""
-        held, self.lengths, self.offsets, self.slots, left = cache_slots(
+        held, self.lengths, self.offsets, self.slots, left = _slots(
             self.cached, added, self.held, self._free[:self.pages], self.free_count, self.block_table, self.page_size,
-            rows)
+            rows, self._most, self.missing)
         self.held.copy_(held)
         torch.clamp(left, min=0, out=self.free_count)
-        # tokens without a place, whatever they lacked; the pages that were not free are those of each request, rounded up
-        lost = added.clamp(min=0).sum() - (self.slots >= 0).sum()
-        self.missing.copy_(torch.maximum(left.neg(), (lost + self.page_size - 1) // self.page_size))
         return self.lengths, self.offsets, self.slots
 
     def write(self, layer, k, v):
@@ -176,9 +178,8 @@ class TokenCache:
         """The first tokens[b] (device, or one number for all) of request b's planned ones stay: no more than were
         planned, and none in a place without a request, which planned none.  Of a step that did not fit nothing does:
         `missing` says so, also behind a captured step, which can be run again once there is room."""
-        planned = self.offsets[1:] - self.offsets[:-1]
-        kept = torch.minimum(planned, tokens) if torch.is_tensor(tokens) else planned.clamp(max=tokens)
-        self.cached.add_(kept * (self.missing == 0))
+        self.cached.add_(tokens)
+        torch.minimum(self.cached, self._most, out=self.cached)
 
     def release(self, request):
         """Request number `request` has ended: its pages are free, its place is empty."""
@@ -191,3 +192,4 @@ class TokenCache:
         row.fill_(-1)
         self.held[request] = 0
         self.cached[request] = 0
+        self._most[request] = 0

@@ -137,6 +137,79 @@ def test_rows_that_are_left_out_shift_nobody(most):
     one.assert_attention(got, want)
 
 
+# ------------------------------------------------------------- whether a batch fits --
+
+def _fit(cached, added, held, free, count, table, page, capacity):
+    """lik_cache_slots_fit beside lik_cache_slots, which it has to equal in all but the lengths; most, missing, lengths."""
+    n = len(cached)
+    plain = one.run_slots(cached, added, held, free, count, table, page, capacity)
+    held_out, lengths, most = (torch.full((n,), -9, dtype=torch.int32, device="cuda") for _ in range(3))
+    offsets, left, missing = (torch.full((k,), -9, dtype=torch.int32, device="cuda") for k in (n + 1, 1, 1))
+    slots, own = torch.full((capacity,), -9, dtype=torch.int64, device="cuda"), table.cuda()
+    binding.lik_cache_slots_fit(_dev(cached), _dev(added), _dev(held), _dev(free), _dev([count]), own, held_out, lengths,
+                                offsets, slots, left, most, missing, page_size=page)
+    assert torch.equal(own.cpu(), plain[0]) and held_out.tolist() == plain[1] and offsets.tolist() == plain[3]
+    assert slots.tolist() == plain[4] and int(left) == plain[5]
+    # by the definition: a token has its place if it has a slot, as long as no page that is held is missing in the table
+    has = [max(c, 0) for c in cached]
+    want = [min(c + b - a, 2 ** 31 - 1) for c, a, b in zip(has, plain[3], plain[3][1:])]
+    lost = sum(max(a, 0) for a in added) - sum(s >= 0 for s in plain[4])
+    short = max(-plain[5], -(-lost // page))
+    assert lengths.tolist() == want and int(missing) == min(short, 2 ** 31 - 1)
+    assert most.tolist() == (has if short else want)
+    return short
+
+
+@pytest.mark.parametrize("n,page", [(1, 16), (7, 64), (33, 32), (513, 16), (1500, 128), (8192, 16)])
+def test_whether_a_batch_fits(n, page):
+    """Batches that fit, and the same ones with fewer pages, columns or rows."""
+    gen = one._gen(n)
+    cols = -(-(90 + 40) // page) + 1
+    cached, added, held, free, table = one._batch(gen, n, 90, 40, page, cols, extra=0.3)
+    rows = sum(added)
+    assert _fit(cached, added, held, free, len(free), table, page, rows + 5) == 0
+    assert _fit(cached, added, held, free, len(free), table, page, rows) == 0
+    assert _fit(cached, added, held, free, 2, table, page, rows + 5) == max(0, sum(
+        max(0, -(-(c + a) // page) - h) for c, a, h in zip(cached, added, held)) - 2)
+    _fit(cached, added, held, free, len(free), table, page, max(rows - 7, 0))
+    _fit(cached, added, held, free, len(free), table, page, rows // 3)
+    few = max(1, cols // 2)
+    _fit(cached, added, [min(h, few) for h in held], free, len(free), table[:, :few].contiguous(), page, rows + 3)
+
+
+def test_whether_odd_batches_fit():
+    """No request, no row, no page, no column; negative numbers; lengths next to 2^31."""
+    assert _fit([], [], [], [3, 4], 2, torch.zeros((0, 4), dtype=torch.int32), 16, 5) == 0
+    table = torch.arange(20, dtype=torch.int32).reshape(4, 5)
+    assert _fit([3, 0, 0, 9], [0, 0, 0, 0], [1, 0, 0, 1], [50], 1, table, 16, 0) == 0
+    assert _fit([3, 0, 0, 9], [1, 0, 0, 0], [1, 0, 0, 1], [50], 1, table, 16, 0) == 1
+    assert _fit([0, 0], [3, 20], [0, 0], [], 0, table[:2], 16, 30) == 3
+    assert _fit([0, 0], [3, 20], [0, 0], [5], 1, torch.zeros((2, 0), dtype=torch.int32), 16, 30) == 2
+    assert _fit([-5, 40, 70, 3], [10, 30, 40, -2], [0, 5, 9, -1], [90, 91, 92], 7, table, 16, 200) == 2
+    _fit([2 ** 31 - 1, 4], [2 ** 31 - 1, 2 ** 31 - 1], [0, 0], [1], 1, table[:2].clone(), 256, 300)
+
+
+def test_fit_refusals():
+    i = _dev([1, 2])
+    one_, table, slots = _dev([1]), torch.zeros((2, 4), dtype=torch.int32, device="cuda"), torch.zeros(4, dtype=torch.int64,
+                                                                                                  device="cuda")
+
+    def call(most=None, missing=None, page=16):
+        binding.lik_cache_slots_fit(i, i, i, i, one_, table, i.clone(), i.clone(), _dev([0, 0, 0]), slots, one_.clone(),
+                                    i.clone() if most is None else most, one_.clone() if missing is None else missing,
+                                    page_size=page)
+
+    call()
+    both = i.clone()
+    for bad in (dict(page=24), dict(most=i), dict(missing=one_), dict(most=both, missing=both[1:]),
+                dict(most=table.view(-1)[2:4])):
+        with pytest.raises(binding.LIKError):
+            call(**bad)
+    for bad in (dict(most=i.long()), dict(most=_dev([1])), dict(missing=i), dict(missing=one_.cpu())):
+        with pytest.raises(ValueError):
+            call(**bad)
+
+
 # ------------------------------------------------- requests that come and go --
 
 def test_rows_of_the_logits():
