@@ -36,12 +36,12 @@ def cache_slots(cached, added, held, free_pages, free_count, block_table, page_s
     zero says how many were missing.  slots [rows] (int64, -1: none) says where
     each row's token goes; lengths are the requests' tokens with the new ones
     that have a row: where `rows` are too few, the last tokens are left out."""
-    return _slots(cached, added, held, free_pages, free_count, block_table, page_size, rows,
-                  *torch.empty((2, cached.shape[0] + 1), dtype=torch.int32, device=cached.device))
+    most, missing = (torch.empty(n, dtype=torch.int32, device=cached.device) for n in (cached.shape[0], 1))
+    return _slots(cached, added, held, free_pages, free_count, block_table, page_size, rows, most, missing)
 
 
 def _slots(cached, added, held, free_pages, free_count, block_table, page_size, rows, most, missing):
-    """cache_slots, with the buffers (at least as long) for whether the step fits."""
+    """cache_slots, with the buffers for what the requests may have after the step and for what is missing."""
     def int32(n):
         return torch.empty(n, dtype=torch.int32, device=cached.device)
 
@@ -49,7 +49,7 @@ def _slots(cached, added, held, free_pages, free_count, block_table, page_size, 
     held_out, lengths, offsets, left = int32(n), int32(n), int32(n + 1), int32(1)
     slots = torch.empty(rows, dtype=torch.int64, device=cached.device)
     binding.lik_cache_slots_fit(cached, added, held, free_pages, free_count, block_table, held_out, lengths, offsets,
-                                slots, left, most[:n], missing[:1], page_size)
+                                slots, left, most, missing, page_size)
     return held_out, lengths, offsets, slots, left
 
 
