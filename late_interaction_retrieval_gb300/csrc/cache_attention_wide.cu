@@ -809,8 +809,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             // O times `keep` (1 in rows that need none) in step st > 0.  It is at rest once the step before is in it:
             // this step's product waits for its weights.  The next step's scores are issued behind the product of the
             // step before, and their commit covers it; they wait for nothing of this step.  An item's last step has none
-            // behind it: its barrier is waited for in every item, before the weights are handed over.  So either barrier
-            // is waited for in each of its phases, and is at most one ahead.
+            // behind it: its barrier is waited for in every item, at the latest at its end.  So either barrier is waited
+            // for in each of its phases, and is at most one ahead.
             auto rescale = [&](bool last, float keep) {
                 const int next = count + 1;
                 const uint32_t bar = smem_u32(last ? &sm.o_most[s] : &sm.s_full[s][next & 1]);
@@ -1001,11 +1001,6 @@ __global__ void __launch_bounds__(kThreads, 1)
                         for (int k = 0; k < 4; ++k) l = fmaf(sum[k], exp2_fast(-lw[k]), l);
                     }
                 }
-                if (st > 0 && st + 1 == steps) {
-                    ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.o_most[s]), most_phase, err));
-                    if (!ok) break;
-                    most_phase ^= 1;
-                }
                 ptx::tmem_wait_st();
                 ptx::tc_fence_before();
                 __syncwarp();
@@ -1020,6 +1015,10 @@ __global__ void __launch_bounds__(kThreads, 1)
             if (steps > 0) {
                 ok = __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.o_full[s]), o_phase, err));
                 o_phase ^= 1;
+                if (steps > 1) {
+                    ok = ok && __all_sync(0xffffffffu, ptx::mbar_wait(smem_u32(&sm.o_most[s]), most_phase, err));
+                    most_phase ^= 1;
+                }
                 if (!ok) break;
                 ptx::tc_fence_after();
             }
