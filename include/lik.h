@@ -672,13 +672,15 @@ lik_status lik_cache_write(const void* k, const void* v, lik_dtype dtype, int64_
  * does not matter to it, whatever it holds (NaN codes, scales of pages that
  * are not its own).  Rows that belong to no request are left as they are.
  * Sums and softmax statistics are fp32; the products' operands are fp16: codes
- * exact, q brought into its range by a power of two, and the softmax weights
+ * exact, q brought into its range by a power of two (where it is not fp16
+ * already), and the softmax weights
  * rounded to 11 bits (for fp16 outputs in two parts, 22 bits) over the 20
  * binades below a row's largest one; what is smaller keeps fewer bits, and
  * below 2^-31 of it none.  Scores are fp32 numbers: off by up to 2^-21 of
  * their size, and of at most 2^27 (a row with a larger one is not defined).
  * Results do not depend on the run.  A scale of a seen page that is not finite makes its tokens'
- * scores (k_scale) or the row's output (v_scale) not finite.
+ * scores (k_scale) or the row's output (v_scale) not finite.  A v_scale below
+ * 2^-60 of the largest among the request's pages may count as one of that size.
  *   q, out [rows, q_heads, dim], fp16 or bf16, element (t, h, d) at t *
  *   token_stride + h * head_stride + d, those of out without overlaps; lse
  *   [rows, q_heads] fp32 or NULL;
@@ -731,8 +733,8 @@ lik_status lik_cache_attention(const void* q, lik_dtype dtype, int64_t rows, int
  *   [drafts] int32; offsets [requests + 1]; uniform [drafts], noise
  *   [requests, cols] fp32; tokens [drafts + requests] int32, accepted
  *   [requests] int32, logp [drafts + requests] fp32.  Rows behind the last
- *   request's (offsets[requests] < drafts) are not read, and written as -1, 0.
- *   1 <= cols <= 2^30; 1e-30 <= scale <= 1e30.
+ *   request's (offsets[requests] < drafts) do not matter, and are written as
+ *   -1, 0.  drafts <= 2^20; 1 <= cols <= 2^30; 1e-30 <= scale <= 1e30.
  *   workspace: 16-byte aligned, of lik_verify_drafts_workspace_bytes bytes;
  *   its contents do not matter before and after.  Calls that may overlap need
  *   one each.

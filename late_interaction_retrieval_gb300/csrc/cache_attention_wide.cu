@@ -30,8 +30,9 @@
 // weights -> O and next scores -> weights of a stream (2000 clocks a tile, of
 // which the tensor cores take 620), 14000 clocks at an item's start and end,
 // and with one stream's rows the widening of the codes.  8191 new tokens over
-// 16381, 32 heads, bf16: 504 us, 818 TFLOP/s; 48 requests of 5 drafts over
-// 150001 tokens, 64 heads, fp16: 180 us.
+// 16381, 32 heads, bf16: 480 to 530 us, 780 to 860 TFLOP/s; fp16 with its second
+// product 630 to 720 us; 48 requests of 5 drafts over 150001 tokens, 64 heads,
+// fp16: 178 us.
 #include "cache_attention.h"
 #include "tmap.h"
 

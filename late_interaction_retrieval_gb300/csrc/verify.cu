@@ -6,10 +6,10 @@
 // draft that does not pass, and races its share of that row's columns against
 // the noise; the last block of a request to finish writes its tokens.
 //
-// What bounds them: the first reads every logit once at 63% of the DRAM's
-// cycles, its issue slots 76% used (an exponential a logit); the second reads
+// What bounds them: the first reads every logit once at 66% of the DRAM's
+// cycles, its issue slots 72% used (an exponential a logit); the second reads
 // a row of either model and the noise for each request.  64 requests of 4
-// drafts, 128000 columns, bf16: 48 us, 30 and 23 with cold caches; what the
+// drafts, 128000 columns, bf16: 48 us, 29 and 23 with cold caches; what the
 // second launch does before it needs the first's results overlaps its end.
 #include <cuda_runtime.h>
 

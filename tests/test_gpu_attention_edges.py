@@ -161,3 +161,12 @@ def test_lengths_out_of_range():
         want = ref.attention(q, kc, vc, ks, vs, wide[5], offsets, [51, 0, 49], 0.2)
         one.assert_attention((out, lse), want)
         assert bool((out[3:5] == 0).all()) and bool((lse[3:5] == -math.inf).all())
+
+
+@pytest.mark.parametrize("hint", [1, 1000])
+def test_no_columns_no_pages(hint):
+    """Tables without a column, a cache without a page: rows that see nothing."""
+    q, kc, vc, ks, vs, table, offsets, lengths = one._requests(one._gen(6), [20, 5], [3, 1], 2, 4, 32, 16, "bf16")
+    for case in ((q, kc, vc, ks, vs, table[:, :0], offsets, lengths), (q, kc[:0], vc[:0], ks[:0], vs[:0], table, offsets, lengths)):
+        out, lse = one.run_attention(*case, 0.2, max_added=hint)
+        assert bool((out == 0).all()) and bool((lse == -math.inf).all())
