@@ -726,8 +726,9 @@ lik_status lik_cache_attention(const void* q, lik_dtype dtype, int64_t rows, int
  * drawn from r's distribution.  A column of -inf has probability 0.  A target
  * row with a NaN or +inf logit, or of -inf alone, passes nothing and draws -1;
  * a draft whose own row is such a row does not pass and is replaced from p; a
- * drafted token outside [0, cols) does not pass.  Probabilities are fp32,
- * sums fp32 or wider.
+ * drafted token outside [0, cols) does not pass.  Probabilities are fp32
+ * (below 2^-126 they are 0, and a draft of such a p does not pass), sums fp32
+ * or wider.
  *   target_logits [drafts + requests, cols], draft_logits [drafts, cols] of
  *   one dtype (fp32, fp16, bf16), row r at element r * stride; drafted
  *   [drafts] int32; offsets [requests + 1]; uniform [drafts], noise

@@ -90,7 +90,8 @@ def verify_drafts(target_logits, drafted, offsets, uniform, noise, draft_logits=
     drafted drafted[offsets[b] .. offsets[b + 1]] (none: plain sampling) from
     draft_logits [drafts, cols] (None: looked up, not drawn); its rows of
     target_logits [drafts + requests, cols], tokens and logp begin at
-    offsets[b] + b and are one more.  The accepted[b] drafts that pass come
+    offsets[b] + b and are one more (offsets count drafts alone: not a plan's,
+    see TokenCache.verify_rows).  The accepted[b] drafts that pass come
     first, then one token drawn where they end, then -1.  uniform [drafts] in
     [0, 1) and noise [requests, cols] from the exponential distribution make the
     tokens the target's own; logp are their log-probabilities."""
